@@ -7,6 +7,10 @@ been built, :func:`load` raises; there is no other code path.
 
     o, hT = kda_delta_rule_fwd_gb300.fwd(q, k, v, g, beta, cu_seqlens=..., h0=...)
     o = kda_delta_rule_fwd_gb300.decode(q, k, v, g, beta, state)   # state updated in place
+
+The operators around the recurrence (``conv_fwd``, ``conv_step``, ``conv_bwd``,
+``scan_fwd``, ``scan_step``, ``norm_fwd``, ``norm_bwd``) are documented in
+``layer.py`` and ``include/kda_layer.h``.
 """
 from __future__ import annotations
 
@@ -110,6 +114,7 @@ def load(path: str | None = None):
         lib.kda_status_string.argtypes = [ctypes.c_int]
         lib.kda_version.restype = ctypes.c_char_p
         lib.kda_version.argtypes = []
+        layer.declare(lib)
         if path is None:
             _lib = lib
         return lib
@@ -361,3 +366,9 @@ def decode_commit(q, k, v, g, beta, state, num_commit, *, scale=None, out_dtype=
 def read_device_status(workspace, stream=None) -> int:
     """Synchronise the stream and return (and clear) the status latched on the device."""
     return int(load().kda_read_device_status(_ptr(workspace), _stream_ptr(stream)))
+
+
+# the operators around the recurrence; the module takes the names above
+from . import layer  # noqa: E402
+from .layer import (conv_bwd, conv_fwd, conv_step, norm_bwd, norm_fwd, scan_fwd,  # noqa: E402,F401
+                    scan_step)

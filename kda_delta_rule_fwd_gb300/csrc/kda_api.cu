@@ -7,6 +7,28 @@
 
 using namespace kda;
 
+namespace kda {
+// SMs of the current device for the segment plan, looked up once per device;
+// 152 (a GB300) when there is no device to ask, so sizes computed without a
+// GPU match a GB300's.
+int64_t device_sms() {
+  constexpr int kMaxDev = 64;
+  static int64_t cache[kMaxDev] = {};
+  int dev = -1, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
+    cudaGetLastError();  // clear the error a device-less host leaves behind
+    return kGb300Sms;
+  }
+  if (dev < kMaxDev && cache[dev] > 0) return cache[dev];
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    return kGb300Sms;
+  }
+  if (dev < kMaxDev) cache[dev] = n;
+  return n;
+}
+}  // namespace kda
+
 namespace {
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -38,26 +60,6 @@ kda_status check_ws(const kda_shape* s, void* ws, size_t bytes, bool packed) {
   if (packed && s->num_seqs > 0) need += ws_order_bytes(s->num_seqs);
   if (bytes < need) return KDA_ERR_WORKSPACE;
   return KDA_OK;
-}
-
-// SMs of the current device for the segment plan, looked up once per device;
-// 152 (a GB300) when there is no device to ask, so sizes computed without a
-// GPU match a GB300's.
-int64_t device_sms() {
-  constexpr int kMaxDev = 64;
-  static int64_t cache[kMaxDev] = {};
-  int dev = -1, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
-    cudaGetLastError();  // clear the error a device-less host leaves behind
-    return kGb300Sms;
-  }
-  if (dev < kMaxDev && cache[dev] > 0) return cache[dev];
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-    cudaGetLastError();
-    return kGb300Sms;
-  }
-  if (dev < kMaxDev) cache[dev] = n;
-  return n;
 }
 
 }  // namespace

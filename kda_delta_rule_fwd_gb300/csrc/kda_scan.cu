@@ -1,0 +1,231 @@
+// Selective state-space scan, token by token on the CUDA cores: float32 prompts
+// and the single-token step over resident states.
+//
+//     S <- exp(delta_t A) S + delta_t B_t x_t^T;   y_t = S^T C_t + D x_t
+#include "kda_layer.cuh"
+
+namespace kda {
+namespace layer {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Prompts.  One block per (sequence, head, 32 state columns): a lane owns one
+// column, a warp DS/4 of its rows, in registers.  kTile tokens are staged in
+// shared memory as float32 at a time; the four warps' parts of y are added once
+// per tile.  Bound by the float32 multiply-adds (2 per state element and token).
+// ---------------------------------------------------------------------------
+constexpr int kTile = 16;
+
+template <typename T, typename TO, int DS>
+__global__ void __launch_bounds__(128)
+scan_recurrent_kernel(ScanArgs a) {
+  constexpr int R = DS / 4;  // rows per warp
+  __shared__ __align__(16) float s_b[kTile][DS], s_c[kTile][DS];
+  __shared__ float s_x[kTile][32], s_y[kTile][4][32], s_a[kTile], s_d[kTile];
+  if (blockIdx.x == 0) check_seqlens(a.q, a.status);
+  const int slices = a.dx / 32;
+  const int sl = blockIdx.x % slices;
+  const int64_t chain = blockIdx.x / slices;
+  const int h = (int)(chain % a.H), n = (int)(chain / a.H), g = h / (a.H / a.G);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = sl * 32 + lane;
+  int64_t s0, s1;
+  a.q.range(n, s0, s1);
+  const int64_t base = (chain * DS + warp * R) * (int64_t)a.dx + col;
+  float S[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) S[i] = a.h0 ? a.h0[base + (int64_t)i * a.dx] : 0.f;
+  const float decay = a.A[h], skip = a.D ? a.D[h] : 0.f, bias = a.dtb ? a.dtb[h] : 0.f;
+  const T* x = static_cast<const T*>(a.x) + (int64_t)h * a.dx + sl * 32;
+  const T* dt = static_cast<const T*>(a.dt) + h;
+  const T* Bm = static_cast<const T*>(a.Bm) + (int64_t)g * DS;
+  const T* Cm = static_cast<const T*>(a.Cm) + (int64_t)g * DS;
+  TO* y = static_cast<TO*>(a.y) + (int64_t)h * a.dx + sl * 32;
+  const int64_t ldy = (int64_t)a.H * a.dx;
+  for (int64_t t0 = s0; t0 < s1; t0 += kTile) {
+    const int nt = s1 - t0 < kTile ? (int)(s1 - t0) : kTile;
+    for (int i = threadIdx.x; i < nt * DS; i += 128) {
+      const int t = i / DS, c = i % DS;
+      s_b[t][c] = to_f32(Bm[(t0 + t) * a.ldb + c]);
+      s_c[t][c] = to_f32(Cm[(t0 + t) * a.ldc + c]);
+    }
+    for (int i = threadIdx.x; i < nt * 32; i += 128)
+      s_x[i / 32][i % 32] = to_f32(x[(t0 + i / 32) * a.ldx + i % 32]);
+    if (threadIdx.x < nt) {
+      const float d = step_size(to_f32(dt[(t0 + threadIdx.x) * a.lddt]), bias, a.softplus);
+      s_d[threadIdx.x] = d;
+      s_a[threadIdx.x] = expf(d * decay);
+    }
+    __syncthreads();
+    for (int t = 0; t < nt; ++t) {
+      const float at = s_a[t], xw = s_d[t] * s_x[t][lane];
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < R; i += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(&s_b[t][warp * R + i]);
+        const float4 c = *reinterpret_cast<const float4*>(&s_c[t][warp * R + i]);
+        S[i] = fmaf(at, S[i], b.x * xw);
+        S[i + 1] = fmaf(at, S[i + 1], b.y * xw);
+        S[i + 2] = fmaf(at, S[i + 2], b.z * xw);
+        S[i + 3] = fmaf(at, S[i + 3], b.w * xw);
+        acc[0] = fmaf(c.x, S[i], acc[0]);
+        acc[1] = fmaf(c.y, S[i + 1], acc[1]);
+        acc[2] = fmaf(c.z, S[i + 2], acc[2]);
+        acc[3] = fmaf(c.w, S[i + 3], acc[3]);
+      }
+      s_y[t][warp][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nt * 32; i += 128) {
+      const int t = i / 32, c = i % 32;
+      const float v = (s_y[t][0][c] + s_y[t][1][c]) + (s_y[t][2][c] + s_y[t][3][c]);
+      y[(t0 + t) * ldy + c] = from_f32<TO>(fmaf(skip, s_x[t][c], v));
+    }
+    __syncthreads();
+  }
+  if (a.hT) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) a.hT[base + (int64_t)i * a.dx] = S[i];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Single tokens.  One block of 256 threads per (sequence, head): the state is
+// read once with 16-byte loads (a warp covers whole rows), kept in registers for
+// the step's tokens and written once.  Bound by the state's traffic.
+// ---------------------------------------------------------------------------
+constexpr int kMaxStep = 8;
+
+template <typename T, typename TO, int DS, int DX, bool kCommit>
+__global__ void __launch_bounds__(256, 2)
+scan_step_kernel(ScanArgs a) {
+  constexpr int CQ = DX / 4;        // threads per state row
+  constexpr int RG = 256 / CQ;      // rows per pass
+  constexpr int R = DS / RG;        // rows per thread
+  constexpr int YP = 8;             // y parts: one per warp
+  __shared__ __align__(16) float s_b[kMaxStep][DS], s_c[kMaxStep][DS], s_x[kMaxStep][DX];
+  __shared__ __align__(16) float s_y[kMaxStep][YP][DX];
+  __shared__ float s_a[kMaxStep], s_d[kMaxStep];
+  if (blockIdx.x == 0) check_counts(a.counts, a.q.N, a.T, a.status);
+  const int64_t chain = blockIdx.x;
+  const int h = (int)(chain % a.H), n = (int)(chain / a.H), g = h / (a.H / a.G);
+  const int tid = threadIdx.x, cq = tid % CQ, rg = tid / CQ;
+  float* st = a.state + chain * (int64_t)(DS * DX) + cq * 4;
+  float4 S[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    S[i] = *reinterpret_cast<const float4*>(st + (int64_t)(rg + i * RG) * DX);
+  const T* x = static_cast<const T*>(a.x) + (int64_t)h * DX;
+  const T* Bm = static_cast<const T*>(a.Bm) + (int64_t)g * DS;
+  const T* Cm = static_cast<const T*>(a.Cm) + (int64_t)g * DS;
+  const int64_t tok = (int64_t)n * a.T;
+  for (int i = tid; i < a.T * DS; i += 256) {
+    s_b[i / DS][i % DS] = to_f32(Bm[(tok + i / DS) * a.ldb + i % DS]);
+    s_c[i / DS][i % DS] = to_f32(Cm[(tok + i / DS) * a.ldc + i % DS]);
+  }
+  for (int i = tid; i < a.T * DX; i += 256) s_x[i / DX][i % DX] = to_f32(x[(tok + i / DX) * a.ldx + i % DX]);
+  if (tid < a.T) {
+    const float d = step_size(to_f32(static_cast<const T*>(a.dt)[(tok + tid) * a.lddt + h]),
+                              a.dtb ? a.dtb[h] : 0.f, a.softplus);
+    s_d[tid] = d;
+    s_a[tid] = expf(d * a.A[h]);
+  }
+  int keep = a.T;
+  if (kCommit) {
+    keep = a.counts[n];
+    if (keep < 0 || keep > a.T) keep = 0;
+  }
+  __syncthreads();
+  for (int t = 0; t < a.T; ++t) {
+    const float at = s_a[t], d = s_d[t];
+    const float4 xv = *reinterpret_cast<const float4*>(&s_x[t][cq * 4]);
+    const float4 xw = make_float4(d * xv.x, d * xv.y, d * xv.z, d * xv.w);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float b = s_b[t][rg + i * RG], c = s_c[t][rg + i * RG];
+      S[i].x = fmaf(at, S[i].x, b * xw.x);
+      S[i].y = fmaf(at, S[i].y, b * xw.y);
+      S[i].z = fmaf(at, S[i].z, b * xw.z);
+      S[i].w = fmaf(at, S[i].w, b * xw.w);
+      acc.x = fmaf(c, S[i].x, acc.x);
+      acc.y = fmaf(c, S[i].y, acc.y);
+      acc.z = fmaf(c, S[i].z, acc.z);
+      acc.w = fmaf(c, S[i].w, acc.w);
+    }
+    if constexpr (CQ < 32) {  // two rows per warp pass
+      acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+      acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+      acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+      acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+    }
+    if (CQ == 32 || (tid & 31) < 16)
+      *reinterpret_cast<float4*>(&s_y[t][tid >> 5][cq * 4]) = acc;
+    if (kCommit && t + 1 == keep) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        *reinterpret_cast<float4*>(st + (int64_t)(rg + i * RG) * DX) = S[i];
+    }
+  }
+  if (!kCommit) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      *reinterpret_cast<float4*>(st + (int64_t)(rg + i * RG) * DX) = S[i];
+  }
+  if (!a.y) return;
+  __syncthreads();
+  const float skip = a.D ? a.D[h] : 0.f;
+  TO* y = static_cast<TO*>(a.y) + (int64_t)h * DX;
+  for (int i = tid; i < a.T * DX; i += 256) {
+    const int t = i / DX, c = i % DX;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < YP; ++w) v += s_y[t][w][c];
+    y[(tok + t) * (int64_t)a.H * DX + c] = from_f32<TO>(fmaf(skip, s_x[t][c], v));
+  }
+}
+
+template <typename T, typename TO, int DS>
+cudaError_t recurrent(const ScanArgs& a) {
+  const int64_t grid = (int64_t)a.q.N * a.H * (a.dx / 32);
+  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  scan_recurrent_kernel<T, TO, DS><<<(unsigned)grid, 128, 0, a.stream>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, typename TO>
+cudaError_t recurrent_ds(const ScanArgs& a) {
+  return a.ds == 64 ? recurrent<T, TO, 64>(a) : recurrent<T, TO, 128>(a);
+}
+
+template <typename T, typename TO, int DS, int DX>
+cudaError_t step(const ScanArgs& a) {
+  const int64_t grid = (int64_t)a.q.N * a.H;
+  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (a.counts) scan_step_kernel<T, TO, DS, DX, true><<<(unsigned)grid, 256, 0, a.stream>>>(a);
+  else scan_step_kernel<T, TO, DS, DX, false><<<(unsigned)grid, 256, 0, a.stream>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, typename TO>
+cudaError_t step_size_of(const ScanArgs& a) {
+  if (a.ds == 64) return a.dx == 64 ? step<T, TO, 64, 64>(a) : step<T, TO, 64, 128>(a);
+  return a.dx == 64 ? step<T, TO, 128, 64>(a) : step<T, TO, 128, 128>(a);
+}
+
+}  // namespace
+
+using bf = __nv_bfloat16;
+cudaError_t launch_scan_recurrent(const ScanArgs& a) {
+  if ((int64_t)a.q.N * a.H == 0)
+    return a.status ? cudaMemsetAsync(a.status, 0, sizeof(unsigned int), a.stream) : cudaSuccess;
+  if (a.bf16) return a.out_bf16 ? recurrent_ds<bf, bf>(a) : recurrent_ds<bf, float>(a);
+  return a.out_bf16 ? recurrent_ds<float, bf>(a) : recurrent_ds<float, float>(a);
+}
+cudaError_t launch_scan_step(const ScanArgs& a) {
+  if (a.q.N == 0)
+    return a.status ? cudaMemsetAsync(a.status, 0, sizeof(unsigned int), a.stream) : cudaSuccess;
+  if (a.bf16) return a.out_bf16 ? step_size_of<bf, bf>(a) : step_size_of<bf, float>(a);
+  return a.out_bf16 ? step_size_of<float, bf>(a) : step_size_of<float, float>(a);
+}
+
+}  // namespace layer
+}  // namespace kda
