@@ -167,6 +167,12 @@ struct ScanArgs {
 };
 cudaError_t launch_scan_recurrent(const ScanArgs& a);
 cudaError_t launch_scan_step(const ScanArgs& a);
+// the tensor-core path of bf16 prompts: whether the operands' alignment allows it, what it
+// needs of the workspace past the header, and the call
+bool scan_bf16_ok(const ScanArgs& a);
+size_t scan_bf16_workspace(bool packed, int64_t N, int64_t T, int64_t total, int H, int G, int ds,
+                           int dx, int64_t sms);
+cudaError_t launch_scan_bf16(const ScanArgs& a);
 
 struct NormArgs {
   const void *x, *gate, *res, *dr, *dy;

@@ -90,6 +90,16 @@ kda_status check_scan(const kda_scan_shape* s, bool packed, ScanArgs& a) {
   return KDA_OK;
 }
 
+size_t scan_bytes(const kda_scan_shape* s, bool packed) {
+  if (!s || s->B < 0 || s->T < 0 || s->H < 1 || s->G < 1 || s->num_seqs < 0 ||
+      (s->ds != 64 && s->ds != 128) || (s->dx != 64 && s->dx != 128))
+    return 0;
+  if (s->in_dtype != KDA_BF16) return kWsHeader;
+  return kWsHeader + scan_bf16_workspace(packed, packed ? s->num_seqs : s->B, s->T,
+                                         (int64_t)s->B * s->T, s->H, s->G, s->ds, s->dx,
+                                         device_sms());
+}
+
 void fill_scan(const kda_scan_shape* s, ScanArgs& a, bool packed, const int32_t* cu, const void* x,
                const void* dt, const float* A, const void* Bm, const void* Cm, const float* D,
                const float* dtb, void* y, void* ws, void* stream) {
@@ -206,8 +216,7 @@ kda_status kda_conv_bwd(const kda_conv_shape* s, const void* x, const float* wei
 }
 
 size_t kda_scan_workspace_size(const kda_scan_shape* s) {
-  if (!s) return 0;
-  return kWsHeader;
+  return scan_bytes(s, s && s->num_seqs > 0);
 }
 
 kda_status kda_scan_fwd(const kda_scan_shape* s, const void* x, const void* dt, const float* A,
@@ -226,12 +235,13 @@ kda_status kda_scan_fwd(const kda_scan_shape* s, const void* x, const void* dt, 
                     (const void*)cu_seqlens}, 4) ||
       !all_aligned({(const void*)h0, (const void*)hT}, 16))
     return KDA_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < kda_scan_workspace_size(s))
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < scan_bytes(s, packed))
     return KDA_ERR_WORKSPACE;
   fill_scan(s, a, packed, cu_seqlens, x, dt, A, Bm, Cm, D, dt_bias, y, workspace, stream);
   a.h0 = h0;
   a.hT = hT;
-  return launched(launch_scan_recurrent(a));
+  a.ws = static_cast<char*>(workspace) + kWsHeader;
+  return launched(scan_bf16_ok(a) ? launch_scan_bf16(a) : launch_scan_recurrent(a));
 }
 
 kda_status kda_scan_step(const kda_scan_shape* s, const void* x, const void* dt, const float* A,
