@@ -13,8 +13,9 @@
 //     U  [channel][state row] = (w x)^T B
 //     Yi [channel][token]     = Sb C^T     (Sb: S^T, A operand in tensor memory)
 //     Yx [channel][token]     = x^T M^T    (one per head)
-// B, C and x are bf16 as given; w x, Sb and M enter as bf16 hi + lo (16 bits).  D sits on
-// M's diagonal.  S itself stays float32 in the registers of the state warps.
+// B, C and x are bf16 as given; Sb and M enter as bf16 hi + lo (16 bits), w x in three parts
+// (24 bits, as S is kept in float32).  D sits on M's diagonal.  S itself stays float32 in the
+// registers of the state warps.
 //
 // One persistent CTA per SM; its warps are specialised and hand chunks on through
 // mbarriers, so that the tensor core works on one chunk while other warps prepare the next
@@ -22,9 +23,9 @@
 //     warps 0-7    state: S = 2^c_last S + U in registers (columns split in two), Sb
 //     warps 8-11   outputs: y = 2^c Yi + Yx to global memory
 //     warps 12,13,17   M from G (the three 32 x 32 blocks on and below the diagonal)
-//     warps 14,15,18,19  w x hi/lo from the x tile; zero rows past the sequence's end
-//     warp 20      work items, tile loads (TMA, 128-byte swizzle, two stages)
-//     warps 21, 23 tcgen05.mma: G and U; Yi and Yx (one thread each)
+//     warps 14,15,18,19,24-27  w x in parts from the x tile; zero rows past the sequence's end
+//     warps 21, 23, 16 tcgen05.mma: G and U; Yi; Yx (one thread each)
+//     warp 20      work items, tile loads (TMA, 128-byte swizzle)
 //     warp 22      per-token factors (delta, running sums, weights)
 // The code of one chunk's steady state has to stay inside the SM's instruction cache with
 // all roles at work: loops that need no register arrays are kept rolled, and items are decoded
@@ -49,21 +50,20 @@ using pf::bf16_hi;
 using pf::bf16_lo;
 using pf::ex2;
 using pf::pack2;
-using pf::split_pack2;
 
 constexpr int Q = 64;              // tokens per chunk
-constexpr int kScanThreads = 768;  // 24 warps
-constexpr int kStages = 2;         // tile stages
+constexpr int kScanThreads = 896;  // 28 warps
 constexpr int kRing = 4;           // chunks of per-token factors
 constexpr int kItems = 4;          // items handed out ahead
-constexpr int kLoadWarp = 20, kStateMmaWarp = 21, kFactorWarp = 22, kOutMmaWarp = 23;
+constexpr int kLoadWarp = 20, kStateMmaWarp = 21, kFactorWarp = 22, kYiMmaWarp = 23, kYxMmaWarp = 16;
 constexpr int kTile = 8192;        // 64 tokens x 64 channels of bf16, 128-byte rows
 
 // tensor memory columns: U, Sb hi and lo, G, then Yi and Yx.  One head of 128 channels
 // leaves room for two Yi; two heads have a Yx each.
 constexpr uint32_t TM_U = 0, TM_SB = 128, TM_G = 256, TM_YI = 320, TM_YX = 448, TM_ALL = 512;
 constexpr uint32_t TM_YX2 = 384;  // two heads: the second one's Yx
-constexpr int kStateRegs = 120, kOtherRegs = 56;  // of 80 at launch: 2 * 120 + 4 * 56 <= 6 * 80
+// of 72 at launch: 2 * 120 + 72 + 4 * 48 <= 7 * 72
+constexpr int kStateRegs = 120, kOutRegs = 72, kOtherRegs = 48;
 
 // per-token factors of one head and chunk, in shared memory
 struct Factors {
@@ -79,36 +79,41 @@ struct Factors {
 
 template <int DS, int HPC>
 struct Layout {
-  static constexpr int kB = DS / 64 * kTile;        // bytes of a B or C tile
+  static constexpr int kStages = HPC == 1 ? 3 : 2;   // tile stages, as many as fit
+  static constexpr int kB = DS / 64 * kTile;         // bytes of a B or C tile
   static constexpr int kStage = 2 * kB + 2 * kTile;  // C, B, x
   static constexpr int kC = 0, kBt = kB, kX = 2 * kB;
-  static constexpr int kWx = kStages * kStage;       // [2][hi, lo][2 tiles]
-  static constexpr int kM = kWx + 2 * 4 * kTile;     // [HPC][hi, lo]
-  static constexpr int kF = kM + 2 * HPC * kTile;    // Factors [kRing][HPC]
-  static constexpr int kY = (kF + kRing * HPC * (int)sizeof(Factors) + 1023) / 1024 * 1024;  // y
-  static constexpr int kBars = kY + 2 * kTile;
+  static constexpr int kWx = kStages * kStage;       // [3 parts][2 tiles]
+  static constexpr int kM = kWx + 6 * kTile;         // [HPC][hi, lo]
+  static constexpr int kY = kM + 2 * HPC * kTile;    // 32 tokens of y
+  static constexpr int kF = kY + kTile;              // Factors [kRing][HPC]
+  static constexpr int kBars = kF + kRing * HPC * (int)sizeof(Factors);
   static constexpr int kBytes = kBars + 768 + 1024;  // + alignment of the base to 1024
 };
 
-enum Bar {  // mbarriers
-  B_FULL = 0,               // [kStages] tiles have landed
-  B_EMPTY = 2,              // [kStages] the chunk's products are done
-  B_FFULL = 4,              // [kRing] factors written
-  B_FEMPTY = 8,             // [kRing] factors read
-  B_G = 12,                 // G complete
-  B_M = 13,                 // M written (and G read)
-  B_X = 14,                 // [2] w x written
-  B_S = 16,                 // Sb written
-  B_U = 17,                 // [2] U complete (and its w x buffer free)
-  B_UFREE = 19,             // U read
-  B_YI = 20,                // Yi complete (Sb free)
-  B_Y = 21,                 // Yi and Yx complete
-  B_YFREE = 22,             // Yi and Yx read
-  B_DRAIN = 23,
-  B_IFULL = 24,             // [kItems] item published
-  B_IEMPTY = 28,            // [kItems] item read by every warp that takes items
-  B_FULLX = 32,             // [kStages] the x tile has landed (B_FULL: B and C)
-  B_COUNT = 34
+// mbarriers.  A phase is waited for by its parity, so that a barrier may not complete the phase
+// after the next before every one of its waiters has seen this one: where the waiters do not
+// hold each other up, there is one barrier per stage or per parity of the chunk.
+enum Bar {
+  B_FULL = 0,               // [stages] B and C tiles have landed
+  B_FULLX = 3,              // [stages] the x tile has
+  B_EMPTY = 6,              // [stages] the chunk's products are done
+  B_FFULL = 9,              // [kRing] factors written
+  B_FEMPTY = 13,            // [kRing] factors read
+  B_IFULL = 17,             // [kItems] item published
+  B_IEMPTY = 21,            // [kItems] item read by every warp that takes items
+  B_G = 25,                 // G complete
+  B_M = 26,                 // M written (and G read)
+  B_X = 27,                 // [stages][2] w x written, tokens 0-31 and 32-63
+  B_WX = 33,                // [2] those w x free
+  B_U = 35,                 // U complete
+  B_UFREE = 36,             // U read
+  B_S = 37,                 // Sb written
+  B_YI = 38,                // [2] Yi complete (and Sb free)
+  B_YX = 40,                // Yx complete (and M free)
+  B_YFREE = 41,             // [2] Yi and Yx read
+  B_DRAIN = 43,
+  B_COUNT = 44
 };
 
 struct ScanParams {
@@ -225,40 +230,107 @@ __device__ __forceinline__ float step_size_fast(float dt, float bias, bool softp
   return fmaf(2.f * s, v, fmaxf(x, 0.f));
 }
 
+// bf16 parts of two values, packed (first value in the low half); each remainder is exact
+__device__ __forceinline__ float2 part_of(float2 v, uint32_t& p) {
+  p = pack2(v.x, v.y);
+  return fma2(make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)), make_float2(-1.f, -1.f), v);
+}
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const float2 r = part_of(make_float2(a, b), hi);
+  lo = pack2(r.x, r.y);
+}
+__device__ __forceinline__ void split3(float2 v, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+  const float2 r = part_of(part_of(v, p0), p1);
+  p2 = pack2(r.x, r.y);
+}
+
+// Wait for the phase of a barrier with the given parity; 0 when it does not come.  Each try
+// suspends the thread for a while (about half a microsecond); the limit is between 20 ms and a
+// second.  In few instructions: there are many waits, and the code has to stay small.
+__device__ __forceinline__ uint32_t wait_phase(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n"
+      "TRY:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.and.u32 q, n, 0x100000, !p;\n\t"
+      "@q bra TRY;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+
+__device__ __forceinline__ uint32_t try_phase(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+
 struct Ctx {
-  uint64_t* bars;
-  volatile uint32_t* abort;
-  // wait for the phase with the given parity; false when the CTA gives up.  Each try suspends
-  // the thread for a while (about half a microsecond); the limit is between 20 ms and a second.
+  uint32_t bars;             // shared address of the barriers
+  volatile uint32_t* abort;  // raised when a wait ran out
+  uint32_t lane;
   __device__ __forceinline__ bool wait_one(int bar, uint32_t parity) const {
-    uint32_t tries = 0;
-    while (!mbar_try_wait(bars + bar, parity)) {
-      if (*abort || ++tries > (1u << 20)) {
-        *abort = 1u;
-        return false;
-      }
-    }
-    return true;
+    if (wait_phase(bars + 8 * bar, parity)) return true;
+    *abort = 1u;
+    return false;
+  }
+  // up to three phases, whose first tries overlap (a try alone takes about 200 cycles)
+  __device__ __forceinline__ bool wait_all(int bar, uint32_t parity, int bar2, uint32_t parity2, int bar3 = -1,
+                                           uint32_t parity3 = 0) const {
+    const uint32_t a = try_phase(bars + 8 * bar, parity);
+    const uint32_t b = bar2 < 0 ? 1u : try_phase(bars + 8 * bar2, parity2);
+    const uint32_t d = bar3 < 0 ? 1u : try_phase(bars + 8 * bar3, parity3);
+    return (a || wait_one(bar, parity)) && (b || wait_one(bar2, parity2)) && (d || wait_one(bar3, parity3));
   }
   // the same by a whole warp, which stays converged
   __device__ __forceinline__ bool wait(int bar, uint32_t parity) const {
     return __all_sync(0xffffffffu, wait_one(bar, parity));
   }
-  // by a group of `count` threads that meets at named barrier `id`: its first warp waits for one
-  // or two phases (every waiting warp takes issue slots from the working ones)
+  __device__ __forceinline__ bool wait(int bar, uint32_t parity, int bar2, uint32_t parity2, int bar3 = -1,
+                                       uint32_t parity3 = 0) const {
+    return __all_sync(0xffffffffu, wait_all(bar, parity, bar2, parity2, bar3, parity3));
+  }
+  // by the warps of a group, which meet at named barrier `id`: its first warp waits (every waiting
+  // warp takes issue slots from the working ones) and all of them get the same answer, so that
+  // none leaves while another stays.
   __device__ __forceinline__ bool wait_group(int id, int count, bool first, int bar, uint32_t parity,
-                                             int bar2 = -1, uint32_t parity2 = 0) const {
+                                             int bar2 = -1, uint32_t parity2 = 0, int bar3 = -1,
+                                             uint32_t parity3 = 0) const {
+    int ok = 1;
     if (first) {
-      wait_one(bar, parity);
-      if (bar2 >= 0) wait_one(bar2, parity2);
+      ok = wait_all(bar, parity, bar2, parity2, bar3, parity3);
       __syncwarp();
     }
-    pf::named_bar_sync(id, count);
-    return *abort == 0;
+    int all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.s32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+        "selp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(ok), "r"(id), "r"(count)
+        : "memory");
+    return all != 0;
   }
   __device__ __forceinline__ void arrive_warp(int bar) const {  // one arrival per warp
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bars + bar);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.eq.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bars + 8 * bar),
+        "r"(lane)
+        : "memory");
   }
 };
 
@@ -284,6 +356,42 @@ __device__ __forceinline__ uint64_t op_desc(uint32_t lo) {
   return ((uint64_t)hi << 32) | lo;
 }
 __device__ __forceinline__ uint32_t op_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+
+// Products and commits by one lane of a converged warp: the whole warp runs the code around them,
+// so that descriptors are formed in uniform registers.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_ss_by(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "setp.ne.u32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_by(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "setp.ne.u32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_by(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.u32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
 
 // 32 columns of 16 lanes as 8 x 8 matrix fragments: r[4 q ..] holds columns 8 q + 2 (lane % 4)
 // + {0, 1} of rows lane / 4 and lane / 4 + 8
@@ -311,6 +419,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
                   const __grid_constant__ CUtensorMap tm_c, const ScanParams p) {
   using L = Layout<DS, HPC>;
+  constexpr int kStages = L::kStages;
   constexpr int DX = 128 / HPC;
   extern __shared__ unsigned char raw[];
   unsigned char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -329,23 +438,23 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     auto init = [&](int b, int n, uint32_t count) {
       for (int i = 0; i < n; ++i) mbar_init(bars + b + i, count);
     };
-    init(B_FULL, kStages, 1);
-    init(B_FULLX, kStages, 1);
-    init(B_EMPTY, kStages, kState ? 1 : 2);
+    init(B_FULL, 6, 1);
+    init(B_EMPTY, 3, kState ? 1 : 3);
     init(B_FFULL, kRing, 1);
-    init(B_FEMPTY, kRing, kState ? 12 : 19);
+    init(B_FEMPTY, kRing, kState ? 16 : 23);  // state 8, w x 8, outputs 4, M 3
+    init(B_IFULL, kItems, 1);
+    init(B_IEMPTY, kItems, kState ? 18 : 27);  // those, the products' warps, the factors'
     init(B_G, 1, 1);
     init(B_M, 1, 3);
-    init(B_X, 2, 4);
-    init(B_S, 1, 8);
-    init(B_U, 2, 1);
+    init(B_X, 6, 8);
+    init(B_WX, 2, 1);
+    init(B_U, 1, 1);
     init(B_UFREE, 1, 8);
-    init(B_YI, 1, 1);
-    init(B_Y, 1, 1);
-    init(B_YFREE, 1, 4);
-    init(B_DRAIN, 1, kState ? 1 : 2);
-    init(B_IFULL, kItems, 1);
-    init(B_IEMPTY, kItems, kState ? 14 : 22);  // state, outputs, M, w x, products, factors
+    init(B_S, 1, 8);
+    init(B_YI, 2, 1);
+    init(B_YX, 1, 1);
+    init(B_YFREE, 2, 4);
+    init(B_DRAIN, 1, kState ? 1 : 3);
     *s_abort = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_x);
@@ -365,10 +474,17 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
   tc_fence_after();
   const uint32_t tb = *s_tmem;
   const uint32_t sbase = smem_u32(sm);
-  const Ctx cx{bars, s_abort};
+  const Ctx cx{smem_u32(bars), s_abort, (uint32_t)lane};
 
-  // the next item; false when there is none (or the CTA gives up)
-  auto next_item = [&](uint32_t& m, Item& it) {
+  // the next item, for the warps of a group; false when there is none (or the CTA gives up)
+  auto next_item = [&](int id, int count, bool first, uint32_t& m, Item& it) {
+    if (!cx.wait_group(id, count, first, B_IFULL + m % kItems, (m / kItems) & 1)) return false;
+    it = s_items[m % kItems];
+    cx.arrive_warp(B_IEMPTY + m % kItems);
+    ++m;
+    return it.valid != 0;
+  };
+  auto next_item_alone = [&](uint32_t& m, Item& it) {  // for one warp
     if (!cx.wait(B_IFULL + m % kItems, (m / kItems) & 1)) return false;
     it = s_items[m % kItems];
     cx.arrive_warp(B_IEMPTY + m % kItems);
@@ -388,7 +504,7 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const uint32_t tu = tb + lane_base + TM_U + half * kCols;
     const uint32_t tsb = tb + lane_base + TM_SB + half * (kCols / 2);
     bool alive = true;
-    while (alive && next_item(m, it)) {
+    while (alive && next_item(2, 256, warp == 0, m, it)) {
       const bool on = k < it.nh;
       const int head = it.h0 + k;
       const int64_t at = ((int64_t)head * DS + half * kCols) * DX + (HPC == 2 ? ch & 63 : ch);
@@ -415,7 +531,7 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 #pragma unroll 1
       for (int ci = 0; ci <= it.chunks; ++ci) {
         if (ci > 0) {  // S = alpha S + U of the chunk before
-          if (!cx.wait_group(2, 256, warp == 0, B_U + ((c - 1) & 1), ((c - 1) >> 1) & 1)) { alive = false; break; }
+          if (!cx.wait_group(2, 256, warp == 0, B_U, (c - 1) & 1)) { alive = false; break; }
           tc_fence_after();
           const float2 al = make_float2(alpha, alpha);
 #pragma unroll
@@ -436,19 +552,22 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         } else if (it.chunks == 0) {
           break;
         }
-        if (!cx.wait(B_FFULL + c % kRing, (c / kRing) & 1)) { alive = false; break; }
+        // the factors; Sb may be rewritten once the last product with it is done
+        if (!cx.wait_group(2, 256, warp == 0, B_FFULL + c % kRing, (c / kRing) & 1,
+                           !kState && c > 0 ? B_YI + (int)((c - 1) & 1) : -1, ((c - 1) >> 1) & 1)) {
+          alive = false;
+          break;
+        }
         alpha = factors[(c % kRing) * HPC + k].alpha;
         decay *= alpha;
         cx.arrive_warp(B_FEMPTY + c % kRing);
         if (!kState) {
-          // Sb may be rewritten once the last product with it is done
-          if (c > 0 && !cx.wait_group(2, 256, warp == 0, B_YI, (c - 1) & 1)) { alive = false; break; }
           tc_fence_after();
 #pragma unroll
           for (int col = 0; col < kCols; col += 32) {
             uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) split_pack2(S[col + 2 * e], S[col + 2 * e + 1], hi[e], lo[e]);
+            for (int e = 0; e < 16; ++e) split2(S[col + 2 * e], S[col + 2 * e + 1], hi[e], lo[e]);
             tmem_st16(tsb + col / 2, hi);
             tmem_st16(tsb + DS / 2 + col / 2, lo);
           }
@@ -475,17 +594,19 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
   }
 
   if (warp >= 8 && warp < 12 && !kState) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     // ---- outputs
     const int64_t ldy = (int64_t)p.H * DX;
     bool alive = true;
-    while (alive && next_item(m, it)) {
+    while (alive && next_item(1, 128, warp == 8, m, it)) {
 #pragma unroll 1
       for (int ci = 0; ci < it.chunks; ++ci, ++c) {
         const int left = it.len - ci * Q;
         const int n = left < Q ? left : Q;
         const int k = HPC == 2 ? quad >> 1 : 0;
         const Factors& f = factors[(c % kRing) * HPC + k];
-        if (!cx.wait(B_FFULL + c % kRing, (c / kRing) & 1) || !cx.wait_group(1, 128, warp == 8, B_Y, c & 1)) {
+        if (!cx.wait_group(1, 128, warp == 8, B_FFULL + c % kRing, (c / kRing) & 1, B_YI + (c & 1),
+                           (c >> 1) & 1, B_YX, c & 1)) {
           alive = false;
           break;
         }
@@ -494,45 +615,56 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         const uint32_t tx = tb + lane_base + (HPC == 2 && k ? TM_YX2 : TM_YX);
         const int64_t row0 = it.t0 + ci * Q;
         if (p.out_bf16) {
-          // y^T fragments, transposed into a [token][channel] tile (128-byte swizzle) and out
-          const uint32_t ys = sbase + L::kY + (quad >> 1) * kTile;
-#pragma unroll 1
+          // y^T fragments, transposed into a [token][channel] tile (128-byte swizzle) and out,
+          // 32 tokens at a time
+          const uint32_t ys = sbase + L::kY + (quad >> 1) * (kTile / 2);
+          const int u = threadIdx.x - 256;  // 16-byte unit within 8 rows of both halves
+          const int hf = (u >> 3) & 1, ck = u & 7;
+          uint16_t* y = static_cast<uint16_t*>(p.y) + row0 * ldy + (int64_t)it.h0 * DX + hf * 64 + ck * 8;
+          const int most = HPC == 1 || hf < it.nh ? n : 0;
+          uint32_t w[4][8];  // both halves leave tensor memory first
+#pragma unroll
           for (int part = 0; part < 4; ++part) {
-            const int rows = (part >> 1) * 16, j = (part & 1) * 32;
+            const int rows = (part & 1) * 16, j = (part >> 1) * 32;
             float a[16], b[16];
             tmem_ld_frag(ti + ((uint32_t)rows << 16) + j, a);
             tmem_ld_frag(tx + ((uint32_t)rows << 16) + j, b);
             tmem_wait_ld();
-            uint32_t w[8];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float2 e = *reinterpret_cast<const float2*>(&f.e[j + 8 * q + 2 * (lane & 3)]);
               const float2 y0 = fma2(e, make_float2(a[4 * q], a[4 * q + 1]), make_float2(b[4 * q], b[4 * q + 1]));
               const float2 y1 = fma2(e, make_float2(a[4 * q + 2], a[4 * q + 3]), make_float2(b[4 * q + 2], b[4 * q + 3]));
-              w[2 * q] = pack2(y0.x, y0.y);
-              w[2 * q + 1] = pack2(y1.x, y1.y);
+              w[part][2 * q] = pack2(y0.x, y0.y);
+              w[part][2 * q + 1] = pack2(y1.x, y1.y);
             }
-            // matrices (token block, channel block) in the order (q, 0), (q, 1), (q + 1, 0), (q + 1, 1)
-            const int tok = j + ((lane >> 4) << 3) + (lane & 7);
-            const int chunk = ((quad & 1) << 2) + (rows >> 3) + ((lane >> 3) & 1);
-            const uint32_t ad = ys + tok * 128 + ((chunk ^ (tok & 7)) << 4);
-            stmatrix4_trans(ad, w[0], w[1], w[2], w[3]);
-            stmatrix4_trans(ad + 16 * 128, w[4], w[5], w[6], w[7]);
           }
           tc_fence_before();
-          cx.arrive_warp(B_YFREE);
+          cx.arrive_warp(B_YFREE + (c & 1));
           cx.arrive_warp(B_FEMPTY + c % kRing);
-          pf::named_bar_sync(1, 128);
-          const int u = threadIdx.x - 256;  // 16-byte unit within 8 rows of both halves
-          const int hf = (u >> 3) & 1, ck = u & 7;
-          uint16_t* y = static_cast<uint16_t*>(p.y) + row0 * ldy + (int64_t)it.h0 * DX + hf * 64 + ck * 8;
-          if (HPC == 1 || hf < it.nh) {
-#pragma unroll 4
-            for (int r = u >> 4; r < n; r += 8)
-              *reinterpret_cast<uint4*>(y + r * ldy) = *reinterpret_cast<const uint4*>(
-                  sm + L::kY + hf * kTile + r * 128 + ((ck ^ (r & 7)) << 4));
+          // matrices (token block, channel block) in the order (q, 0), (q, 1), (q + 1, 0), (q + 1, 1)
+          const int tok = ((lane >> 4) << 3) + (lane & 7);
+          const int chunk = ((quad & 1) << 2) + ((lane >> 3) & 1);
+          const uint32_t ad = ys + tok * 128;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t o = ((chunk + 2 * r) ^ (tok & 7)) << 4;
+              const uint32_t(&v)[8] = w[2 * j + r];
+              stmatrix4_trans(ad + o, v[0], v[1], v[2], v[3]);
+              stmatrix4_trans(ad + o + 16 * 128, v[4], v[5], v[6], v[7]);
+            }
+            pf::named_bar_sync(1, 128);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = (u >> 4) + 8 * i;
+              if (32 * j + r < most)
+                *reinterpret_cast<uint4*>(y + (32 * j + r) * ldy) = *reinterpret_cast<const uint4*>(
+                    sm + L::kY + hf * (kTile / 2) + r * 128 + ((ck ^ (r & 7)) << 4));
+            }
+            pf::named_bar_sync(1, 128);
           }
-          pf::named_bar_sync(1, 128);
         } else {
           const int ch = quad * 32 + lane;
           float* y = static_cast<float*>(p.y) + row0 * ldy + (int64_t)it.h0 * DX + ch;
@@ -550,27 +682,26 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             }
           }
           tc_fence_before();
-          cx.arrive_warp(B_YFREE);
+          cx.arrive_warp(B_YFREE + (c & 1));
           cx.arrive_warp(B_FEMPTY + c % kRing);
         }
       }
     }
-  } else if (warp >= 12 && warp < 20 && quad < 2) {
+  } else if (warp == 12 || warp == 13 || warp == 17) {
     // ---- M = decayed G, the blocks on and below the diagonal
     const int jb = warp >= 16 ? 32 : 0;  // first column
-    if (!kState && !(jb == 32 && quad == 0)) {
+    if (!kState) {
       const int row = quad * 32 + lane;
       const bool diag = quad * 32 == jb;
       bool alive = true;
-      while (alive && next_item(m, it)) {
+      while (alive && next_item_alone(m, it)) {
         float skip[HPC];
 #pragma unroll
         for (int k = 0; k < HPC; ++k) skip[k] = p.D && k < it.nh ? p.D[it.h0 + k] : 0.f;
 #pragma unroll 1
         for (int ci = 0; ci < it.chunks; ++ci, ++c) {
           // G is there, and the products that read the last M are done
-          if (!cx.wait(B_FFULL + c % kRing, (c / kRing) & 1) ||
-              !cx.wait_group(3, 96, warp == 12, B_G, c & 1, c > 0 ? B_Y : -1, (c - 1) & 1)) {
+          if (!cx.wait(B_FFULL + c % kRing, (c / kRing) & 1, B_G, c & 1, c > 0 ? B_YX : -1, (c - 1) & 1)) {
             alive = false;
             break;
           }
@@ -598,14 +729,17 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = g[e] * (u * f.v[j + e]);
               }
-              uint4 hi, lo;
-              split_pack2(v[0], v[1], hi.x, lo.x);
-              split_pack2(v[2], v[3], hi.y, lo.y);
-              split_pack2(v[4], v[5], hi.z, lo.z);
-              split_pack2(v[6], v[7], hi.w, lo.w);
-              const int o = (((jb + j) >> 3) ^ (row & 7)) << 4;
-              *reinterpret_cast<uint4*>(mt + o) = hi;
-              *reinterpret_cast<uint4*>(mt + kTile + o) = lo;
+#pragma unroll
+              for (int e = 0; e < 8; e += 8) {
+                uint4 hi, lo;
+                split2(v[e], v[e + 1], hi.x, lo.x);
+                split2(v[e + 2], v[e + 3], hi.y, lo.y);
+                split2(v[e + 4], v[e + 5], hi.z, lo.z);
+                split2(v[e + 6], v[e + 7], hi.w, lo.w);
+                const int o = (((jb + j + e) >> 3) ^ (row & 7)) << 4;
+                *reinterpret_cast<uint4*>(mt + o) = hi;
+                *reinterpret_cast<uint4*>(mt + kTile + o) = lo;
+              }
             }
           }
           fence_proxy_async_smem();
@@ -615,59 +749,63 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         }
       }
     }
-  } else if (warp >= 12 && warp < 20) {
-    // ---- w x, hi and lo, in the x tile's own layout
-    const int xt = ((warp - 14) >> 2) * 64 + (warp & 1) * 32 + lane;  // 0 .. 127
+  } else if (warp == 14 || warp == 15 || warp == 18 || warp == 19 || warp >= 24) {
+    // ---- w x in three parts, in the x tile's own layout
+    const int xw = warp >= 24 ? warp - 20 : ((warp - 14) >> 2) * 2 + (warp & 1);
+    const int xt = xw * 32 + lane;  // 0 .. 255
+    uint32_t st = 0, ph = 0;
     bool alive = true;
-    while (alive && next_item(m, it)) {
+    while (alive && next_item_alone(m, it)) {
 #pragma unroll 1
       for (int ci = 0; ci < it.chunks; ++ci, ++c) {
         const int left = it.len - ci * Q;
         const int n = left < Q ? left : Q;
-        const int st = c % kStages;
-        if (!cx.wait(B_FFULL + c % kRing, (c / kRing) & 1) ||
-            !cx.wait_group(4, 128, warp == 14, B_FULLX + st, (c / kStages) & 1,
-                           c >= 2 ? B_U + (int)(c & 1) : -1, ((c >> 1) - 1) & 1)) {
-          alive = false;
-          break;
-        }
         unsigned char* x = sm + st * L::kStage + L::kX + xt * 16;
-        unsigned char* hi = sm + L::kWx + (c & 1) * 4 * kTile + xt * 16;
+        unsigned char* wx = sm + L::kWx + xt * 16;
         const Factors* f = factors + (c % kRing) * HPC;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 2
-        for (int q = 0; q < 8; ++q) {
-          const int tok = (xt >> 3) + (q & 3) * 16;  // row of this 16-byte unit
-          uint4 a = zero, b = zero;
-          if (tok < n) {
-            const float w = f[HPC == 2 ? q >> 2 : 0].w[tok];
-            const float2 w2 = make_float2(w, w);
-            const uint4 v = *reinterpret_cast<const uint4*>(x + q * 2048);
-            float2 r;
-            r = mul2(w2, make_float2(bf16_lo(v.x), bf16_hi(v.x)));
-            split_pack2(r.x, r.y, a.x, b.x);
-            r = mul2(w2, make_float2(bf16_lo(v.y), bf16_hi(v.y)));
-            split_pack2(r.x, r.y, a.y, b.y);
-            r = mul2(w2, make_float2(bf16_lo(v.z), bf16_hi(v.z)));
-            split_pack2(r.x, r.y, a.z, b.z);
-            r = mul2(w2, make_float2(bf16_lo(v.w), bf16_hi(v.w)));
-            split_pack2(r.x, r.y, a.w, b.w);
-          } else {  // what follows the sequence may hold anything
-            *reinterpret_cast<uint4*>(x + q * 2048) = zero;
-          }
-          *reinterpret_cast<uint4*>(hi + q * 2048) = a;
-          *reinterpret_cast<uint4*>(hi + 2 * kTile + q * 2048) = b;
-        }
-        if (n < Q) {
-          if (!cx.wait(B_FULL + st, (c / kStages) & 1)) { alive = false; break; }
-          unsigned char* bt = sm + st * L::kStage + L::kBt;
+        // 32 tokens at a time: the state update takes the first while the others are formed
 #pragma unroll 1
-          for (int idx = xt; idx < L::kB / 16; idx += 128)
-            if (((idx >> 3) & 63) >= n) *reinterpret_cast<uint4*>(bt + idx * 16) = zero;
+        for (int h = 0; h < 2; ++h) {
+          if (!(h == 0 ? cx.wait(B_FULLX + st, ph, B_FFULL + c % kRing, (c / kRing) & 1, c > 0 ? B_WX : -1, (c - 1) & 1)
+                       : c == 0 || cx.wait(B_WX + 1, (c - 1) & 1))) {
+            alive = false;
+            break;
+          }
+#pragma unroll 1
+          for (int q = 0; q < 512 / 256; ++q) {
+            // 16-byte unit: tile (64 channels) q / (256 / 256), token row in the half
+            const int o = (q / (256 / 256)) * kTile + h * (kTile / 2) + (q % (256 / 256)) * 256 * 16;
+            const int tok = h * 32 + (xt >> 3) + (q % (256 / 256)) * (256 / 8);
+            uint4 a = zero, b = zero, d = zero;
+            if (tok < n) {
+              const float w = f[HPC == 2 ? q / (256 / 256) : 0].w[tok];
+              const float2 w2 = make_float2(w, w);
+              const uint4 v = *reinterpret_cast<const uint4*>(x + o);
+              split3(mul2(w2, make_float2(bf16_lo(v.x), bf16_hi(v.x))), a.x, b.x, d.x);
+              split3(mul2(w2, make_float2(bf16_lo(v.y), bf16_hi(v.y))), a.y, b.y, d.y);
+              split3(mul2(w2, make_float2(bf16_lo(v.z), bf16_hi(v.z))), a.z, b.z, d.z);
+              split3(mul2(w2, make_float2(bf16_lo(v.w), bf16_hi(v.w))), a.w, b.w, d.w);
+            } else {  // what follows the sequence may hold anything
+              *reinterpret_cast<uint4*>(x + o) = zero;
+            }
+            *reinterpret_cast<uint4*>(wx + o) = a;
+            *reinterpret_cast<uint4*>(wx + 2 * kTile + o) = b;
+            *reinterpret_cast<uint4*>(wx + 4 * kTile + o) = d;
+          }
+          if (n < Q && h == 0) {  // B's rows past the end, before either half is used
+            if (!cx.wait(B_FULL + st, ph)) { alive = false; break; }
+            unsigned char* bt = sm + st * L::kStage + L::kBt;
+#pragma unroll 1
+            for (int idx = xt; idx < L::kB / 16; idx += 256)
+              if (((idx >> 3) & 63) >= n) *reinterpret_cast<uint4*>(bt + idx * 16) = zero;
+          }
+          fence_proxy_async_smem();
+          cx.arrive_warp(B_X + 2 * st + h);
         }
-        fence_proxy_async_smem();
-        cx.arrive_warp(B_X + (c & 1));
+        if (!alive) break;
         cx.arrive_warp(B_FEMPTY + c % kRing);
+        if (++st == kStages) { st = 0; ph ^= 1; }
       }
     }
   } else if (warp == kLoadWarp) {
@@ -690,7 +828,7 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         if (!publish(it)) { alive = false; break; }
 #pragma unroll 1
         for (int ci = 0; ci < it.chunks; ++ci, ++c) {
-          const int st = c % kStages;
+          const uint32_t st = c % kStages;
           if (c >= kStages && !cx.wait_one(B_EMPTY + st, ((c / kStages) - 1) & 1)) { alive = false; break; }
           unsigned char* s = sm + st * L::kStage;
           uint64_t* bar = bars + B_FULL + st;
@@ -720,87 +858,101 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         }
     }
     __syncwarp();
-  } else if (warp == kStateMmaWarp || (warp == kOutMmaWarp && !kState)) {
-    // ---- products, issued by one thread: G and U, or Yi and Yx.  The loops are rolled: a warp
-    // alone on its code pays for every line of it.
-    if (lane == 0) {
-      constexpr uint32_t id_g = idesc_bf16(128, 64, 0, 0);
-      constexpr uint32_t id_x = idesc_bf16(128, 64, 1, 0);
-      constexpr uint32_t id_u = idesc_bf16(128, DS, 1, 1);
-      const uint32_t kmaj = op_lo(sbase, 0), mnmaj = op_lo(sbase, kTile);
-      bool alive = true;
-      while (alive) {
-        if (!cx.wait_one(B_IFULL + m % kItems, (m / kItems) & 1)) break;
-        const int chunks = s_items[m % kItems].chunks, valid = s_items[m % kItems].valid;
-        mbar_arrive(bars + B_IEMPTY + m % kItems);
-        ++m;
-        if (!valid) break;
+  } else if (warp == kStateMmaWarp || (!kState && (warp == kYiMmaWarp || warp == kYxMmaWarp))) {
+    // ---- products: G and U, Yi, or Yx (what arrives last is waited for last)
+    constexpr uint32_t id_g = idesc_bf16(128, 64, 0, 0);
+    constexpr uint32_t id_x = idesc_bf16(128, 64, 1, 0);
+    constexpr uint32_t id_u = idesc_bf16(128, DS, 1, 1);
+    const uint32_t lead = elect_lane();
+    const uint32_t kmaj = op_lo(sbase, 0), mnmaj = op_lo(sbase, kTile);
+    uint32_t st = 0, ph = 0;
+    bool alive = true;
+    while (alive) {
+      if (!cx.wait(B_IFULL + m % kItems, (m / kItems) & 1)) break;
+      const int chunks = __shfl_sync(0xffffffffu, s_items[m % kItems].chunks, 0);
+      const int len = __shfl_sync(0xffffffffu, s_items[m % kItems].len, 0);
+      const int valid = __shfl_sync(0xffffffffu, s_items[m % kItems].valid, 0);
+      cx.arrive_warp(B_IEMPTY + m % kItems);
+      ++m;
+      if (!valid) break;
 #pragma unroll 1
-        for (int ci = 0; ci < chunks; ++ci, ++c) {
-          const uint32_t st = (c % kStages) * (L::kStage >> 4);
-          if (!cx.wait_one(B_FULL + c % kStages, (c / kStages) & 1)) { alive = false; break; }
-          if (warp == kStateMmaWarp) {
-            if (!kState) {
-              if (c > 0 && !cx.wait_one(B_M, (c - 1) & 1)) { alive = false; break; }
-              tc_fence_after();
-              uint32_t a = kmaj + st + (L::kC >> 4), b = kmaj + st + (L::kBt >> 4);
-#pragma unroll 1
-              for (int h = 0; h < DS / 64; ++h, a += kTile >> 4, b += kTile >> 4)
+      for (int ci = 0; ci < chunks; ++ci, ++c) {
+        const uint32_t so = st * (L::kStage >> 4);
+        const uint32_t now = c & 1, last = now ^ 1;  // parities of this chunk's and the last one's phases
+        if (warp == kStateMmaWarp) {
+          if (!cx.wait(B_FULL + st, ph, !kState && c > 0 ? B_M : -1, last)) { alive = false; break; }
+          if (!kState) {
+            tc_fence_after();
+            uint32_t a = kmaj + so + (L::kC >> 4), b = kmaj + so + (L::kBt >> 4);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  mma_ss(tb + TM_G, op_desc(a + 2 * kk), op_desc(b + 2 * kk), id_g, h + kk > 0);
-              mma_commit(bars + B_G);
+            for (int kk = 0; kk < DS / 16; ++kk) {
+              const uint32_t o = ((kk >> 2) * kTile + (kk & 3) * 32) >> 4;
+              mma_ss_by(lead, tb + TM_G, op_desc(a + o), op_desc(b + o), id_g, kk > 0);
             }
-            if (!cx.wait_one(B_X + (c & 1), (c >> 1) & 1) ||
-                (c > 0 && !cx.wait_one(B_UFREE, (c - 1) & 1))) { alive = false; break; }
-            tc_fence_after();
-            uint32_t a = mnmaj + ((L::kWx + (c & 1) * 4 * kTile) >> 4);
-            const uint32_t b = mnmaj + st + (L::kBt >> 4);
-#pragma unroll 1
-            for (int part = 0; part < 2; ++part, a += 2 * kTile >> 4)
-#pragma unroll
-              for (int kk = 0; kk < Q / 16; ++kk)
-                mma_ss(tb + TM_U, op_desc(a + kk * 128), op_desc(b + kk * 128), id_u, part + kk > 0);
-            mma_commit(bars + B_U + (c & 1));
-          } else {
-            if (!cx.wait_one(B_S, c & 1) ||
-                (HPC == 2 && c > 0 && !cx.wait_one(B_YFREE, (c - 1) & 1))) { alive = false; break; }  // one Yi
-            tc_fence_after();
-            uint32_t sb = tb + TM_SB;
-            const uint32_t yi = tb + TM_YI + (HPC == 1 ? (c & 1) * 64 : 0);
-#pragma unroll 1
-            for (int h = 0; h < 2 * (DS / 64); ++h, sb += 32) {
-              const uint32_t b = kmaj + st + ((L::kC + (h & (DS / 64 - 1)) * kTile) >> 4);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mma_ts(yi, sb + kk * 8, op_desc(b + 2 * kk), id_g, h + kk > 0);
-            }
-            mma_commit(bars + B_YI);
-            if (!cx.wait_one(B_FULLX + c % kStages, (c / kStages) & 1) || !cx.wait_one(B_M, c & 1) || !cx.wait_one(B_X + (c & 1), (c >> 1) & 1) ||
-                (HPC == 1 && c > 0 && !cx.wait_one(B_YFREE, (c - 1) & 1))) { alive = false; break; }
-            tc_fence_after();
-            const uint32_t a = mnmaj + st + (L::kX >> 4);
-            uint32_t b = kmaj + (L::kM >> 4);
-#pragma unroll 1
-            for (int h = 0; h < 2 * HPC; ++h, b += kTile >> 4)
-#pragma unroll
-              for (int kk = 0; kk < Q / 16; ++kk)
-                mma_ss(tb + (h >= 2 ? TM_YX2 : TM_YX), op_desc(a + kk * 128), op_desc(b + 2 * kk), id_x,
-                       (h & 1) + kk > 0);
-            mma_commit(bars + B_Y);
+            commit_by(lead, cx.bars + 8 * B_G);
           }
-          mma_commit(bars + B_EMPTY + c % kStages);
+          if (c > 0 && !cx.wait(B_UFREE, last)) { alive = false; break; }
+          const uint32_t a = mnmaj + (L::kWx >> 4), b = mnmaj + so + (L::kBt >> 4);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (alive && !cx.wait(B_X + 2 * st + h, ph)) alive = false;
+            tc_fence_after();
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk)
+                mma_ss_by(lead, tb + TM_U, op_desc(a + ((part * 2 * kTile + h * (kTile / 2) + kk * 2048) >> 4)),
+                          op_desc(b + ((h * (kTile / 2) + kk * 2048) >> 4)), id_u, h + part + kk > 0);
+            commit_by(lead, cx.bars + 8 * (B_WX + h));
+          }
+          if (!alive) break;
+          commit_by(lead, cx.bars + 8 * B_U);
+        } else if (warp == kYiMmaWarp) {
+          // the Yi used last time has been read: two chunks ago, or the last with two heads' one Yi
+          const uint32_t back = HPC == 1 ? 2 : 1;
+          if (!cx.wait(B_S, now, B_FULL + st, ph, c >= back ? B_YFREE + (int)((c - back) & 1) : -1,
+                       ((c - back) >> 1) & 1)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t yi = tb + TM_YI + (HPC == 1 ? now * 64 : 0), b = kmaj + so + (L::kC >> 4);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < DS / 16; ++kk)
+              mma_ts_by(lead, yi, tb + TM_SB + part * (DS / 2) + kk * 8,
+                        op_desc(b + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4)), id_g, part + kk > 0);
+          commit_by(lead, cx.bars + 8 * (B_YI + now));
+        } else {
+          // a last chunk's x has its rows past the end cleared
+          if (!cx.wait(B_M, now, B_FULLX + st, ph, c > 0 ? B_YFREE + (int)last : -1, ((c - 1) >> 1) & 1) ||
+              (len - ci * Q < Q && !cx.wait(B_X + 2 * st, ph, B_X + 2 * st + 1, ph))) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = mnmaj + so + (L::kX >> 4), b = kmaj + (L::kM >> 4);
+#pragma unroll
+          for (int h = 0; h < 2 * HPC; ++h)
+#pragma unroll
+            for (int kk = 0; kk < Q / 16; ++kk)
+              mma_ss_by(lead, tb + (h >= 2 ? TM_YX2 : TM_YX), op_desc(a + kk * 128),
+                        op_desc(b + ((h * kTile + kk * 32) >> 4)), id_x, (h & 1) + kk > 0);
+          commit_by(lead, cx.bars + 8 * B_YX);
         }
+        commit_by(lead, cx.bars + 8 * (B_EMPTY + st));
+        if (++st == kStages) { st = 0; ph ^= 1; }
       }
-      // every product is done before the memory goes away
-      mma_commit(bars + B_DRAIN);
-      const long long t0 = clock64();
-      while (!mbar_try_wait(bars + B_DRAIN, 0) && clock64() - t0 < 400000000ll) {}
     }
+    // every product is done before the memory goes away
+    commit_by(lead, cx.bars + 8 * B_DRAIN);
+    wait_phase(cx.bars + 8 * B_DRAIN, 0);
     __syncwarp();
   } else if (warp == kFactorWarp) {
     // ---- per-token factors
     bool alive = true;
-    while (alive && next_item(m, it)) {
+    while (alive && next_item_alone(m, it)) {
       float rate[HPC], bias[HPC];
 #pragma unroll
       for (int k = 0; k < HPC; ++k) {
