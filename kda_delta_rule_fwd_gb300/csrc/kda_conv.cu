@@ -5,10 +5,11 @@
 //
 // Every input and output is touched once and there are W multiply-adds per
 // element: the work is bound by memory traffic.  A thread owns VEC channels (16
-// bytes) and walks a tile of tokens with the window of W - 1 earlier inputs in
-// registers, so a tile re-reads only the W - 1 tokens before it; the loads of
-// kAhead tokens are issued together, ahead of their use.  Sequence boundaries
-// of a packed batch are found once per tile by bisection and then followed.
+// bytes) and walks a tile of tokens with the window of
+// W - 1 earlier inputs in registers, so a tile re-reads only the W - 1 tokens
+// before it; the loads of kAhead tokens are issued together, ahead of their use,
+// and held as they came.  Sequence boundaries of a packed batch are found once
+// per tile by bisection and then followed.
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -16,8 +17,6 @@ namespace layer {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 8;  // tokens whose loads are in flight together
-
 // the window of W - 1 inputs before token t of sequence n, whose tokens start at s0
 template <int VEC, int W, typename T>
 __device__ __forceinline__ void load_window(const T* x, int64_t ldx, const T* init, int64_t t,
@@ -42,8 +41,13 @@ __device__ __forceinline__ void load_params(const float* w, const float* b, int 
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
     br[e] = b ? b[c + e] : 0.f;
+    if constexpr (W == 4 && VEC > 1) {  // 16-byte aligned where the wide path is taken
+      const float4 v = *reinterpret_cast<const float4*>(w + (int64_t)(c + e) * 4);
+      wr[0][e] = v.x; wr[1][e] = v.y; wr[2][e] = v.z; wr[3][e] = v.w;
+    } else {
 #pragma unroll
-    for (int j = 0; j < W; ++j) wr[j][e] = w[(int64_t)(c + e) * W + j];
+      for (int j = 0; j < W; ++j) wr[j][e] = w[(int64_t)(c + e) * W + j];
+    }
   }
 }
 
@@ -57,11 +61,24 @@ __device__ __forceinline__ void shift_in(float (&win)[W - 1][VEC], const float (
   for (int e = 0; e < VEC; ++e) win[W - 2][e] = x[e];
 }
 
+// u of one token from its window
+template <int VEC, int W>
+__device__ __forceinline__ void taps(const float (&wr)[W][VEC], const float (&br)[VEC],
+                                     const float (&win)[W - 1][VEC], const float (&x)[VEC],
+                                     float (&u)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) u[e] = br[e];
+  fma_v(wr[W - 1], x, u);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) fma_v(wr[j], win[j], u);
+}
+
 // Blocks [0, cblocks * tiles): one tile of tokens and kThreads * VEC channels
 // each; the rest: the final state of one sequence.
 template <typename T, int VEC, int W, bool kSilu>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
 conv_fwd_kernel(ConvArgs a, int cblocks) {
+  constexpr int kAhead = VEC == 1 ? 8 : 4;  // tokens whose loads are in flight together
   const T* x = static_cast<const T*>(a.x);
   const T* init = static_cast<const T*>(a.init);
   const int cb = blockIdx.x % cblocks;
@@ -89,67 +106,93 @@ conv_fwd_kernel(ConvArgs a, int cblocks) {
   a.q.range(n, s0, s1);
   load_window<VEC, W>(x, a.ldx, init, t0, s0, n, a.D, c, win);
   T* y = static_cast<T*>(a.y) + c;
-  for (int64_t t = t0; t < t1; t += kAhead) {
-    float xa[kAhead][VEC];
+  auto token = [&](int64_t t, const Raw<T, VEC>& raw) {
+    float xt[VEC], u[VEC];
+    open<T, VEC>(raw, xt);
+    taps<VEC, W>(wr, br, win, xt, u);
+    if (kSilu) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (t + i < t1) load<VEC>(x + (t + i) * a.ldx + c, xa[i]);
+      for (int e = 0; e < VEC; ++e) u[e] *= sigmoid(u[e]);
+    }
+    store<VEC>(y + t * a.D, u);
+    shift_in<VEC, W>(win, xt);
+  };
+  int64_t t = t0;
+  while (t < t1) {
+    Raw<T, VEC> raw[kAhead];
+    if (t + kAhead <= t1 && t + kAhead <= s1) {  // inside one sequence
+      const T* p = x + t * a.ldx + c;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (t + i >= t1) break;
-      if (t + i >= s1 && n + 1 < a.q.N) {  // the next sequence with tokens starts here
+      for (int i = 0; i < kAhead; ++i) raw[i] = fetch<T, VEC>(p + i * a.ldx);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) token(t + i, raw[i]);
+      t += kAhead;
+    } else {
+      if (t >= s1 && n + 1 < a.q.N) {  // the next sequence with tokens starts here
         do a.q.range(++n, s0, s1);
-        while (t + i >= s1 && n + 1 < a.q.N);
-        load_window<VEC, W>(x, a.ldx, init, t + i, s0, n, a.D, c, win);
+        while (t >= s1 && n + 1 < a.q.N);
+        load_window<VEC, W>(x, a.ldx, init, t, s0, n, a.D, c, win);
       }
-      float u[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        u[e] = fmaf(wr[W - 1][e], xa[i][e], br[e]);
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) u[e] = fmaf(wr[j][e], win[j][e], u[e]);
-        if (kSilu) u[e] *= sigmoid(u[e]);
-      }
-      store<VEC>(y + (t + i) * a.D, u);
-      shift_in<VEC, W>(win, xa[i]);
+      raw[0] = fetch<T, VEC>(x + t * a.ldx + c);
+      token(t++, raw[0]);
     }
   }
 }
 
-// One block row per sequence: T tokens in order, the state in registers.
-template <typename T, int VEC, int W, bool kSilu>
+// Single tokens.  A block owns kThreads * VEC channels, loads their taps once and
+// walks sequences n = j, j + jobs, ..., kSeqs of them at a time so that their loads
+// are in flight together; T tokens in order, the state in registers.
+template <typename T, int VEC, int W, bool kSilu, int kSeqs>
 __global__ void __launch_bounds__(kThreads)
 conv_step_kernel(ConvArgs a, int cblocks) {
   const T* x = static_cast<const T*>(a.x);
-  const int cb = blockIdx.x % cblocks, n = blockIdx.x / cblocks;
+  const int cb = blockIdx.x % cblocks;
+  const int64_t jobs = gridDim.x / cblocks;
   if (blockIdx.x == 0) check_counts(a.counts, a.q.N, a.T, a.status);
   const int c = (cb * kThreads + threadIdx.x) * VEC;
   if (c >= a.D) return;
-  T* st = static_cast<T*>(a.state) + (int64_t)n * (W - 1) * a.D + c;
-  float wr[W][VEC], br[VEC], win[W - 1][VEC];
-#pragma unroll
-  for (int i = 0; i < W - 1; ++i) load<VEC>(st + (int64_t)i * a.D, win[i]);
+  float wr[W][VEC], br[VEC];
   load_params<VEC, W>(a.w, a.b, c, wr, br);
-  int keep = a.T;
-  if (a.counts) {
-    keep = a.counts[n];
-    if (keep < 0 || keep > a.T) keep = 0;
-  }
-  for (int t = 0; t < a.T; ++t) {
-    float xt[VEC], u[VEC];
-    load<VEC>(x + ((int64_t)n * a.T + t) * a.ldx + c, xt);
+  for (int64_t n0 = blockIdx.x / cblocks; n0 < a.q.N; n0 += jobs * kSeqs) {
+    Raw<T, VEC> old[kSeqs][W - 1], first[kSeqs];
+    int keep[kSeqs];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      u[e] = fmaf(wr[W - 1][e], xt[e], br[e]);
+    for (int q = 0; q < kSeqs; ++q) {
+      const int64_t n = n0 + q * jobs;
+      if (n < a.q.N) {
+        const T* st = static_cast<const T*>(a.state) + n * (W - 1) * a.D + c;
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) u[e] = fmaf(wr[j][e], win[j][e], u[e]);
-      if (kSilu) u[e] *= sigmoid(u[e]);
+        for (int i = 0; i < W - 1; ++i) old[q][i] = fetch<T, VEC>(st + (int64_t)i * a.D);
+        first[q] = fetch<T, VEC>(x + n * a.T * a.ldx + c);
+        keep[q] = a.counts ? a.counts[n] : a.T;
+        if (keep[q] < 0 || keep[q] > a.T) keep[q] = 0;
+      }
     }
-    if (a.y) store<VEC>(static_cast<T*>(a.y) + ((int64_t)n * a.T + t) * a.D + c, u);
-    shift_in<VEC, W>(win, xt);
-    if (t + 1 == keep) {
 #pragma unroll
-      for (int i = 0; i < W - 1; ++i) store<VEC>(st + (int64_t)i * a.D, win[i]);
+    for (int q = 0; q < kSeqs; ++q) {
+      const int64_t n = n0 + q * jobs;
+      if (n >= a.q.N) break;
+      T* st = static_cast<T*>(a.state) + n * (W - 1) * a.D + c;
+      float win[W - 1][VEC];
+#pragma unroll
+      for (int i = 0; i < W - 1; ++i) open<T, VEC>(old[q][i], win[i]);
+#pragma unroll 1
+      for (int t = 0; t < a.T; ++t) {
+        float xt[VEC], u[VEC];
+        if (t == 0) open<T, VEC>(first[q], xt);
+        else load<VEC>(x + (n * a.T + t) * a.ldx + c, xt);
+        taps<VEC, W>(wr, br, win, xt, u);
+        if (kSilu) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) u[e] *= sigmoid(u[e]);
+        }
+        if (a.y) store<VEC>(static_cast<T*>(a.y) + (n * a.T + t) * a.D + c, u);
+        shift_in<VEC, W>(win, xt);
+        if (t + 1 == keep[q]) {
+#pragma unroll
+          for (int i = 0; i < W - 1; ++i) store<VEC>(st + (int64_t)i * a.D, win[i]);
+        }
+      }
     }
   }
 }
@@ -161,8 +204,9 @@ conv_step_kernel(ConvArgs a, int cblocks) {
 // sums for dw and dbias go to part[tile][W + 1][D] and are added in the order of
 // the tiles by conv_reduce_kernel, so the results do not depend on scheduling.
 template <typename T, int VEC, int W, bool kSilu>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
 conv_bwd_kernel(ConvArgs a, int cblocks) {
+  constexpr int kAhead = 4;  // tokens whose loads are in flight together
   const T* x = static_cast<const T*>(a.x);
   const T* init = static_cast<const T*>(a.init);
   const T* dy = static_cast<const T*>(a.dy);
@@ -175,17 +219,17 @@ conv_bwd_kernel(ConvArgs a, int cblocks) {
   float wr[W][VEC], br[VEC], win[W - 1][VEC];
   load_params<VEC, W>(a.w, a.b, c, wr, br);
   auto grad_u = [&](const float (&xt)[VEC], const float (&g)[VEC], float (&du)[VEC]) {
+    if (kSilu) {
+      float u[VEC];
+      taps<VEC, W>(wr, br, win, xt, u);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      if (kSilu) {
-        float u = fmaf(wr[W - 1][e], xt[e], br[e]);
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) u = fmaf(wr[j][e], win[j][e], u);
-        const float s = sigmoid(u);
-        du[e] = g[e] * s * fmaf(u, 1.f - s, 1.f);
-      } else {
-        du[e] = g[e];
+      for (int e = 0; e < VEC; ++e) {
+        const float s = sigmoid(u[e]);
+        du[e] = g[e] * s * fmaf(u[e], 1.f - s, 1.f);
       }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) du[e] = g[e];
     }
   };
   if (job >= a.tiles) {  // gradient of the start state of one sequence
@@ -264,52 +308,65 @@ conv_bwd_kernel(ConvArgs a, int cblocks) {
       for (int e = 0; e < VEC; ++e) pend[k][e] = 0.f;
     }
   };
-  int64_t stop = t1 + W - 1 < a.q.total ? t1 + W - 1 : a.q.total;
+  const int64_t stop = t1 + W - 1 < a.q.total ? t1 + W - 1 : a.q.total;
   bool ended = false;  // the walk stops at a sequence's end at or after t1
-  for (int64_t t = t0; t < stop && !ended; t += kAhead) {
-    float xa[kAhead][VEC], ga[kAhead][VEC];
+  // one token; emit: the dx W - 1 tokens back is finished by it; sum: it counts for this tile
+  auto token = [&](int64_t p, const Raw<T, VEC>& xr, const Raw<T, VEC>& gr, bool emit, bool sum) {
+    float xt[VEC], g[VEC], du[VEC];
+    open<T, VEC>(xr, xt);
+    open<T, VEC>(gr, g);
+    grad_u(xt, g, du);
+    if (emit) {
+      fma_v(wr[0], du, pend[W - 2]);
+      store<VEC>(dx + (p - (W - 1)) * a.D, pend[W - 2]);
+    }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (t + i < stop) {
-        load<VEC>(x + (t + i) * a.ldx + c, xa[i]);
-        load<VEC>(dy + (t + i) * a.D + c, ga[i]);
+    for (int k = W - 2; k > 0; --k) {
+      fma_v(wr[W - 1 - k], du, pend[k - 1]);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) pend[k][e] = pend[k - 1][e];
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) pend[0][e] = wr[W - 1][e] * du[e];
+    if (sum) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) db[e] += du[e];
+      fma_v(du, xt, dw[W - 1]);
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) fma_v(du, win[j], dw[j]);
+    }
+    shift_in<VEC, W>(win, xt);
+  };
+  int64_t t = t0;
+  while (t < stop && !ended) {
+    Raw<T, VEC> xa[kAhead], ga[kAhead];
+    if (t + kAhead <= t1 && t + kAhead <= s1 && t - (W - 1) >= t0 && t - (W - 1) >= s0) {
+      const T* px = x + t * a.ldx + c;
+      const T* pg = dy + t * a.D + c;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        xa[i] = fetch<T, VEC>(px + i * a.ldx);
+        ga[i] = fetch<T, VEC>(pg + (int64_t)i * a.D);
       }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int64_t p = t + i;
-      if (p >= stop || ended) break;
-      if (p >= s1 && n + 1 < a.q.N) {
+      for (int i = 0; i < kAhead; ++i) token(t + i, xa[i], ga[i], true, true);
+      t += kAhead;
+    } else {
+      if (t >= s1 && n + 1 < a.q.N) {
         flush(s1);
-        if (p >= t1) {
+        if (t >= t1) {
           ended = true;
           break;
         }
         do a.q.range(++n, s0, s1);
-        while (p >= s1 && n + 1 < a.q.N);
-        load_window<VEC, W>(x, a.ldx, init, p, s0, n, a.D, c, win);
+        while (t >= s1 && n + 1 < a.q.N);
+        load_window<VEC, W>(x, a.ldx, init, t, s0, n, a.D, c, win);
       }
-      float du[VEC];
-      grad_u(xa[i], ga[i], du);
-      const int64_t s = p - (W - 1);
-      if (s >= t0 && s >= s0) {
-        float o[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = fmaf(wr[0][e], du[e], pend[W - 2][e]);
-        store<VEC>(dx + s * a.D, o);
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-        for (int k = W - 2; k > 0; --k) pend[k][e] = fmaf(wr[W - 1 - k][e], du[e], pend[k - 1][e]);
-        pend[0][e] = wr[W - 1][e] * du[e];
-        if (p < t1) {
-          db[e] += du[e];
-          dw[W - 1][e] = fmaf(du[e], xa[i][e], dw[W - 1][e]);
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(du[e], win[j][e], dw[j][e]);
-        }
-      }
-      shift_in<VEC, W>(win, xa[i]);
+      xa[0] = fetch<T, VEC>(x + t * a.ldx + c);
+      ga[0] = fetch<T, VEC>(dy + t * a.D + c);
+      const int64_t s = t - (W - 1);
+      token(t, xa[0], ga[0], s >= t0 && s >= s0, t < t1);
+      ++t;
     }
   }
   if (!ended && s1 <= stop) flush(s1);
@@ -319,13 +376,22 @@ conv_bwd_kernel(ConvArgs a, int cblocks) {
   store<VEC>(pt + (int64_t)W * a.D, db);
 }
 
+// 8 warps take every 8th tile's sums of 32 columns, then fold in a fixed order
 __global__ void __launch_bounds__(256) conv_reduce_kernel(ConvArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  __shared__ float fold[8][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t per = (int64_t)(a.W + 1) * a.D;
-  if (i >= per) return;
+  const int64_t i = (int64_t)blockIdx.x * 32 + lane;
   float sum = 0.f;
+  if (i < per) {
 #pragma unroll 8
-  for (int64_t t = 0; t < a.tiles; ++t) sum += a.part[t * per + i];
+    for (int64_t t = warp; t < a.tiles; t += 8) sum += a.part[t * per + i];
+  }
+  fold[warp][lane] = sum;
+  __syncthreads();
+  if (warp > 0 || i >= per) return;
+#pragma unroll
+  for (int q = 1; q < 8; ++q) sum += fold[q][lane];
   const int j = (int)(i / a.D), c = (int)(i % a.D);
   if (j < a.W) a.dw[(int64_t)c * a.W + j] = sum;
   else if (a.db) a.db[c] = sum;
@@ -335,21 +401,33 @@ bool al16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
 template <typename T, int VEC, int W>
 cudaError_t run(const ConvArgs& a, int what) {
+  constexpr bool kGrad = !(sizeof(T) == 2 && VEC == 8), kRest = !(sizeof(T) == 2 && VEC == 4);
   const int cblocks = (a.D + kThreads * VEC - 1) / (kThreads * VEC);
   const int64_t extra = what == 0 ? (a.fin ? a.q.N : 0) : what == 2 ? (a.dinit ? a.q.N : 0) : 0;
-  const int64_t jobs = what == 1 ? a.q.N : a.tiles + extra;
+  // single tokens: enough blocks to fill the device, each with several sequences
+  const int64_t fill = (a.sms * 12 + cblocks - 1) / cblocks;
+  const int64_t jobs = what == 1 ? (a.q.N < fill ? a.q.N : fill) : a.tiles + extra;
   const int64_t grid = jobs * cblocks;
   if (grid == 0)  // nothing to check or to compute
     return a.status ? cudaMemsetAsync(a.status, 0, sizeof(unsigned int), a.stream) : cudaSuccess;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-#define KDA_CONV(KERNEL)                                                             \
-  (a.silu ? KERNEL<T, VEC, W, true><<<(unsigned)grid, kThreads, 0, a.stream>>>(a, cblocks) \
-          : KERNEL<T, VEC, W, false><<<(unsigned)grid, kThreads, 0, a.stream>>>(a, cblocks))
-  if (what == 0) KDA_CONV(conv_fwd_kernel);
-  else if (what == 1) KDA_CONV(conv_step_kernel);
-  else KDA_CONV(conv_bwd_kernel);
-#undef KDA_CONV
-  return cudaGetLastError();
+  auto go = [&](auto* kernel) {
+    kernel<<<(unsigned)grid, kThreads, 0, a.stream>>>(a, cblocks);
+    return cudaGetLastError();
+  };
+  if constexpr (kGrad) {
+    if (what == 2)
+      return a.silu ? go(conv_bwd_kernel<T, VEC, W, true>) : go(conv_bwd_kernel<T, VEC, W, false>);
+  }
+  if constexpr (kRest) {
+    if (what == 0)
+      return a.silu ? go(conv_fwd_kernel<T, VEC, W, true>) : go(conv_fwd_kernel<T, VEC, W, false>);
+    constexpr int kSeqs = VEC == 8 ? 2 : 4;
+    if (what == 1)
+      return a.silu ? go(conv_step_kernel<T, VEC, W, true, kSeqs>)
+                    : go(conv_step_kernel<T, VEC, W, false, kSeqs>);
+  }
+  return cudaErrorInvalidValue;
 }
 template <typename T, int VEC>
 cudaError_t by_width(const ConvArgs& a, int what) {
@@ -359,18 +437,16 @@ cudaError_t by_width(const ConvArgs& a, int what) {
     default: return run<T, VEC, 4>(a, what);
   }
 }
-// wide loads where every row of every operand starts on a 16-byte boundary
+// wide loads where every row of every operand starts on a 16-byte boundary (the
+// gradient, with more to keep in registers, takes half as many bf16 channels)
 cudaError_t by_type(const ConvArgs& a, int what) {
-  const int v = what == 2 ? 4 : (a.bf16 ? 8 : 4);
   const void* ptrs[] = {a.x, a.init, a.dy, a.dfinal, a.y, a.fin, a.dx, a.dinit, a.state};
-  bool wide = a.D % v == 0 && a.ldx % v == 0;
+  const int v = a.bf16 ? 8 : 4;
+  bool wide = a.D % v == 0 && a.ldx % v == 0 && al16(a.w);
   for (const void* p : ptrs) wide = wide && al16(p);
-  if (what == 2)
-    return a.bf16 ? (wide ? by_width<__nv_bfloat16, 4>(a, what) : by_width<__nv_bfloat16, 1>(a, what))
-                  : (wide ? by_width<float, 4>(a, what) : by_width<float, 1>(a, what));
-  if (a.bf16)
-    return wide ? by_width<__nv_bfloat16, 8>(a, what) : by_width<__nv_bfloat16, 1>(a, what);
-  return wide ? by_width<float, 4>(a, what) : by_width<float, 1>(a, what);
+  if (!a.bf16) return wide ? by_width<float, 4>(a, what) : by_width<float, 1>(a, what);
+  if (!wide) return by_width<__nv_bfloat16, 1>(a, what);
+  return what == 2 ? by_width<__nv_bfloat16, 4>(a, what) : by_width<__nv_bfloat16, 8>(a, what);
 }
 
 }  // namespace
@@ -381,7 +457,7 @@ cudaError_t launch_conv_fwd(const ConvArgs& a0) {
   const int64_t per = kThreads * (a.bf16 ? 8 : 4);
   const int64_t cb = (a.D + per - 1) / per;
   a.tile = 64;
-  while (a.tile > 8 && cb * ((a.q.total + a.tile - 1) / a.tile) < 4 * 152) a.tile /= 2;
+  while (a.tile > 8 && cb * ((a.q.total + a.tile - 1) / a.tile) < 8 * a.sms) a.tile /= 2;
   a.tiles = (a.q.total + a.tile - 1) / a.tile;
   return by_type(a, 0);
 }
@@ -399,7 +475,7 @@ cudaError_t launch_conv_bwd(const ConvArgs& a) {
   cudaError_t e = by_type(a, 2);
   if (e != cudaSuccess) return e;
   const int64_t per = (int64_t)(a.W + 1) * a.D;
-  conv_reduce_kernel<<<(unsigned)((per + 255) / 256), 256, 0, a.stream>>>(a);
+  conv_reduce_kernel<<<(unsigned)((per + 31) / 32), 256, 0, a.stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -71,8 +71,47 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[VEC]) {
   }
 }
 
-// sigmoid with the fast exponential and division (a few ulp; 0 below x ~ -87)
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// VEC consecutive elements as they lie in memory, to be held while in flight
+template <typename T, int VEC> struct Raw;
+template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
+template <> struct Raw<__nv_bfloat16, 4> { uint2 v; };
+template <> struct Raw<float, 8> { float4 v, w; };
+template <> struct Raw<float, 4> { float4 v; };
+template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 v; };
+template <> struct Raw<float, 1> { float v; };
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> fetch(const T* p) {
+  return *reinterpret_cast<const Raw<T, VEC>*>(p);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void open(const Raw<T, VEC>& r, float (&x)[VEC]) {
+  load<VEC>(reinterpret_cast<const T*>(&r), x);
+}
+
+// sigmoid on the special-function unit: 2^(-x log2 e), then the reciprocal (a few ulp; 0
+// below x ~ -88, 1 above 17)
+__device__ __forceinline__ float sigmoid(float x) {
+  float e, y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + e));
+  return y;
+}
+// a b + c on pairs of neighbouring elements
+template <int VEC>
+__device__ __forceinline__ void fma_v(const float (&a)[VEC], const float (&b)[VEC], float (&c)[VEC]) {
+  if constexpr (VEC % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const float2 r = fma2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]),
+                            make_float2(c[e], c[e + 1]));
+      c[e] = r.x;
+      c[e + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) c[e] = fmaf(a[e], b[e], c[e]);
+  }
+}
 // delta = softplus(dt + bias), or dt as given
 __device__ __forceinline__ float step_size(float dt, float bias, bool softplus) {
   if (!softplus) return dt;
@@ -142,6 +181,7 @@ struct ConvArgs {
   int64_t ldx;
   bool bf16, silu;
   int64_t tile, tiles;
+  int64_t sms;
   unsigned int* status;
   cudaStream_t stream;
 };
@@ -182,7 +222,9 @@ struct NormArgs {
   int64_t tokens, ldx, ldg;
   int heads, d, gate_act;
   bool bf16, res_bf16, gate_first;
-  float scale, eps;
+  float scale, eps, inv_d;
+  bool dense;    // x and gate rows lie d apart
+  int64_t sms;
   int64_t ctas;  // backward: CTAs, each with its own row of partial sums
   cudaStream_t stream;
 };

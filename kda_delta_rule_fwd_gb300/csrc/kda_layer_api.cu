@@ -61,6 +61,7 @@ ConvArgs conv_args(const kda_conv_shape* s, bool packed, const int32_t* cu, int6
   a.ldx = ldx;
   a.bf16 = s->dtype == KDA_BF16;
   a.silu = s->silu != 0;
+  a.sms = device_sms();
   a.status = static_cast<unsigned int*>(ws);
   a.stream = static_cast<cudaStream_t>(stream);
   return a;
@@ -134,6 +135,9 @@ kda_status check_norm(const kda_norm_shape* s, NormArgs& a) {
   a.gate_act = s->gate;
   a.gate_first = s->gate_first != 0;
   a.scale = s->scale; a.eps = s->eps;
+  a.inv_d = 1.f / (float)s->d;
+  a.sms = device_sms();
+  a.dense = a.ldx == row && a.ldg == row;
   return KDA_OK;
 }
 

@@ -1,0 +1,151 @@
+// RMS norms before and after a block, fused with the block's gate and residual
+// scale, and their gradients.  Per row of d channels:
+//
+//     z = act(gate);  v = x z (gate first) or x;  m = v k w,  k = 1 / rms(v)
+//     b = m z (gate after) or m;  r = residual + scale ls b;  y = r k' w'
+//
+// One pass: a row stays in registers between its reductions, so each input is read
+// once and each output written once, and the work is bound by memory traffic.  A row
+// of d channels is held by TPR threads with NC chunks of VEC channels each; rows of
+// up to 32 chunks reduce by shuffles alone.  Blocks are persistent: each walks rows
+// and requests the next one's inputs before it works on the present one, so that the
+// reductions' latency is covered; the parameters are loaded once where a row's chunks
+// leave room for them (up to 32 threads per row).
+#pragma once
+
+#include "kda_layer.cuh"
+
+namespace kda {
+namespace layer {
+namespace norm {
+
+// sum over the TPR threads of a row; every thread gets it.  Above 32 threads the
+// row is the whole block: two alternating scratch rows leave one barrier per sum.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float (*scratch)[32], int& flip) {
+  constexpr int kIn = TPR < 32 ? TPR : 32;
+#pragma unroll
+  for (int o = kIn / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (TPR > 32) {
+    constexpr int kWarps = TPR / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) scratch[flip][warp] = v;
+    __syncthreads();
+    v = lane < kWarps ? scratch[flip][lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    flip ^= 1;
+  }
+  return v;
+}
+
+template <int TPR> constexpr int block_of() { return TPR < 128 ? 128 : TPR; }
+
+// where the gate sits
+enum Place { kNoGate = 0, kAfter = 1, kFirst = 2 };
+
+// the gate z and its slope from s = sigmoid(g)
+__device__ __forceinline__ float gate_of(float g, float s, bool silu) { return silu ? g * s : s; }
+__device__ __forceinline__ float gate_slope(float g, float s, bool silu) {
+  return s * (silu ? fmaf(g, 1.f - s, 1.f) : 1.f - s);
+}
+
+// a row's inputs as they come from memory
+template <typename T, typename TR, int VEC, int NC, bool kBwd>
+struct RowIn {
+  Raw<T, VEC> x[NC], g[NC], dy[kBwd ? NC : 1];
+  Raw<TR, VEC> res[NC], dr[kBwd ? NC : 1];
+};
+
+template <typename T, typename TR, int VEC, int NC, int TPR, int PLACE, bool kBwd>
+__device__ __forceinline__ void request(const NormArgs& a, int64_t row, int lane,
+                                        RowIn<T, TR, VEC, NC, kBwd>& in) {
+  int64_t xo = row * a.d, go = xo;
+  if (!a.dense) {
+    const int64_t tok = row / a.heads;
+    const int64_t head = (row - tok * a.heads) * a.d;
+    xo = tok * a.ldx + head;
+    go = tok * a.ldg + head;
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = (lane + i * TPR) * VEC;
+    if (c < a.d) {
+      in.x[i] = fetch<T, VEC>(static_cast<const T*>(a.x) + xo + c);
+      if (PLACE != kNoGate) in.g[i] = fetch<T, VEC>(static_cast<const T*>(a.gate) + go + c);
+      // the gradient needs the residual only to form y's norm again
+      if (a.res && (!kBwd || a.ow)) in.res[i] = fetch<TR, VEC>(static_cast<const TR*>(a.res) + row * a.d + c);
+      if constexpr (kBwd) {
+        if (a.dr) in.dr[i] = fetch<TR, VEC>(static_cast<const TR*>(a.dr) + row * a.d + c);
+        if (a.dy) in.dy[i] = fetch<T, VEC>(static_cast<const T*>(a.dy) + row * a.d + c);
+      }
+    }
+  }
+}
+
+// VEC parameters times `scale`, or the scale alone where there are none
+template <int VEC>
+__device__ __forceinline__ void param(const float* p, int c, float scale, float (&v)[VEC]) {
+  if (p) {
+    load<VEC>(p + c, v);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] *= scale;
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = scale;
+  }
+}
+
+inline bool al16(const void* p) { return (uintptr_t)p % 16 == 0; }
+inline bool wide_ok(const NormArgs& a) {
+  const int v = a.bf16 ? 8 : 4;
+  const void* ptrs[] = {a.x, a.gate, a.res, a.dr, a.dy, a.w, a.ls, a.ow, a.r,
+                        a.y, a.dx, a.dgate, a.dres};
+  bool wide = a.d % v == 0 && a.ldx % v == 0 && a.ldg % v == 0;
+  for (const void* p : ptrs) wide = wide && al16(p);
+  return wide;
+}
+
+// Threads per row by the row's chunks: up to 32 chunks the row stays inside a warp, with two
+// chunks per thread (F::kPairs) up to 64.  `F<T, TR, VEC, NC, TPR, PLACE>::run` is the launch.
+template <template <typename, typename, int, int, int, int> class F, typename T, typename TR, int VEC, int PLACE>
+cudaError_t by_size(const NormArgs& a) {
+  const int chunks = (a.d + VEC - 1) / VEC;
+  if constexpr (VEC == 1) {
+    if (chunks <= 128) return F<T, TR, 1, 4, 32, PLACE>::run(a);
+    if (chunks <= 1024) return F<T, TR, 1, 4, 256, PLACE>::run(a);
+    return F<T, TR, 1, 8, 1024, PLACE>::run(a);
+  } else {
+    if constexpr (F<T, TR, VEC, 1, 32, PLACE>::kPairs) {
+      if (chunks <= 16) return F<T, TR, VEC, 2, 8, PLACE>::run(a);
+      if (chunks <= 64) return F<T, TR, VEC, 2, 32, PLACE>::run(a);
+    } else {
+      if (chunks <= 16) return F<T, TR, VEC, 1, 16, PLACE>::run(a);
+      if (chunks <= 32) return F<T, TR, VEC, 1, 32, PLACE>::run(a);
+    }
+    if (chunks <= 128) return F<T, TR, VEC, 1, 128, PLACE>::run(a);
+    if (chunks <= 256) return F<T, TR, VEC, 1, 256, PLACE>::run(a);
+    if (chunks <= 512) return F<T, TR, VEC, 1, 512, PLACE>::run(a);
+    if constexpr (VEC == 4) {  // float32 rows past 4096 channels
+      if (chunks > 1024) return F<T, TR, VEC, 2, 1024, PLACE>::run(a);
+    }
+    return F<T, TR, VEC, 1, 1024, PLACE>::run(a);
+  }
+}
+template <template <typename, typename, int, int, int, int> class F, typename T, typename TR, int VEC>
+cudaError_t by_place(const NormArgs& a) {
+  if (!a.gate_act) return by_size<F, T, TR, VEC, kNoGate>(a);
+  return a.gate_first ? by_size<F, T, TR, VEC, kFirst>(a) : by_size<F, T, TR, VEC, kAfter>(a);
+}
+template <template <typename, typename, int, int, int, int> class F>
+cudaError_t by_type(const NormArgs& a) {
+  using bf = __nv_bfloat16;
+  const bool wide = wide_ok(a);
+  if (!a.bf16) return wide ? by_place<F, float, float, 4>(a) : by_place<F, float, float, 1>(a);
+  if (a.res_bf16) return wide ? by_place<F, bf, bf, 8>(a) : by_place<F, bf, bf, 1>(a);
+  return wide ? by_place<F, bf, float, 8>(a) : by_place<F, bf, float, 1>(a);
+}
+
+}  // namespace norm
+}  // namespace layer
+}  // namespace kda

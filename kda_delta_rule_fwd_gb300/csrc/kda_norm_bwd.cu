@@ -1,0 +1,251 @@
+// RMS norms with gate and residual scale: the gradient (see kda_norm.cuh).
+//
+// For n = v k, y = n w:  dv = k (p - n mean(p n)) with p = dy w, and dw = sum over rows
+// of dy n.  Each block keeps its rows' sums for the parameters in registers; they go to
+// part[block][3][d] and are added in the order of the blocks, so that the results do not
+// depend on scheduling.
+#include "kda_norm.cuh"
+
+namespace kda {
+namespace layer {
+namespace {
+
+using namespace norm;
+
+template <typename T, typename TR, int VEC, int NC, int TPR, int PLACE>
+__global__ void __launch_bounds__(block_of<TPR>())
+norm_bwd_kernel(NormArgs a) {
+  constexpr int kRows = block_of<TPR>() / TPR;
+  __shared__ float scratch[2][32];
+  int flip = 0;
+  const int64_t rows = a.tokens * a.heads, step = (int64_t)gridDim.x * kRows;
+  const int lane = threadIdx.x % TPR;
+  const bool silu = a.gate_act == KDA_GATE_SILU;
+  float sw[NC][VEC], sl[NC][VEC], so[NC][VEC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sw[i][e] = sl[i][e] = so[i][e] = 0.f;
+  RowIn<T, TR, VEC, NC, true> in;
+  int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  if (row < rows) request<T, TR, VEC, NC, TPR, PLACE, true>(a, row, lane, in);
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < rows; base += step, row += step) {
+    const bool on = row < rows;
+    // n: the norm's input v, then v k;  z, sz: the gate and (x's factor in) its slope;
+    // r: residual, then n of the outer norm;  dr: gradient of r, then of the branch
+    float n[NC][VEC], z[NC][VEC], sz[NC][VEC], r[NC][VEC], dr[NC][VEC], dy[NC][VEC];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) n[i][e] = z[i][e] = r[i][e] = dr[i][e] = dy[i][e] = 0.f;
+      if (on && (lane + i * TPR) * VEC < a.d) {
+        open<T, VEC>(in.x[i], n[i]);
+        if (PLACE != kNoGate) open<T, VEC>(in.g[i], z[i]);
+        if (a.res && a.ow) open<TR, VEC>(in.res[i], r[i]);
+        if (a.dr) open<TR, VEC>(in.dr[i], dr[i]);
+        if (a.dy) open<T, VEC>(in.dy[i], dy[i]);
+      }
+    }
+    if (row + step < rows) request<T, TR, VEC, NC, TPR, PLACE, true>(a, row + step, lane, in);
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        if (PLACE != kNoGate) {
+          const float s = sigmoid(z[i][e]);
+          sz[i][e] = gate_slope(z[i][e], s, silu);
+          z[i][e] = gate_of(z[i][e], s, silu);
+        }
+        if (PLACE == kFirst) {
+          sz[i][e] *= n[i][e];
+          n[i][e] *= z[i][e];
+        }
+        ss = fmaf(n[i][e], n[i][e], ss);
+      }
+    float k = 1.f;
+    if (a.w) {
+      k = rsqrtf(fmaf(row_sum<TPR>(ss, scratch, flip), a.inv_d, a.eps));
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) n[i][e] *= k;
+    }
+    if (a.ow) {
+      ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = (lane + i * TPR) * VEC;
+        if (c < a.d) {
+          float w[VEC], ls[VEC];
+          param<VEC>(a.w, c, 1.f, w);
+          param<VEC>(a.ls, c, a.scale, ls);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            float b = n[i][e] * w[e];
+            if (PLACE == kAfter) b *= z[i][e];
+            r[i][e] = fmaf(ls[e], b, r[i][e]);
+            ss = fmaf(r[i][e], r[i][e], ss);
+          }
+        }
+      }
+      const float k2 = rsqrtf(fmaf(row_sum<TPR>(ss, scratch, flip), a.inv_d, a.eps));
+      float pn = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = (lane + i * TPR) * VEC;
+        if (c < a.d) {
+          float ow[VEC];
+          param<VEC>(a.ow, c, 1.f, ow);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            r[i][e] *= k2;  // n of the outer norm
+            so[i][e] = fmaf(dy[i][e], r[i][e], so[i][e]);
+            dy[i][e] *= ow[e];  // p
+            pn = fmaf(dy[i][e], r[i][e], pn);
+          }
+        }
+      }
+      pn = row_sum<TPR>(pn, scratch, flip) * a.inv_d;
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dr[i][e] = fmaf(k2, fmaf(-pn, r[i][e], dy[i][e]), dr[i][e]);
+    }
+    // through the residual sum and the branch; dgate (gate after) in sz
+    float pn = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = (lane + i * TPR) * VEC;
+      if (c < a.d) {
+        float w[VEC], ls[VEC];
+        param<VEC>(a.w, c, 1.f, w);
+        param<VEC>(a.ls, c, a.scale, ls);
+        if (a.dres && on) store<VEC>(static_cast<TR*>(a.dres) + row * a.d + c, dr[i]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float m = n[i][e] * w[e];
+          const float b = PLACE == kAfter ? m * z[i][e] : m;
+          sl[i][e] = fmaf(dr[i][e], b, sl[i][e]);  // times the scale at the end
+          float db = ls[e] * dr[i][e];
+          if (PLACE == kAfter) {
+            sz[i][e] *= db * m;
+            db *= z[i][e];
+          }
+          sw[i][e] = fmaf(db, n[i][e], sw[i][e]);
+          dr[i][e] = db * w[e];  // p
+          pn = fmaf(dr[i][e], n[i][e], pn);
+        }
+      }
+    }
+    pn = a.w ? row_sum<TPR>(pn, scratch, flip) * a.inv_d : 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = (lane + i * TPR) * VEC;
+      if (on && c < a.d) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float dv = k * fmaf(-pn, n[i][e], dr[i][e]);
+          if (PLACE == kFirst) {
+            sz[i][e] *= dv;
+            dv *= z[i][e];
+          }
+          dr[i][e] = dv;
+        }
+        store<VEC>(static_cast<T*>(a.dx) + row * a.d + c, dr[i]);
+        if (PLACE != kNoGate && a.dgate) store<VEC>(static_cast<T*>(a.dgate) + row * a.d + c, sz[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sl[i][e] *= a.scale;
+  // the block's sums: with several rows per block, its row groups are added first
+  float* part = a.part + (int64_t)blockIdx.x * 3 * a.d;
+  if constexpr (kRows > 1) {
+    __shared__ float fold[kRows][TPR * VEC];
+    auto put = [&](float (&s)[NC][VEC], int which) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) fold[threadIdx.x / TPR][lane * VEC + e] = s[i][e];
+        __syncthreads();
+        for (int j = threadIdx.x; j < TPR * VEC; j += blockDim.x) {
+          float t = 0.f;
+#pragma unroll
+          for (int q = 0; q < kRows; ++q) t += fold[q][j];
+          const int c = i * TPR * VEC + j;
+          if (c < a.d) part[(int64_t)which * a.d + c] = t;
+        }
+      }
+    };
+    if (a.dw) put(sw, 0);
+    if (a.dls) put(sl, 1);
+    if (a.dow) put(so, 2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = (lane + i * TPR) * VEC;
+      if (c < a.d) {
+        if (a.dw) store<VEC>(part + c, sw[i]);
+        if (a.dls) store<VEC>(part + a.d + c, sl[i]);
+        if (a.dow) store<VEC>(part + 2 * (int64_t)a.d + c, so[i]);
+      }
+    }
+  }
+}
+
+// one warp row per 32 columns: 8 warps take every 8th block's sums, then fold
+__global__ void __launch_bounds__(256) norm_reduce_kernel(NormArgs a) {
+  __shared__ float fold[8][33];
+  const int which = blockIdx.y;
+  float* out = which == 0 ? a.dw : which == 1 ? a.dls : a.dow;
+  if (!out) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < a.d) {
+#pragma unroll 8
+    for (int64_t b = warp; b < a.ctas; b += 8) s += a.part[(b * 3 + which) * a.d + c];
+  }
+  fold[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < a.d) {
+#pragma unroll
+    for (int q = 1; q < 8; ++q) s += fold[q][lane];
+    out[c] = s;
+  }
+}
+
+template <typename T, typename TR, int VEC, int NC, int TPR, int PLACE>
+struct Backward {
+  static constexpr bool kPairs = false;
+  static cudaError_t run(const NormArgs& a) {
+    norm_bwd_kernel<T, TR, VEC, NC, TPR, PLACE>
+        <<<(unsigned)a.ctas, block_of<TPR>(), 0, a.stream>>>(a);
+    return cudaGetLastError();
+  }
+};
+
+}  // namespace
+
+// Blocks of the backward: those that are resident together (a thread takes about 128
+// registers), no more than there are rows for.
+int64_t norm_bwd_ctas(int64_t rows, int d, bool bf16, int64_t sms) {
+  const int chunks = (d + (bf16 ? 8 : 4) - 1) / (bf16 ? 8 : 4);
+  const int64_t most = chunks <= 128 ? 4 * sms : chunks <= 256 ? 2 * sms : sms;
+  return rows < 1 ? 1 : rows < most ? rows : most;
+}
+
+cudaError_t launch_norm_bwd(const NormArgs& a) {
+  cudaError_t e = by_type<Backward>(a);
+  if (e != cudaSuccess) return e;
+  if (!a.dw && !a.dls && !a.dow) return cudaSuccess;
+  norm_reduce_kernel<<<dim3((unsigned)((a.d + 31) / 32), 3), 256, 0, a.stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace layer
+}  // namespace kda
