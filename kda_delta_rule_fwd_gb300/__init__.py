@@ -78,6 +78,8 @@ _lock = threading.Lock()
 def load(path: str | None = None):
     """Open ``libkda.so`` (built by ``__graft_entry__.build()``); raise if it is missing."""
     global _lib
+    if path is None and _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib

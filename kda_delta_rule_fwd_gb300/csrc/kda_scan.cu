@@ -11,23 +11,27 @@ namespace {
 // ---------------------------------------------------------------------------
 // Prompts.  One block per (sequence, head, 32 state columns): a lane owns one
 // column, a warp DS/4 of its rows, in registers.  kTile tokens are staged in
-// shared memory as float32 at a time; the four warps' parts of y are added once
-// per tile.  Bound by the float32 multiply-adds (2 per state element and token).
+// shared memory as float32 at a time, two tiles in turn: the next tile's inputs are
+// requested before this one's tokens are worked on and stored after; the four warps'
+// parts of y are added once per tile.  Bound by the float32 multiply-adds (2 per state
+// element and token), or with few blocks by the chain of tokens.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 16;
 
 template <typename T, typename TO, int DS>
 __global__ void __launch_bounds__(128)
 scan_recurrent_kernel(ScanArgs a) {
-  constexpr int R = DS / 4;  // rows per warp
-  __shared__ __align__(16) float s_b[kTile][DS], s_c[kTile][DS];
-  __shared__ float s_x[kTile][32], s_y[kTile][4][32], s_a[kTile], s_d[kTile];
+  constexpr int R = DS / 4;                // rows per warp
+  constexpr int kB = kTile * DS / 128;     // elements of B (and C) a thread stages
+  constexpr int kX = kTile * 32 / 128;
+  __shared__ __align__(16) float s_b[2][kTile][DS], s_c[2][kTile][DS];
+  __shared__ float s_x[2][kTile][32], s_y[kTile][4][33], s_a[2][kTile], s_d[2][kTile];
   if (blockIdx.x == 0) check_seqlens(a.q, a.status);
   const int slices = a.dx / 32;
   const int sl = blockIdx.x % slices;
   const int64_t chain = blockIdx.x / slices;
   const int h = (int)(chain % a.H), n = (int)(chain / a.H), g = h / (a.H / a.G);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int col = sl * 32 + lane;
   int64_t s0, s1;
   a.q.range(n, s0, s1);
@@ -42,44 +46,76 @@ scan_recurrent_kernel(ScanArgs a) {
   const T* Cm = static_cast<const T*>(a.Cm) + (int64_t)g * DS;
   TO* y = static_cast<TO*>(a.y) + (int64_t)h * a.dx + sl * 32;
   const int64_t ldy = (int64_t)a.H * a.dx;
-  for (int64_t t0 = s0; t0 < s1; t0 += kTile) {
+  T rb[kB], rc[kB], rx[kX], rd;
+  auto request = [&](int64_t t0) {
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+      const int t = (i * 128 + tid) / DS, c = (i * 128 + tid) % DS;
+      if (t0 + t < s1) {
+        rb[i] = Bm[(t0 + t) * a.ldb + c];
+        rc[i] = Cm[(t0 + t) * a.ldc + c];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kX; ++i) {
+      const int t = i * 4 + warp;
+      if (t0 + t < s1) rx[i] = x[(t0 + t) * a.ldx + lane];
+    }
+    if (tid < kTile && t0 + tid < s1) rd = dt[(t0 + tid) * a.lddt];
+  };
+  auto stage = [&](int64_t t0, int b) {
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+      const int t = (i * 128 + tid) / DS, c = (i * 128 + tid) % DS;
+      if (t0 + t < s1) {
+        s_b[b][t][c] = to_f32(rb[i]);
+        s_c[b][t][c] = to_f32(rc[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kX; ++i) {
+      const int t = i * 4 + warp;
+      if (t0 + t < s1) s_x[b][t][lane] = to_f32(rx[i]);
+    }
+    if (tid < kTile && t0 + tid < s1) {
+      const float d = step_size(to_f32(rd), bias, a.softplus);
+      s_d[b][tid] = d;
+      s_a[b][tid] = expf(d * decay);
+    }
+  };
+  if (s0 < s1) {
+    request(s0);
+    stage(s0, 0);
+  }
+  __syncthreads();
+  int b = 0;
+  for (int64_t t0 = s0; t0 < s1; t0 += kTile, b ^= 1) {
     const int nt = s1 - t0 < kTile ? (int)(s1 - t0) : kTile;
-    for (int i = threadIdx.x; i < nt * DS; i += 128) {
-      const int t = i / DS, c = i % DS;
-      s_b[t][c] = to_f32(Bm[(t0 + t) * a.ldb + c]);
-      s_c[t][c] = to_f32(Cm[(t0 + t) * a.ldc + c]);
-    }
-    for (int i = threadIdx.x; i < nt * 32; i += 128)
-      s_x[i / 32][i % 32] = to_f32(x[(t0 + i / 32) * a.ldx + i % 32]);
-    if (threadIdx.x < nt) {
-      const float d = step_size(to_f32(dt[(t0 + threadIdx.x) * a.lddt]), bias, a.softplus);
-      s_d[threadIdx.x] = d;
-      s_a[threadIdx.x] = expf(d * decay);
-    }
-    __syncthreads();
+    if (t0 + kTile < s1) request(t0 + kTile);
     for (int t = 0; t < nt; ++t) {
-      const float at = s_a[t], xw = s_d[t] * s_x[t][lane];
+      const float at = s_a[b][t], xw = s_d[b][t] * s_x[b][t][lane];
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < R; i += 4) {
-        const float4 b = *reinterpret_cast<const float4*>(&s_b[t][warp * R + i]);
-        const float4 c = *reinterpret_cast<const float4*>(&s_c[t][warp * R + i]);
-        S[i] = fmaf(at, S[i], b.x * xw);
-        S[i + 1] = fmaf(at, S[i + 1], b.y * xw);
-        S[i + 2] = fmaf(at, S[i + 2], b.z * xw);
-        S[i + 3] = fmaf(at, S[i + 3], b.w * xw);
-        acc[0] = fmaf(c.x, S[i], acc[0]);
-        acc[1] = fmaf(c.y, S[i + 1], acc[1]);
-        acc[2] = fmaf(c.z, S[i + 2], acc[2]);
-        acc[3] = fmaf(c.w, S[i + 3], acc[3]);
+        const float4 bv = *reinterpret_cast<const float4*>(&s_b[b][t][warp * R + i]);
+        const float4 cv = *reinterpret_cast<const float4*>(&s_c[b][t][warp * R + i]);
+        S[i] = fmaf(at, S[i], bv.x * xw);
+        S[i + 1] = fmaf(at, S[i + 1], bv.y * xw);
+        S[i + 2] = fmaf(at, S[i + 2], bv.z * xw);
+        S[i + 3] = fmaf(at, S[i + 3], bv.w * xw);
+        acc[0] = fmaf(cv.x, S[i], acc[0]);
+        acc[1] = fmaf(cv.y, S[i + 1], acc[1]);
+        acc[2] = fmaf(cv.z, S[i + 2], acc[2]);
+        acc[3] = fmaf(cv.w, S[i + 3], acc[3]);
       }
       s_y[t][warp][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
     }
+    if (t0 + kTile < s1) stage(t0 + kTile, b ^ 1);
     __syncthreads();
-    for (int i = threadIdx.x; i < nt * 32; i += 128) {
+    for (int i = tid; i < nt * 32; i += 128) {
       const int t = i / 32, c = i % 32;
       const float v = (s_y[t][0][c] + s_y[t][1][c]) + (s_y[t][2][c] + s_y[t][3][c]);
-      y[(t0 + t) * ldy + c] = from_f32<TO>(fmaf(skip, s_x[t][c], v));
+      y[(t0 + t) * ldy + c] = from_f32<TO>(fmaf(skip, s_x[b][t][c], v));
     }
     __syncthreads();
   }
