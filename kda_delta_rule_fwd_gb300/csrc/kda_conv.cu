@@ -7,9 +7,10 @@
 // element: the work is bound by memory traffic.  A thread owns VEC channels (16
 // bytes) and walks a tile of tokens with the window of
 // W - 1 earlier inputs in registers, so a tile re-reads only the W - 1 tokens
-// before it; the loads of kAhead tokens are issued together, ahead of their use,
-// and held as they came.  Sequence boundaries of a packed batch are found once
-// per tile by bisection and then followed.
+// before it.  The wide path keeps the next tokens' inputs in flight into shared
+// memory (cp.async, each thread for itself, so that no barrier is needed): bytes in
+// flight then cost no registers.  Sequence boundaries of a packed batch are found
+// once per tile by bisection and then followed.
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -17,6 +18,28 @@ namespace layer {
 namespace {
 
 constexpr int kThreads = 128;
+// A thread's own ring of kSlots vectors in shared memory, filled ahead by cp.async.
+// Narrow elements (VEC = 1) are below the copy's smallest size: they are loaded in place.
+template <typename T, int VEC, int kSlots>
+struct Ring {
+  Raw<T, VEC>* mine;  // this thread's slot 0
+  __device__ __forceinline__ Raw<T, VEC>& slot(int64_t i) const { return mine[(i % kSlots) * kThreads]; }
+  __device__ __forceinline__ void request(int64_t i, const T* src) const {
+    if constexpr (VEC > 1) {
+      const uint32_t dst = (uint32_t)__cvta_generic_to_shared(&slot(i));
+      if constexpr (sizeof(Raw<T, VEC>) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+    } else {
+      slot(i) = fetch<T, VEC>(src);
+    }
+  }
+};
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ring_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // the window of W - 1 inputs before token t of sequence n, whose tokens start at s0
 template <int VEC, int W, typename T>
 __device__ __forceinline__ void load_window(const T* x, int64_t ldx, const T* init, int64_t t,
@@ -78,7 +101,8 @@ __device__ __forceinline__ void taps(const float (&wr)[W][VEC], const float (&br
 template <typename T, int VEC, int W, bool kSilu>
 __global__ void __launch_bounds__(kThreads, 5)
 conv_fwd_kernel(ConvArgs a, int cblocks) {
-  constexpr int kAhead = VEC == 1 ? 8 : 4;  // tokens whose loads are in flight together
+  constexpr int kGroup = 4, kGroups = 4;  // tokens per group of copies, groups in the ring
+  __shared__ __align__(16) Raw<T, VEC> ring_mem[kGroup * kGroups * kThreads];
   const T* x = static_cast<const T*>(a.x);
   const T* init = static_cast<const T*>(a.init);
   const int cb = blockIdx.x % cblocks;
@@ -117,81 +141,94 @@ conv_fwd_kernel(ConvArgs a, int cblocks) {
     store<VEC>(y + t * a.D, u);
     shift_in<VEC, W>(win, xt);
   };
-  int64_t t = t0;
-  while (t < t1) {
-    Raw<T, VEC> raw[kAhead];
-    if (t + kAhead <= t1 && t + kAhead <= s1) {  // inside one sequence
-      const T* p = x + t * a.ldx + c;
+  const Ring<T, VEC, kGroup * kGroups> ring{ring_mem + threadIdx.x};
+  const int count = (int)(t1 - t0);
+  const T* src = x + t0 * a.ldx + c;
+  auto request = [&](int i0) {  // the group of copies that starts at the tile's token i0
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) raw[i] = fetch<T, VEC>(p + i * a.ldx);
+    for (int i = 0; i < kGroup; ++i)
+      if (i0 + i < count) ring.request(i0 + i, src + (i0 + i) * a.ldx);
+    ring_commit();
+  };
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) token(t + i, raw[i]);
-      t += kAhead;
+  for (int g = 0; g < kGroups - 1; ++g) request(g * kGroup);
+  for (int i0 = 0; i0 < count; i0 += kGroup) {
+    request(i0 + (kGroups - 1) * kGroup);
+    ring_wait<kGroups - 1>();
+    const int64_t t = t0 + i0;
+    if (i0 + kGroup <= count && t + kGroup <= s1) {  // inside one sequence
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) token(t + i, ring.slot(i0 + i));
     } else {
-      if (t >= s1 && n + 1 < a.q.N) {  // the next sequence with tokens starts here
-        do a.q.range(++n, s0, s1);
-        while (t >= s1 && n + 1 < a.q.N);
-        load_window<VEC, W>(x, a.ldx, init, t, s0, n, a.D, c, win);
+#pragma unroll 1
+      for (int i = i0; i < i0 + kGroup && i < count; ++i) {
+        if (t0 + i >= s1 && n + 1 < a.q.N) {  // the next sequence with tokens starts here
+          do a.q.range(++n, s0, s1);
+          while (t0 + i >= s1 && n + 1 < a.q.N);
+          load_window<VEC, W>(x, a.ldx, init, t0 + i, s0, n, a.D, c, win);
+        }
+        token(t0 + i, ring.slot(i));
       }
-      raw[0] = fetch<T, VEC>(x + t * a.ldx + c);
-      token(t++, raw[0]);
     }
   }
 }
 
 // Single tokens.  A block owns kThreads * VEC channels, loads their taps once and
-// walks sequences n = j, j + jobs, ..., kSeqs of them at a time so that their loads
-// are in flight together; T tokens in order, the state in registers.
-template <typename T, int VEC, int W, bool kSilu, int kSeqs>
-__global__ void __launch_bounds__(kThreads)
+// walks sequences j, j + jobs, ...; the state and the first token of the next kSeqs
+// sequences are in flight into shared memory meanwhile.  T tokens in order, the state
+// in registers.
+template <typename T, int VEC, int W, bool kSilu>
+__global__ void __launch_bounds__(kThreads, 4)
 conv_step_kernel(ConvArgs a, int cblocks) {
+  constexpr int kSeqs = 4;
+  __shared__ __align__(16) Raw<T, VEC> ring_mem[kSeqs * W * kThreads];
+  const Ring<T, VEC, kSeqs * W> ring{ring_mem + threadIdx.x};
   const T* x = static_cast<const T*>(a.x);
   const int cb = blockIdx.x % cblocks;
   const int64_t jobs = gridDim.x / cblocks;
   if (blockIdx.x == 0) check_counts(a.counts, a.q.N, a.T, a.status);
   const int c = (cb * kThreads + threadIdx.x) * VEC;
   if (c >= a.D) return;
+  const int64_t n0 = blockIdx.x / cblocks;
+  auto request = [&](int64_t k) {  // this block's k-th sequence
+    const int64_t n = n0 + k * jobs;
+    if (n < a.q.N) {
+      const T* st = static_cast<const T*>(a.state) + n * (W - 1) * a.D + c;
+#pragma unroll
+      for (int i = 0; i < W - 1; ++i) ring.request(k * W + i, st + (int64_t)i * a.D);
+      ring.request(k * W + W - 1, x + n * a.T * a.ldx + c);
+    }
+    ring_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kSeqs - 1; ++k) request(k);
   float wr[W][VEC], br[VEC];
   load_params<VEC, W>(a.w, a.b, c, wr, br);
-  for (int64_t n0 = blockIdx.x / cblocks; n0 < a.q.N; n0 += jobs * kSeqs) {
-    Raw<T, VEC> old[kSeqs][W - 1], first[kSeqs];
-    int keep[kSeqs];
-#pragma unroll
-    for (int q = 0; q < kSeqs; ++q) {
-      const int64_t n = n0 + q * jobs;
-      if (n < a.q.N) {
-        const T* st = static_cast<const T*>(a.state) + n * (W - 1) * a.D + c;
-#pragma unroll
-        for (int i = 0; i < W - 1; ++i) old[q][i] = fetch<T, VEC>(st + (int64_t)i * a.D);
-        first[q] = fetch<T, VEC>(x + n * a.T * a.ldx + c);
-        keep[q] = a.counts ? a.counts[n] : a.T;
-        if (keep[q] < 0 || keep[q] > a.T) keep[q] = 0;
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kSeqs; ++q) {
-      const int64_t n = n0 + q * jobs;
-      if (n >= a.q.N) break;
-      T* st = static_cast<T*>(a.state) + n * (W - 1) * a.D + c;
-      float win[W - 1][VEC];
-#pragma unroll
-      for (int i = 0; i < W - 1; ++i) open<T, VEC>(old[q][i], win[i]);
 #pragma unroll 1
-      for (int t = 0; t < a.T; ++t) {
-        float xt[VEC], u[VEC];
-        if (t == 0) open<T, VEC>(first[q], xt);
-        else load<VEC>(x + (n * a.T + t) * a.ldx + c, xt);
-        taps<VEC, W>(wr, br, win, xt, u);
-        if (kSilu) {
+  for (int64_t k = 0, n = n0; n < a.q.N; ++k, n += jobs) {
+    request(k + kSeqs - 1);
+    ring_wait<kSeqs - 1>();
+    T* st = static_cast<T*>(a.state) + n * (W - 1) * a.D + c;
+    float win[W - 1][VEC];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) u[e] *= sigmoid(u[e]);
-        }
-        if (a.y) store<VEC>(static_cast<T*>(a.y) + (n * a.T + t) * a.D + c, u);
-        shift_in<VEC, W>(win, xt);
-        if (t + 1 == keep[q]) {
+    for (int i = 0; i < W - 1; ++i) open<T, VEC>(ring.slot(k * W + i), win[i]);
+    int keep = a.counts ? a.counts[n] : a.T;
+    if (keep < 0 || keep > a.T) keep = 0;
+#pragma unroll 1
+    for (int t = 0; t < a.T; ++t) {
+      float xt[VEC], u[VEC];
+      if (t == 0) open<T, VEC>(ring.slot(k * W + W - 1), xt);
+      else load<VEC>(x + (n * a.T + t) * a.ldx + c, xt);
+      taps<VEC, W>(wr, br, win, xt, u);
+      if (kSilu) {
 #pragma unroll
-          for (int i = 0; i < W - 1; ++i) store<VEC>(st + (int64_t)i * a.D, win[i]);
-        }
+        for (int e = 0; e < VEC; ++e) u[e] *= sigmoid(u[e]);
+      }
+      if (a.y) store<VEC>(static_cast<T*>(a.y) + (n * a.T + t) * a.D + c, u);
+      shift_in<VEC, W>(win, xt);
+      if (t + 1 == keep) {
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) store<VEC>(st + (int64_t)i * a.D, win[i]);
       }
     }
   }
@@ -204,9 +241,13 @@ conv_step_kernel(ConvArgs a, int cblocks) {
 // sums for dw and dbias go to part[tile][W + 1][D] and are added in the order of
 // the tiles by conv_reduce_kernel, so the results do not depend on scheduling.
 template <typename T, int VEC, int W, bool kSilu>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, 3)
 conv_bwd_kernel(ConvArgs a, int cblocks) {
-  constexpr int kAhead = 4;  // tokens whose loads are in flight together
+  // W - 1 tokens per group: after as many shifts the window holds new values only, and no
+  // register has to move
+  constexpr int kGroup = W - 1, kGroups = 8 / (W - 1) + 1;
+  __shared__ __align__(16) Raw<T, VEC> ring_x[kGroup * kGroups * kThreads];
+  __shared__ __align__(16) Raw<T, VEC> ring_g[kGroup * kGroups * kThreads];
   const T* x = static_cast<const T*>(a.x);
   const T* init = static_cast<const T*>(a.init);
   const T* dy = static_cast<const T*>(a.dy);
@@ -337,36 +378,44 @@ conv_bwd_kernel(ConvArgs a, int cblocks) {
     }
     shift_in<VEC, W>(win, xt);
   };
-  int64_t t = t0;
-  while (t < stop && !ended) {
-    Raw<T, VEC> xa[kAhead], ga[kAhead];
-    if (t + kAhead <= t1 && t + kAhead <= s1 && t - (W - 1) >= t0 && t - (W - 1) >= s0) {
-      const T* px = x + t * a.ldx + c;
-      const T* pg = dy + t * a.D + c;
+  const Ring<T, VEC, kGroup * kGroups> rx{ring_x + threadIdx.x}, rg{ring_g + threadIdx.x};
+  const int count = (int)(stop - t0);
+  const T* px = x + t0 * a.ldx + c;
+  const T* pg = dy + t0 * a.D + c;
+  auto request = [&](int i0) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        xa[i] = fetch<T, VEC>(px + i * a.ldx);
-        ga[i] = fetch<T, VEC>(pg + (int64_t)i * a.D);
+    for (int i = 0; i < kGroup; ++i)
+      if (i0 + i < count) {
+        rx.request(i0 + i, px + (i0 + i) * a.ldx);
+        rg.request(i0 + i, pg + (i0 + i) * (int64_t)a.D);
       }
+    ring_commit();
+  };
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) token(t + i, xa[i], ga[i], true, true);
-      t += kAhead;
+  for (int g = 0; g < kGroups - 1; ++g) request(g * kGroup);
+  for (int i0 = 0; i0 < count && !ended; i0 += kGroup) {
+    request(i0 + (kGroups - 1) * kGroup);
+    ring_wait<kGroups - 1>();
+    const int64_t t = t0 + i0;
+    if (t + kGroup <= t1 && t + kGroup <= s1 && t - (W - 1) >= t0 && t - (W - 1) >= s0) {
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) token(t + i, rx.slot(i0 + i), rg.slot(i0 + i), true, true);
     } else {
-      if (t >= s1 && n + 1 < a.q.N) {
-        flush(s1);
-        if (t >= t1) {
-          ended = true;
-          break;
+#pragma unroll 1
+      for (int i = i0; i < i0 + kGroup && i < count; ++i) {
+        const int64_t p = t0 + i;
+        if (p >= s1 && n + 1 < a.q.N) {
+          flush(s1);
+          if (p >= t1) {
+            ended = true;
+            break;
+          }
+          do a.q.range(++n, s0, s1);
+          while (p >= s1 && n + 1 < a.q.N);
+          load_window<VEC, W>(x, a.ldx, init, p, s0, n, a.D, c, win);
         }
-        do a.q.range(++n, s0, s1);
-        while (t >= s1 && n + 1 < a.q.N);
-        load_window<VEC, W>(x, a.ldx, init, t, s0, n, a.D, c, win);
+        token(p, rx.slot(i), rg.slot(i), p - (W - 1) >= t0 && p - (W - 1) >= s0, p < t1);
       }
-      xa[0] = fetch<T, VEC>(x + t * a.ldx + c);
-      ga[0] = fetch<T, VEC>(dy + t * a.D + c);
-      const int64_t s = t - (W - 1);
-      token(t, xa[0], ga[0], s >= t0 && s >= s0, t < t1);
-      ++t;
     }
   }
   if (!ended && s1 <= stop) flush(s1);
@@ -401,11 +450,10 @@ bool al16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
 template <typename T, int VEC, int W>
 cudaError_t run(const ConvArgs& a, int what) {
-  constexpr bool kGrad = !(sizeof(T) == 2 && VEC == 8), kRest = !(sizeof(T) == 2 && VEC == 4);
   const int cblocks = (a.D + kThreads * VEC - 1) / (kThreads * VEC);
   const int64_t extra = what == 0 ? (a.fin ? a.q.N : 0) : what == 2 ? (a.dinit ? a.q.N : 0) : 0;
-  // single tokens: enough blocks to fill the device, each with several sequences
-  const int64_t fill = (a.sms * 12 + cblocks - 1) / cblocks;
+  // single tokens: the blocks that are resident together, each with its share of sequences
+  const int64_t fill = (a.sms * 4 + cblocks - 1) / cblocks;
   const int64_t jobs = what == 1 ? (a.q.N < fill ? a.q.N : fill) : a.tiles + extra;
   const int64_t grid = jobs * cblocks;
   if (grid == 0)  // nothing to check or to compute
@@ -415,19 +463,11 @@ cudaError_t run(const ConvArgs& a, int what) {
     kernel<<<(unsigned)grid, kThreads, 0, a.stream>>>(a, cblocks);
     return cudaGetLastError();
   };
-  if constexpr (kGrad) {
-    if (what == 2)
-      return a.silu ? go(conv_bwd_kernel<T, VEC, W, true>) : go(conv_bwd_kernel<T, VEC, W, false>);
-  }
-  if constexpr (kRest) {
-    if (what == 0)
-      return a.silu ? go(conv_fwd_kernel<T, VEC, W, true>) : go(conv_fwd_kernel<T, VEC, W, false>);
-    constexpr int kSeqs = VEC == 8 ? 2 : 4;
-    if (what == 1)
-      return a.silu ? go(conv_step_kernel<T, VEC, W, true, kSeqs>)
-                    : go(conv_step_kernel<T, VEC, W, false, kSeqs>);
-  }
-  return cudaErrorInvalidValue;
+  if (what == 0)
+    return a.silu ? go(conv_fwd_kernel<T, VEC, W, true>) : go(conv_fwd_kernel<T, VEC, W, false>);
+  if (what == 1)
+    return a.silu ? go(conv_step_kernel<T, VEC, W, true>) : go(conv_step_kernel<T, VEC, W, false>);
+  return a.silu ? go(conv_bwd_kernel<T, VEC, W, true>) : go(conv_bwd_kernel<T, VEC, W, false>);
 }
 template <typename T, int VEC>
 cudaError_t by_width(const ConvArgs& a, int what) {
@@ -437,8 +477,7 @@ cudaError_t by_width(const ConvArgs& a, int what) {
     default: return run<T, VEC, 4>(a, what);
   }
 }
-// wide loads where every row of every operand starts on a 16-byte boundary (the
-// gradient, with more to keep in registers, takes half as many bf16 channels)
+// wide loads where every row of every operand starts on a 16-byte boundary
 cudaError_t by_type(const ConvArgs& a, int what) {
   const void* ptrs[] = {a.x, a.init, a.dy, a.dfinal, a.y, a.fin, a.dx, a.dinit, a.state};
   const int v = a.bf16 ? 8 : 4;
@@ -446,7 +485,7 @@ cudaError_t by_type(const ConvArgs& a, int what) {
   for (const void* p : ptrs) wide = wide && al16(p);
   if (!a.bf16) return wide ? by_width<float, 4>(a, what) : by_width<float, 1>(a, what);
   if (!wide) return by_width<__nv_bfloat16, 1>(a, what);
-  return what == 2 ? by_width<__nv_bfloat16, 4>(a, what) : by_width<__nv_bfloat16, 8>(a, what);
+  return by_width<__nv_bfloat16, 8>(a, what);
 }
 
 }  // namespace
@@ -465,9 +504,9 @@ cudaError_t launch_conv_fwd(const ConvArgs& a0) {
 cudaError_t launch_conv_step(const ConvArgs& a) { return by_type(a, 1); }
 
 int64_t conv_bwd_tile(int64_t tokens, int D, int64_t sms) {
-  const int64_t cb = (D + kThreads * 4 - 1) / (kThreads * 4);
+  const int64_t cb = (D + kThreads * 8 - 1) / (kThreads * 8);
   int64_t tile = 256;
-  while (tile > 16 && cb * ((tokens + tile - 1) / tile) < 8 * sms) tile /= 2;
+  while (tile > 16 && cb * ((tokens + tile - 1) / tile) < 6 * sms) tile /= 2;
   return tile;
 }
 

@@ -13,7 +13,7 @@ __global__ void __launch_bounds__(block_of<TPR>())
 norm_fwd_kernel(NormArgs a) {
   constexpr int kRows = block_of<TPR>() / TPR;  // rows per block
   constexpr bool kKeep = TPR <= 32;             // parameters stay in registers
-  __shared__ float scratch[2][32];
+  __shared__ float2 scratch[2][32];
   int flip = 0;
   const int64_t rows = a.tokens * a.heads, step = (int64_t)gridDim.x * kRows;
   const int lane = threadIdx.x % TPR;
@@ -33,23 +33,18 @@ norm_fwd_kernel(NormArgs a) {
   if (kKeep) params();
   RowIn<T, TR, VEC, NC, false> in;
   int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
-  if (row < rows) request<T, TR, VEC, NC, TPR, PLACE, false>(a, row, lane, in);
+  request<T, TR, VEC, NC, TPR, PLACE, false>(a, row, lane, in);
   for (int64_t base = (int64_t)blockIdx.x * kRows; base < rows; base += step, row += step) {
     const bool on = row < rows;
     float v[NC][VEC], z[NC][VEC], rs[NC][VEC];
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const bool have = on && (lane + i * TPR) * VEC < a.d;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[i][e] = z[i][e] = rs[i][e] = 0.f;
-      if (have) {
-        open<T, VEC>(in.x[i], v[i]);
-        if (PLACE != kNoGate) open<T, VEC>(in.g[i], z[i]);
-        if (kFull && a.res) open<TR, VEC>(in.res[i], rs[i]);
-      }
+      open<T, VEC>(in.x[i], v[i]);
+      if (PLACE != kNoGate) open<T, VEC>(in.g[i], z[i]);
+      open<TR, VEC>(in.res[i], rs[i]);
     }
-    if (row + step < rows) request<T, TR, VEC, NC, TPR, PLACE, false>(a, row + step, lane, in);
+    request<T, TR, VEC, NC, TPR, PLACE, false>(a, row + step, lane, in);
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll

@@ -13,6 +13,8 @@
 // leave room for them (up to 32 threads per row).
 #pragma once
 
+#include <type_traits>
+
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -22,21 +24,48 @@ namespace norm {
 // sum over the TPR threads of a row; every thread gets it.  Above 32 threads the
 // row is the whole block: two alternating scratch rows leave one barrier per sum.
 template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float (*scratch)[32], int& flip) {
+__device__ __forceinline__ float row_sum(float v, float2 (*scratch)[32], int& flip) {
   constexpr int kIn = TPR < 32 ? TPR : 32;
 #pragma unroll
   for (int o = kIn / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (TPR > 32) {
     constexpr int kWarps = TPR / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) scratch[flip][warp] = v;
+    if (lane == 0) scratch[flip][warp].x = v;
     __syncthreads();
-    v = lane < kWarps ? scratch[flip][lane] : 0.f;
+    v = lane < kWarps ? scratch[flip][lane].x : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     flip ^= 1;
   }
   return v;
+}
+
+// the same for two sums at once
+template <int TPR>
+__device__ __forceinline__ float2 row_sums(float a, float b, float2 (*scratch)[32], int& flip) {
+  constexpr int kIn = TPR < 32 ? TPR : 32;
+#pragma unroll
+  for (int o = kIn / 2; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if constexpr (TPR > 32) {
+    constexpr int kWarps = TPR / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) scratch[flip][warp] = make_float2(a, b);
+    __syncthreads();
+    const float2 v = lane < kWarps ? scratch[flip][lane] : make_float2(0.f, 0.f);
+    a = v.x;
+    b = v.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    flip ^= 1;
+  }
+  return make_float2(a, b);
 }
 
 template <int TPR> constexpr int block_of() { return TPR < 128 ? 128 : TPR; }
@@ -61,7 +90,9 @@ template <typename T, typename TR, int VEC, int NC, int TPR, int PLACE, bool kBw
 __device__ __forceinline__ void request(const NormArgs& a, int64_t row, int lane,
                                         RowIn<T, TR, VEC, NC, kBwd>& in) {
   int64_t xo = row * a.d, go = xo;
-  if (!a.dense) {
+  // chunks past the row (and rows past the last) are zeros
+  const bool on = row < a.tokens * a.heads;
+  if (on && !a.dense) {
     const int64_t tok = row / a.heads;
     const int64_t head = (row - tok * a.heads) * a.d;
     xo = tok * a.ldx + head;
@@ -70,15 +101,19 @@ __device__ __forceinline__ void request(const NormArgs& a, int64_t row, int lane
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = (lane + i * TPR) * VEC;
-    if (c < a.d) {
-      in.x[i] = fetch<T, VEC>(static_cast<const T*>(a.x) + xo + c);
-      if (PLACE != kNoGate) in.g[i] = fetch<T, VEC>(static_cast<const T*>(a.gate) + go + c);
-      // the gradient needs the residual only to form y's norm again
-      if (a.res && (!kBwd || a.ow)) in.res[i] = fetch<TR, VEC>(static_cast<const TR*>(a.res) + row * a.d + c);
-      if constexpr (kBwd) {
-        if (a.dr) in.dr[i] = fetch<TR, VEC>(static_cast<const TR*>(a.dr) + row * a.d + c);
-        if (a.dy) in.dy[i] = fetch<T, VEC>(static_cast<const T*>(a.dy) + row * a.d + c);
-      }
+    const bool in_row = on && c < a.d;
+    auto get = [&](auto& raw, const auto* p, int64_t o, bool have) {
+      using E = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
+      if (in_row && have) raw = fetch<E, VEC>(p + o + c);
+      else raw = Raw<E, VEC>{};
+    };
+    get(in.x[i], static_cast<const T*>(a.x), xo, true);
+    if (PLACE != kNoGate) get(in.g[i], static_cast<const T*>(a.gate), go, true);
+    // the gradient needs the residual only to form y's norm again
+    get(in.res[i], static_cast<const TR*>(a.res), row * a.d, a.res && (!kBwd || a.ow));
+    if constexpr (kBwd) {
+      get(in.dr[i], static_cast<const TR*>(a.dr), row * a.d, a.dr != nullptr);
+      get(in.dy[i], static_cast<const T*>(a.dy), row * a.d, a.dy != nullptr);
     }
   }
 }

@@ -16,7 +16,7 @@ template <typename T, typename TR, int VEC, int NC, int TPR, int PLACE>
 __global__ void __launch_bounds__(block_of<TPR>())
 norm_bwd_kernel(NormArgs a) {
   constexpr int kRows = block_of<TPR>() / TPR;
-  __shared__ float scratch[2][32];
+  __shared__ float2 scratch[2][32];
   int flip = 0;
   const int64_t rows = a.tokens * a.heads, step = (int64_t)gridDim.x * kRows;
   const int lane = threadIdx.x % TPR;
@@ -28,7 +28,7 @@ norm_bwd_kernel(NormArgs a) {
     for (int e = 0; e < VEC; ++e) sw[i][e] = sl[i][e] = so[i][e] = 0.f;
   RowIn<T, TR, VEC, NC, true> in;
   int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
-  if (row < rows) request<T, TR, VEC, NC, TPR, PLACE, true>(a, row, lane, in);
+  request<T, TR, VEC, NC, TPR, PLACE, true>(a, row, lane, in);
   for (int64_t base = (int64_t)blockIdx.x * kRows; base < rows; base += step, row += step) {
     const bool on = row < rows;
     // n: the norm's input v, then v k;  z, sz: the gate and (x's factor in) its slope;
@@ -37,17 +37,13 @@ norm_bwd_kernel(NormArgs a) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) n[i][e] = z[i][e] = r[i][e] = dr[i][e] = dy[i][e] = 0.f;
-      if (on && (lane + i * TPR) * VEC < a.d) {
-        open<T, VEC>(in.x[i], n[i]);
-        if (PLACE != kNoGate) open<T, VEC>(in.g[i], z[i]);
-        if (a.res && a.ow) open<TR, VEC>(in.res[i], r[i]);
-        if (a.dr) open<TR, VEC>(in.dr[i], dr[i]);
-        if (a.dy) open<T, VEC>(in.dy[i], dy[i]);
-      }
+      open<T, VEC>(in.x[i], n[i]);
+      if (PLACE != kNoGate) open<T, VEC>(in.g[i], z[i]);
+      open<TR, VEC>(in.res[i], r[i]);
+      open<TR, VEC>(in.dr[i], dr[i]);
+      open<T, VEC>(in.dy[i], dy[i]);
     }
-    if (row + step < rows) request<T, TR, VEC, NC, TPR, PLACE, true>(a, row + step, lane, in);
+    request<T, TR, VEC, NC, TPR, PLACE, true>(a, row + step, lane, in);
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -72,25 +68,27 @@ norm_bwd_kernel(NormArgs a) {
         for (int e = 0; e < VEC; ++e) n[i][e] *= k;
     }
     if (a.ow) {
-      ss = 0.f;
+      float rr = 0.f, pr = 0.f;  // sums of r^2 and of p r: p n's is k2 times the second
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = (lane + i * TPR) * VEC;
         if (c < a.d) {
-          float w[VEC], ls[VEC];
+          float w[VEC], ls[VEC], ow[VEC];
           param<VEC>(a.w, c, 1.f, w);
           param<VEC>(a.ls, c, a.scale, ls);
+          param<VEC>(a.ow, c, 1.f, ow);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
             float b = n[i][e] * w[e];
             if (PLACE == kAfter) b *= z[i][e];
             r[i][e] = fmaf(ls[e], b, r[i][e]);
-            ss = fmaf(r[i][e], r[i][e], ss);
+            rr = fmaf(r[i][e], r[i][e], rr);
+            pr = fmaf(dy[i][e] * ow[e], r[i][e], pr);
           }
         }
       }
-      const float k2 = rsqrtf(fmaf(row_sum<TPR>(ss, scratch, flip), a.inv_d, a.eps));
-      float pn = 0.f;
+      const float2 s = row_sums<TPR>(rr, pr, scratch, flip);
+      const float k2 = rsqrtf(fmaf(s.x, a.inv_d, a.eps)), mean = k2 * k2 * s.y * a.inv_d;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = (lane + i * TPR) * VEC;
@@ -99,18 +97,11 @@ norm_bwd_kernel(NormArgs a) {
           param<VEC>(a.ow, c, 1.f, ow);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            r[i][e] *= k2;  // n of the outer norm
-            so[i][e] = fmaf(dy[i][e], r[i][e], so[i][e]);
-            dy[i][e] *= ow[e];  // p
-            pn = fmaf(dy[i][e], r[i][e], pn);
+            so[i][e] = fmaf(dy[i][e], k2 * r[i][e], so[i][e]);
+            dr[i][e] = fmaf(k2, fmaf(-mean, r[i][e], dy[i][e] * ow[e]), dr[i][e]);
           }
         }
       }
-      pn = row_sum<TPR>(pn, scratch, flip) * a.inv_d;
-#pragma unroll
-      for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) dr[i][e] = fmaf(k2, fmaf(-pn, r[i][e], dy[i][e]), dr[i][e]);
     }
     // through the residual sum and the branch; dgate (gate after) in sz
     float pn = 0.f;

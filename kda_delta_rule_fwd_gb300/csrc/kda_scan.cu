@@ -9,57 +9,60 @@ namespace layer {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Prompts.  One block per (sequence, head, 32 state columns): a lane owns one
-// column, a warp DS/4 of its rows, in registers.  kTile tokens are staged in
-// shared memory as float32 at a time, two tiles in turn: the next tile's inputs are
-// requested before this one's tokens are worked on and stored after; the four warps'
-// parts of y are added once per tile.  Bound by the float32 multiply-adds (2 per state
-// element and token), or with few blocks by the chain of tokens.
+// Prompts.  One block of 128 threads per (sequence, head, COLS state columns): a
+// thread owns one column and DS * COLS / 128 of its rows, in registers.  kTile tokens
+// are staged in shared memory as float32 at a time, two tiles in turn: the next tile's
+// inputs are requested before this one's tokens are worked on and stored after; the
+// row groups' parts of y meet by shuffles inside a warp and once per tile across the
+// warps.  With many blocks it is bound by the float32 multiply-adds (2 per state element
+// and token), and 32 columns share each read of B and C best; with few, by the chain of
+// tokens, which 8 columns per block keep short.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 16;
 
-template <typename T, typename TO, int DS>
+template <typename T, typename TO, int DS, int COLS>
 __global__ void __launch_bounds__(128)
 scan_recurrent_kernel(ScanArgs a) {
-  constexpr int R = DS / 4;                // rows per warp
+  constexpr int R = DS * COLS / 128;       // rows per thread
   constexpr int kB = kTile * DS / 128;     // elements of B (and C) a thread stages
-  constexpr int kX = kTile * 32 / 128;
+  constexpr int kX = kTile * COLS / 128;
   __shared__ __align__(16) float s_b[2][kTile][DS], s_c[2][kTile][DS];
-  __shared__ float s_x[2][kTile][32], s_y[kTile][4][33], s_a[2][kTile], s_d[2][kTile];
+  __shared__ float s_x[2][kTile][COLS], s_y[kTile][4][COLS], s_a[2][kTile], s_d[2][kTile];
   if (blockIdx.x == 0) check_seqlens(a.q, a.status);
-  const int slices = a.dx / 32;
+  const int slices = a.dx / COLS;
   const int sl = blockIdx.x % slices;
   const int64_t chain = blockIdx.x / slices;
   const int h = (int)(chain % a.H), n = (int)(chain / a.H), g = h / (a.H / a.G);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int col = sl * 32 + lane;
+  const int cl = lane % COLS;                              // column in the slice
+  const int row0 = (warp * (32 / COLS) + lane / COLS) * R;
   int64_t s0, s1;
   a.q.range(n, s0, s1);
-  const int64_t base = (chain * DS + warp * R) * (int64_t)a.dx + col;
+  const int64_t base = (chain * DS + row0) * (int64_t)a.dx + sl * COLS + cl;
   float S[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) S[i] = a.h0 ? a.h0[base + (int64_t)i * a.dx] : 0.f;
   const float decay = a.A[h], skip = a.D ? a.D[h] : 0.f, bias = a.dtb ? a.dtb[h] : 0.f;
-  const T* x = static_cast<const T*>(a.x) + (int64_t)h * a.dx + sl * 32;
+  const T* x = static_cast<const T*>(a.x) + (int64_t)h * a.dx + sl * COLS;
   const T* dt = static_cast<const T*>(a.dt) + h;
   const T* Bm = static_cast<const T*>(a.Bm) + (int64_t)g * DS;
   const T* Cm = static_cast<const T*>(a.Cm) + (int64_t)g * DS;
-  TO* y = static_cast<TO*>(a.y) + (int64_t)h * a.dx + sl * 32;
+  TO* y = static_cast<TO*>(a.y) + (int64_t)h * a.dx + sl * COLS;
   const int64_t ldy = (int64_t)a.H * a.dx;
+  // tokens past the end enter as zeros with a decay of 1
   T rb[kB], rc[kB], rx[kX], rd;
   auto request = [&](int64_t t0) {
 #pragma unroll
     for (int i = 0; i < kB; ++i) {
       const int t = (i * 128 + tid) / DS, c = (i * 128 + tid) % DS;
-      if (t0 + t < s1) {
-        rb[i] = Bm[(t0 + t) * a.ldb + c];
-        rc[i] = Cm[(t0 + t) * a.ldc + c];
-      }
+      const bool in = t0 + t < s1;
+      rb[i] = in ? Bm[(t0 + t) * a.ldb + c] : from_f32<T>(0.f);
+      rc[i] = in ? Cm[(t0 + t) * a.ldc + c] : from_f32<T>(0.f);
     }
 #pragma unroll
     for (int i = 0; i < kX; ++i) {
-      const int t = i * 4 + warp;
-      if (t0 + t < s1) rx[i] = x[(t0 + t) * a.ldx + lane];
+      const int t = (i * 128 + tid) / COLS, c = (i * 128 + tid) % COLS;
+      rx[i] = t0 + t < s1 ? x[(t0 + t) * a.ldx + c] : from_f32<T>(0.f);
     }
     if (tid < kTile && t0 + tid < s1) rd = dt[(t0 + tid) * a.lddt];
   };
@@ -67,18 +70,14 @@ scan_recurrent_kernel(ScanArgs a) {
 #pragma unroll
     for (int i = 0; i < kB; ++i) {
       const int t = (i * 128 + tid) / DS, c = (i * 128 + tid) % DS;
-      if (t0 + t < s1) {
-        s_b[b][t][c] = to_f32(rb[i]);
-        s_c[b][t][c] = to_f32(rc[i]);
-      }
+      s_b[b][t][c] = to_f32(rb[i]);
+      s_c[b][t][c] = to_f32(rc[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kX; ++i) {
-      const int t = i * 4 + warp;
-      if (t0 + t < s1) s_x[b][t][lane] = to_f32(rx[i]);
-    }
-    if (tid < kTile && t0 + tid < s1) {
-      const float d = step_size(to_f32(rd), bias, a.softplus);
+    for (int i = 0; i < kX; ++i)
+      s_x[b][(i * 128 + tid) / COLS][(i * 128 + tid) % COLS] = to_f32(rx[i]);
+    if (tid < kTile) {
+      const float d = t0 + tid < s1 ? step_size(to_f32(rd), bias, a.softplus) : 0.f;
       s_d[b][tid] = d;
       s_a[b][tid] = expf(d * decay);
     }
@@ -90,15 +89,15 @@ scan_recurrent_kernel(ScanArgs a) {
   __syncthreads();
   int b = 0;
   for (int64_t t0 = s0; t0 < s1; t0 += kTile, b ^= 1) {
-    const int nt = s1 - t0 < kTile ? (int)(s1 - t0) : kTile;
     if (t0 + kTile < s1) request(t0 + kTile);
-    for (int t = 0; t < nt; ++t) {
-      const float at = s_a[b][t], xw = s_d[b][t] * s_x[b][t][lane];
+#pragma unroll 4
+    for (int t = 0; t < kTile; ++t) {
+      const float at = s_a[b][t], xw = s_d[b][t] * s_x[b][t][cl];
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < R; i += 4) {
-        const float4 bv = *reinterpret_cast<const float4*>(&s_b[b][t][warp * R + i]);
-        const float4 cv = *reinterpret_cast<const float4*>(&s_c[b][t][warp * R + i]);
+        const float4 bv = *reinterpret_cast<const float4*>(&s_b[b][t][row0 + i]);
+        const float4 cv = *reinterpret_cast<const float4*>(&s_c[b][t][row0 + i]);
         S[i] = fmaf(at, S[i], bv.x * xw);
         S[i + 1] = fmaf(at, S[i + 1], bv.y * xw);
         S[i + 2] = fmaf(at, S[i + 2], bv.z * xw);
@@ -108,14 +107,17 @@ scan_recurrent_kernel(ScanArgs a) {
         acc[2] = fmaf(cv.z, S[i + 2], acc[2]);
         acc[3] = fmaf(cv.w, S[i + 3], acc[3]);
       }
-      s_y[t][warp][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      float v = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+#pragma unroll
+      for (int o = COLS; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane < COLS) s_y[t][warp][cl] = v;
     }
     if (t0 + kTile < s1) stage(t0 + kTile, b ^ 1);
     __syncthreads();
-    for (int i = tid; i < nt * 32; i += 128) {
-      const int t = i / 32, c = i % 32;
+    for (int i = tid; i < kTile * COLS; i += 128) {
+      const int t = i / COLS, c = i % COLS;
       const float v = (s_y[t][0][c] + s_y[t][1][c]) + (s_y[t][2][c] + s_y[t][3][c]);
-      y[(t0 + t) * ldy + c] = from_f32<TO>(fmaf(skip, s_x[b][t][c], v));
+      if (t0 + t < s1) y[(t0 + t) * ldy + c] = from_f32<TO>(fmaf(skip, s_x[b][t][c], v));
     }
     __syncthreads();
   }
@@ -221,12 +223,18 @@ scan_step_kernel(ScanArgs a) {
   }
 }
 
+template <typename T, typename TO, int DS, int COLS>
+cudaError_t recurrent_cols(const ScanArgs& a) {
+  const int64_t grid = (int64_t)a.q.N * a.H * (a.dx / COLS);
+  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  scan_recurrent_kernel<T, TO, DS, COLS><<<(unsigned)grid, 128, 0, a.stream>>>(a);
+  return cudaGetLastError();
+}
 template <typename T, typename TO, int DS>
 cudaError_t recurrent(const ScanArgs& a) {
-  const int64_t grid = (int64_t)a.q.N * a.H * (a.dx / 32);
-  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  scan_recurrent_kernel<T, TO, DS><<<(unsigned)grid, 128, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  // 8 columns per block while even those blocks find an SM each
+  return (int64_t)a.q.N * a.H * (a.dx / 8) <= a.sms ? recurrent_cols<T, TO, DS, 8>(a)
+                                                    : recurrent_cols<T, TO, DS, 32>(a);
 }
 template <typename T, typename TO>
 cudaError_t recurrent_ds(const ScanArgs& a) {

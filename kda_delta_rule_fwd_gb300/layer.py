@@ -87,6 +87,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _new(x, dtype):
+    """An output of x's shape (empty_like is the cheaper call where x is dense)."""
+    if dtype is x.dtype and x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, dtype=dtype, device=x.device)
+
+
 def _elsewhere(x, stream):
     """Whether the call has to be made under another device or stream than the current ones."""
     index = x.get_device()  # -1 for a CPU tensor, which _under refuses
@@ -220,7 +227,7 @@ def conv_fwd(x, weight, bias=None, *, activation=None, cu_seqlens=None, init_sta
     _dense(out, "out", x.dtype, x.shape, x)
     _dense(final_state, "final_state", x.dtype, state, x)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(x, x.dtype)
     if final_state is None and output_final_state:
         final_state = torch.empty(state, dtype=x.dtype, device=x.device)
     _check(load().kda_conv_fwd(shape, x.data_ptr(), weight.data_ptr(), _ptr(bias),
@@ -245,7 +252,7 @@ def conv_step(x, weight, state, bias=None, *, activation=None, num_commit=None, 
     _dense(out, "out", x.dtype, x.shape, x)
     _counts(num_commit, N, x)
     if out is None and want_out:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(x, x.dtype)
     _check(load().kda_conv_step(shape, x.data_ptr(), weight.data_ptr(), _ptr(bias),
                                 _ptr(num_commit), state.data_ptr(), _ptr(out), *_ws(workspace),
                                 _stream(x.get_device())), "kda_conv_step")
@@ -268,7 +275,7 @@ def conv_bwd(x, weight, dy, bias=None, *, activation=None, cu_seqlens=None, init
     _dense(init_state, "init_state", x.dtype, state, x)
     _dense(dfinal, "dfinal", x.dtype, state, x)
     lib = load()
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dx = _new(x, x.dtype)
     dw = torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
     dinit = torch.empty(state, dtype=x.dtype, device=x.device) if want_dinit else None
@@ -327,7 +334,7 @@ def scan_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, dt_softplus=False, cu_seql
     _dense(hT, "hT", _F32, state, x)
     lib = load()
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+        out = _new(x, out_dtype)
     if hT is None and output_final_state:
         hT = torch.empty(state, dtype=_F32, device=x.device)
     if workspace is None:
@@ -354,7 +361,7 @@ def scan_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, dt_softplus=False,
     _dense(out, "out", out_dtype, x.shape, x)
     _counts(num_commit, N, x)
     if out is None and want_out:
-        out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+        out = _new(x, out_dtype)
     _check(load().kda_scan_step(shape, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
                                 C.data_ptr(), _ptr(D), _ptr(dt_bias), _ptr(num_commit),
                                 state.data_ptr(), _ptr(out), *_ws(workspace),
@@ -425,9 +432,9 @@ def norm_fwd(x, *, weight=None, gate=None, gate_act="sigmoid", gate_first=False,
     _dense(r, "r", res_dtype, x.shape, x)
     _dense(y, "y", x.dtype, x.shape, x)
     if r is None and want_r:
-        r = torch.empty(x.shape, dtype=res_dtype, device=x.device)
+        r = _new(x, res_dtype)
     if y is None and out_weight is not None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _new(x, x.dtype)
     _check(load().kda_norm_fwd(shape, x.data_ptr(), _ptr(weight), _ptr(gate), _ptr(residual),
                                _ptr(res_scale), _ptr(out_weight), _ptr(r), _ptr(y),
                                _stream(x.get_device())), "kda_norm_fwd")
@@ -453,7 +460,7 @@ def norm_bwd(x, dr, dy=None, *, weight=None, gate=None, gate_act="sigmoid", gate
     _dense(dr, "dr", res_dtype, x.shape, x)
     _dense(dy, "dy", x.dtype, x.shape, x)
     lib = load()
-    new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    new = lambda t: None if t is None else _new(t, t.dtype)
     dx, dgate, dres = new(x), new(gate), new(residual)
     dw, dls, dow = new(weight), new(res_scale), new(out_weight)
     if workspace is None:
