@@ -1153,32 +1153,44 @@ struct Sizes {
 
 // Segment length in tokens.  Fixed length: the number of segments that a model of the
 // two launches favours, in chunk-steps on `sms` CTAs: the state launch runs all segments
-// but the last at kStateCost of a full chunk's time, the output launch all of them.
-// Packed: a sequence may be as long as the SMs' mean share of the batch's work; longer
-// ones are cut to that length.  Segments have at least kMinSeg chunks.
-constexpr double kStateCost = 0.8;
-constexpr int64_t kMinSeg = 32;
+// but the last at kStateCost of a full chunk's time, the output launch all of them, each
+// item pays kStart chunk-steps to fill its pipeline, and a segment's start state sums up
+// those before it (kJoin each).  Packed: a sequence may be as long as the SMs' mean share
+// of the batch's work; longer ones are cut to that length.  Segments have at least kMinSeg
+// chunks.
+constexpr double kStateCost = 0.8, kStart = 4.0, kJoin = 0.4;
+constexpr int64_t kMinSeg = 8, kMaxSegs = 64;
 Sizes plan_sizes(const Seqs& q, bool packed, int64_t tiles, int H, int ds, int dx, int64_t sms) {
   Sizes s;
   if (q.total == 0 || q.N == 0) return s;
+  auto waves = [&](int64_t n) { return (double)((n + sms - 1) / sms); };
+  auto cost = [&](int64_t chains, int64_t chunks, int64_t ns) {
+    const double len = (double)((chunks + ns - 1) / ns) + kStart;
+    return ns == 1 ? waves(chains) * len
+                   : (kStateCost * waves(chains * (ns - 1)) + waves(chains * ns)) * len + kJoin * (double)ns;
+  };
   if (packed) {
     const int64_t chunks = (q.total + Q - 1) / Q;
     int64_t share = (chunks * tiles + sms - 1) / sms;
-    if (share < kMinSeg) share = kMinSeg;
+    // with few tiles the share is short: no more segments than the model would take of one
+    // sequence as long as the batch
+    int64_t best = 1;
+    for (int64_t ns = 2; ns <= kMaxSegs && chunks / ns >= kMinSeg; ++ns)
+      if (cost(tiles, chunks, ns) < cost(tiles, chunks, best)) best = ns;
+    if (share < (chunks + best - 1) / best) share = (chunks + best - 1) / best;
     if (chunks > share) s.seg = share * Q;
     s.slots = s.seg > 0 ? q.total / s.seg : 0;
     s.most = s.slots + q.N;
     s.plan = round256(16 + 2 * (size_t)s.most * 8 + (size_t)q.N * 4);
   } else {
     const int64_t chunks = (q.T + Q - 1) / Q, chains = q.N * tiles;
-    auto waves = [&](int64_t n) { return (n + sms - 1) / sms; };
-    double best = 0.95 * (double)waves(chains) * (double)chunks;
+    double best = 0.95 * cost(chains, chunks, 1);
     int64_t nseg = 1;
-    for (int64_t ns = 2; ns <= 64 && chunks / ns >= kMinSeg; ++ns) {
-      const int64_t len = (chunks + ns - 1) / ns;
-      const double t = (kStateCost * (double)waves(chains * (ns - 1)) + (double)waves(chains * ns)) * (double)len;
+    for (int64_t ns = 2; ns <= kMaxSegs && chunks / ns >= kMinSeg; ++ns) {
+      const double t = cost(chains, chunks, ns);
       if (t < best) {
         best = t;
+        const int64_t len = (chunks + ns - 1) / ns;
         nseg = (chunks + len - 1) / len;
         s.seg = len * Q;
       }
