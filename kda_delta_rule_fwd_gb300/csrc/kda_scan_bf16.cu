@@ -884,25 +884,28 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
           if (!kState) {
             tc_fence_after();
             uint32_t a = kmaj + so + (L::kC >> 4), b = kmaj + so + (L::kBt >> 4);
-#pragma unroll
-            for (int kk = 0; kk < DS / 16; ++kk) {
-              const uint32_t o = ((kk >> 2) * kTile + (kk & 3) * 32) >> 4;
-              mma_ss_by(lead, tb + TM_G, op_desc(a + o), op_desc(b + o), id_g, kk > 0);
+#pragma unroll 1
+            for (uint32_t kk = 0; kk < DS / 16; kk += 2) {  // 32 K elements, 64 bytes
+              mma_ss_by(lead, tb + TM_G, op_desc(a), op_desc(b), id_g, kk);
+              mma_ss_by(lead, tb + TM_G, op_desc(a + 2), op_desc(b + 2), id_g, 1);
+              const uint32_t d = kk & 2 ? (kTile >> 4) - 4 : 4;
+              a += d;
+              b += d;
             }
             commit_by(lead, cx.bars + 8 * B_G);
           }
           if (c > 0 && !cx.wait(B_UFREE, last)) { alive = false; break; }
-          const uint32_t a = mnmaj + (L::kWx >> 4), b = mnmaj + so + (L::kBt >> 4);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (alive && !cx.wait(B_X + 2 * st + h, ph)) alive = false;
+          uint32_t a = mnmaj + (L::kWx >> 4), b = mnmaj + so + (L::kBt >> 4);
+#pragma unroll 1
+          for (uint32_t h = 0; h < 2; ++h, a += kTile >> 5, b += kTile >> 5) {
+            if (!cx.wait(B_X + 2 * st + h, ph)) { alive = false; break; }
             tc_fence_after();
-#pragma unroll
-            for (int part = 0; part < 3; ++part)
-#pragma unroll
-              for (int kk = 0; kk < 2; ++kk)
-                mma_ss_by(lead, tb + TM_U, op_desc(a + ((part * 2 * kTile + h * (kTile / 2) + kk * 2048) >> 4)),
-                          op_desc(b + ((h * (kTile / 2) + kk * 2048) >> 4)), id_u, h + part + kk > 0);
+            uint32_t w = a;
+#pragma unroll 1
+            for (uint32_t part = 0; part < 3; ++part, w += 2 * kTile >> 4) {
+              mma_ss_by(lead, tb + TM_U, op_desc(w), op_desc(b), id_u, h + part);
+              mma_ss_by(lead, tb + TM_U, op_desc(w + 128), op_desc(b + 128), id_u, 1);
+            }
             commit_by(lead, cx.bars + 8 * (B_WX + h));
           }
           if (!alive) break;
@@ -916,13 +919,15 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             break;
           }
           tc_fence_after();
-          const uint32_t yi = tb + TM_YI + (HPC == 1 ? now * 64 : 0), b = kmaj + so + (L::kC >> 4);
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int kk = 0; kk < DS / 16; ++kk)
-              mma_ts_by(lead, yi, tb + TM_SB + part * (DS / 2) + kk * 8,
-                        op_desc(b + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4)), id_g, part + kk > 0);
+          const uint32_t yi = tb + TM_YI + (HPC == 1 ? now * 64 : 0);
+          uint32_t s = tb + TM_SB, b = kmaj + so + (L::kC >> 4);
+#pragma unroll 1
+          for (uint32_t kk = 0; kk < DS / 8; kk += 2, s += 16) {  // hi, then lo
+            mma_ts_by(lead, yi, s, op_desc(b), id_g, kk);
+            mma_ts_by(lead, yi, s + 8, op_desc(b + 2), id_g, 1);
+            b += kk & 2 ? (kTile >> 4) - 4 : 4;
+            if (kk == DS / 16 - 2) b = kmaj + so + (L::kC >> 4);
+          }
           commit_by(lead, cx.bars + 8 * (B_YI + now));
         } else {
           // a last chunk's x has its rows past the end cleared
@@ -932,13 +937,16 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             break;
           }
           tc_fence_after();
-          const uint32_t a = mnmaj + so + (L::kX >> 4), b = kmaj + (L::kM >> 4);
+          const uint32_t a = mnmaj + so + (L::kX >> 4);
+          uint32_t b = kmaj + (L::kM >> 4);
+#pragma unroll 1
+          for (uint32_t h = 0; h < 2 * HPC; ++h, b += kTile >> 4) {
+            const uint32_t d = tb + (h >= 2 ? TM_YX2 : TM_YX);
+            mma_ss_by(lead, d, op_desc(a), op_desc(b), id_x, h & 1);
 #pragma unroll
-          for (int h = 0; h < 2 * HPC; ++h)
-#pragma unroll
-            for (int kk = 0; kk < Q / 16; ++kk)
-              mma_ss_by(lead, tb + (h >= 2 ? TM_YX2 : TM_YX), op_desc(a + kk * 128),
-                        op_desc(b + ((h * kTile + kk * 32) >> 4)), id_x, (h & 1) + kk > 0);
+            for (int kk = 1; kk < Q / 16; ++kk)
+              mma_ss_by(lead, d, op_desc(a + kk * 128), op_desc(b + 2 * kk), id_x, 1);
+          }
           commit_by(lead, cx.bars + 8 * B_YX);
         }
         commit_by(lead, cx.bars + 8 * (B_EMPTY + st));
