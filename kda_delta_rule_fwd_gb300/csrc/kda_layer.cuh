@@ -96,7 +96,8 @@ __device__ __forceinline__ float sigmoid(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + e));
   return y;
 }
-// a b + c on pairs of neighbouring elements
+// Element-wise work on VEC values, two per instruction where they come in pairs:
+// c += a b;  c += a s;  a *= b;  a *= s;  acc += a . b (two partial sums)
 template <int VEC>
 __device__ __forceinline__ void fma_v(const float (&a)[VEC], const float (&b)[VEC], float (&c)[VEC]) {
   if constexpr (VEC % 2 == 0) {
@@ -112,6 +113,51 @@ __device__ __forceinline__ void fma_v(const float (&a)[VEC], const float (&b)[VE
     for (int e = 0; e < VEC; ++e) c[e] = fmaf(a[e], b[e], c[e]);
   }
 }
+template <int VEC>
+__device__ __forceinline__ void fma_v(const float (&a)[VEC], float s, float (&c)[VEC]) {
+  float b[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) b[e] = s;
+  fma_v(a, b, c);
+}
+template <int VEC>
+__device__ __forceinline__ void mul_v(float (&a)[VEC], const float (&b)[VEC]) {
+  if constexpr (VEC % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const float2 r = mul2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+      a[e] = r.x;
+      a[e + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) a[e] *= b[e];
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void mul_v(float (&a)[VEC], float s) {
+  float b[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) b[e] = s;
+  mul_v(a, b);
+}
+template <int VEC>
+__device__ __forceinline__ void dot_v(const float (&a)[VEC], const float (&b)[VEC], float2& acc) {
+  if constexpr (VEC % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2)
+      acc = fma2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), acc);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc.x = fmaf(a[e], b[e], acc.x);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void copy_v(const float (&a)[VEC], float (&b)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) b[e] = a[e];
+}
+
 // delta = softplus(dt + bias), or dt as given
 __device__ __forceinline__ float step_size(float dt, float bias, bool softplus) {
   if (!softplus) return dt;

@@ -37,7 +37,6 @@ norm_fwd_kernel(NormArgs a) {
   for (int64_t base = (int64_t)blockIdx.x * kRows; base < rows; base += step, row += step) {
     const bool on = row < rows;
     float v[NC][VEC], z[NC][VEC], rs[NC][VEC];
-    float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       open<T, VEC>(in.x[i], v[i]);
@@ -45,40 +44,43 @@ norm_fwd_kernel(NormArgs a) {
       open<TR, VEC>(in.res[i], rs[i]);
     }
     request<T, TR, VEC, NC, TPR, PLACE, false>(a, row + step, lane, in);
+    float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < NC; ++i) {
+      if (PLACE != kNoGate) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if (PLACE != kNoGate) z[i][e] = gate_of(z[i][e], sigmoid(z[i][e]), silu);
-        if (PLACE == kFirst) v[i][e] *= z[i][e];
-        ss = fmaf(v[i][e], v[i][e], ss);
+        for (int e = 0; e < VEC; ++e) z[i][e] = gate_of(z[i][e], sigmoid(z[i][e]), silu);
       }
+      if (PLACE == kFirst) mul_v(v[i], z[i]);
+      dot_v(v[i], v[i], ss);
+    }
     float k = 1.f;
-    if (a.w) k = rsqrtf(fmaf(row_sum<TPR>(ss, scratch, flip), a.inv_d, a.eps));
+    if (a.w) k = rsqrtf(fmaf(row_sum<TPR>(ss.x + ss.y, scratch, flip), a.inv_d, a.eps));
     if (!kKeep) params();
-    ss = 0.f;
+    ss = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = (lane + i * TPR) * VEC;
       if (c < a.d) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          float m = v[i][e] * k * w[i][e];
-          if (PLACE == kAfter) m *= z[i][e];
-          v[i][e] = kFull ? fmaf(ls[i][e], m, rs[i][e]) : m;
-          if (kFull) ss = fmaf(v[i][e], v[i][e], ss);
+        mul_v(v[i], k);
+        mul_v(v[i], w[i]);
+        if (PLACE == kAfter) mul_v(v[i], z[i]);
+        if (kFull) {
+          fma_v(ls[i], v[i], rs[i]);
+          copy_v(rs[i], v[i]);
+          dot_v(v[i], v[i], ss);
         }
         if (a.r && on) store<VEC>(static_cast<TR*>(a.r) + row * a.d + c, v[i]);
       }
     }
     if (!kFull || !a.ow) continue;
-    k = rsqrtf(fmaf(row_sum<TPR>(ss, scratch, flip), a.inv_d, a.eps));
+    k = rsqrtf(fmaf(row_sum<TPR>(ss.x + ss.y, scratch, flip), a.inv_d, a.eps));
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = (lane + i * TPR) * VEC;
       if (on && c < a.d) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] *= k * ow[i][e];
+        mul_v(v[i], k);
+        mul_v(v[i], ow[i]);
         store<VEC>(static_cast<T*>(a.y) + row * a.d + c, v[i]);
       }
     }

@@ -34,7 +34,6 @@ norm_bwd_kernel(NormArgs a) {
     // n: the norm's input v, then v k;  z, sz: the gate and (x's factor in) its slope;
     // r: residual, then n of the outer norm;  dr: gradient of r, then of the branch
     float n[NC][VEC], z[NC][VEC], sz[NC][VEC], r[NC][VEC], dr[NC][VEC], dy[NC][VEC];
-    float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       open<T, VEC>(in.x[i], n[i]);
@@ -44,104 +43,100 @@ norm_bwd_kernel(NormArgs a) {
       open<T, VEC>(in.dy[i], dy[i]);
     }
     request<T, TR, VEC, NC, TPR, PLACE, true>(a, row + step, lane, in);
+    float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < NC; ++i) {
+      if (PLACE != kNoGate) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if (PLACE != kNoGate) {
+        for (int e = 0; e < VEC; ++e) {
           const float s = sigmoid(z[i][e]);
           sz[i][e] = gate_slope(z[i][e], s, silu);
           z[i][e] = gate_of(z[i][e], s, silu);
         }
-        if (PLACE == kFirst) {
-          sz[i][e] *= n[i][e];
-          n[i][e] *= z[i][e];
-        }
-        ss = fmaf(n[i][e], n[i][e], ss);
       }
+      if (PLACE == kFirst) {
+        mul_v(sz[i], n[i]);
+        mul_v(n[i], z[i]);
+      }
+      dot_v(n[i], n[i], ss);
+    }
     float k = 1.f;
     if (a.w) {
-      k = rsqrtf(fmaf(row_sum<TPR>(ss, scratch, flip), a.inv_d, a.eps));
+      k = rsqrtf(fmaf(row_sum<TPR>(ss.x + ss.y, scratch, flip), a.inv_d, a.eps));
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) n[i][e] *= k;
+      for (int i = 0; i < NC; ++i) mul_v(n[i], k);
     }
     if (a.ow) {
-      float rr = 0.f, pr = 0.f;  // sums of r^2 and of p r: p n's is k2 times the second
+      float2 rr = make_float2(0.f, 0.f), pr = rr;  // r . r and p . r: p . n is k2 times the second
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = (lane + i * TPR) * VEC;
         if (c < a.d) {
-          float w[VEC], ls[VEC], ow[VEC];
+          float w[VEC], ls[VEC], p[VEC];
           param<VEC>(a.w, c, 1.f, w);
           param<VEC>(a.ls, c, a.scale, ls);
-          param<VEC>(a.ow, c, 1.f, ow);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            float b = n[i][e] * w[e];
-            if (PLACE == kAfter) b *= z[i][e];
-            r[i][e] = fmaf(ls[e], b, r[i][e]);
-            rr = fmaf(r[i][e], r[i][e], rr);
-            pr = fmaf(dy[i][e] * ow[e], r[i][e], pr);
-          }
+          param<VEC>(a.ow, c, 1.f, p);
+          mul_v(w, n[i]);
+          if (PLACE == kAfter) mul_v(w, z[i]);
+          fma_v(ls, w, r[i]);
+          dot_v(r[i], r[i], rr);
+          mul_v(p, dy[i]);
+          dot_v(p, r[i], pr);
         }
       }
-      const float2 s = row_sums<TPR>(rr, pr, scratch, flip);
+      const float2 s = row_sums<TPR>(rr.x + rr.y, pr.x + pr.y, scratch, flip);
       const float k2 = rsqrtf(fmaf(s.x, a.inv_d, a.eps)), mean = k2 * k2 * s.y * a.inv_d;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = (lane + i * TPR) * VEC;
         if (c < a.d) {
-          float ow[VEC];
-          param<VEC>(a.ow, c, 1.f, ow);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            so[i][e] = fmaf(dy[i][e], k2 * r[i][e], so[i][e]);
-            dr[i][e] = fmaf(k2, fmaf(-mean, r[i][e], dy[i][e] * ow[e]), dr[i][e]);
-          }
+          float p[VEC], t[VEC];
+          param<VEC>(a.ow, c, 1.f, p);
+          mul_v(p, dy[i]);
+          fma_v(r[i], -mean, p);
+          fma_v(p, k2, dr[i]);
+          copy_v(r[i], t);
+          mul_v(t, k2);
+          fma_v(dy[i], t, so[i]);
         }
       }
     }
     // through the residual sum and the branch; dgate (gate after) in sz
-    float pn = 0.f;
+    float2 pn = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = (lane + i * TPR) * VEC;
       if (c < a.d) {
-        float w[VEC], ls[VEC];
+        float w[VEC], db[VEC], b[VEC];
         param<VEC>(a.w, c, 1.f, w);
-        param<VEC>(a.ls, c, a.scale, ls);
+        param<VEC>(a.ls, c, a.scale, db);
         if (a.dres && on) store<VEC>(static_cast<TR*>(a.dres) + row * a.d + c, dr[i]);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float m = n[i][e] * w[e];
-          const float b = PLACE == kAfter ? m * z[i][e] : m;
-          sl[i][e] = fmaf(dr[i][e], b, sl[i][e]);  // times the scale at the end
-          float db = ls[e] * dr[i][e];
-          if (PLACE == kAfter) {
-            sz[i][e] *= db * m;
-            db *= z[i][e];
-          }
-          sw[i][e] = fmaf(db, n[i][e], sw[i][e]);
-          dr[i][e] = db * w[e];  // p
-          pn = fmaf(dr[i][e], n[i][e], pn);
+        mul_v(db, dr[i]);
+        copy_v(n[i], b);
+        mul_v(b, w);
+        if (PLACE == kAfter) {
+          mul_v(sz[i], b);
+          mul_v(sz[i], db);
+          mul_v(b, z[i]);
+          mul_v(db, z[i]);
         }
+        fma_v(dr[i], b, sl[i]);  // times the scale at the end
+        fma_v(db, n[i], sw[i]);
+        mul_v(db, w);  // p
+        dot_v(db, n[i], pn);
+        copy_v(db, dr[i]);
       }
     }
-    pn = a.w ? row_sum<TPR>(pn, scratch, flip) * a.inv_d : 0.f;
+    const float mean = a.w ? row_sum<TPR>(pn.x + pn.y, scratch, flip) * a.inv_d : 0.f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = (lane + i * TPR) * VEC;
       if (on && c < a.d) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          float dv = k * fmaf(-pn, n[i][e], dr[i][e]);
-          if (PLACE == kFirst) {
-            sz[i][e] *= dv;
-            dv *= z[i][e];
-          }
-          dr[i][e] = dv;
+        fma_v(n[i], -mean, dr[i]);
+        mul_v(dr[i], k);
+        if (PLACE == kFirst) {
+          mul_v(sz[i], dr[i]);
+          mul_v(dr[i], z[i]);
         }
         store<VEC>(static_cast<T*>(a.dx) + row * a.d + c, dr[i]);
         if (PLACE != kNoGate && a.dgate) store<VEC>(static_cast<T*>(a.dgate) + row * a.d + c, sz[i]);
