@@ -135,8 +135,9 @@ conv_fwd_kernel(ConvArgs a, int cblocks) {
     open<T, VEC>(raw, xt);
     taps<VEC, W>(wr, br, win, xt, u);
     if (kSilu) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) u[e] *= sigmoid(u[e]);
+      float s[VEC];
+      sigmoid_v(u, s);
+      mul_v(u, s);
     }
     store<VEC>(y + t * a.D, u);
     shift_in<VEC, W>(win, xt);
@@ -221,8 +222,9 @@ conv_step_kernel(ConvArgs a, int cblocks) {
       else load<VEC>(x + (n * a.T + t) * a.ldx + c, xt);
       taps<VEC, W>(wr, br, win, xt, u);
       if (kSilu) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) u[e] *= sigmoid(u[e]);
+        float s[VEC];
+        sigmoid_v(u, s);
+        mul_v(u, s);
       }
       if (a.y) store<VEC>(static_cast<T*>(a.y) + (n * a.T + t) * a.D + c, u);
       shift_in<VEC, W>(win, xt);

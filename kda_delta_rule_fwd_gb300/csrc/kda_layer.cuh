@@ -152,6 +152,22 @@ __device__ __forceinline__ void dot_v(const float (&a)[VEC], const float (&b)[VE
     for (int e = 0; e < VEC; ++e) acc.x = fmaf(a[e], b[e], acc.x);
   }
 }
+// s = sigmoid(x), as sigmoid()
+template <int VEC>
+__device__ __forceinline__ void sigmoid_v(const float (&x)[VEC], float (&s)[VEC]) {
+  float one[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    s[e] = x[e];
+    one[e] = 1.f;
+  }
+  mul_v(s, -1.4426950408889634f);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s[e]) : "f"(s[e]));
+  fma_v(s, 1.f, one);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[e]) : "f"(one[e]));
+}
 template <int VEC>
 __device__ __forceinline__ void copy_v(const float (&a)[VEC], float (&b)[VEC]) {
 #pragma unroll

@@ -33,9 +33,9 @@ __device__ __forceinline__ float row_sum(float v, float2 (*scratch)[32], int& fl
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) scratch[flip][warp].x = v;
     __syncthreads();
-    v = lane < kWarps ? scratch[flip][lane].x : 0.f;
+    v = scratch[flip][lane % kWarps].x;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = kWarps / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     flip ^= 1;
   }
   return v;
@@ -55,11 +55,11 @@ __device__ __forceinline__ float2 row_sums(float a, float b, float2 (*scratch)[3
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) scratch[flip][warp] = make_float2(a, b);
     __syncthreads();
-    const float2 v = lane < kWarps ? scratch[flip][lane] : make_float2(0.f, 0.f);
+    const float2 v = scratch[flip][lane % kWarps];
     a = v.x;
     b = v.y;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
       a += __shfl_xor_sync(0xffffffffu, a, o);
       b += __shfl_xor_sync(0xffffffffu, b, o);
     }

@@ -47,11 +47,12 @@ norm_bwd_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       if (PLACE != kNoGate) {
+        float s[VEC];
+        sigmoid_v(z[i], s);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float s = sigmoid(z[i][e]);
-          sz[i][e] = gate_slope(z[i][e], s, silu);
-          z[i][e] = gate_of(z[i][e], s, silu);
+          sz[i][e] = gate_slope(z[i][e], s[e], silu);
+          z[i][e] = gate_of(z[i][e], s[e], silu);
         }
       }
       if (PLACE == kFirst) {
