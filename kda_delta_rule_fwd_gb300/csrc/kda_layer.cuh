@@ -291,8 +291,8 @@ struct NormArgs {
   cudaStream_t stream;
 };
 cudaError_t launch_norm_fwd(const NormArgs& a);
-cudaError_t launch_norm_bwd(const NormArgs& a);
-int64_t norm_bwd_ctas(int64_t rows, int d, bool bf16, int64_t sms);
+cudaError_t launch_norm_bwd(NormArgs a);
+int64_t norm_bwd_ctas(int64_t rows, int d, bool bf16, int64_t sms);  // the most of a call
 
 }  // namespace layer
 int64_t device_sms();  // SMs of the current device (152 when there is none)

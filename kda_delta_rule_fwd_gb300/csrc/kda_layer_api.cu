@@ -324,7 +324,6 @@ kda_status kda_norm_bwd(const kda_norm_shape* s, const void* x, const float* wei
   a.dr = dr; a.dy = dy; a.dx = dx; a.dgate = dgate; a.dres = dresidual;
   a.dw = dweight; a.dls = dres_scale; a.dow = dout_weight;
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWsHeader);
-  a.ctas = norm_bwd_ctas(s->tokens * s->heads, s->d, a.bf16, device_sms());
   a.stream = static_cast<cudaStream_t>(stream);
   return launched(launch_norm_bwd(a));
 }

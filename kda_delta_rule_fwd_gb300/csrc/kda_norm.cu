@@ -7,9 +7,14 @@ namespace {
 
 using namespace norm;
 
+// threads per SM: what the registers of one row allow
+template <int NC, int TPR, bool kFull> constexpr int resident() {
+  return TPR > 512 ? TPR : kFull ? 512 : NC > 1 ? 640 : 1024;
+}
+
 // kFull: with a residual, a per-channel scale or an outer norm; otherwise r = scale m alone
 template <typename T, typename TR, int VEC, int NC, int TPR, int PLACE, bool kFull>
-__global__ void __launch_bounds__(block_of<TPR>())
+__global__ void __launch_bounds__(block_of<TPR>(), resident<NC, TPR, kFull>() / block_of<TPR>())
 norm_fwd_kernel(NormArgs a) {
   constexpr int kRows = block_of<TPR>() / TPR;  // rows per block
   constexpr bool kKeep = TPR <= 32;             // parameters stay in registers
@@ -22,7 +27,7 @@ norm_fwd_kernel(NormArgs a) {
   auto params = [&]() {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = (lane + i * TPR) * VEC;
+      const int c = (lane + i * row_threads<TPR>()) * VEC;
       if (c < a.d) {
         param<VEC>(a.w, c, kFull ? 1.f : a.scale, w[i]);
         if (kFull) param<VEC>(a.ls, c, a.scale, ls[i]);
@@ -60,7 +65,7 @@ norm_fwd_kernel(NormArgs a) {
     ss = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = (lane + i * TPR) * VEC;
+      const int c = (lane + i * row_threads<TPR>()) * VEC;
       if (c < a.d) {
         mul_v(v[i], k);
         mul_v(v[i], w[i]);
@@ -77,7 +82,7 @@ norm_fwd_kernel(NormArgs a) {
     k = rsqrtf(fmaf(row_sum<TPR>(ss.x + ss.y, scratch, flip), a.inv_d, a.eps));
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = (lane + i * TPR) * VEC;
+      const int c = (lane + i * row_threads<TPR>()) * VEC;
       if (on && c < a.d) {
         mul_v(v[i], k);
         mul_v(v[i], ow[i]);
@@ -93,13 +98,13 @@ struct Kind {
   struct Forward {
     static constexpr bool kPairs = !kFull;
     static cudaError_t run(const NormArgs& a) {
-      constexpr int kBlock = block_of<TPR>(), kRows = kBlock / TPR;
-      // about as many blocks as are resident together
+      constexpr int kRows = block_of<TPR>() / TPR;
+      const int threads = threads_of<VEC, NC, TPR>(a.d);
       const int64_t rows = a.tokens * a.heads;
-      const int64_t blocks = (rows + kRows - 1) / kRows, most = a.sms * (1024 / kBlock);
+      const int64_t blocks = (rows + kRows - 1) / kRows, most = a.sms * (resident<NC, TPR, kFull>() / threads);
       if (blocks == 0) return cudaSuccess;
       norm_fwd_kernel<T, TR, VEC, NC, TPR, PLACE, kFull>
-          <<<(unsigned)(blocks < most ? blocks : most), kBlock, 0, a.stream>>>(a);
+          <<<(unsigned)(blocks < most ? blocks : most), threads, 0, a.stream>>>(a);
       return cudaGetLastError();
     }
   };

@@ -6,11 +6,12 @@
 //
 // One pass: a row stays in registers between its reductions, so each input is read
 // once and each output written once, and the work is bound by memory traffic.  A row
-// of d channels is held by TPR threads with NC chunks of VEC channels each; rows of
-// up to 32 chunks reduce by shuffles alone.  Blocks are persistent: each walks rows
-// and requests the next one's inputs before it works on the present one, so that the
-// reductions' latency is covered; the parameters are loaded once where a row's chunks
-// leave room for them (up to 32 threads per row).
+// of d channels is held by up to TPR threads with NC chunks of VEC channels each; rows
+// of up to 32 threads reduce by shuffles alone, longer ones have a block of their own
+// with as many warps as they fill.  Blocks are persistent: as many as are resident
+// together, each walks rows and requests the next one's inputs before it works on the
+// present one, so that the reductions' latency is covered; the parameters are loaded
+// once where a row's chunks leave room for them (up to 32 threads per row).
 #pragma once
 
 #include <type_traits>
@@ -21,19 +22,22 @@ namespace kda {
 namespace layer {
 namespace norm {
 
-// sum over the TPR threads of a row; every thread gets it.  Above 32 threads the
-// row is the whole block: two alternating scratch rows leave one barrier per sum.
+// the warps of a long row's block, up to a power of two
+template <int TPR> constexpr int warps_of() { return TPR > 512 ? 32 : TPR / 32; }
+
+// sum over the threads of a row; every thread gets it.  With TPR above 32 the row is
+// the whole block: two alternating scratch rows leave one barrier per sum.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float2 (*scratch)[32], int& flip) {
   constexpr int kIn = TPR < 32 ? TPR : 32;
 #pragma unroll
   for (int o = kIn / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (TPR > 32) {
-    constexpr int kWarps = TPR / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kWarps = warps_of<TPR>();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, at = lane % kWarps;
     if (lane == 0) scratch[flip][warp].x = v;
     __syncthreads();
-    v = scratch[flip][lane % kWarps].x;
+    v = at * 32 < blockDim.x ? scratch[flip][at].x : 0.f;
 #pragma unroll
     for (int o = kWarps / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     flip ^= 1;
@@ -51,11 +55,11 @@ __device__ __forceinline__ float2 row_sums(float a, float b, float2 (*scratch)[3
     b += __shfl_xor_sync(0xffffffffu, b, o);
   }
   if constexpr (TPR > 32) {
-    constexpr int kWarps = TPR / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kWarps = warps_of<TPR>();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, at = lane % kWarps;
     if (lane == 0) scratch[flip][warp] = make_float2(a, b);
     __syncthreads();
-    const float2 v = scratch[flip][lane % kWarps];
+    const float2 v = at * 32 < blockDim.x ? scratch[flip][at] : make_float2(0.f, 0.f);
     a = v.x;
     b = v.y;
 #pragma unroll
@@ -68,7 +72,13 @@ __device__ __forceinline__ float2 row_sums(float a, float b, float2 (*scratch)[3
   return make_float2(a, b);
 }
 
+// The most threads of a block, and those of a call: long rows leave out the warps that
+// their d does not need.  Chunk i of a thread follows chunk i - 1 by the row's threads.
 template <int TPR> constexpr int block_of() { return TPR < 128 ? 128 : TPR; }
+template <int VEC, int NC, int TPR> int threads_of(int d) {
+  return TPR > 32 ? (d + VEC * NC * 32 - 1) / (VEC * NC * 32) * 32 : block_of<TPR>();
+}
+template <int TPR> __device__ __forceinline__ int row_threads() { return TPR > 32 ? blockDim.x : TPR; }
 
 // where the gate sits
 enum Place { kNoGate = 0, kAfter = 1, kFirst = 2 };
@@ -100,7 +110,7 @@ __device__ __forceinline__ void request(const NormArgs& a, int64_t row, int lane
   }
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int c = (lane + i * TPR) * VEC;
+    const int c = (lane + i * row_threads<TPR>()) * VEC;
     const bool in_row = on && c < a.d;
     auto get = [&](auto& raw, const auto* p, int64_t o, bool have) {
       using E = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
@@ -142,7 +152,9 @@ inline bool wide_ok(const NormArgs& a) {
 }
 
 // Threads per row by the row's chunks: up to 32 chunks the row stays inside a warp, with two
-// chunks per thread (F::kPairs) up to 64.  `F<T, TR, VEC, NC, TPR, PLACE>::run` is the launch.
+// chunks per thread (F::kPairs) up to 64.  Eight threads for rows of up to 8 chunks leave few
+// lanes idle: rows of 64 bf16 channels, 128 MB of them with a gate, take 69 us forward against
+// 96 with 16 lanes per row.  `F<T, TR, VEC, NC, TPR, PLACE>::run` is the launch.
 template <template <typename, typename, int, int, int, int> class F, typename T, typename TR, int VEC, int PLACE>
 cudaError_t by_size(const NormArgs& a) {
   const int chunks = (a.d + VEC - 1) / VEC;
@@ -151,8 +163,10 @@ cudaError_t by_size(const NormArgs& a) {
     if (chunks <= 1024) return F<T, TR, 1, 4, 256, PLACE>::run(a);
     return F<T, TR, 1, 8, 1024, PLACE>::run(a);
   } else {
+    if (chunks <= 8) return F<T, TR, VEC, 1, 8, PLACE>::run(a);
     if constexpr (F<T, TR, VEC, 1, 32, PLACE>::kPairs) {
       if (chunks <= 16) return F<T, TR, VEC, 2, 8, PLACE>::run(a);
+      if (chunks <= 32) return F<T, TR, VEC, 2, 16, PLACE>::run(a);
       if (chunks <= 64) return F<T, TR, VEC, 2, 32, PLACE>::run(a);
     } else {
       if (chunks <= 16) return F<T, TR, VEC, 1, 16, PLACE>::run(a);
@@ -161,6 +175,7 @@ cudaError_t by_size(const NormArgs& a) {
     if (chunks <= 128) return F<T, TR, VEC, 1, 128, PLACE>::run(a);
     if (chunks <= 256) return F<T, TR, VEC, 1, 256, PLACE>::run(a);
     if (chunks <= 512) return F<T, TR, VEC, 1, 512, PLACE>::run(a);
+    if (chunks <= 768) return F<T, TR, VEC, 1, 768, PLACE>::run(a);
     if constexpr (VEC == 4) {  // float32 rows past 4096 channels
       if (chunks > 1024) return F<T, TR, VEC, 2, 1024, PLACE>::run(a);
     }

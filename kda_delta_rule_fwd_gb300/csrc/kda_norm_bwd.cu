@@ -4,6 +4,8 @@
 // of dy n.  Each block keeps its rows' sums for the parameters in registers; they go to
 // part[block][3][d] and are added in the order of the blocks, so that the results do not
 // depend on scheduling.
+#include <algorithm>
+
 #include "kda_norm.cuh"
 
 namespace kda {
@@ -12,8 +14,11 @@ namespace {
 
 using namespace norm;
 
+// threads per SM: what the registers of one row allow (rows inside a warp take more of them)
+constexpr int resident(bool long_row) { return long_row ? 512 : 384; }
+
 template <typename T, typename TR, int VEC, int NC, int TPR, int PLACE>
-__global__ void __launch_bounds__(block_of<TPR>())
+__global__ void __launch_bounds__(block_of<TPR>(), TPR > 256 ? 1 : resident(TPR > 32) / block_of<TPR>())
 norm_bwd_kernel(NormArgs a) {
   constexpr int kRows = block_of<TPR>() / TPR;
   __shared__ float2 scratch[2][32];
@@ -71,7 +76,7 @@ norm_bwd_kernel(NormArgs a) {
       float2 rr = make_float2(0.f, 0.f), pr = rr;  // r . r and p . r: p . n is k2 times the second
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int c = (lane + i * TPR) * VEC;
+        const int c = (lane + i * row_threads<TPR>()) * VEC;
         if (c < a.d) {
           float w[VEC], ls[VEC], p[VEC];
           param<VEC>(a.w, c, 1.f, w);
@@ -89,7 +94,7 @@ norm_bwd_kernel(NormArgs a) {
       const float k2 = rsqrtf(fmaf(s.x, a.inv_d, a.eps)), mean = k2 * k2 * s.y * a.inv_d;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int c = (lane + i * TPR) * VEC;
+        const int c = (lane + i * row_threads<TPR>()) * VEC;
         if (c < a.d) {
           float p[VEC], t[VEC];
           param<VEC>(a.ow, c, 1.f, p);
@@ -106,7 +111,7 @@ norm_bwd_kernel(NormArgs a) {
     float2 pn = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = (lane + i * TPR) * VEC;
+      const int c = (lane + i * row_threads<TPR>()) * VEC;
       if (c < a.d) {
         float w[VEC], db[VEC], b[VEC];
         param<VEC>(a.w, c, 1.f, w);
@@ -131,7 +136,7 @@ norm_bwd_kernel(NormArgs a) {
     const float mean = a.w ? row_sum<TPR>(pn.x + pn.y, scratch, flip) * a.inv_d : 0.f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = (lane + i * TPR) * VEC;
+      const int c = (lane + i * row_threads<TPR>()) * VEC;
       if (on && c < a.d) {
         fma_v(n[i], -mean, dr[i]);
         mul_v(dr[i], k);
@@ -174,7 +179,7 @@ norm_bwd_kernel(NormArgs a) {
   } else {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = (lane + i * TPR) * VEC;
+      const int c = (lane + i * row_threads<TPR>()) * VEC;
       if (c < a.d) {
         if (a.dw) store<VEC>(part + c, sw[i]);
         if (a.dls) store<VEC>(part + a.d + c, sl[i]);
@@ -184,9 +189,9 @@ norm_bwd_kernel(NormArgs a) {
   }
 }
 
-// one warp row per 32 columns: 8 warps take every 8th block's sums, then fold
-__global__ void __launch_bounds__(256) norm_reduce_kernel(NormArgs a) {
-  __shared__ float fold[8][33];
+// 32 columns per block: its 32 warps take every 32nd block's sums, then fold
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(NormArgs a) {
+  __shared__ float fold[32][33];
   const int which = blockIdx.y;
   float* out = which == 0 ? a.dw : which == 1 ? a.dls : a.dow;
   if (!out) return;
@@ -195,13 +200,13 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(NormArgs a) {
   float s = 0.f;
   if (c < a.d) {
 #pragma unroll 8
-    for (int64_t b = warp; b < a.ctas; b += 8) s += a.part[(b * 3 + which) * a.d + c];
+    for (int64_t b = warp; b < a.ctas; b += 32) s += a.part[(b * 3 + which) * a.d + c];
   }
   fold[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < a.d) {
 #pragma unroll
-    for (int q = 1; q < 8; ++q) s += fold[q][lane];
+    for (int q = 1; q < 32; ++q) s += fold[q][lane];
     out[c] = s;
   }
 }
@@ -211,26 +216,41 @@ struct Backward {
   static constexpr bool kPairs = false;
   static cudaError_t run(const NormArgs& a) {
     norm_bwd_kernel<T, TR, VEC, NC, TPR, PLACE>
-        <<<(unsigned)a.ctas, block_of<TPR>(), 0, a.stream>>>(a);
+        <<<(unsigned)a.ctas, threads_of<VEC, NC, TPR>(a.d), 0, a.stream>>>(a);
     return cudaGetLastError();
   }
 };
 
 }  // namespace
 
-// Blocks of the backward: those that are resident together (a thread takes about 128
-// registers), no more than there are rows for.
-int64_t norm_bwd_ctas(int64_t rows, int d, bool bf16, int64_t sms) {
+// Blocks of the backward: those that are resident together, no more than there are rows for.
+// It follows by_size; without the alignment for wide accesses a row takes more threads.
+static int64_t blocks_of(int64_t rows, int d, bool bf16, bool wide, int64_t sms) {
   const int chunks = (d + (bf16 ? 8 : 4) - 1) / (bf16 ? 8 : 4);
-  const int64_t most = chunks <= 128 ? 4 * sms : chunks <= 256 ? 2 * sms : sms;
-  return rows < 1 ? 1 : rows < most ? rows : most;
+  int per, threads;  // rows and threads of a block
+  if (wide) {
+    per = chunks <= 8 ? 16 : chunks <= 16 ? 8 : chunks <= 32 ? 4 : 1;
+    threads = per > 1 ? 128 : (chunks + 31) / 32 * 32;
+  } else {
+    const int part = d <= 1024 ? 128 : 256;  // elements of a warp
+    per = d <= 128 ? 4 : 1;
+    threads = per > 1 ? 128 : (d + part - 1) / part * 32;
+  }
+  const int64_t most = threads > 512 ? sms : resident(per == 1) / threads * sms;
+  const int64_t blocks = (rows + per - 1) / per;
+  return blocks < 1 ? 1 : blocks < most ? blocks : most;
 }
 
-cudaError_t launch_norm_bwd(const NormArgs& a) {
+int64_t norm_bwd_ctas(int64_t rows, int d, bool bf16, int64_t sms) {
+  return std::max(blocks_of(rows, d, bf16, true, sms), blocks_of(rows, d, bf16, false, sms));
+}
+
+cudaError_t launch_norm_bwd(NormArgs a) {
+  a.ctas = blocks_of(a.tokens * a.heads, a.d, a.bf16, wide_ok(a), a.sms);
   cudaError_t e = by_type<Backward>(a);
   if (e != cudaSuccess) return e;
   if (!a.dw && !a.dls && !a.dow) return cudaSuccess;
-  norm_reduce_kernel<<<dim3((unsigned)((a.d + 31) / 32), 3), 256, 0, a.stream>>>(a);
+  norm_reduce_kernel<<<dim3((unsigned)((a.d + 31) / 32), 3), 1024, 0, a.stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -25,11 +25,11 @@
 //     warps 12,13,17   M from G (the three 32 x 32 blocks on and below the diagonal)
 //     warps 14,15,18,19,24-27  w x in parts from the x tile; zero rows past the sequence's end
 //     warps 21, 23, 16 tcgen05.mma: G and U; Yi; Yx (one thread each)
-//     warp 20      work items, tile loads (TMA, 128-byte swizzle)
-//     warp 22      per-token factors (delta, running sums, weights)
+//     warp 22      work items, tile loads (TMA, 128-byte swizzle)
+//     warp 20      per-token factors (delta, running sums, weights)
 // The code of one chunk's steady state has to stay inside the SM's instruction cache with
 // all roles at work: loops that need no register arrays are kept rolled, and items are decoded
-// once, by warp 20.
+// once, by warp 22.
 // U does not depend on S, so the chain from chunk to chunk is one multiply-add per state
 // element; every product is off it.  The state warps take registers from the others.
 //
@@ -55,7 +55,8 @@ constexpr int Q = 64;              // tokens per chunk
 constexpr int kScanThreads = 896;  // 28 warps
 constexpr int kRing = 4;           // chunks of per-token factors
 constexpr int kItems = 4;          // items handed out ahead
-constexpr int kLoadWarp = 20, kStateMmaWarp = 21, kFactorWarp = 22, kYiMmaWarp = 23, kYxMmaWarp = 16;
+// the roles are spread so that the SM's four schedulers (warp % 4) get about the same work
+constexpr int kFactorWarp = 20, kStateMmaWarp = 21, kLoadWarp = 22, kYiMmaWarp = 23, kYxMmaWarp = 16;
 constexpr int kTile = 8192;        // 64 tokens x 64 channels of bf16, 128-byte rows
 
 // tensor memory columns: U, Sb hi and lo, G, then Yi and Yx.  One head of 128 channels
