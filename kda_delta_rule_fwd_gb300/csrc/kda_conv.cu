@@ -18,6 +18,7 @@ namespace layer {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kStepBlocks = 4, kBwdBlocks = 3;  // resident per SM, by their registers
 // A thread's own ring of kSlots vectors in shared memory, filled ahead by cp.async.
 // Narrow elements (VEC = 1) are below the copy's smallest size: they are loaded in place.
 template <typename T, int VEC, int kSlots>
@@ -27,10 +28,8 @@ struct Ring {
   __device__ __forceinline__ void request(int64_t i, const T* src) const {
     if constexpr (VEC > 1) {
       const uint32_t dst = (uint32_t)__cvta_generic_to_shared(&slot(i));
-      if constexpr (sizeof(Raw<T, VEC>) == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-      else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+      static_assert(sizeof(Raw<T, VEC>) == 16, "one copy per vector");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     } else {
       slot(i) = fetch<T, VEC>(src);
     }
@@ -179,7 +178,7 @@ conv_fwd_kernel(ConvArgs a, int cblocks) {
 // sequences are in flight into shared memory meanwhile.  T tokens in order, the state
 // in registers.
 template <typename T, int VEC, int W, bool kSilu>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kStepBlocks)
 conv_step_kernel(ConvArgs a, int cblocks) {
   constexpr int kSeqs = 4;
   __shared__ __align__(16) Raw<T, VEC> ring_mem[kSeqs * W * kThreads];
@@ -243,7 +242,7 @@ conv_step_kernel(ConvArgs a, int cblocks) {
 // sums for dw and dbias go to part[tile][W + 1][D] and are added in the order of
 // the tiles by conv_reduce_kernel, so the results do not depend on scheduling.
 template <typename T, int VEC, int W, bool kSilu>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kBwdBlocks)
 conv_bwd_kernel(ConvArgs a, int cblocks) {
   // W - 1 tokens per group: after as many shifts the window holds new values only, and no
   // register has to move
@@ -427,7 +426,7 @@ conv_bwd_kernel(ConvArgs a, int cblocks) {
   store<VEC>(pt + (int64_t)W * a.D, db);
 }
 
-// 8 warps take every 8th tile's sums of 32 columns, then fold in a fixed order
+// 32 columns per block: its 8 warps take every 8th tile's sums, then fold in a fixed order
 __global__ void __launch_bounds__(256) conv_reduce_kernel(ConvArgs a) {
   __shared__ float fold[8][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -454,8 +453,8 @@ template <typename T, int VEC, int W>
 cudaError_t run(const ConvArgs& a, int what) {
   const int cblocks = (a.D + kThreads * VEC - 1) / (kThreads * VEC);
   const int64_t extra = what == 0 ? (a.fin ? a.q.N : 0) : what == 2 ? (a.dinit ? a.q.N : 0) : 0;
-  // single tokens: the blocks that are resident together, each with its share of sequences
-  const int64_t fill = (a.sms * 4 + cblocks - 1) / cblocks;
+  // single tokens: no more blocks than are resident together, each with its share of sequences
+  const int64_t fill = a.sms * kStepBlocks / cblocks > 0 ? a.sms * kStepBlocks / cblocks : 1;
   const int64_t jobs = what == 1 ? (a.q.N < fill ? a.q.N : fill) : a.tiles + extra;
   const int64_t grid = jobs * cblocks;
   if (grid == 0)  // nothing to check or to compute
@@ -505,11 +504,15 @@ cudaError_t launch_conv_fwd(const ConvArgs& a0) {
 
 cudaError_t launch_conv_step(const ConvArgs& a) { return by_type(a, 1); }
 
-int64_t conv_bwd_tile(int64_t tokens, int D, int64_t sms) {
-  const int64_t cb = (D + kThreads * 8 - 1) / (kThreads * 8);
-  int64_t tile = 256;
-  while (tile > 16 && cb * ((tokens + tile - 1) / tile) < 6 * sms) tile /= 2;
-  return tile;
+// One tile for each block that is resident: all of them end together, and there are few sums to
+// add up.  16384 tokens of 12288 channels: 250 us with 38 tiles, 254 with two rounds of blocks,
+// 266 with four, 281 with tiles of 128 tokens.
+int64_t conv_bwd_tile(int64_t tokens, int D, bool bf16, int64_t sms) {
+  const int64_t per = kThreads * (bf16 ? 8 : 4);
+  const int64_t cb = (D + per - 1) / per;
+  const int64_t tiles = kBwdBlocks * sms / cb;
+  const int64_t tile = tiles > 0 ? (tokens + tiles - 1) / tiles : 0;
+  return tile < 16 ? 16 : tile;
 }
 
 cudaError_t launch_conv_bwd(const ConvArgs& a) {

@@ -9,7 +9,7 @@
 namespace kda {
 namespace layer {
 
-// VEC consecutive elements (16 bytes, 8 bytes or one element) as float32
+// VEC consecutive elements (whole 16-byte words, or one element) as float32
 template <int VEC>
 __device__ __forceinline__ void load(const float* p, float (&x)[VEC]) {
   if constexpr (VEC == 8) {
@@ -39,9 +39,6 @@ __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[VEC]) {
     const uint4 u = *reinterpret_cast<const uint4*>(p);
     unpack2(u.x, x[0], x[1]); unpack2(u.y, x[2], x[3]);
     unpack2(u.z, x[4], x[5]); unpack2(u.w, x[6], x[7]);
-  } else if constexpr (VEC == 4) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    unpack2(u.x, x[0], x[1]); unpack2(u.y, x[2], x[3]);
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) x[e] = __bfloat162float(p[e]);
@@ -63,8 +60,6 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[VEC]) {
   if constexpr (VEC == 8) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
                                               pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-  } else if constexpr (VEC == 4) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) p[e] = __float2bfloat16_rn(x[e]);
@@ -74,7 +69,6 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[VEC]) {
 // VEC consecutive elements as they lie in memory, to be held while in flight
 template <typename T, int VEC> struct Raw;
 template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
-template <> struct Raw<__nv_bfloat16, 4> { uint2 v; };
 template <> struct Raw<float, 8> { float4 v, w; };
 template <> struct Raw<float, 4> { float4 v; };
 template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 v; };
@@ -249,7 +243,7 @@ struct ConvArgs {
 };
 cudaError_t launch_conv_fwd(const ConvArgs& a);
 cudaError_t launch_conv_step(const ConvArgs& a);
-int64_t conv_bwd_tile(int64_t tokens, int D, int64_t sms);
+int64_t conv_bwd_tile(int64_t tokens, int D, bool bf16, int64_t sms);
 cudaError_t launch_conv_bwd(const ConvArgs& a);
 
 struct ScanArgs {

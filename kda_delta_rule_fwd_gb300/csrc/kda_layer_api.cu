@@ -69,7 +69,7 @@ ConvArgs conv_args(const kda_conv_shape* s, bool packed, const int32_t* cu, int6
 
 int64_t conv_tiles(const kda_conv_shape* s, int64_t& tile) {
   const int64_t tokens = (int64_t)s->B * s->T;
-  tile = conv_bwd_tile(tokens, s->D, device_sms());
+  tile = conv_bwd_tile(tokens, s->D, s->dtype == KDA_BF16, device_sms());
   return (tokens + tile - 1) / tile;
 }
 

@@ -139,7 +139,7 @@ struct ScanParams {
 
 // packed plan: [0] output items, [1] state items, then at 4: output items (sequence, segment),
 // state items, and per sequence its first slot
-struct PlanView2 {
+struct PlanView {
   const int32_t* p;
   int64_t most;
   __device__ const int2* out() const { return reinterpret_cast<const int2*>(p + 4); }
@@ -175,7 +175,7 @@ __device__ __forceinline__ Item get_item(const ScanParams& p, int64_t i) {
   it.h0 = it.g * p.hpg + in;
   it.nh = p.hpg - in < HPC ? p.hpg - in : HPC;
   if (p.plan) {
-    const PlanView2 v{p.plan, p.plan_most};
+    const PlanView v{p.plan, p.plan_most};
     const int2 e = kState ? v.st()[k] : v.out()[k];
     it.n = e.x;
     it.seg = e.y;
@@ -209,10 +209,6 @@ __device__ __forceinline__ int64_t item_at(int64_t round) {
   return round * gridDim.x + b;
 }
 
-// 128-byte-swizzle operands.  K-major (rows of 64 K elements): 8-row groups 1024 bytes
-// apart, the next 64 K elements one tile further.  MN-major (rows are K, 64 M/N elements
-// each): 8-row groups 1024 bytes apart, the next 64 M/N elements one tile (the leading
-// offset) further.
 // softplus(x) = max(x, 0) + log1p(y), y = e^-|x|: with s = y / (2 + y) <= 1/3, log1p(y) =
 // 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ...), cut after s^12/13 (2e-8 of the sum).  In few
 // instructions, and a few 1e-7 of the result for small results too.
@@ -351,7 +347,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
 }
-// descriptor words: the high one is the same for every operand here
+// 128-byte-swizzle operands.  K-major (rows of 64 K elements): 8-row groups 1024 bytes
+// apart, the next 64 K elements one tile further.  MN-major (rows are K, 64 M/N elements
+// each): 8-row groups 1024 bytes apart, the next 64 M/N elements one tile (the leading
+// offset) further.  The descriptors' high word is the same for all of them.
 __device__ __forceinline__ uint64_t op_desc(uint32_t lo) {
   constexpr uint32_t hi = (1024 >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1024 apart, version 1, swizzle 128
   return ((uint64_t)hi << 32) | lo;
@@ -730,17 +729,14 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = g[e] * (u * f.v[j + e]);
               }
-#pragma unroll
-              for (int e = 0; e < 8; e += 8) {
-                uint4 hi, lo;
-                split2(v[e], v[e + 1], hi.x, lo.x);
-                split2(v[e + 2], v[e + 3], hi.y, lo.y);
-                split2(v[e + 4], v[e + 5], hi.z, lo.z);
-                split2(v[e + 6], v[e + 7], hi.w, lo.w);
-                const int o = (((jb + j + e) >> 3) ^ (row & 7)) << 4;
-                *reinterpret_cast<uint4*>(mt + o) = hi;
-                *reinterpret_cast<uint4*>(mt + kTile + o) = lo;
-              }
+              uint4 hi, lo;
+              split2(v[0], v[1], hi.x, lo.x);
+              split2(v[2], v[3], hi.y, lo.y);
+              split2(v[4], v[5], hi.z, lo.z);
+              split2(v[6], v[7], hi.w, lo.w);
+              const int o = (((jb + j) >> 3) ^ (row & 7)) << 4;
+              *reinterpret_cast<uint4*>(mt + o) = hi;
+              *reinterpret_cast<uint4*>(mt + kTile + o) = lo;
             }
           }
           fence_proxy_async_smem();
@@ -774,13 +770,12 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             break;
           }
 #pragma unroll 1
-          for (int q = 0; q < 512 / 256; ++q) {
-            // 16-byte unit: tile (64 channels) q / (256 / 256), token row in the half
-            const int o = (q / (256 / 256)) * kTile + h * (kTile / 2) + (q % (256 / 256)) * 256 * 16;
-            const int tok = h * 32 + (xt >> 3) + (q % (256 / 256)) * (256 / 8);
+          for (int q = 0; q < 2; ++q) {  // tiles of 64 channels; this thread's 16 bytes of a row
+            const int o = q * kTile + h * (kTile / 2);
+            const int tok = h * 32 + (xt >> 3);
             uint4 a = zero, b = zero, d = zero;
             if (tok < n) {
-              const float w = f[HPC == 2 ? q / (256 / 256) : 0].w[tok];
+              const float w = f[HPC == 2 ? q : 0].w[tok];
               const float2 w2 = make_float2(w, w);
               const uint4 v = *reinterpret_cast<const uint4*>(x + o);
               split3(mul2(w2, make_float2(bf16_lo(v.x), bf16_hi(v.x))), a.x, b.x, d.x);
