@@ -12,13 +12,16 @@ namespace {
 // Prompts.  One block of 128 threads per (sequence, head, COLS state columns): a
 // thread owns one column and DS * COLS / 128 of its rows, in registers.  kTile tokens
 // are staged in shared memory as float32 at a time, two tiles in turn: the next tile's
-// inputs are requested before this one's tokens are worked on and stored after; the
-// row groups' parts of y meet by shuffles inside a warp and once per tile across the
-// warps.  With many blocks it is bound by the float32 multiply-adds (2 per state element
-// and token), and 32 columns share each read of B and C best; with few, by the chain of
-// tokens, which 8 columns per block keep short.
+// inputs are requested before this one's tokens are worked on and stored after.  Four
+// tokens' parts of y are reduced together, each exchange between lanes halving the
+// tokens that a lane still holds; the warps' parts meet once per tile.
+// With many blocks it is bound by issue (2 multiply-adds per state element and token) and
+// shared memory reads, and 32 columns share each read of B and C best; with few, by the
+// chain of tokens, which 8 columns per block keep short.  512 tokens, state 64 x 64: 8
+// chains take 35 us with 8 columns and 60 with 32, 512 chains 390 and 230.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 16;
+constexpr int kStep = 4;  // tokens whose parts of y are reduced together
 
 template <typename T, typename TO, int DS, int COLS>
 __global__ void __launch_bounds__(128)
@@ -26,8 +29,9 @@ scan_recurrent_kernel(ScanArgs a) {
   constexpr int R = DS * COLS / 128;       // rows per thread
   constexpr int kB = kTile * DS / 128;     // elements of B (and C) a thread stages
   constexpr int kX = kTile * COLS / 128;
+  constexpr int kUnroll = COLS == 8 ? 4 : 2;  // as measured: 35 and 60 us at the sizes below, 48 and 85 without
   __shared__ __align__(16) float s_b[2][kTile][DS], s_c[2][kTile][DS];
-  __shared__ float s_x[2][kTile][COLS], s_y[kTile][4][COLS], s_a[2][kTile], s_d[2][kTile];
+  __shared__ float s_x[2][kTile][COLS], s_y[2][kTile][4][COLS], s_a[2][kTile], s_d[2][kTile];
   if (blockIdx.x == 0) check_seqlens(a.q, a.status);
   const int slices = a.dx / COLS;
   const int sl = blockIdx.x % slices;
@@ -39,9 +43,12 @@ scan_recurrent_kernel(ScanArgs a) {
   int64_t s0, s1;
   a.q.range(n, s0, s1);
   const int64_t base = (chain * DS + row0) * (int64_t)a.dx + sl * COLS + cl;
-  float S[R];
+  float2 S[R / 2];  // rows in pairs
 #pragma unroll
-  for (int i = 0; i < R; ++i) S[i] = a.h0 ? a.h0[base + (int64_t)i * a.dx] : 0.f;
+  for (int i = 0; i < R / 2; ++i) {
+    const float* p = a.h0 + base + (int64_t)(2 * i) * a.dx;
+    S[i] = a.h0 ? make_float2(p[0], p[a.dx]) : make_float2(0.f, 0.f);
+  }
   const float decay = a.A[h], skip = a.D ? a.D[h] : 0.f, bias = a.dtb ? a.dtb[h] : 0.f;
   const T* x = static_cast<const T*>(a.x) + (int64_t)h * a.dx + sl * COLS;
   const T* dt = static_cast<const T*>(a.dt) + h;
@@ -90,40 +97,60 @@ scan_recurrent_kernel(ScanArgs a) {
   int b = 0;
   for (int64_t t0 = s0; t0 < s1; t0 += kTile, b ^= 1) {
     if (t0 + kTile < s1) request(t0 + kTile);
-#pragma unroll 4
-    for (int t = 0; t < kTile; ++t) {
-      const float at = s_a[b][t], xw = s_d[b][t] * s_x[b][t][cl];
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll kUnroll
+    for (int tt = 0; tt < kTile; tt += kStep) {
+      float v[kStep];
 #pragma unroll
-      for (int i = 0; i < R; i += 4) {
-        const float4 bv = *reinterpret_cast<const float4*>(&s_b[b][t][row0 + i]);
-        const float4 cv = *reinterpret_cast<const float4*>(&s_c[b][t][row0 + i]);
-        S[i] = fmaf(at, S[i], bv.x * xw);
-        S[i + 1] = fmaf(at, S[i + 1], bv.y * xw);
-        S[i + 2] = fmaf(at, S[i + 2], bv.z * xw);
-        S[i + 3] = fmaf(at, S[i + 3], bv.w * xw);
-        acc[0] = fmaf(cv.x, S[i], acc[0]);
-        acc[1] = fmaf(cv.y, S[i + 1], acc[1]);
-        acc[2] = fmaf(cv.z, S[i + 2], acc[2]);
-        acc[3] = fmaf(cv.w, S[i + 3], acc[3]);
+      for (int k = 0; k < kStep; ++k) {
+        const int t = tt + k;
+        const float at = s_a[b][t], xw = s_d[b][t] * s_x[b][t][cl];
+        const float2 at2 = make_float2(at, at), xw2 = make_float2(xw, xw);
+        float2 p = make_float2(row0 == 0 ? skip * s_x[b][t][cl] : 0.f, 0.f), q = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < R / 2; i += 2) {
+          const float4 bv = *reinterpret_cast<const float4*>(&s_b[b][t][row0 + 2 * i]);
+          const float4 cv = *reinterpret_cast<const float4*>(&s_c[b][t][row0 + 2 * i]);
+          S[i] = fma2(at2, S[i], mul2(make_float2(bv.x, bv.y), xw2));
+          S[i + 1] = fma2(at2, S[i + 1], mul2(make_float2(bv.z, bv.w), xw2));
+          p = fma2(make_float2(cv.x, cv.y), S[i], p);
+          q = fma2(make_float2(cv.z, cv.w), S[i + 1], q);
+        }
+        v[k] = (p.x + p.y) + (q.x + q.y);
       }
-      float v = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      // the row groups' parts meet, and every group ends up with tokens of its own
+      int t = tt;
+      int n = kStep;
 #pragma unroll
-      for (int o = COLS; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane < COLS) s_y[t][warp][cl] = v;
+      for (int o = 16; o >= COLS; o >>= 1) {
+        n >>= 1;
+        const bool up = lane & o;
+#pragma unroll
+        for (int k = 0; k < kStep / 2; ++k)
+          if (k < n) {
+            const float mine = up ? v[n + k] : v[k], other = up ? v[k] : v[n + k];
+            v[k] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+          }
+        if (up) t += n;
+      }
+#pragma unroll
+      for (int k = 0; k < kStep; ++k)
+        if (k < kStep * COLS / 32) s_y[b][t + k][warp][cl] = v[k];
     }
     if (t0 + kTile < s1) stage(t0 + kTile, b ^ 1);
     __syncthreads();
     for (int i = tid; i < kTile * COLS; i += 128) {
       const int t = i / COLS, c = i % COLS;
-      const float v = (s_y[t][0][c] + s_y[t][1][c]) + (s_y[t][2][c] + s_y[t][3][c]);
-      if (t0 + t < s1) y[(t0 + t) * ldy + c] = from_f32<TO>(fmaf(skip, s_x[b][t][c], v));
+      const float v = (s_y[b][t][0][c] + s_y[b][t][1][c]) + (s_y[b][t][2][c] + s_y[b][t][3][c]);
+      if (t0 + t < s1) y[(t0 + t) * ldy + c] = from_f32<TO>(v);
     }
-    __syncthreads();
   }
   if (a.hT) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) a.hT[base + (int64_t)i * a.dx] = S[i];
+    for (int i = 0; i < R / 2; ++i) {
+      float* p = a.hT + base + (int64_t)(2 * i) * a.dx;
+      p[0] = S[i].x;
+      p[a.dx] = S[i].y;
+    }
   }
 }
 
@@ -232,9 +259,10 @@ cudaError_t recurrent_cols(const ScanArgs& a) {
 }
 template <typename T, typename TO, int DS>
 cudaError_t recurrent(const ScanArgs& a) {
-  // 8 columns per block while even those blocks find an SM each
-  return (int64_t)a.q.N * a.H * (a.dx / 8) <= a.sms ? recurrent_cols<T, TO, DS, 8>(a)
-                                                    : recurrent_cols<T, TO, DS, 32>(a);
+  // 8 columns per block while there are up to two such blocks per SM (512 tokens, 128 x 64: 32
+  // chains take 56 us against 89 with 32 columns, 64 chains 105 against 89)
+  return (int64_t)a.q.N * a.H * (a.dx / 8) <= 2 * a.sms ? recurrent_cols<T, TO, DS, 8>(a)
+                                                        : recurrent_cols<T, TO, DS, 32>(a);
 }
 template <typename T, typename TO>
 cudaError_t recurrent_ds(const ScanArgs& a) {
