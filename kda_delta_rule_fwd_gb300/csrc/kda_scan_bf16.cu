@@ -700,14 +700,13 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         for (int k = 0; k < HPC; ++k) skip[k] = p.D && k < it.nh ? p.D[it.h0 + k] : 0.f;
 #pragma unroll 1
         for (int ci = 0; ci < it.chunks; ++ci, ++c) {
-          // G is there, and the products that read the last M are done
-          if (!cx.wait(B_FFULL + c % kRing, (c / kRing) & 1, B_G, c & 1, c > 0 ? B_YX : -1, (c - 1) & 1)) {
+          if (!cx.wait(B_FFULL + c % kRing, (c / kRing) & 1, B_G, c & 1)) {
             alive = false;
             break;
           }
           tc_fence_after();
 #pragma unroll 1
-          for (int j = 0; j < 32; j += 8) {
+          for (int j = 0; j < 32 && alive; j += 8) {
             float g[8];
             tmem_ld8(tb + lane_base + TM_G + jb + j, g);
             tmem_wait_ld();
@@ -717,17 +716,21 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
               unsigned char* mt = sm + L::kM + k * 2 * kTile + row * 128;
               float v[8];
               if (diag) {
+                const int at = lane - j;
                 const float ci_ = f.c[row];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                  const float x = g[e] * (ex2(ci_ - f.c[jb + j + e]) * f.delta[jb + j + e]);
-                  v[e] = j + e <= lane ? x : 0.f;
-                  if (j + e == lane) v[e] += skip[k];
+                  const float x = fmaf(g[e], ex2(ci_ - f.c[jb + j + e]) * f.delta[jb + j + e], e == at ? skip[k] : 0.f);
+                  v[e] = e <= at ? x : 0.f;
                 }
               } else {
                 const float u = f.u[lane];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = g[e] * (u * f.v[j + e]);
+                for (int e = 0; e < 8; e += 2) {
+                  const float2 r = mul2(make_float2(g[e], g[e + 1]), mul2(make_float2(u, u), make_float2(f.v[j + e], f.v[j + e + 1])));
+                  v[e] = r.x;
+                  v[e + 1] = r.y;
+                }
               }
               uint4 hi, lo;
               split2(v[0], v[1], hi.x, lo.x);
@@ -735,10 +738,13 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
               split2(v[4], v[5], hi.z, lo.z);
               split2(v[6], v[7], hi.w, lo.w);
               const int o = (((jb + j) >> 3) ^ (row & 7)) << 4;
+              // the products that read the last M are done
+              if (k == 0 && j == 0 && c > 0 && !cx.wait(B_YX, (c - 1) & 1)) { alive = false; break; }
               *reinterpret_cast<uint4*>(mt + o) = hi;
               *reinterpret_cast<uint4*>(mt + kTile + o) = lo;
             }
           }
+          if (!alive) break;
           fence_proxy_async_smem();
           tc_fence_before();
           cx.arrive_warp(B_M);
