@@ -11,6 +11,12 @@
 // memory (cp.async, each thread for itself, so that no barrier is needed): bytes in
 // flight then cost no registers.  Sequence boundaries of a packed batch are found
 // once per tile by bisection and then followed.
+//
+// 12288 channels of width 4 in bf16 on one GB300: 58511 packed tokens take 433 us (6.6 TB/s,
+// a copy's rate); one token of each of 1024 sequences 37 us (5.4 TB/s; the
+// floor is 30 us, and 33 us pass on the GPU when the launch is replayed from a graph); the
+// gradient of 16384 tokens 246 us (4.9 TB/s): 32 instructions per element leave it bound by issue (65% of the
+// slots, 12 warps per SM at 168 registers).
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -493,7 +499,9 @@ cudaError_t by_type(const ConvArgs& a, int what) {
 
 cudaError_t launch_conv_fwd(const ConvArgs& a0) {
   ConvArgs a = a0;
-  // tiles of 64 tokens re-read 5% of x at W = 4; short inputs take smaller ones, for more blocks
+  // tiles of 64 tokens re-read 5% of x at W = 4; short inputs take smaller ones, for more blocks:
+  // 256 tokens of 12288 channels run 6.4 us on the GPU, with tiles of 64 13.6, 1024 tokens 16.7
+  // and 16.9
   const int64_t per = kThreads * (a.bf16 ? 8 : 4);
   const int64_t cb = (a.D + per - 1) / per;
   a.tile = 64;

@@ -12,6 +12,11 @@
 // together, each walks rows and requests the next one's inputs before it works on the
 // present one, so that the reductions' latency is covered; the parameters are loaded
 // once where a row's chunks leave room for them (up to 32 threads per row).
+//
+// One GB300, bf16: 16384 x 32 gated rows of 128 take 64 us forward (6.3 TB/s, 92% of a copy's
+// rate); the gradient through both norms, gate and residual scale over 16384 rows of 4096 takes
+// 283 us (3.8 TB/s): three sums over a row's 512 threads follow each other, with half the
+// issue slots used and no registers left for a second row.
 #pragma once
 
 #include <type_traits>
@@ -154,7 +159,8 @@ inline bool wide_ok(const NormArgs& a) {
 // Threads per row by the row's chunks: up to 32 chunks the row stays inside a warp, with two
 // chunks per thread (F::kPairs) up to 64.  Eight threads for rows of up to 8 chunks leave few
 // lanes idle: rows of 64 bf16 channels, 128 MB of them with a gate, take 69 us forward against
-// 96 with 16 lanes per row.  `F<T, TR, VEC, NC, TPR, PLACE>::run` is the launch.
+// 96 with 16 lanes per row.  Two chunks per thread where their registers allow it: rows of 128
+// take 65 us, with one chunk 69.  `F<T, TR, VEC, NC, TPR, PLACE>::run` is the launch.
 template <template <typename, typename, int, int, int, int> class F, typename T, typename TR, int VEC, int PLACE>
 cudaError_t by_size(const NormArgs& a) {
   const int chunks = (a.d + VEC - 1) / VEC;

@@ -14,7 +14,8 @@ namespace {
 
 using namespace norm;
 
-// threads per SM: what the registers of one row allow (rows inside a warp take more of them)
+// threads per SM: what the registers of one row allow (rows inside a warp take more of them:
+// 128 MB in rows of 128 take 161 us with 384 threads, 166 with 512, which spill)
 constexpr int resident(bool long_row) { return long_row ? 512 : 384; }
 
 template <typename T, typename TR, int VEC, int NC, int TPR, int PLACE>
