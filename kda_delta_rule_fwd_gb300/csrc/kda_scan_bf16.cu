@@ -1174,13 +1174,13 @@ struct Sizes {
 // two launches favours, in chunk-steps on `sms` CTAs: the state launch runs all segments
 // but the last at kStateCost of a full chunk's time, the output launch all of them, each
 // item pays kStart chunk-steps to fill its pipeline, and a segment's start state sums up
-// those before it (kJoin each; the constants are fitted to measured calls).  131071 tokens of
-// 32 heads take 1.60 ms in segments and 4.96 ms whole, 16384 tokens of one head 47 and 548 us,
-// 2048 tokens of 8 heads 50 and 82.  Packed: a sequence may be as long as the SMs' mean share
-// of the batch's work; longer ones are cut to that length.  Segments have at least kMinSeg
-// chunks.
+// those before it (kJoin each; the times are flat around these constants).  Packed: a
+// sequence may be as long as the SMs' mean share of the batch's work; longer ones are cut to
+// that length.  Segments have at least kMinSeg chunks.  On the GPU, in segments and whole:
+// 131071 tokens of 32 heads 1.39 and 3.75 ms, 16384 tokens of one head 39 and 484 us, 2048 of 8
+// heads 30 and 65, 700 of two heads 23 and 27 (with 8 chunks at least 40 and 27 for the last two).
 constexpr double kStateCost = 0.8, kStart = 4.0, kJoin = 0.4;
-constexpr int64_t kMinSeg = 8, kMaxSegs = 64;
+constexpr int64_t kMinSeg = 2, kMaxSegs = 64;
 Sizes plan_sizes(const Seqs& q, bool packed, int64_t tiles, int H, int ds, int dx, int64_t sms) {
   Sizes s;
   if (q.total == 0 || q.N == 0) return s;
