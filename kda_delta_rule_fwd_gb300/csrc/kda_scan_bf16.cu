@@ -37,12 +37,12 @@
 // launch forms each segment's own end state (all but the last; no outputs) and its
 // total decay, the second starts each segment from the decayed sum of those before.
 //
-// One GB300: 4 x 4096 tokens of 32 heads of 128 (4 groups, state 128) take 165 us, 16 packed
-// sequences (58511 tokens) of 64 heads of 64 take 702 us, 131071 tokens of 32 heads 1.61 ms.
-// A chunk takes about 4600 cycles (6000 for two heads): no unit is full (tensor pipe 33%, issue
-// 48%, shared memory about 390 KB or 3000 cycles per chunk, four fifths of them operands of
-// the products), and each role's turn (wait, work, hand on) is about as long as the period, as
-// the roles slow each other down.
+// One GB300: 4 x 4096 tokens of 32 heads of 128 (4 groups, state 128) take 130 us, 16 packed
+// sequences (58511 tokens) of 64 heads of 64 take 622 us, 131071 tokens of 32 heads 1.40 ms.
+// A chunk takes about 3800 cycles (5000 for two heads): no unit is full (tensor pipe 40%, issue
+// 50%, shared memory about 390 KB or 3000 cycles per chunk, half of them operands of the
+// products), and the longest turn is M's: wait for the products with the last M, form it, hand
+// it to the tensor core.
 #include <cudaTypedefs.h>
 
 #include "kda_layer.cuh"
