@@ -18,7 +18,7 @@ namespace {
 // With many blocks it is bound by issue (2 multiply-adds per state element and token) and
 // shared memory reads, and 32 columns share each read of B and C best; with few, by the
 // chain of tokens, which 8 columns per block keep short.  512 tokens, state 64 x 64: 8
-// chains take 35 us with 8 columns and 60 with 32, 512 chains 390 and 230.
+// chains take 37 us with 8 columns and 60 with 32, 512 chains 390 and 230.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 16;
 constexpr int kStep = 4;  // tokens whose parts of y are reduced together
@@ -29,7 +29,9 @@ scan_recurrent_kernel(ScanArgs a) {
   constexpr int R = DS * COLS / 128;       // rows per thread
   constexpr int kB = kTile * DS / 128;     // elements of B (and C) a thread stages
   constexpr int kX = kTile * COLS / 128;
-  constexpr int kUnroll = COLS == 8 ? 4 : 2;  // as measured: 35 and 60 us at the sizes below, 48 and 85 without
+  // groups of tokens per trip, as measured for 8 chains of 512 tokens: 8 columns take 37 us with 4
+  // and 47 with 2, 32 columns 86 with 4 and 60 with 2
+  constexpr int kUnroll = COLS == 8 ? 4 : 2;
   __shared__ __align__(16) float s_b[2][kTile][DS], s_c[2][kTile][DS];
   __shared__ float s_x[2][kTile][COLS], s_y[2][kTile][4][COLS], s_a[2][kTile], s_d[2][kTile];
   if (blockIdx.x == 0) check_seqlens(a.q, a.status);
