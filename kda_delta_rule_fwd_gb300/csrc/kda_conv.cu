@@ -45,7 +45,9 @@ __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void ring_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// the window of W - 1 inputs before token t of sequence n, whose tokens start at s0
+// The window of W - 1 inputs before token t of sequence n, whose tokens start at s0.  Offsets
+// that do not begin with 0 leave tokens before the first sequence (t < s0): they have neither
+// inputs nor a row of the start state before them, and get zeros.
 template <int VEC, int W, typename T>
 __device__ __forceinline__ void load_window(const T* x, int64_t ldx, const T* init, int64_t t,
                                             int64_t s0, int n, int D, int c, float (&win)[W - 1][VEC]) {
@@ -54,7 +56,7 @@ __device__ __forceinline__ void load_window(const T* x, int64_t ldx, const T* in
     const int64_t p = t - (W - 1) + i;
     if (p >= s0) {
       load<VEC>(x + p * ldx + c, win[i]);
-    } else if (init) {  // row p - s0 + W - 1 of the start state
+    } else if (init && p - s0 + W - 1 >= 0) {  // that row of the start state
       load<VEC>(init + ((int64_t)n * (W - 1) + (p - s0 + W - 1)) * D + c, win[i]);
     } else {
 #pragma unroll
