@@ -92,7 +92,7 @@ kda_status check_scan(const kda_scan_shape* s, bool packed, ScanArgs& a) {
 }
 
 size_t scan_bytes(const kda_scan_shape* s, bool packed) {
-  if (!s || s->B < 0 || s->T < 0 || s->H < 1 || s->G < 1 || s->num_seqs < 0 ||
+  if (!s || s->B < 0 || s->T < 0 || s->H < 1 || s->G < 1 || (packed && s->num_seqs < 0) ||
       (s->ds != 64 && s->ds != 128) || (s->dx != 64 && s->dx != 128))
     return 0;
   if (s->in_dtype != KDA_BF16) return kWsHeader;
@@ -220,7 +220,10 @@ kda_status kda_conv_bwd(const kda_conv_shape* s, const void* x, const float* wei
 }
 
 size_t kda_scan_workspace_size(const kda_scan_shape* s) {
-  return scan_bytes(s, s && s->num_seqs > 0);
+  // a fixed-length call ignores num_seqs, which may hold anything: enough for either call
+  const size_t fixed = scan_bytes(s, false);
+  const size_t packed = s && s->B == 1 && s->num_seqs > 0 ? scan_bytes(s, true) : 0;
+  return fixed > packed ? fixed : packed;
 }
 
 kda_status kda_scan_fwd(const kda_scan_shape* s, const void* x, const void* dt, const float* A,

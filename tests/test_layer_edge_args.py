@@ -1,0 +1,25 @@
+"""Further refusals of the operators around the recurrence, on a machine without a GPU."""
+import pytest
+import torch
+
+from test_layer_args import FAKE, call, conv, lib, norm, scan  # noqa: F401
+
+
+def test_scan_workspace_of_fixed_lengths_ignores_num_seqs(lib):
+    """A fixed-length call never gets less than it needs, whatever is in the field that it ignores."""
+    m, layer, L = lib
+    shape = dict(B=8, T=8192, H=2, G=1, ds=128, dx=128)
+    fixed = lambda s, size: call(L.kda_scan_fwd, s, 11, p7=None, size=size)  # p7: cu_seqlens
+    for few in (shape, dict(shape, B=1), dict(shape, B=1, T=2200)):
+        need = L.kda_scan_workspace_size(scan(layer, m, **few))
+        assert need > 256
+        for n in (-1, -2 ** 31, 1, 3, 2 ** 31 - 1):
+            s = scan(layer, m, num_seqs=n, **few)
+            assert fixed(s, need - 1) == m.KDA_ERR_WORKSPACE, n
+            if n <= 3:
+                assert L.kda_scan_workspace_size(s) >= need, n
+    # a packed call still gets what it needs
+    packed = scan(layer, m, B=1, T=131072, H=4, G=1, ds=128, dx=128, num_seqs=3)
+    size = L.kda_scan_workspace_size(packed)
+    assert size > 256
+    assert call(L.kda_scan_fwd, packed, 11, size=255) == m.KDA_ERR_WORKSPACE
