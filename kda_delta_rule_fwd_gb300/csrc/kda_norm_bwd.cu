@@ -67,9 +67,12 @@ norm_bwd_kernel(NormArgs a) {
       }
       dot_v(n[i], n[i], ss);
     }
+    // A place without a row holds zeros, of which 1 / rms is infinite with eps = 0: it gets 0, so that
+    // the sums over rows take nothing from it.
     float k = 1.f;
     if (a.w) {
       k = rsqrtf(fmaf(row_sum<TPR>(ss.x + ss.y, scratch, flip), a.inv_d, a.eps));
+      if (!on) k = 0.f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) mul_v(n[i], k);
     }
@@ -92,7 +95,7 @@ norm_bwd_kernel(NormArgs a) {
         }
       }
       const float2 s = row_sums<TPR>(rr.x + rr.y, pr.x + pr.y, scratch, flip);
-      const float k2 = rsqrtf(fmaf(s.x, a.inv_d, a.eps)), mean = k2 * k2 * s.y * a.inv_d;
+      const float k2 = on ? rsqrtf(fmaf(s.x, a.inv_d, a.eps)) : 0.f, mean = k2 * k2 * s.y * a.inv_d;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = (lane + i * row_threads<TPR>()) * VEC;

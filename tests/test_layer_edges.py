@@ -3,7 +3,9 @@ values that are not finite.  Tolerances as in test_layer where a test does not d
 import pytest
 import torch
 
-from test_layer import BF, DEV, F32, gen, rnd
+import _layer_ref as ref
+from _layer_ref import close
+from test_layer import BF, DEV, F32, TIGHT, gen, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +39,25 @@ def test_malformed_offsets_stay_inside_the_states(kda, dtype, D, cu):
                                  activation="silu", workspace=ws)
     assert kda.read_device_status(ws) == kda.KDA_ERR_BAD_SEQLENS
     assert torch.isfinite(dw).all() and torch.isfinite(di).all()
+
+
+@pytest.mark.parametrize("dtype,rdtype", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("rows,d", [(5, 64), (1, 128), (9, 256), (3, 37), (601, 96)])
+def test_norm_without_eps(kda, dtype, rdtype, rows, d):
+    """eps = 0 with rows that do not fill the last block: no part of a block without a row counts."""
+    g = gen(rows + d)
+    x, dr, dy = rnd(g, rows, d, dtype=dtype), rnd(g, rows, d, dtype=rdtype), rnd(g, rows, d, dtype=dtype)
+    v = dict(weight=1 + rnd(g, d, std=0.2), gate=rnd(g, rows, d, dtype=dtype),
+             residual=rnd(g, rows, d, dtype=rdtype), res_scale=1 + rnd(g, d, std=0.2),
+             out_weight=1 + rnd(g, d, std=0.2))
+    ps = {k: t.double().requires_grad_() for k, t in dict(v, x=x).items()}
+    rr, ry = ref.norm(ps["x"], **{k: ps[k] for k in v}, eps=0.0)
+    ((rr * dr.double()).sum() + (ry * dy.double()).sum()).backward()
+    dev = {k: t.to(DEV) for k, t in v.items()}
+    r, y = kda.norm_fwd(x.to(DEV), eps=0.0, **dev)
+    close(r, rr, what="r", **TIGHT[rdtype])
+    close(y, ry, what="y", **TIGHT[dtype])
+    got = kda.norm_bwd(x.to(DEV), dr.to(DEV), dy.to(DEV), eps=0.0, **dev)
+    for name, a in zip(("x", "gate", "residual", "weight", "res_scale", "out_weight"), got):
+        sums = name in ("weight", "res_scale", "out_weight")
+        close(a, ps[name].grad, what=f"d{name}", **(dict(rel=6e-6, rms=3e-5) if sums else TIGHT[a.dtype]))
