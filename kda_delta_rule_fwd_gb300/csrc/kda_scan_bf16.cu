@@ -5,8 +5,14 @@
 //     y_i = 2^c_i S^T C_i + sum_{j <= i} M_ij x_j + D x_i,   M_ij = 2^(c_i - c_j) delta_j (C_i . B_j)
 //     S  <- 2^c_last S + sum_j B_j (w_j x_j)^T,              w_j = 2^(c_last - c_j) delta_j
 //
-// Every exponent is a difference that is at most 0, so nothing overflows for any
-// decay.  Per chunk and 128 state columns (one head of 128 channels or two
+// Every exponent is a sum over the tokens between two others, at most 0: nothing overflows.  It is
+// never the rounded difference of two long sums, of which a token that forgets nearly everything
+// (c far below -1000) would leave few digits: w and the factors of M's lower left block are summed
+// from their own ends, and the c of M's diagonal blocks start with each block and are exact in
+// steps of 2^-9, with what is left summed apart (with c in one float the outputs after a step of
+// 300 at A = -1e4 were off by up to 1.8 of their rms).  A token's own exponent is not let below
+// -1024, which is nothing in float32 too, so that the sums stay finite.
+// Per chunk and 128 state columns (one head of 128 channels or two
 // neighbouring heads of 64 that share B and C) the products are, as D[lane][column]
 // in tensor memory:
 //     G  [token i][token j]   = C B^T      (rows 64.. of its M = 128 are unused)
@@ -65,6 +71,9 @@ constexpr int kItems = 4;          // items handed out ahead
 // the roles are spread so that the SM's four schedulers (warp % 4) get about the same work
 constexpr int kFactorWarp = 20, kStateMmaWarp = 21, kLoadWarp = 22, kYiMmaWarp = 23, kYxMmaWarp = 16;
 constexpr int kTile = 8192;        // 64 tokens x 64 channels of bf16, 128-byte rows
+// Exponents in [-1024, 0]: (x + kGrid) - kGrid rounds to a multiple of 2^-9, of which float32 holds
+// every sum over 32 tokens exactly
+constexpr float kFloor = -1024.f, kGrid = 24576.f;
 
 // tensor memory columns: U, Sb hi and lo, G, then Yi and Yx.  One head of 128 channels
 // leaves room for two Yi; two heads have a Yx each.
@@ -75,10 +84,11 @@ constexpr int kStateRegs = 120, kOutRegs = 72, kOtherRegs = 48;
 
 // per-token factors of one head and chunk, in shared memory
 struct Factors {
-  float c[Q];      // running log2 decay
-  float delta[Q];  // step sizes (0 past the end)
+  // running log2 decay since token 0 or 32 in steps of 2^-9; 2^(what that leaves out), and the step
+  // sizes (0 past the end) over it: 2^(c_i - c_j) delta_j = r_i 2^(c[i] - c[j]) delta[j]
+  float c[Q], r[Q], delta[Q];
   float w[Q];      // weights of the state update
-  float e[Q];      // 2^c
+  float e[Q];      // 2^(running decay since token 0)
   float u[32];     // 2^(c_i - c_31), i = 32 ..
   float v[32];     // 2^(c_31 - c_j) delta_j, j = .. 31
   float alpha;     // 2^c_last
@@ -726,11 +736,16 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
               float v[8];
               if (diag) {
                 const int at = lane - j;
-                const float ci_ = f.c[row];
+                const float ci_ = f.c[row], ri = f.r[row];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float x = fmaf(g[e], ex2(ci_ - f.c[jb + j + e]) * f.delta[jb + j + e], e == at ? skip[k] : 0.f);
-                  v[e] = e <= at ? x : 0.f;
+                for (int e = 0; e < 8; e += 2) {
+                  const int j0 = jb + j + e;
+                  const float2 dc = fma2(make_float2(f.c[j0], f.c[j0 + 1]), make_float2(-1.f, -1.f), make_float2(ci_, ci_));
+                  const float2 wt = mul2(make_float2(ex2(dc.x), ex2(dc.y)), make_float2(f.delta[j0], f.delta[j0 + 1]));
+                  const float2 t = mul2(make_float2(g[e], g[e + 1]), make_float2(ri, ri));
+                  const float x0 = fmaf(t.x, wt.x, e == at ? skip[k] : 0.f), x1 = fmaf(t.y, wt.y, e + 1 == at ? skip[k] : 0.f);
+                  v[e] = e <= at ? x0 : 0.f;
+                  v[e + 1] = e + 1 <= at ? x1 : 0.f;
                 }
               } else {
                 const float u = f.u[lane];
@@ -976,7 +991,7 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 #pragma unroll
       for (int k = 0; k < HPC; ++k) {
         const bool on = k < it.nh;
-        rate[k] = on ? p.A[it.h0 + k] * 1.4426950408889634f : 0.f;
+        rate[k] = on ? p.A[it.h0 + k] : 0.f;
         bias[k] = on && p.dtb ? p.dtb[it.h0 + k] : 0.f;
       }
 #pragma unroll 1
@@ -995,23 +1010,31 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 #pragma unroll 1
         for (int k = 0; k < HPC; ++k) {
           const bool on = k < it.nh;
-          float d[2], pre[2], suf[2];
+          float d[2], pre[2], err[2], suf[2];  // the running sum is pre + err
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float v = step_size_fast(k == 0 ? raw[0][h] : raw[HPC - 1][h], k == 0 ? bias[0] : bias[HPC - 1], p.softplus);
             d[h] = on && h * 32 + lane < left ? v : 0.f;
-            pre[h] = suf[h] = d[h] * (k == 0 ? rate[0] : rate[HPC - 1]);
+            float x = d[h] * (k == 0 ? rate[0] : rate[HPC - 1]) * 1.4426950408889634f;
+            x = x < kFloor ? kFloor : x;  // (a NaN stays one)
+            suf[h] = x;
+            pre[h] = (x + kGrid) - kGrid;
+            err[h] = x - pre[h];
           }
-#pragma unroll
+#pragma unroll 1
           for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float a = __shfl_up_sync(0xffffffffu, pre[h], o);
+              const float ae = __shfl_up_sync(0xffffffffu, err[h], o);
               const float b = __shfl_down_sync(0xffffffffu, suf[h], o);
-              if (lane >= o) pre[h] += a;
+              if (lane >= o) {
+                pre[h] += a;
+                err[h] += ae;
+              }
               if (lane + o < 32) suf[h] += b;
             }
-          const float low = __shfl_sync(0xffffffffu, pre[0], 31);   // the sum over tokens 0 .. 31
+          const float low = __shfl_sync(0xffffffffu, pre[0] + err[0], 31);   // the sum over tokens 0 .. 31
           const float high = __shfl_sync(0xffffffffu, suf[1], 0);   // over tokens 32 .. 63
           // the sum after a token, exclusive: each from its own end, where it is small
           float aft[2];
@@ -1022,14 +1045,16 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
           }
           Factors& f = factors[(c % kRing) * HPC + k];
           f.c[lane] = pre[0];
-          f.c[32 + lane] = low + pre[1];
-          f.delta[lane] = d[0];
-          f.delta[32 + lane] = d[1];
+          f.c[32 + lane] = pre[1];
+          f.r[lane] = ex2(err[0]);
+          f.r[32 + lane] = ex2(err[1]);
+          f.delta[lane] = ex2(-err[0]) * d[0];
+          f.delta[32 + lane] = ex2(-err[1]) * d[1];
           f.w[lane] = ex2(aft[0] + high) * d[0];
           f.w[32 + lane] = ex2(aft[1]) * d[1];
-          f.e[lane] = ex2(pre[0]);
-          f.e[32 + lane] = ex2(low + pre[1]);
-          f.u[lane] = ex2(pre[1]);
+          f.e[lane] = ex2(pre[0] + err[0]);
+          f.e[32 + lane] = ex2(low + (pre[1] + err[1]));
+          f.u[lane] = ex2(pre[1] + err[1]);
           f.v[lane] = ex2(aft[0]) * d[0];
           if (lane == 0) f.alpha = ex2(low + high);
         }

@@ -5,7 +5,7 @@ import torch
 
 import _layer_ref as ref
 from _layer_ref import close
-from test_layer import BF, DEV, F32, TIGHT, gen, rnd
+from test_layer import BF, DEV, F32, SCAN_Y, TIGHT, gen, rnd, scan_call, scan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,48 @@ def test_norm_without_eps(kda, dtype, rdtype, rows, d):
     for name, a in zip(("x", "gate", "residual", "weight", "res_scale", "out_weight"), got):
         sums = name in ("weight", "res_scale", "out_weight")
         close(a, ps[name].grad, what=f"d{name}", **(dict(rel=6e-6, rms=3e-5) if sums else TIGHT[a.dtype]))
+
+
+def within(got, ref_, size, tol, what):
+    """|got - ref| <= tol * size, element by element; `size` is the sum of the terms' magnitudes."""
+    got, ref_ = got.detach().cpu().double(), ref_.detach().cpu().double()
+    assert got.shape == ref_.shape and torch.isfinite(got).all(), what
+    worst = ((got - ref_).abs() / (tol * size + 1e-30)).max().item()
+    assert worst <= 1, f"{what}: {worst:.3f} times the bound"
+
+
+def scan_sizes(v, **kw):
+    """y and hT of the magnitudes: what the roundings of single terms are relative to."""
+    return ref.scan(v["x"].abs(), v["dt"], v["A"], v["B"].abs(), v["C"].abs(), v["D"].abs(),
+                    bias=v["bias"], softplus=True, h0=v["h0"].abs(), **kw)
+
+
+# float32 outputs of bf16 prompts, relative to the magnitudes of an output's terms.  Each term has
+# one operand of two bf16 parts (2^-18); sums of up to 64 + 128 float32 terms, as much again; the
+# exponent of a decay by 2^-20, computed in float32, is off by 20 times a few 2^-24 (2^-17; stronger
+# decays leave less of the term than that): together 2^-16.
+SCAN_Y_TERMS = 2.0 ** -16
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dx", [64, 128])
+@pytest.mark.parametrize("at", [0, 10, 31, 40, 55])
+def test_scan_after_steps_that_forget(kda, dtype, dx, at):
+    """Steps in the middle of a chunk that leave nothing of the state, with ordinary tokens after
+    them; the last head's log decay is past float32's range."""
+    v = scan_inputs(3, 2, 150, 6, 2, 128, dx, dtype, 2, fast=True)
+    v["dt"][:, 20:30] = -200.0
+    v["dt"][:, at:at + 4] = 300.0
+    v["dt"][:, 64 + at] = 100.0
+    for h, a in enumerate((-2.0, 0.0, -1e4, -148.0, -16.0, -3e38)):
+        v["A"][h] = a
+    ry, rh = ref.scan(v["x"], v["dt"], v["A"], v["B"], v["C"], v["D"], bias=v["bias"], softplus=True,
+                      h0=v["h0"])
+    size, _ = scan_sizes(v)
+    for out in (BF, F32):
+        y, hT = scan_call(kda, v, out_dtype=out)
+        for h in range(6):
+            close(y[:, :, h], ry[:, :, h], what=f"y {h}", **SCAN_Y[BF if BF in (dtype, out) else F32])
+            close(hT[:, h], rh[:, h], rel=0, rms=1e-4, what=f"hT {h}")
+            if out == F32:
+                within(y[:, :, h], ry[:, :, h], size[:, :, h], SCAN_Y_TERMS, f"y {h}")
