@@ -109,7 +109,10 @@ typedef struct {
  * h0 f32 [N,H,ds,dx] or NULL (zeros), y [B,T,H,dx] dense, hT f32 [N,H,ds,dx] or
  * NULL (may alias h0).  workspace: kda_scan_workspace_size(s) bytes, 256-byte
  * aligned.  delta >= 0 is expected; a token whose delta is 0 leaves the state
- * as it is.  Zero-length sequences write hT = h0 (or 0).
+ * as it is.  Decays of any strength are exact to float32's rounding.  An x, dt,
+ * Bm or Cm that is not finite reaches no earlier token and no other sequence; an
+ * x makes its own channel's outputs from its token on and final state unspecified
+ * (in general NaN, also where the sum would be an infinity).  Zero-length sequences write hT = h0 (or 0).
  * kda_scan_workspace_size: with B = 1 and num_seqs > 0 enough for a packed call
  * and for a fixed-length one; otherwise for a fixed-length one. */
 size_t kda_scan_workspace_size(const kda_scan_shape* s);

@@ -68,6 +68,7 @@ constexpr int Q = 64;              // tokens per chunk
 constexpr int kScanThreads = 896;  // 28 warps
 constexpr int kRing = 4;           // chunks of per-token factors
 constexpr int kItems = 4;          // items handed out ahead
+constexpr int kFlags = 2 * kRing;  // flags of chunks: w x is at most kRing ahead of the outputs
 // the roles are spread so that the SM's four schedulers (warp % 4) get about the same work
 constexpr int kFactorWarp = 20, kStateMmaWarp = 21, kLoadWarp = 22, kYiMmaWarp = 23, kYxMmaWarp = 16;
 constexpr int kTile = 8192;        // 64 tokens x 64 channels of bf16, 128-byte rows
@@ -136,12 +137,12 @@ enum Bar {
 
 struct ScanParams {
   Seqs q;
-  const __nv_bfloat16* dt;
+  const __nv_bfloat16 *x, *dt;
   const float *A, *D, *dtb, *h0;
   void* y;
   float* hT;
   int H, G, hpg, tpg;        // heads, groups, heads and 128-column tiles per group
-  int64_t lddt;
+  int64_t ldx, lddt;
   int softplus, out_bf16;
   // segments: tokens each (0: none); the states before segments 1 .. of split
   // sequences, [slot][H][DS][dx], and their decays [slot][H]
@@ -256,6 +257,19 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 __device__ __forceinline__ void split3(float2 v, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
   const float2 r = part_of(part_of(v, p0), p1);
   p2 = pack2(r.x, r.y);
+}
+
+// whether one of four pairs of bf16 is a NaN
+__device__ __forceinline__ bool any_nan(const uint4& v) {
+  const auto h = [](const uint32_t& u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+  const __nv_bfloat162 t = __hadd2(__hadd2(h(v.x), h(v.y)), __hadd2(h(v.z), h(v.w)));
+  return !__hbeq2(t, t);
+}
+// a pair of bf16 with zeros for what is not finite
+__device__ __forceinline__ uint32_t finite_part(uint32_t u) {
+  if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
+  if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
+  return u;
 }
 
 // Wait for the phase of a barrier with the given parity; 0 when it does not come.  Each try
@@ -444,7 +458,9 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + B_COUNT);
   volatile uint32_t* s_abort = s_tmem + 1;
   Item* s_items = reinterpret_cast<Item*>(s_tmem + 4);
-  static_assert(B_COUNT * 8 + 16 + kItems * sizeof(Item) <= 768, "barrier area");
+  // [kFlags] set by the w x warps: the chunk has an x that is not finite; cleared by the outputs' warps
+  volatile int* s_odd = reinterpret_cast<volatile int*>(s_items + kItems);
+  static_assert(B_COUNT * 8 + 16 + kItems * sizeof(Item) + kFlags * 4 <= 768, "barrier area");
   Factors* factors = reinterpret_cast<Factors*>(sm + L::kF);
   // The shuffle tells the compiler that a warp's role is the same for all its lanes: addresses and
   // descriptors then go through the uniform registers (4 x 4096 tokens of 32 heads: 132 us, 167 without).
@@ -475,6 +491,7 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     init(B_YFREE, 2, 4);
     init(B_DRAIN, 1, kState ? 1 : 3);
     *s_abort = 0;
+    for (int i = 0; i < kFlags; ++i) s_odd[i] = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_x);
     tma_prefetch_desc(&tm_b);
@@ -704,6 +721,23 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
           cx.arrive_warp(B_YFREE + (c & 1));
           cx.arrive_warp(B_FEMPTY + c % kRing);
         }
+        // A channel's outputs from its first x on that is not finite are NaN (its 16 upper bits here)
+        if (s_odd[c % kFlags]) {
+          if (HPC == 1 || k < it.nh) {
+            const int64_t ch = (int64_t)it.h0 * DX + quad * 32 + lane;
+            const __nv_bfloat16* x = p.x + row0 * p.ldx + ch;
+            const int step = p.out_bf16 ? 1 : 2;
+            uint16_t* y = static_cast<uint16_t*>(p.y) + (row0 * ldy + ch) * step + (step - 1);
+            bool nan = false;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i, x += p.ldx, y += ldy * step) {
+              nan |= !isfinite(to_f32(*x));
+              if (nan) asm volatile("st.global.u16 [%0], %1;" ::"l"(y), "h"((uint16_t)0x7fff) : "memory");
+            }
+          }
+          pf::named_bar_sync(1, 128);
+          s_odd[c % kFlags] = 0;
+        }
       }
     }
   } else if (warp == 12 || warp == 13 || warp == 17) {
@@ -738,14 +772,9 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 const int at = lane - j;
                 const float ci_ = f.c[row], ri = f.r[row];
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                  const int j0 = jb + j + e;
-                  const float2 dc = fma2(make_float2(f.c[j0], f.c[j0 + 1]), make_float2(-1.f, -1.f), make_float2(ci_, ci_));
-                  const float2 wt = mul2(make_float2(ex2(dc.x), ex2(dc.y)), make_float2(f.delta[j0], f.delta[j0 + 1]));
-                  const float2 t = mul2(make_float2(g[e], g[e + 1]), make_float2(ri, ri));
-                  const float x0 = fmaf(t.x, wt.x, e == at ? skip[k] : 0.f), x1 = fmaf(t.y, wt.y, e + 1 == at ? skip[k] : 0.f);
-                  v[e] = e <= at ? x0 : 0.f;
-                  v[e + 1] = e + 1 <= at ? x1 : 0.f;
+                for (int e = 0; e < 8; ++e) {
+                  const float x = fmaf(g[e] * ri, ex2(ci_ - f.c[jb + j + e]) * f.delta[jb + j + e], e == at ? skip[k] : 0.f);
+                  v[e] = e <= at ? x : 0.f;
                 }
               } else {
                 const float u = f.u[lane];
@@ -812,6 +841,13 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
               split3(mul2(w2, make_float2(bf16_lo(v.y), bf16_hi(v.y))), a.y, b.y, d.y);
               split3(mul2(w2, make_float2(bf16_lo(v.z), bf16_hi(v.z))), a.z, b.z, d.z);
               split3(mul2(w2, make_float2(bf16_lo(v.w), bf16_hi(v.w))), a.w, b.w, d.w);
+              // The third part of what is not finite is NaN.  M's zeros above the diagonal would carry
+              // x to earlier tokens: the tile gets a zero, and the outputs' warps write the NaN.
+              if (!kState && any_nan(d)) {
+                *reinterpret_cast<uint4*>(x + o) =
+                    make_uint4(finite_part(v.x), finite_part(v.y), finite_part(v.z), finite_part(v.w));
+                s_odd[c % kFlags] = 1;
+              }
             } else {  // what follows the sequence may hold anything
               *reinterpret_cast<uint4*>(x + o) = zero;
             }
@@ -896,7 +932,6 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     while (alive) {
       if (!cx.wait(B_IFULL + m % kItems, (m / kItems) & 1)) break;
       const int chunks = __shfl_sync(0xffffffffu, s_items[m % kItems].chunks, 0);
-      const int len = __shfl_sync(0xffffffffu, s_items[m % kItems].len, 0);
       const int valid = __shfl_sync(0xffffffffu, s_items[m % kItems].valid, 0);
       cx.arrive_warp(B_IEMPTY + m % kItems);
       ++m;
@@ -956,9 +991,8 @@ scan_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
           }
           commit_by(lead, cx.bars + 8 * (B_YI + now));
         } else {
-          // a last chunk's x has its rows past the end cleared
-          if (!cx.wait(B_M, now, B_FULLX + st, ph, c > 0 ? B_YFREE + (int)last : -1, ((c - 1) >> 1) & 1) ||
-              (len - ci * Q < Q && !cx.wait(B_X + 2 * st, ph, B_X + 2 * st + 1, ph))) {
+          // x with zeros past the end and for what is not finite (B_X's second phase follows the first)
+          if (!cx.wait(B_M, now, B_X + 2 * st + 1, ph, c > 0 ? B_YFREE + (int)last : -1, ((c - 1) >> 1) & 1)) {
             alive = false;
             break;
           }
@@ -1279,12 +1313,14 @@ cudaError_t launch_scan_bf16(const ScanArgs& a) {
     return cudaErrorInvalidValue;
   ScanParams p{};
   p.q = a.q;
+  p.x = static_cast<const __nv_bfloat16*>(a.x);
   p.dt = static_cast<const __nv_bfloat16*>(a.dt);
   p.A = a.A; p.D = a.D; p.dtb = a.dtb; p.h0 = a.h0;
   p.y = a.y; p.hT = a.hT;
   p.H = a.H; p.G = a.G;
   p.hpg = a.H / a.G;
   p.tpg = (p.hpg + hpc - 1) / hpc;
+  p.ldx = a.ldx;
   p.lddt = a.lddt;
   p.softplus = a.softplus;
   p.out_bf16 = a.out_bf16;

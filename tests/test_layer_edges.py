@@ -106,3 +106,40 @@ def test_scan_after_steps_that_forget(kda, dtype, dx, at):
             close(hT[:, h], rh[:, h], rel=0, rms=1e-4, what=f"hT {h}")
             if out == F32:
                 within(y[:, :, h], ry[:, :, h], size[:, :, h], SCAN_Y_TERMS, f"y {h}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("dx,H,G", [(64, 3, 1), (64, 4, 2), (128, 2, 1)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_scan_of_a_value_that_is_not_finite(kda, dtype, out, dx, H, G, bad):
+    """Such a value of one token reaches no earlier token, no other sequence, and (of x and dt) no
+    other channel or head; what the definition makes of it is not finite."""
+    B, T, at, h, ch = 2, 150, 70, 1, 37
+    v = scan_inputs(5, B, T, H, G, 128, dx, dtype, B)
+    y, hT = scan_call(kda, v, out_dtype=out)
+    for k in ("x", "x first", "x last", "dt", "B", "C"):
+        t = {"x first": 64, "x last": 127}.get(k, at)
+        w = {n: u.clone() for n, u in v.items()}
+        if k.startswith("x"):
+            w["x"][1, t, h, ch] = bad
+        else:
+            w[k][1, t, h if k == "dt" else 0] = float("nan")
+        y2, h2 = scan_call(kda, w, out_dtype=out)
+        assert torch.equal(y2[0], y[0]) and torch.equal(h2[0], hT[0]), k
+        assert torch.equal(y2[1, :t], y[1, :t]), k
+        if k.startswith("x"):
+            assert not torch.isfinite(y2[1, t:, h, ch]).any() and not torch.isfinite(h2[1, h, :, ch]).any(), k
+            y2[1, t:, h, ch], h2[1, h, :, ch] = y[1, t:, h, ch], hT[1, h, :, ch]
+        elif k == "dt":
+            assert not torch.isfinite(y2[1, t:, h]).any() and not torch.isfinite(h2[1, h]).any(), k
+            y2[1, t:, h], h2[1, h] = y[1, t:, h], hT[1, h]
+        else:
+            n = H // G
+            assert not torch.isfinite(y2[1, t, :n]).any(), k
+            if k == "C":
+                y2[1, t, :n] = y[1, t, :n]
+            else:
+                assert not torch.isfinite(h2[1, :n]).any()
+                y2[1, t:, :n], h2[1, :n] = y[1, t:, :n], hT[1, :n]
+        assert torch.equal(y2, y) and torch.equal(h2, hT), k
