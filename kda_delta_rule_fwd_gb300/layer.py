@@ -187,8 +187,12 @@ def _check(rc, where):
         raise KDAError(rc, where)
 
 
-def _ws(workspace):
-    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+def _ws(workspace, x):
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != x.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor beside x")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 # ---------------------------------------------------------------------------
@@ -232,7 +236,7 @@ def conv_fwd(x, weight, bias=None, *, activation=None, cu_seqlens=None, init_sta
         final_state = torch.empty(state, dtype=x.dtype, device=x.device)
     _check(load().kda_conv_fwd(shape, x.data_ptr(), weight.data_ptr(), _ptr(bias),
                                _ptr(cu_seqlens), _ptr(init_state), out.data_ptr(),
-                               _ptr(final_state), *_ws(workspace), _stream(x.get_device())),
+                               _ptr(final_state), *_ws(workspace, x), _stream(x.get_device())),
            "kda_conv_fwd")
     return out, final_state
 
@@ -254,7 +258,7 @@ def conv_step(x, weight, state, bias=None, *, activation=None, num_commit=None, 
     if out is None and want_out:
         out = _new(x, x.dtype)
     _check(load().kda_conv_step(shape, x.data_ptr(), weight.data_ptr(), _ptr(bias),
-                                _ptr(num_commit), state.data_ptr(), _ptr(out), *_ws(workspace),
+                                _ptr(num_commit), state.data_ptr(), _ptr(out), *_ws(workspace, x),
                                 _stream(x.get_device())), "kda_conv_step")
     return out
 
@@ -284,7 +288,7 @@ def conv_bwd(x, weight, dy, bias=None, *, activation=None, cu_seqlens=None, init
                                 device=x.device)
     _check(lib.kda_conv_bwd(shape, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(cu_seqlens),
                             _ptr(init_state), dy.data_ptr(), _ptr(dfinal), dx.data_ptr(),
-                            dw.data_ptr(), _ptr(db), _ptr(dinit), *_ws(workspace),
+                            dw.data_ptr(), _ptr(db), _ptr(dinit), *_ws(workspace, x),
                             _stream(x.get_device())), "kda_conv_bwd")
     return dx, dw, db, dinit
 
@@ -342,7 +346,7 @@ def scan_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, dt_softplus=False, cu_seql
                                 device=x.device)
     _check(lib.kda_scan_fwd(shape, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
                             C.data_ptr(), _ptr(D), _ptr(dt_bias), _ptr(cu_seqlens), _ptr(h0),
-                            out.data_ptr(), _ptr(hT), *_ws(workspace), _stream(x.get_device())),
+                            out.data_ptr(), _ptr(hT), *_ws(workspace, x), _stream(x.get_device())),
            "kda_scan_fwd")
     return out, hT
 
@@ -364,7 +368,7 @@ def scan_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, dt_softplus=False,
         out = _new(x, out_dtype)
     _check(load().kda_scan_step(shape, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
                                 C.data_ptr(), _ptr(D), _ptr(dt_bias), _ptr(num_commit),
-                                state.data_ptr(), _ptr(out), *_ws(workspace),
+                                state.data_ptr(), _ptr(out), *_ws(workspace, x),
                                 _stream(x.get_device())), "kda_scan_step")
     return out
 
@@ -469,5 +473,5 @@ def norm_bwd(x, dr, dy=None, *, weight=None, gate=None, gate_act="sigmoid", gate
     _check(lib.kda_norm_bwd(shape, x.data_ptr(), _ptr(weight), _ptr(gate), _ptr(residual),
                             _ptr(res_scale), _ptr(out_weight), _ptr(dr), _ptr(dy), dx.data_ptr(),
                             _ptr(dgate), _ptr(dres), _ptr(dw), _ptr(dls), _ptr(dow),
-                            *_ws(workspace), _stream(x.get_device())), "kda_norm_bwd")
+                            *_ws(workspace, x), _stream(x.get_device())), "kda_norm_bwd")
     return dx, dgate, dres, dw, dls, dow

@@ -1,6 +1,8 @@
 """Further refusals of the operators around the recurrence, on a machine without a GPU."""
 import pytest
 import torch
+import pytest
+import torch
 
 from test_layer_args import FAKE, call, conv, lib, norm, scan  # noqa: F401
 
@@ -23,3 +25,21 @@ def test_scan_workspace_of_fixed_lengths_ignores_num_seqs(lib):
     size = L.kda_scan_workspace_size(packed)
     assert size > 256
     assert call(L.kda_scan_fwd, packed, 11, size=255) == m.KDA_ERR_WORKSPACE
+
+
+def test_workspace_of_another_device_or_layout(lib):
+    """The bytes passed on are bytes that the tensor has, on the device that writes them."""
+    m, layer, L = lib
+    x = torch.zeros(2, 5, 8)
+    assert layer._ws(None, x) == (None, 0)
+    ws = torch.zeros(512, dtype=torch.float32)
+    assert layer._ws(ws, x) == (ws.data_ptr(), 2048)
+    with pytest.raises(ValueError, match="workspace"):
+        layer._ws(torch.zeros(1, dtype=torch.uint8).expand(1 << 20), x)
+    with pytest.raises(ValueError, match="workspace"):
+        layer._ws(ws[::2], x)
+
+    class Elsewhere:  # stands for a tensor on a GPU
+        get_device = staticmethod(lambda: 0)
+    with pytest.raises(ValueError, match="workspace"):
+        layer._ws(ws, Elsewhere)

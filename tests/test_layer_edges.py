@@ -143,3 +143,19 @@ def test_scan_of_a_value_that_is_not_finite(kda, dtype, out, dx, H, G, bad):
                 assert not torch.isfinite(h2[1, :n]).any()
                 y2[1, t:, :n], h2[1, :n] = y[1, t:, :n], hT[1, :n]
         assert torch.equal(y2, y) and torch.equal(h2, hT), k
+
+
+def test_workspace_on_the_host_is_refused(kda):
+    """Before anything is launched."""
+    x, w, A = torch.zeros(1, 8, 16, device=DEV), torch.zeros(16, 4, device=DEV), torch.zeros(2, device=DEV)
+    xs, b = torch.zeros(1, 8, 2, 64, device=DEV), torch.zeros(1, 8, 1, 64, device=DEV)
+    state = torch.zeros(1, 2, 64, 64, device=DEV)
+    one = torch.ones(16, device=DEV)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    for call in (lambda: kda.conv_fwd(x, w, workspace=ws), lambda: kda.conv_bwd(x, w, x, workspace=ws),
+                 lambda: kda.conv_step(x, w, torch.zeros(1, 3, 16, device=DEV), workspace=ws),
+                 lambda: kda.scan_fwd(xs, xs[..., 0].contiguous(), A, b, b, workspace=ws),
+                 lambda: kda.scan_step(xs, xs[..., 0].contiguous(), A, b, b, state, workspace=ws),
+                 lambda: kda.norm_bwd(x, x, weight=one, workspace=ws)):
+        with pytest.raises(ValueError, match="workspace"):
+            call()
