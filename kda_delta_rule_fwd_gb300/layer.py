@@ -75,9 +75,17 @@ def declare(lib):
 # argument checks.  The smallest calls take about as long here as on the device: every check
 # is one comparison when it holds, and the structs are built once per set of sizes.
 # ---------------------------------------------------------------------------
-_conv_struct = functools.lru_cache(maxsize=1024)(ConvShape)
-_scan_struct = functools.lru_cache(maxsize=1024)(ScanShape)
-_norm_struct = functools.lru_cache(maxsize=1024)(NormShape)
+def _structs(cls):
+    @functools.lru_cache(maxsize=1024)
+    def of(*sizes):
+        for (name, kind), v in zip(cls._fields_, sizes):
+            if kind is _C.c_int32 and v >= 1 << 31:  # ctypes would keep the low bits
+                raise ValueError(f"{name} = {v} is more than 2^31 - 1")
+        return cls(*sizes)
+    return of
+
+
+_conv_struct, _scan_struct, _norm_struct = (_structs(c) for c in (ConvShape, ScanShape, NormShape))
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                   lambda index: torch.cuda.current_stream(index).cuda_stream)

@@ -43,3 +43,20 @@ def test_workspace_of_another_device_or_layout(lib):
         get_device = staticmethod(lambda: 0)
     with pytest.raises(ValueError, match="workspace"):
         layer._ws(ws, Elsewhere)
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    """Not cut to their low bits: 2^32 + 10 tokens are not 10."""
+    m, layer, L = lib
+    big = 2 ** 32 + 10
+    x = torch.empty(1, big, 1, dtype=torch.bfloat16, device="meta")
+    w = torch.empty(1, 4, device="meta")
+    with pytest.raises(ValueError, match="T = 4294967306"):
+        layer._conv_shape(x, w, None, None, None)
+    b = torch.empty(1, big, 1, 64, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="T = 4294967306"):
+        layer._scan_shape(b, x, torch.empty(1, device="meta"), b, b, None, None, False, None, torch.float32)
+    with pytest.raises(ValueError, match="B = 4294967306"):
+        layer._conv_shape(x.transpose(0, 1), w, None, None, None)
+    rows = layer._norm_shape(x, None, None, "silu", False, None, 1, None, None, 1e-6, None)[0]
+    assert rows.tokens == big and rows.d == 1  # 64 bits
