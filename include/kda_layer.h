@@ -41,7 +41,7 @@ extern "C" {
 typedef struct {
   int32_t B;          /* fixed length: batch size.  Packed: must be 1. */
   int32_t T;          /* tokens per sequence (fixed) or in total (packed), >= 0 */
-  int32_t D;          /* channels, >= 1 */
+  int32_t D;          /* channels, 1 .. 2^31 - 1024 */
   int32_t W;          /* taps: 2, 3 or 4 */
   int32_t num_seqs;   /* packed: number of sequences; ignored when cu_seqlens is NULL */
   kda_dtype dtype;    /* x, y and the states (and dy, dx, dinit, dfinal) */

@@ -12,6 +12,7 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 bool dtype_ok(kda_dtype t) { return t == KDA_F32 || t == KDA_BF16; }
 size_t dsize(kda_dtype t) { return t == KDA_F32 ? 4 : 2; }
 constexpr int64_t kMaxElems = (int64_t)1 << 40;  // elements of one tensor
+constexpr int kMaxChannels = 0x7fffffff - 1023;  // a block's last channel stays below 2^31
 
 // every pointer of the list (NULLs aside) a multiple of `a`
 template <int N>
@@ -42,7 +43,7 @@ bool stride_ok(int64_t& ld, int64_t row) {
 
 kda_status check_conv(const kda_conv_shape* s, bool packed, int64_t& ldx) {
   if (!s) return KDA_ERR_INVALID_ARG;
-  if (s->D < 1 || !dtype_ok(s->dtype)) return KDA_ERR_INVALID_ARG;
+  if (s->D < 1 || s->D > kMaxChannels || !dtype_ok(s->dtype)) return KDA_ERR_INVALID_ARG;
   kda_status st = check_tokens(s->B, s->T, s->num_seqs, packed);
   if (st != KDA_OK) return st;
   if (s->W < 2 || s->W > 4) return KDA_ERR_UNSUPPORTED;

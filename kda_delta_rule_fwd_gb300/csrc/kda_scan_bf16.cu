@@ -1295,12 +1295,13 @@ size_t scan_bf16_workspace(bool packed, int64_t N, int64_t T, int64_t total, int
   return plan_sizes(q, packed, tiles_of(H, G, dx), H, ds, dx, sms).total();
 }
 
-// TMA and the output rows need 16-byte alignment
+// TMA and the output rows need 16-byte alignment, and coordinates of 31 bits
 bool scan_bf16_ok(const ScanArgs& a) {
   const void* ptrs[] = {a.x, a.Bm, a.Cm, a.y};
   for (const void* p : ptrs)
     if ((uintptr_t)p % 16) return false;
   return a.bf16 && a.q.T < (1 << 30) && a.ldx % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0 &&
+         (int64_t)a.H * a.dx < 0x7fffffffll && (int64_t)a.G * a.ds < 0x7fffffffll &&
          a.q.total > 0 && a.q.total < 0x7fffffffll - Q;
 }
 

@@ -60,3 +60,13 @@ def test_sizes_past_32_bits_are_refused(lib):
         layer._conv_shape(x.transpose(0, 1), w, None, None, None)
     rows = layer._norm_shape(x, None, None, "silu", False, None, 1, None, None, 1e-6, None)[0]
     assert rows.tokens == big and rows.d == 1  # 64 bits
+
+
+@pytest.mark.parametrize("D", [2 ** 31 - 1, 2 ** 31 - 8, 2 ** 31 - 1023])
+def test_channels_near_31_bits_are_refused(lib, D):
+    """Before a block's last channel, or the number of blocks, passes 31 bits."""
+    m, layer, L = lib
+    s = conv(layer, m, B=1, T=1, D=D)
+    assert call(L.kda_conv_fwd, s, 7, p3=None) == m.KDA_ERR_INVALID_ARG
+    assert call(L.kda_conv_step, s, 6) == m.KDA_ERR_INVALID_ARG
+    assert call(L.kda_conv_bwd, s, 11, p3=None, size=1 << 60) == m.KDA_ERR_INVALID_ARG
