@@ -5,7 +5,7 @@ import torch
 
 import _layer_ref as ref
 from _layer_ref import close
-from test_layer import BF, DEV, F32, SCAN_Y, TIGHT, gen, rnd, scan_call, scan_inputs
+from test_layer import BF, DEV, F32, SCAN_Y, TIGHT, cu_of, gen, rnd, scan_call, scan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +159,70 @@ def test_workspace_on_the_host_is_refused(kda):
                  lambda: kda.norm_bwd(x, x, weight=one, workspace=ws)):
         with pytest.raises(ValueError, match="workspace"):
             call()
+
+
+@pytest.mark.parametrize("ds,dx", [(64, 64), (128, 64), (64, 128), (128, 128)])
+@pytest.mark.parametrize("B,T,lens", [(2, 200, None), (1, 2200, None), (1, 0, [1, 0, 64, 130, 63])])
+def test_scan_float32_outputs_of_bf16_prompts(kda, ds, dx, B, T, lens):
+    """Before any rounding to bf16: the read-out's and M's operands hold 16 bits."""
+    T = T if lens is None else sum(lens)
+    v = scan_inputs(T + ds, B, T, 2, 1, ds, dx, BF, B if lens is None else len(lens))
+    y, _ = scan_call(kda, v, cu=None if lens is None else cu_of(lens), out_dtype=F32)
+    ry, _ = ref.scan(v["x"], v["dt"], v["A"], v["B"], v["C"], v["D"], bias=v["bias"], softplus=True,
+                     lens=lens, h0=v["h0"])
+    within(y, ry, scan_sizes(v, lens=lens)[0], SCAN_Y_TERMS, "y")
+
+
+@pytest.mark.parametrize("ds,dx", [(64, 64), (128, 64), (64, 128), (128, 128)])
+def test_scan_keeps_every_bit_of_an_update(kda, ds, dx):
+    """The state after two tokens, relative to its two terms: the weight of the first one (an
+    exponential, 2^-22) and a few float32 roundings, 2^-20.  Updates of two bf16 parts would be off by
+    up to 2^-18."""
+    v = scan_inputs(31 + ds, 2, 2, 4, 2, ds, dx, BF, 2)
+    v["dt"] = v["dt"].abs() * 0.5
+    v["A"] = -0.5 - 0.5 * torch.rand(4, generator=gen(32))
+    d = {k: t.to(DEV) for k, t in v.items()}
+    _, hT = kda.scan_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"])
+    _, rh = ref.scan(v["x"], v["dt"], v["A"], v["B"], v["C"])
+    size = ref.scan(v["x"].abs(), v["dt"], v["A"], v["B"].abs(), v["C"])[1]
+    within(hT, rh, size, 2.0 ** -20, "hT")
+
+
+def test_every_entry_point_runs_on_the_stream_it_is_given(kda):
+    """Inputs that another stream writes late: calls made with that stream see them, others would
+    see the NaN that was there."""
+    g = gen(33)
+    up = lambda *s, **kw: rnd(g, *s, **kw).to(DEV)
+    x, w, dy = up(2, 200, 256, dtype=BF), up(256, 4), up(2, 200, 256, dtype=BF)
+    conv = dict(x=x, w=w, dy=dy, state=up(2, 3, 256, dtype=BF))
+    step = dict(conv, x=x[:, :3].contiguous(), state=conv["state"])
+    bf, f32 = ({k: t.to(DEV) for k, t in scan_inputs(34, 1, 2200, 2, 1, 128, 64, dt, 1).items()}
+               for dt in (BF, F32))
+    one = {k: t[:, :5].contiguous() if t.dim() > 1 and k != "h0" else t for k, t in bf.items()}
+    norm = dict(x=x, gate=dy, dr=up(2, 200, 256, dtype=BF), dy=up(2, 200, 256, dtype=BF), w=up(256))
+    scan = lambda f, i, *state, **kw: f(i["x"], i["dt"], i["A"], i["B"], i["C"], *state, D=i["D"],
+                                        dt_bias=i["bias"], dt_softplus=True, **kw)
+    calls = [
+        (conv, lambda i, s: kda.conv_fwd(i["x"], i["w"], init_state=i["state"], stream=s)),
+        (step, lambda i, s: (kda.conv_step(i["x"], i["w"], i["state"], stream=s), i["state"])),
+        (conv, lambda i, s: kda.conv_bwd(i["x"], i["w"], i["dy"], activation="silu", stream=s)[:2]),
+        (bf, lambda i, s: scan(kda.scan_fwd, i, h0=i["h0"], hT=i["h0"], out_dtype=BF, stream=s)),
+        (f32, lambda i, s: scan(kda.scan_fwd, i, h0=i["h0"], stream=s)),
+        (one, lambda i, s: (scan(kda.scan_step, i, i["h0"], stream=s), i["h0"])),
+        (norm, lambda i, s: kda.norm_fwd(i["x"], weight=i["w"], gate=i["gate"], out_weight=i["w"], stream=s)),
+        (norm, lambda i, s: kda.norm_bwd(i["x"], i["dr"], i["dy"], weight=i["w"], gate=i["gate"],
+                                         out_weight=i["w"], stream=s)[:2]),
+    ]
+    side = torch.cuda.Stream()
+    for k, (inputs, call) in enumerate(calls):
+        expect = call({n: t.clone() for n, t in inputs.items()}, None)
+        late = {n: torch.full_like(t, float("nan")) for n, t in inputs.items()}
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+            for n, t in inputs.items():
+                late[n].copy_(t)
+        got = call(late, side)
+        side.synchronize()
+        for a, b in zip(got, expect):
+            assert torch.equal(a, b), k
