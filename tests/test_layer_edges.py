@@ -226,3 +226,23 @@ def test_every_entry_point_runs_on_the_stream_it_is_given(kda):
         side.synchronize()
         for a, b in zip(got, expect):
             assert torch.equal(a, b), k
+
+
+@pytest.mark.parametrize("N", [1024, 1025, 2100])
+def test_scan_of_many_sequences(kda, N):
+    """More sequences than the planning block has threads, most of them empty or of one or two
+    tokens, with one that is cut into segments behind them."""
+    g = gen(N)
+    lens = torch.randint(0, 3, (N,), generator=g).tolist()
+    lens[N - 40] = 1500
+    v = scan_inputs(N, 1, sum(lens), 1, 1, 64, 64, BF, N)
+    v["h0"] *= 3
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
+    y, hT = scan_call(kda, v, cu=cu_of(lens), out_dtype=F32, workspace=ws)
+    assert kda.read_device_status(ws) == kda.KDA_OK
+    ry, rh = ref.scan(v["x"], v["dt"], v["A"], v["B"], v["C"], v["D"], bias=v["bias"], softplus=True,
+                      lens=lens, h0=v["h0"])
+    close(y, ry, what="y", **SCAN_Y[BF])
+    close(hT, rh, rel=0, rms=1e-4, what="hT")
+    empty = [i for i, n in enumerate(lens) if n == 0]
+    assert torch.equal(hT[empty].cpu(), v["h0"][empty])
