@@ -89,7 +89,7 @@ kda_status kda_conv_bwd(const kda_conv_shape* s, const void* x, const float* wei
  *     S  <- exp(delta_t A[h]) S + delta_t B_t x_t^T        (ds x dx)
  *     y_t = S^T C_t + D[h] x_t
  *
- * States are float32 [N,H,ds,dx], dx fastest.
+ * States are float32 [N,H,ds,dx], dx fastest; h0, hT and state are 16-byte aligned.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int32_t B;           /* as kda_conv_shape */
@@ -109,7 +109,12 @@ typedef struct {
  * h0 f32 [N,H,ds,dx] or NULL (zeros), y [B,T,H,dx] dense, hT f32 [N,H,ds,dx] or
  * NULL (may alias h0).  workspace: kda_scan_workspace_size(s) bytes, 256-byte
  * aligned.  delta >= 0 is expected; a token whose delta is 0 leaves the state
- * as it is.  Decays of any strength are exact to float32's rounding.  An x, dt,
+ * as it is.  Decays of any strength are exact to float32's rounding.  float32
+ * inputs are worked on in float32 throughout; with bf16 inputs the tensor-core
+ * path rounds one operand of the output's products to 16 bits (2.4e-6 of the
+ * outputs' rms; the states keep float32's 24).  That path takes x, Bm, Cm and y on
+ * 16-byte boundaries with token strides of x, Bm, Cm that are multiples of 8;
+ * others are worked on token by token.  An x, dt,
  * Bm or Cm that is not finite reaches no earlier token and no other sequence; an
  * x makes its own channel's outputs from its token on and final state unspecified
  * (in general NaN, also where the sum would be an infinity).  Zero-length sequences write hT = h0 (or 0).

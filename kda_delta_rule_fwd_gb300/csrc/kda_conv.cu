@@ -15,8 +15,8 @@
 // 12288 channels of width 4 in bf16 on one GB300: 58511 packed tokens take 433 us (6.6 TB/s,
 // a copy's rate); one token of each of 1024 sequences 37 us (5.4 TB/s; the
 // floor is 30 us, and 33 us pass on the GPU when the launch is replayed from a graph); the
-// gradient of 16384 tokens 246 us (4.9 TB/s): 32 instructions per element leave it bound by issue (65% of the
-// slots, 12 warps per SM at 168 registers).
+// gradient of 16384 tokens 246 us (4.9 TB/s): 32 instructions per element, for which 12 warps per SM
+// (168 registers) fill 65% of the issue slots.
 #include "kda_layer.cuh"
 
 namespace kda {

@@ -19,8 +19,8 @@
 //     U  [channel][state row] = (w x)^T B
 //     Yi [channel][token]     = Sb C^T     (Sb: S^T, A operand in tensor memory)
 //     Yx [channel][token]     = x^T M^T    (one per head)
-// B, C and x are bf16 as given; Sb and M enter as bf16 hi + lo (16 bits), w x in three parts
-// (24 bits, as S is kept in float32).  D sits on M's diagonal.  S itself stays float32 in the
+// B, C and x are bf16 as given; Sb and M enter as bf16 hi + lo (16 bits: 2.4e-6 of the outputs' rms,
+// below what bf16 outputs keep), w x in three parts (24 bits, as S is kept in float32).  D sits on M's diagonal.  S itself stays float32 in the
 // registers of the state warps.
 //
 // One persistent CTA per SM; its warps are specialised and hand chunks on through
@@ -43,9 +43,9 @@
 // launch forms each segment's own end state (all but the last; no outputs) and its
 // total decay, the second starts each segment from the decayed sum of those before.
 //
-// One GB300: 4 x 4096 tokens of 32 heads of 128 (4 groups, state 128) take 130 us, 16 packed
-// sequences (58511 tokens) of 64 heads of 64 take 622 us, 131071 tokens of 32 heads 1.40 ms.
-// A chunk takes about 3800 cycles (5000 for two heads): no unit is full (tensor pipe 40%, issue
+// One GB300: 4 x 4096 tokens of 32 heads of 128 (4 groups, state 128) take 131 us, 16 packed
+// sequences (58511 tokens) of 64 heads of 64 take 635 us, 131071 tokens of 32 heads 1.44 ms.
+// A chunk takes about 3900 cycles (5100 for two heads): no unit is full (tensor pipe 40%, issue
 // 50%, shared memory about 390 KB or 3000 cycles per chunk, half of them operands of the
 // products), and the longest turn is M's: wait for the products with the last M, form it, hand
 // it to the tensor core.

@@ -12,7 +12,9 @@ Argument marshalling only, as in the package's other entry points; the C ABI is
     r, y = norm_fwd(x, weight=w, gate=g, residual=h, out_weight=w2)
 
 Activations may be views with any token stride (column slices of a fused
-projection) as long as the channels of one token are contiguous.
+projection) as long as the channels of one token are contiguous and one stride
+leads from each token to the next, from the last of one sequence to the first of
+the following too.
 """
 from __future__ import annotations
 
