@@ -10,7 +10,9 @@ been built, :func:`load` raises; there is no other code path.
 
 The operators around the recurrence (``conv_fwd``, ``conv_step``, ``conv_bwd``,
 ``scan_fwd``, ``scan_step``, ``norm_fwd``, ``norm_bwd``) are documented in
-``layer.py`` and ``include/kda_layer.h``.
+``layer.py`` and ``include/kda_layer.h``; those of a hybrid stack's attention layers
+(``qknorm_fwd``, ``qknorm_bwd``, ``kv_cache``, ``cache_write``, ``cache_read``,
+``attn_step``, ``draft_verify``) in ``attn.py`` and ``include/kda_attn.h``.
 """
 from __future__ import annotations
 
@@ -117,6 +119,7 @@ def load(path: str | None = None):
         lib.kda_version.restype = ctypes.c_char_p
         lib.kda_version.argtypes = []
         layer.declare(lib)
+        attn.declare(lib)
         if path is None:
             _lib = lib
         return lib
@@ -374,3 +377,7 @@ def read_device_status(workspace, stream=None) -> int:
 from . import layer  # noqa: E402
 from .layer import (conv_bwd, conv_fwd, conv_step, norm_bwd, norm_fwd, scan_fwd,  # noqa: E402,F401
                     scan_step)
+# those of attention layers; the module takes names of both
+from . import attn  # noqa: E402
+from .attn import (KVCache, attn_step, cache_read, cache_write, draft_verify,  # noqa: E402,F401
+                   kv_cache, qknorm_bwd, qknorm_fwd)

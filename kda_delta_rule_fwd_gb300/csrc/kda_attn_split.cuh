@@ -1,0 +1,145 @@
+// How the keys of a call are split over the device, and what the parts leave for the join.
+//
+// An item is a sequence, a key-value head and a chunk of up to `rows` query rows (tokens x query
+// heads of the group); its keys are tiles of kTile places.  All items' tiles in a row, sequence
+// by sequence, are cut into equal shares, one per block: the lengths are on the device, so every
+// block counts the tiles by itself and finds its share.  A block walks the items of its share; an
+// item that lies in it whole is written out, a part goes to the workspace as (maximum, sum,
+// unnormalised output) per row: a block has at most two parts, the rest of an item that begins in
+// an earlier block (slot 0) and the beginning of one that goes on in the next (slot 1).  The join
+// kernel adds an item's parts in the order of the blocks.
+#pragma once
+
+#include "kda_attn.cuh"
+
+namespace kda {
+namespace attn {
+
+constexpr int kTile = 64;          // places of a tile
+constexpr int64_t kMinShare = 4;   // tiles of a block, where there are as many
+constexpr int kRowsMax = 16;
+
+struct Split {
+  unsigned int* status;   // workspace header
+  unsigned int* verdict;  // [blocks]: what each block found
+  int64_t* share;         // tiles per block
+  int64_t* first;         // [items]: position of the item's first tile
+  float* part;            // [blocks][2][rows (d + 2)]
+  int64_t blocks, items;
+  int rows, chunks, part_floats;
+};
+inline int64_t pad256(int64_t b) { return (b + 255) / 256 * 256; }
+
+inline Split split_of(const AttnArgs& a, int rows, int per_sm) {
+  Split s{};
+  s.rows = rows;
+  s.chunks = (a.T * a.rep + rows - 1) / rows;
+  s.items = (int64_t)a.B * a.hk * s.chunks;
+  s.blocks = a.sms * per_sm;
+  // no more blocks than the table has tiles for
+  const int64_t tiles = ((((int64_t)a.t.max_pages << a.t.shift) + kTile - 1) / kTile + 1);
+  const int64_t most = s.items * ((tiles + kMinShare - 1) / kMinShare);
+  if (most < s.blocks) s.blocks = most;
+  s.part_floats = rows * (a.d + 2);
+  return s;
+}
+inline size_t split_bytes(const Split& s) {
+  return kWsHeader + pad256(4 * s.blocks) + pad256(8) + pad256(8 * s.items) +
+         pad256(s.blocks * 2 * s.part_floats * (int64_t)sizeof(float));
+}
+inline void split_place(Split& s, void* ws) {
+  char* p = static_cast<char*>(ws);
+  s.status = reinterpret_cast<unsigned int*>(p);
+  p += kWsHeader;
+  s.verdict = reinterpret_cast<unsigned int*>(p);
+  p += pad256(4 * s.blocks);
+  s.share = reinterpret_cast<int64_t*>(p);
+  p += pad256(8);
+  s.first = reinterpret_cast<int64_t*>(p);
+  p += pad256(8 * s.items);
+  s.part = reinterpret_cast<float*>(p);
+}
+
+// The places of sequence n that any of its tokens sees: [lo, hi), lo rounded down to a tile.
+struct Keys {
+  int64_t lo, hi;
+  int64_t tiles;  // at least 1, so that an empty item has a block that writes its zeros
+};
+__device__ __forceinline__ Keys keys_of(const AttnArgs& a, int n) {
+  const int64_t cap = (int64_t)a.t.max_pages << a.t.shift, len = a.t.lens[n];
+  Keys k;
+  k.hi = len < 0 ? 0 : len < cap ? len : cap;
+  k.lo = 0;
+  if (a.window > 0) {
+    k.lo = len - a.T + 1 - a.window;
+    k.lo = k.lo < 0 ? 0 : k.lo > k.hi ? k.hi : k.lo;
+    k.lo -= k.lo % kTile;
+  }
+  k.tiles = (k.hi - k.lo + kTile - 1) / kTile;
+  if (k.tiles < 1) k.tiles = 1;
+  return k;
+}
+
+// Where a block starts: item (n, j) with j = head and chunk, tile t of it; its tiles.
+struct Start {
+  int64_t at, end;  // positions [at, end)
+  int64_t before;   // tiles of one (head, chunk) of the sequences before n
+  int n;
+};
+// All threads of the block take part (NT of them); `scratch` holds 34 values.
+template <int NT>
+__device__ __forceinline__ bool find_start(const AttnArgs& a, const Split& s, int64_t* scratch, Start& out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.B + NT - 1) / NT, n0 = min(tid * per, a.B), n1 = min(n0 + per, a.B);
+  const int64_t each = (int64_t)a.hk * s.chunks;
+  int64_t mine = 0;
+  for (int n = n0; n < n1; ++n) mine += keys_of(a, n).tiles;
+  int64_t up = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += v;
+  }
+  if (lane == 31) scratch[warp] = up;
+  __syncthreads();
+  int64_t total = 0, before = up - mine;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  int64_t share = (total * each + s.blocks - 1) / s.blocks;
+  if (share < kMinShare) share = kMinShare;
+  if (blockIdx.x == 0 && tid == 0) *s.share = share;
+  out.at = blockIdx.x * share;
+  out.end = min(out.at + share, total * each);
+  if (out.at >= out.end) return false;
+  if (before * each <= out.at && out.at < (before + mine) * each) {
+    int n = n0;
+    for (;; ++n) {
+      const int64_t t = keys_of(a, n).tiles;
+      if (out.at < (before + t) * each) break;
+      before += t;
+    }
+    scratch[32] = before;
+    scratch[33] = n;
+  }
+  __syncthreads();
+  out.before = scratch[32];
+  out.n = (int)scratch[33];
+  return true;
+}
+
+// one part of an item: where it begins in the workspace, [rows] maxima, [rows] sums, [rows][d]
+__device__ __forceinline__ float* part_of(const Split& s, int64_t block, int slot) {
+  return s.part + (block * 2 + slot) * s.part_floats;
+}
+
+cudaError_t launch_attn_join(const AttnArgs& a, const Split& s);
+
+// bf16 caches and codes on the tensor cores; the others (and everything off its alignment) here
+Split attn_general_split(const AttnArgs& a);
+cudaError_t launch_attn_general(const AttnArgs& a);
+
+}  // namespace attn
+}  // namespace kda

@@ -1,0 +1,233 @@
+// The paged key-value cache: rows written as given or as 8-bit codes with a power of two per
+// row, and read back.
+//
+// Codes.  The row's power 2^e is the smallest with max |x| <= top 2^e (top = 448 or 127), read
+// off the exponent and mantissa of the largest magnitude; x 2^-e is exact, so that one rounding
+// (to nearest, ties to even) gives the code.  Magnitudes are compared as integers, which puts
+// NaN above infinity above every number: a row with either is told by its maximum.
+//
+// Both directions move each value once and are bound by memory traffic.  A block takes the rows
+// (heads, keys and values) of a few consecutive tokens: their places are looked up once, then
+// d / 8 lanes move a row, 8 channels each.
+#include "kda_attn.cuh"
+
+namespace kda {
+namespace attn {
+namespace {
+
+using namespace layer;
+
+constexpr int kThreads = 256, kMaxTile = 16;
+
+// Places of the tile's tokens: the page and the row in it, page -1 for a token without a place
+// and -2 for one of no sequence (behind the last).
+__device__ __forceinline__ void find_places(const CacheArgs& a, int64_t t0, int tile, int2* place) {
+  const int i = threadIdx.x;
+  if (i < tile) {
+    int2 r = make_int2(-2, 0);
+    const int64_t t = t0 + i;
+    if (t < a.q.total) {
+      const int n = a.q.find(t);
+      int64_t start, end;
+      a.q.range(n, start, end);
+      if (t >= start && t < end) {
+        const int64_t pos = (int64_t)a.t.lens[n] - (end - t);
+        r.x = -1;
+        if (pos >= 0) {
+          r.x = page_of(a.t, n, pos);
+          r.y = (int)(pos & ((1 << a.t.shift) - 1));
+          if (r.x < 0) latch_status(a.status, KDA_ERR_INVALID_ARG);
+        }
+      }
+    }
+    place[i] = r;
+  }
+  // one block looks over the offsets
+  if (blockIdx.x == 0 && a.status && a.q.cu)
+    for (int n = threadIdx.x; n <= a.q.N; n += blockDim.x) {
+      const int64_t v = a.q.cu[n];
+      if ((n == 0 && v != 0) || (n == a.q.N && v != a.q.total) || (n > 0 && v < a.q.cu[n - 1]))
+        latch_status(a.status, KDA_ERR_BAD_SEQLENS);
+    }
+  __syncthreads();
+}
+
+// 8 values as a cache row's codes, rounded to nearest, ties to even
+template <int CACHE>
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+  uint32_t b[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = x[2 * i] * inv, hi = x[2 * i + 1] * inv;
+    uint32_t two;
+    if constexpr (CACHE == KDA_CACHE_E4M3) {
+      uint16_t h;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
+      two = h;
+    } else {
+      two = (uint32_t)(__float2int_rn(lo) & 0xff) | (uint32_t)(__float2int_rn(hi) & 0xff) << 8;
+    }
+    b[i / 2] |= two << (16 * (i & 1));
+  }
+  return make_uint2(b[0], b[1]);
+}
+template <int CACHE>
+__device__ __forceinline__ void decode8(uint2 v, float scale, float (&x)[8]) {
+  const uint32_t b[2] = {v.x, v.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint16_t h = (uint16_t)(b[i / 2] >> (16 * (i & 1)));
+    if constexpr (CACHE == KDA_CACHE_E4M3) {
+      uint32_t f;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(h));
+      const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&f));
+      x[2 * i] = g.x * scale;
+      x[2 * i + 1] = g.y * scale;
+    } else {
+      x[2 * i] = (float)(int8_t)(h & 0xff) * scale;
+      x[2 * i + 1] = (float)(int8_t)(h >> 8) * scale;
+    }
+  }
+}
+
+template <typename T, bool kWide>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  if constexpr (kWide) {
+    load<8>(p, x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = to_f32(p[e]);
+  }
+}
+template <typename T, bool kWide>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  if constexpr (kWide) {
+    store<8>(p, x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = from_f32<T>(x[e]);
+  }
+}
+
+template <typename T, int CACHE, int D, bool kWide>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a, int tile) {
+  constexpr int L = D / 8;  // lanes of a row
+  constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
+  __shared__ int2 place[kMaxTile];
+  const int64_t t0 = (int64_t)blockIdx.x * tile;
+  find_places(a, t0, tile, place);
+  const int lane = threadIdx.x % L, rows = tile * a.heads * 2;
+  for (int base = 0; base < rows; base += kThreads / L) {
+    const int r = base + threadIdx.x / L;
+    const int kv = r / (tile * a.heads), i = (r / a.heads) % tile, h = r % a.heads;
+    const int2 at = r < rows ? place[i] : make_int2(-2, 0);
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    if (at.x >= 0) {
+      const T* src = static_cast<const T*>(kv ? a.v : a.k) + (t0 + i) * (kv ? a.ldv : a.ldk) + h * D;
+      load8<T, kWide>(src + lane * 8, x);
+    }
+    const int64_t row = ((int64_t)h << a.t.shift) + at.y;
+    const int64_t to = at.x * a.ldpage + row * D + lane * 8;
+    void* pool = kv ? a.vc : a.kc;
+    if constexpr (!kCoded) {
+      if (at.x < 0) continue;
+      if constexpr (CACHE == KDA_CACHE_F32) store<8>(static_cast<float*>(pool) + to, x);
+      else store<8>(static_cast<__nv_bfloat16*>(pool) + to, x);
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (at.x < 0) continue;
+      // 448 = 1.75 2^8, 127 = 1.984375 2^6
+      constexpr uint32_t top = CACHE == KDA_CACHE_E4M3 ? 0x600000u : 0x7e0000u;
+      int e = (int)(m >> 23) - 127 - (CACHE == KDA_CACHE_E4M3 ? 8 : 6) + ((m & 0x7fffffu) > top);
+      e = max(e, -126);
+      const bool finite = m < 0x7f800000u;
+      uint2 code = encode8<CACHE>(x, __uint_as_float((uint32_t)(127 - e) << 23));
+      if (!finite) code = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + to) = code;
+      if (lane == 0)
+        (kv ? a.vs : a.ks)[(((int64_t)at.x * a.heads) << a.t.shift) + row] = finite ? (uint8_t)(e + 127) : 255;
+    }
+  }
+}
+
+template <typename T, int CACHE, int D, bool kWide>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs a, int tile) {
+  constexpr int L = D / 8;
+  constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
+  __shared__ int2 place[kMaxTile];
+  const int64_t t0 = (int64_t)blockIdx.x * tile;
+  find_places(a, t0, tile, place);
+  const int lane = threadIdx.x % L, rows = tile * a.heads * 2;
+  for (int base = 0; base < rows; base += kThreads / L) {
+    const int r = base + threadIdx.x / L;
+    const int kv = r / (tile * a.heads), i = (r / a.heads) % tile, h = r % a.heads;
+    const int2 at = r < rows ? place[i] : make_int2(-2, 0);
+    T* out = static_cast<T*>(kv ? a.vo : a.ko);
+    if (at.x == -2 || !out) continue;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    if (at.x >= 0) {
+      const int64_t row = ((int64_t)h << a.t.shift) + at.y;
+      const int64_t from = at.x * a.ldpage + row * D + lane * 8;
+      const void* pool = kv ? a.vc : a.kc;
+      if constexpr (CACHE == KDA_CACHE_F32) {
+        load<8>(static_cast<const float*>(pool) + from, x);
+      } else if constexpr (CACHE == KDA_CACHE_BF16) {
+        load<8>(static_cast<const __nv_bfloat16*>(pool) + from, x);
+      } else {
+        const float s = power((kv ? a.vs : a.ks)[(((int64_t)at.x * a.heads) << a.t.shift) + row]);
+        decode8<CACHE>(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) + from), s, x);
+      }
+    }
+    store8<T, kWide>(out + ((t0 + i) * a.heads + h) * D + lane * 8, x);
+  }
+}
+
+template <typename T, int CACHE, int D, bool kWide>
+void launch(const CacheArgs& a, bool write) {
+  // few tokens: fewer of them per block, so that the device is filled
+  int tile = kMaxTile;
+  while (tile > 1 && a.q.total < 2 * tile * a.sms) tile /= 2;
+  const unsigned grid = (unsigned)((a.q.total + tile - 1) / tile);
+  if (write) cache_write_kernel<T, CACHE, D, kWide><<<grid, kThreads, 0, a.stream>>>(a, tile);
+  else cache_read_kernel<T, CACHE, D, kWide><<<grid, kThreads, 0, a.stream>>>(a, tile);
+}
+template <typename T, int CACHE>
+void by_size(const CacheArgs& a, bool write, bool wide) {
+  if (a.d == 128) wide ? launch<T, CACHE, 128, true>(a, write) : launch<T, CACHE, 128, false>(a, write);
+  else wide ? launch<T, CACHE, 64, true>(a, write) : launch<T, CACHE, 64, false>(a, write);
+}
+template <typename T>
+void by_cache(const CacheArgs& a, bool write, bool wide) {
+  switch (a.cache) {
+    case KDA_CACHE_F32: return by_size<T, KDA_CACHE_F32>(a, write, wide);
+    case KDA_CACHE_BF16: return by_size<T, KDA_CACHE_BF16>(a, write, wide);
+    case KDA_CACHE_E4M3: return by_size<T, KDA_CACHE_E4M3>(a, write, wide);
+    default: return by_size<T, KDA_CACHE_INT8>(a, write, wide);
+  }
+}
+cudaError_t run(const CacheArgs& a, bool write, bool wide) {
+  if (a.q.total == 0) return cudaSuccess;
+  if (a.bf16) by_cache<__nv_bfloat16>(a, write, wide);
+  else by_cache<float>(a, write, wide);
+  return cudaGetLastError();
+}
+bool al16(const void* p) { return (uintptr_t)p % 16 == 0; }
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheArgs& a) {
+  const int64_t v = a.bf16 ? 8 : 4;
+  return run(a, true, al16(a.k) && al16(a.v) && a.ldk % v == 0 && a.ldv % v == 0);
+}
+cudaError_t launch_cache_read(const CacheArgs& a) { return run(a, false, al16(a.ko) && al16(a.vo)); }
+
+}  // namespace attn
+}  // namespace kda
