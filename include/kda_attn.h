@@ -107,8 +107,8 @@ typedef struct {
  * left out; a place past the table or a page that is not in the pool is left
  * out and reported (KDA_ERR_INVALID_ARG), malformed cu_seqlens are reported
  * (KDA_ERR_BAD_SEQLENS); every access stays inside the buffers.  Two tokens of
- * one call that meet in one row leave either's.  k_cache and v_cache are
- * 16-byte aligned; k_scale and v_scale are given exactly with 8-bit caches.
+ * one call that meet in one row leave either's.  k_cache, v_cache, k_scale and
+ * v_scale are 16-byte aligned; the scales are given exactly with 8-bit caches.
  * workspace: optional, >= 256 bytes, 256-byte aligned. */
 kda_status kda_cache_write(const kda_cache_shape* s, const void* k, const void* v,
                            const int32_t* cu_seqlens, const int32_t* pages, const int32_t* lens,

@@ -1,5 +1,5 @@
-// Attention of new tokens over the paged cache: any types, float32 arithmetic on the CUDA cores,
-// and the join of the parts.
+// Attention of new tokens over the paged cache, float32 queries: float32 arithmetic on the CUDA
+// cores; and the join of the parts.
 //
 // One pass over the keys with the running maximum and sum: a tile of 64 places is brought to
 // shared memory as float32, each thread forms the scores of one place with 8 query rows, a warp
@@ -20,11 +20,6 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <typename TC> __device__ __forceinline__ void load4(const TC* p, float (&x)[4]);
 template <> __device__ __forceinline__ void load4(const float* p, float (&x)[4]) { load<4>(p, x); }
-template <> __device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  unpack2(u.x, x[0], x[1]);
-  unpack2(u.y, x[2], x[3]);
-}
 struct E4M3 { uint8_t v; };
 struct Int8 { int8_t v; };
 template <> __device__ __forceinline__ void load4(const E4M3* p, float (&x)[4]) {
@@ -55,7 +50,7 @@ template <int D> struct Shared {
   int bad;
 };
 
-template <typename T, typename TC, int D>
+template <typename TC, int D>
 __global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a, Split s) {
   constexpr bool kCoded = sizeof(TC) == 1;
   constexpr int kGroups = kThreads / D;       // threads of a channel
@@ -87,8 +82,8 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a, Split s) {
       const int r = i / D, c = i % D, row = row0 + r;
       float x = 0.f;
       if (r < rows) {
-        const T* q = static_cast<const T*>(a.q) + ((int64_t)n * a.T + row / a.rep) * a.ldq;
-        x = to_f32(q[(int64_t)(head * a.rep + row % a.rep) * D + c]) * a.scale * kLog2e;
+        const float* q = static_cast<const float*>(a.q) + ((int64_t)n * a.T + row / a.rep) * a.ldq;
+        x = q[(int64_t)(head * a.rep + row % a.rep) * D + c] * a.scale * kLog2e;
       }
       sh.q[r][c] = x;
     }
@@ -204,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a, Split s) {
         if (r0 + r >= rows) break;
         const int64_t o = ((int64_t)n * a.T + row / a.rep) * a.hq + head * a.rep + row % a.rep;
         const float l = sh.l[r0 + r];
-        static_cast<T*>(a.out)[o * D + c] = from_f32<T>(l == 0.f ? 0.f : acc[r] / l);
+        static_cast<float*>(a.out)[o * D + c] = l == 0.f ? 0.f : acc[r] / l;
         if (c == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (sh.m[r0 + r] + log2f(l)) * kLn2;
       }
     } else {
@@ -264,20 +259,20 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, Split s) {
   }
 }
 
-template <typename T, typename TC, int D>
+template <typename TC, int D>
 cudaError_t launch(const AttnArgs& a, const Split& s) {
   constexpr int bytes = sizeof(Shared<D>);
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, TC, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = cudaFuncSetAttribute(attn_kernel<TC, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  attn_kernel<T, TC, D><<<(unsigned)s.blocks, kThreads, bytes, a.stream>>>(a, s);
+  attn_kernel<TC, D><<<(unsigned)s.blocks, kThreads, bytes, a.stream>>>(a, s);
   return cudaGetLastError();
 }
-template <typename T, int D>
+template <int D>
 cudaError_t by_cache(const AttnArgs& a, const Split& s) {
   switch (a.cache) {
-    case KDA_CACHE_E4M3: return launch<T, E4M3, D>(a, s);
-    case KDA_CACHE_INT8: return launch<T, Int8, D>(a, s);
-    default: return launch<T, T, D>(a, s);  // the cache is of q's type
+    case KDA_CACHE_E4M3: return launch<E4M3, D>(a, s);
+    case KDA_CACHE_INT8: return launch<Int8, D>(a, s);
+    default: return launch<float, D>(a, s);
   }
 }
 
@@ -301,17 +296,17 @@ cudaError_t launch_attn_join(const AttnArgs& a, const Split& s) {
 cudaError_t launch_attn_general(const AttnArgs& a) {
   Split s = attn_general_split(a);
   split_place(s, a.ws);
-  using bf = __nv_bfloat16;
-  cudaError_t e = a.d == 128 ? (a.bf16 ? by_cache<bf, 128>(a, s) : by_cache<float, 128>(a, s))
-                             : (a.bf16 ? by_cache<bf, 64>(a, s) : by_cache<float, 64>(a, s));
+  cudaError_t e = a.d == 128 ? by_cache<128>(a, s) : by_cache<64>(a, s);
   return e != cudaSuccess ? e : launch_attn_join(a, s);
 }
 
-size_t attn_workspace(const AttnArgs& a) { return split_bytes(attn_general_split(a)); }
+size_t attn_workspace(const AttnArgs& a) {
+  return split_bytes(a.bf16 ? attn_mma_split(a) : attn_general_split(a));
+}
 
 cudaError_t launch_attn(const AttnArgs& a) {
   if (a.B == 0) return cudaMemsetAsync(a.ws, 0, 4, a.stream);
-  return launch_attn_general(a);
+  return a.bf16 ? launch_attn_mma(a) : launch_attn_general(a);
 }
 
 }  // namespace attn

@@ -200,7 +200,7 @@ kda_status kda_cache_write(const kda_cache_shape* s, const void* k, const void* 
     return KDA_ERR_INVALID_ARG;
   if (!all_aligned({k, v}, dsize(s->dtype)) ||
       !all_aligned({(const void*)cu_seqlens, (const void*)pages, (const void*)lens}, 4) ||
-      !all_aligned({(const void*)k_cache, (const void*)v_cache}, 16))
+      !all_aligned({(const void*)k_cache, (const void*)v_cache, (const void*)k_scale, (const void*)v_scale}, 16))
     return KDA_ERR_INVALID_ARG;
   if ((st = check_status_ws(workspace, workspace_bytes)) != KDA_OK) return st;
   a.k = k; a.v = v;
@@ -227,7 +227,7 @@ kda_status kda_cache_read(const kda_cache_shape* s, const int32_t* cu_seqlens,
     return KDA_ERR_INVALID_ARG;
   if (!all_aligned({(const void*)k, (const void*)v}, dsize(s->dtype)) ||
       !all_aligned({(const void*)cu_seqlens, (const void*)pages, (const void*)lens}, 4) ||
-      !all_aligned({k_cache, v_cache}, 16))
+      !all_aligned({k_cache, v_cache, (const void*)k_scale, (const void*)v_scale}, 16))
     return KDA_ERR_INVALID_ARG;
   if ((st = check_status_ws(workspace, workspace_bytes)) != KDA_OK) return st;
   a.ko = k; a.vo = v;
@@ -258,7 +258,7 @@ kda_status kda_attn_step(const kda_attn_shape* s, const void* q, const void* k_c
     return KDA_ERR_INVALID_ARG;
   if (!all_aligned({q, (const void*)out}, dsize(s->dtype)) ||
       !all_aligned({(const void*)pages, (const void*)lens, (const void*)lse}, 4) ||
-      !all_aligned({k_cache, v_cache}, 16))
+      !all_aligned({k_cache, v_cache, (const void*)k_scale, (const void*)v_scale}, 16))
     return KDA_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < attn_workspace(a))
     return KDA_ERR_WORKSPACE;

@@ -17,7 +17,6 @@ namespace attn {
 
 constexpr int kTile = 64;          // places of a tile
 constexpr int64_t kMinShare = 4;   // tiles of a block, where there are as many
-constexpr int kRowsMax = 16;
 
 struct Split {
   unsigned int* status;   // workspace header
@@ -137,9 +136,11 @@ __device__ __forceinline__ float* part_of(const Split& s, int64_t block, int slo
 
 cudaError_t launch_attn_join(const AttnArgs& a, const Split& s);
 
-// bf16 caches and codes on the tensor cores; the others (and everything off its alignment) here
+// float32 queries; bf16 queries (on the tensor cores)
 Split attn_general_split(const AttnArgs& a);
 cudaError_t launch_attn_general(const AttnArgs& a);
+Split attn_mma_split(const AttnArgs& a);
+cudaError_t launch_attn_mma(const AttnArgs& a);
 
 }  // namespace attn
 }  // namespace kda

@@ -97,6 +97,7 @@ def test_attn_arguments(lib):
         assert go(shape(), **{f"p{i}": None}) == bad, i
     assert go(shape(cache=1)) == bad  # scales of a bf16 cache
     assert go(shape(), p0=FAKE + 1) == bad and go(shape(), p1=FAKE + 8) == bad and go(shape(), p8=FAKE + 2) == bad
+    assert go(shape(), p3=FAKE + 8) == bad and go(shape(), p4=FAKE + 1) == bad  # scales: 16 bytes
     size = L.kda_attn_workspace_size(shape())
     assert size >= 256
     assert go(shape(), ws=None) == wsp and go(shape(), ws=FAKE + 32) == wsp and go(shape(), size=size - 1) == wsp
