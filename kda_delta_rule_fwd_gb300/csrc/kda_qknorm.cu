@@ -13,14 +13,28 @@ namespace kda {
 namespace attn {
 namespace {
 
-using namespace layer;
+using layer::Raw;
+using layer::dot_v;
+using layer::fetch;
+using layer::fma_v;
+using layer::mul_v;
+using layer::open;
+using layer::store;
 
-__device__ __forceinline__ unsigned long long turn_of(double freq) {
-  const double t = freq * 0.15915494309189533577;  // turns per position
-  return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+using u64 = unsigned long long;
+
+// freq / 2 pi in 64-bit fixed point, modulo 1: the mantissa times 2^66 / 2 pi in 128 bits, moved by
+// the exponent (whole numbers: 64 float64 operations of every thread would take 10 us).
+__device__ __forceinline__ u64 turn_of(double freq) {
+  const u64 bits = (u64)__double_as_longlong(freq), m = (bits & 0xfffffffffffffull) | 1ull << 52;
+  const int s = 54 + 1023 - (int)(bits >> 52 & 0x7ff);
+  constexpr u64 c = 0xa2f9836e4e441529ull;
+  const u64 hi = __umul64hi(m, c), lo = m * c;
+  const u64 t = s <= 0 ? lo : s < 64 ? hi << (64 - s) | lo >> s : s < 128 ? hi >> (s - 64) : 0;
+  return bits >> 63 ? 0 - t : t;
 }
-__device__ __forceinline__ float2 angle(unsigned long long turn, int pos) {  // (cos, sin)
-  const unsigned long long f = turn * (unsigned long long)(long long)pos;
+__device__ __forceinline__ float2 angle(u64 turn, int pos) {  // (cos, sin)
+  const u64 f = turn * (u64)(long long)pos;
   float2 r;
   sincospif((float)(int)(f >> 32) * 4.656612873077392578125e-10f, &r.y, &r.x);  // half turns
   return r;
@@ -50,7 +64,7 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) qknorm_narrow_kernel(QKArgs
   const int64_t rows = a.tokens * p.heads, step = (int64_t)p.ctas * kNarrowWarps;
   const int pairs = a.d / 2, half = a.rot / 2;
   int2 at[kPairs];
-  unsigned long long turn[kPairs];
+  u64 turn[kPairs];
   float2 w[kPairs], dw[kPairs];
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
@@ -127,6 +141,176 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) qknorm_narrow_kernel(QKArgs
   }
 }
 
+// Aligned rows: TPR threads hold a row in two chunks of 16 bytes each, chosen so that both members
+// of a pair are in one thread (chunk c and c + rot / 2 of halves, adjacent channels of one chunk),
+// and nothing but the row's sum leaves a thread.  A group of TPR threads takes a token's heads (or
+// `per` of them, where tokens are few): the angles are made once for them.  Blocks are persistent
+// and request the next row before they work on the present one; a block serves q or k, in
+// proportion to their heads, so that its weights and its sums for their gradient stay in registers.
+constexpr int kWide = 256;  // threads of a block
+template <bool kBwd> constexpr int wide_blocks() { return kBwd ? 2 : 3; }
+
+template <typename T, int TPR, bool kInter, bool kBwd>
+__global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel(QKArgs a, int2 per_of) {
+  constexpr int VEC = 16 / sizeof(T), kGroups = kWide / TPR;
+  __shared__ u64 turns[128];
+  const bool second = (int)blockIdx.x >= a.p[0].ctas;
+  const QKPart& p = a.p[second];
+  const int block = blockIdx.x - (second ? a.p[0].ctas : 0);
+  const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+  const int chunks = a.d / VEC, half = a.rot / 2, per = second ? per_of.y : per_of.x;
+  for (int j = threadIdx.x; j < half; j += kWide) turns[j] = turn_of(a.freqs[j]);
+  __syncthreads();
+  // the thread's chunks: channels at[0] .. and at[1] .., -1 behind the row's end; its first pairs
+  int at[2];
+  bool turned = true;  // halves: whether the chunks are each other's partners
+  if (kInter) {
+    const int width = (chunks + 1) / 2;
+    at[0] = lane < width ? lane * VEC : -1;
+    at[1] = lane < width && lane + width < chunks ? (lane + width) * VEC : -1;
+  } else {
+    const int both = half / VEC, i = lane - both;
+    turned = i < 0;
+    const int c = turned ? lane : 2 * both + 2 * i;
+    at[0] = c < chunks ? c * VEC : -1;
+    at[1] = turned ? (lane + both) * VEC : c + 1 < chunks ? (c + 1) * VEC : -1;
+  }
+  float w[2][VEC], sum[2][VEC];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      w[i][e] = p.w && at[i] >= 0 ? p.w[at[i] + e] : 1.f;
+      sum[i][e] = 0.f;
+    }
+  // items (token, heads [c per, c per + per)) of this group; all groups of a warp run as often as
+  // its first
+  const int parts = (p.heads + per - 1) / per;
+  const int64_t items = a.tokens * parts, step = (int64_t)p.ctas * kGroups;
+  int64_t item = (int64_t)block * kGroups + group;
+  int64_t first = (int64_t)block * kGroups + threadIdx.x / 32 * (32 / TPR);
+  Raw<T, VEC> x[2], dy[2];
+  const auto fetch_row = [&](int64_t it, int h) {
+    const int64_t tok = it / parts;
+    const int head = (int)(it - tok * parts) * per + h;
+    const bool on = it < items && head < p.heads;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[i] = Raw<T, VEC>{};
+      if (kBwd) dy[i] = Raw<T, VEC>{};
+      if (on && at[i] >= 0) {
+        x[i] = fetch<T, VEC>(static_cast<const T*>(p.x) + tok * p.ld + head * a.d + at[i]);
+        if (kBwd) dy[i] = fetch<T, VEC>(static_cast<const T*>(p.dy) + (tok * p.heads + head) * a.d + at[i]);
+      }
+    }
+    return on;
+  };
+  bool on = fetch_row(item, 0);
+  int pos = half && item < items ? a.pos[item / parts] : 0;
+  for (; first < items; first += step, item += step) {
+    float cs[VEC], sn[VEC];  // halves: of the thread's pairs; adjacent: of the two chunks' pairs in a row
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const int c = e < VEC / 2 ? at[0] + 2 * e : at[1] + 2 * e - VEC;
+      const int j = kInter ? c >> 1 : at[0] + e;
+      const bool turn = kInter ? (e < VEC / 2 ? at[0] : at[1]) >= 0 && j < half : turned && j < half;
+      const float2 r = turn ? angle(turns[j], pos) : make_float2(1.f, 0.f);
+      cs[e] = r.x;
+      sn[e] = r.y;
+    }
+    if (half && item + step < items) pos = a.pos[(item + step) / parts];
+    const int64_t tok = item / parts;
+    const int head0 = (int)(item - tok * parts) * per;
+    for (int h = 0; h < per; ++h) {
+      float v[2][VEC], g[2][VEC];
+      const bool here = on;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        open<T, VEC>(x[i], v[i]);
+        if (kBwd) open<T, VEC>(dy[i], g[i]);
+      }
+      on = h + 1 < per ? fetch_row(item, h + 1) : fetch_row(item + step, 0);
+      float k = 1.f;
+      if (p.w) {
+        float2 ss = make_float2(0.f, 0.f);
+        dot_v(v[0], v[0], ss);
+        dot_v(v[1], v[1], ss);
+        float s = ss.x + ss.y;
+#pragma unroll
+        for (int o = TPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        k = here ? rsqrtf(fmaf(s, a.inv_d, a.eps)) : 0.f;
+        mul_v(v[0], k);
+        mul_v(v[1], k);
+      }
+      // (a, b) -> (a cos - b sin, a sin + b cos); back with the other sine
+      const auto turn_pairs = [&](float (&y)[2][VEC], float sign) {
+        if constexpr (kInter) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC / 2; ++e) {
+              const float c = cs[i * (VEC / 2) + e], d = sign * sn[i * (VEC / 2) + e];
+              const float u = y[i][2 * e], t = y[i][2 * e + 1];
+              y[i][2 * e] = u * c - t * d;
+              y[i][2 * e + 1] = u * d + t * c;
+            }
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float d = sign * sn[e], u = y[0][e], t = y[1][e];
+            y[0][e] = u * cs[e] - t * d;
+            y[1][e] = u * d + t * cs[e];
+          }
+        }
+      };
+      if constexpr (!kBwd) {
+        mul_v(v[0], w[0]);
+        mul_v(v[1], w[1]);
+        turn_pairs(v, 1.f);
+      } else {
+        turn_pairs(g, -1.f);
+        fma_v(g[0], v[0], sum[0]);
+        fma_v(g[1], v[1], sum[1]);
+        if (p.w) {
+          mul_v(g[0], w[0]);
+          mul_v(g[1], w[1]);
+          float2 pn = make_float2(0.f, 0.f);
+          dot_v(g[0], v[0], pn);
+          dot_v(g[1], v[1], pn);
+          float s = pn.x + pn.y;
+#pragma unroll
+          for (int o = TPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          const float mean = -s * a.inv_d;
+          fma_v(v[0], mean, g[0]);
+          fma_v(v[1], mean, g[1]);
+          mul_v(g[0], k);
+          mul_v(g[1], k);
+        }
+      }
+      if (here) {
+        T* y = static_cast<T*>(kBwd ? p.dx : p.y) + (tok * p.heads + head0 + h) * a.d;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (at[i] >= 0) store<VEC>(y + at[i], kBwd ? g[i] : v[i]);
+      }
+    }
+  }
+  if (!kBwd || !p.dw) return;
+  __shared__ float fold[kBwd ? kGroups * 2 * TPR * VEC : 1];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (at[i] >= 0) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) fold[group * a.d + at[i] + e] = sum[i][e];
+    }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.d; c += kWide) {
+    float s = 0.f;
+    for (int q = 0; q < kGroups; ++q) s += fold[q * a.d + c];
+    p.part[(int64_t)block * a.d + c] = s;
+  }
+}
+
 // The weights' gradients: 32 columns per block, whose warps take every 32nd block's sums.
 __global__ void __launch_bounds__(1024) qknorm_reduce_kernel(QKArgs a) {
   __shared__ float fold[32][33];
@@ -146,9 +330,66 @@ __global__ void __launch_bounds__(1024) qknorm_reduce_kernel(QKArgs a) {
   }
 }
 
-constexpr int kPerSm = 4;  // blocks of a part
+constexpr int kPerSm = 4;  // blocks of a part, at most
+
+bool al16(const void* p) { return (uintptr_t)p % 16 == 0; }
+// whole 16-byte chunks everywhere, and no chunk that is rotated in part
+bool wide_ok(const QKArgs& a) {
+  const int v = a.bf16 ? 8 : 4;
+  bool ok = a.d % v == 0 && (a.interleaved || a.rot / 2 % v == 0);
+  for (const QKPart& p : a.p)
+    ok = ok && (p.heads == 0 || (p.ld % v == 0 && al16(p.x) && al16(p.dy) && al16(p.y) && al16(p.dx)));
+  return ok;
+}
+
+template <typename T, int TPR, bool kInter, bool kBwd>
+void launch_wide(QKArgs& a) {
+  constexpr int kGroups = kWide / TPR;
+  const int64_t most = a.sms * wide_blocks<kBwd>();
+  const int heads = a.p[0].heads + a.p[1].heads;
+  int per[2] = {1, 1};
+  for (int i = 0; i < 2; ++i) {
+    QKPart& p = a.p[i];
+    p.ctas = 0;
+    if (p.heads == 0) continue;
+    int64_t share = most * p.heads / heads;
+    if (i == 1) share = most - a.p[0].ctas < share + 1 ? share : share + 1;
+    if (share < 1) share = 1;
+    // a token's heads in as few items as still give every group one
+    const int64_t rows = a.tokens * p.heads, each = rows / (share * kGroups);
+    per[i] = (int)(each < 1 ? 1 : each < p.heads ? each : p.heads);
+    const int64_t items = a.tokens * ((p.heads + per[i] - 1) / per[i]);
+    const int64_t need = (items + kGroups - 1) / kGroups;
+    const int64_t limit = qknorm_bwd_ctas(a.tokens, p.heads, a.sms);
+    p.ctas = (int)(need < share ? need : share);
+    if (p.ctas > limit) p.ctas = (int)limit;
+  }
+  const int grid = a.p[0].ctas + a.p[1].ctas;
+  if (grid == 0) return;
+  qknorm_wide_kernel<T, TPR, kInter, kBwd><<<grid, kWide, 0, a.stream>>>(a, make_int2(per[0], per[1]));
+}
+template <typename T, int TPR>
+void by_kind(QKArgs& a, bool bwd) {
+  if (a.interleaved) bwd ? launch_wide<T, TPR, true, true>(a) : launch_wide<T, TPR, true, false>(a);
+  else bwd ? launch_wide<T, TPR, false, true>(a) : launch_wide<T, TPR, false, false>(a);
+}
+template <typename T>
+void by_size(QKArgs& a, bool bwd) {
+  const int chunks = a.d * (int)sizeof(T) / 16;
+  // threads of a row: pairs of chunks, those left over behind the rotated ones two by two
+  const int lanes = (chunks + 1) / 2;
+  if (lanes <= 4) return by_kind<T, 4>(a, bwd);
+  if (lanes <= 8) return by_kind<T, 8>(a, bwd);
+  if (lanes <= 16) return by_kind<T, 16>(a, bwd);
+  by_kind<T, 32>(a, bwd);
+}
 
 cudaError_t run(QKArgs& a, bool bwd) {
+  using bf = __nv_bfloat16;
+  if (wide_ok(a)) {
+    a.bf16 ? by_size<bf>(a, bwd) : by_size<float>(a, bwd);
+    return cudaGetLastError();
+  }
   int most = 0;
   for (QKPart& p : a.p) {
     p.ctas = (int)qknorm_bwd_ctas(a.tokens, p.heads, a.sms);
@@ -156,7 +397,6 @@ cudaError_t run(QKArgs& a, bool bwd) {
   }
   if (most == 0) return cudaSuccess;
   const dim3 grid(most, a.p[1].heads > 0 ? 2 : 1), block(32 * kNarrowWarps);
-  using bf = __nv_bfloat16;
   if (bwd)
     a.bf16 ? qknorm_narrow_kernel<bf, true><<<grid, block, 0, a.stream>>>(a)
            : qknorm_narrow_kernel<float, true><<<grid, block, 0, a.stream>>>(a);
