@@ -3,35 +3,31 @@
 // Probabilities are whole multiples of 2^-44 in 64 bits, so their sums are exact in any order,
 // and with fewer than 2^19 of them below 2^63.  The token drawn is the first whose running sum
 // exceeds floor(m total / 2^24), m the 24 bits of the random number.
+//
+// One pass over the row (or the two rows) of the place where the token is drawn, bound by their
+// bytes: a cluster of blocks per sequence, each with a stretch of the vocabulary, keeps the sum of
+// every run of a warp's 16-byte loads in shared memory; the blocks' totals meet in the cluster, and
+// the block that holds the place reads that one run again.
+#include <cooperative_groups.h>
+
 #include "kda_attn.cuh"
 
 namespace kda {
 namespace attn {
 namespace {
 
-using namespace layer;
+namespace cg = cooperative_groups;
+using layer::Raw;
+using layer::fetch;
+using layer::open;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kRun = 128;  // kRun: tokens of a warp's turn
-constexpr int kRuns = (1 << 19) / kRun;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 using u64 = unsigned long long;
 
 __device__ __forceinline__ long long fixed(float p) {
   p = p > 0.f ? fminf(p, 1.f) : 0.f;  // NaN: 0
   return __float2ll_rn(p * 17592186044416.f);
 }
-
-// the weight of token i
-template <typename T>
-struct Weights {
-  const T *p, *q;  // rows; q may be null
-  int certain;     // the token that the draft was certain of, or -1
-  __device__ __forceinline__ u64 at(int i) const {
-    long long w = fixed(to_f32(p[i]));
-    if (q) w -= fixed(to_f32(q[i]));
-    if (i == certain) w -= 1ll << 44;
-    return w > 0 ? (u64)w : 0;
-  }
-};
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
@@ -49,12 +45,59 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {
   return v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
-  __shared__ u64 run[kRuns];
-  __shared__ u64 total_of[kWarps];
+// Weights of a lane's tokens in a run: VEC in a row (aligned rows), else lane, lane + 32, ...
+template <typename T, bool kWide>
+struct Weights {
+  static constexpr int VEC = 16 / sizeof(T), kRun = 32 * VEC;
+  const T *p, *q;  // rows; q may be null
+  int V, certain;  // certain: the token that the draft was sure of, or -1
+  struct Held { Raw<T, VEC> p, q; };
+  __device__ __forceinline__ int token(int r, int e) const {
+    const int lane = threadIdx.x & 31;
+    return r * kRun + (kWide ? lane * VEC + e : e * 32 + lane);
+  }
+  __device__ __forceinline__ void request(int r, Held& h) const {
+    T* hp = reinterpret_cast<T*>(&h.p);
+    T* hq = reinterpret_cast<T*>(&h.q);
+    if (kWide) {  // V is a multiple of VEC
+      const int i = token(r, 0);
+      h.p = h.q = Raw<T, VEC>{};
+      if (i < V) {
+        h.p = fetch<T, VEC>(p + i);
+        if (q) h.q = fetch<T, VEC>(q + i);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int i = token(r, e);
+        hp[e] = i < V ? p[i] : from_f32<T>(0.f);
+        hq[e] = q && i < V ? q[i] : from_f32<T>(0.f);
+      }
+    }
+  }
+  __device__ __forceinline__ void weigh(int r, const Held& h, u64 (&w)[VEC]) const {
+    float x[VEC], y[VEC];
+    open<T, VEC>(h.p, x);
+    open<T, VEC>(h.q, y);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      long long d = fixed(x[e]);
+      if (q) d -= fixed(y[e]);
+      if (token(r, e) == certain) d -= 1ll << 44;
+      w[e] = d > 0 ? (u64)d : 0;
+    }
+  }
+};
+
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyArgs a, int per) {
+  using W = Weights<T, kWide>;
+  extern __shared__ u64 run[];  // sums of this block's runs [0, per)
+  __shared__ u64 total_of[kWarps], total_here[2];
   __shared__ int kept_of, have_of;
-  const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), blocks = cluster.num_blocks();
+  const int b = blockIdx.x / blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* p = static_cast<const T*>(a.p) + (int64_t)b * (a.K + 1) * a.V;
   const T* q = a.q ? static_cast<const T*>(a.q) + (int64_t)b * a.K * a.V : nullptr;
   const int32_t* drafts = a.drafts + (int64_t)b * a.K;
@@ -79,88 +122,150 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
       }
     }
     const int kept = __ffs(~__ballot_sync(0xffffffffu, keep)) - 1;  // K < 32: a lane is 0
-    if (lane <= a.K) tokens[lane] = lane < kept ? d : -1;
+    if (rank == 0 && lane <= a.K) tokens[lane] = lane < kept ? d : -1;
     if (lane == 0) {
-      a.commit[b] = have < 0 ? 0 : kept + 1;
+      if (rank == 0) a.commit[b] = have < 0 ? 0 : kept + 1;
       kept_of = kept;
       have_of = have;
     }
   }
   __syncthreads();
   const int kept = kept_of, have = have_of;
-  if (have < 0) return;
-  Weights<T> w{p + (int64_t)kept * a.V, nullptr, -1};
+  if (have < 0) return;  // the whole cluster's
+  W w{p + (int64_t)kept * a.V, nullptr, a.V, -1};
   if (kept < have) {
     if (q) w.q = q + (int64_t)kept * a.V;
     else w.certain = drafts[kept];
   }
-  const int runs = (a.V + kRun - 1) / kRun;
+  const int first = rank * per, runs = min(per, (a.V + W::kRun - 1) / W::kRun - first);  // may be below 0
   const u64 m = (u64)(fminf(fmaxf(u[a.K], 0.f), 0.99999994f) * 16777216.f);
-  for (;;) {
+  for (int turn = 0;; ++turn) {
     u64 sum = 0;
-    for (int r = warp; r < runs; r += kWarps) {
-      u64 s = 0;
+    constexpr int kAhead = 4;  // runs in flight
+    for (int r = warp; r < runs; r += kWarps * kAhead) {
+      typename W::Held h[kAhead];
 #pragma unroll
-      for (int e = 0; e < kRun / 32; ++e) {
-        const int i = r * kRun + e * 32 + lane;
-        if (i < a.V) s += w.at(i);
+      for (int i = 0; i < kAhead; ++i)
+        if (r + i * kWarps < runs) w.request(first + r + i * kWarps, h[i]);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (r + i * kWarps >= runs) break;
+        u64 x[W::VEC], s = 0;
+        w.weigh(first + r + i * kWarps, h[i], x);
+#pragma unroll
+        for (int e = 0; e < W::VEC; ++e) s += x[e];
+        s = warp_sum(s);
+        if (lane == 0) run[r + i * kWarps] = s;
+        sum += s;
       }
-      s = warp_sum(s);
-      if (lane == 0) run[r] = s;
-      sum += s;
     }
     if (lane == 0) total_of[warp] = sum;
     __syncthreads();
-    u64 total = 0;
+    if (threadIdx.x == 0) {
+      u64 t = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) total += total_of[i];
-    if (total == 0 && (w.q || w.certain >= 0)) {  // nothing left of p - q: p itself
+      for (int i = 0; i < kWarps; ++i) t += total_of[i];
+      total_here[turn] = t;
+    }
+    cluster.sync();
+    u64 total = 0, before = 0, mine = 0;
+    for (int i = 0; i < blocks; ++i) {
+      const u64 t = *cluster.map_shared_rank(&total_here[turn], i);
+      if (i < rank) before += t;
+      if (i == rank) mine = t;
+      total += t;
+    }
+    if (total == 0 && turn == 0 && (w.q || w.certain >= 0)) {  // nothing left of p - q: p itself
       w.q = nullptr;
       w.certain = -1;
-      __syncthreads();
       continue;
     }
-    if (warp == 0) {
-      if (total == 0) {
-        if (lane == 0) latch_status(a.status, KDA_ERR_INVALID_ARG);
-        return;  // -1 stays
+    if (total == 0) {
+      if (rank == 0 && threadIdx.x == 0) latch_status(a.status, KDA_ERR_INVALID_ARG);
+      break;  // -1 stays
+    }
+    u64 left = m * (total >> 24) + ((m * (total & 0xffffffu)) >> 24);
+    if (warp != 0 || left < before || left >= before + mine) break;
+    left -= before;
+    int at = 0;
+    for (int base = 0; base < runs; base += 32) {
+      const u64 x = base + lane < runs ? run[base + lane] : 0;
+      const u64 up = warp_scan(x);
+      const unsigned past = __ballot_sync(0xffffffffu, up > left);
+      if (past) {
+        const int i = __ffs(past) - 1;
+        at = base + i;
+        left -= __shfl_sync(0xffffffffu, up - x, i);
+        break;
       }
-      u64 left = m * (total >> 24) + ((m * (total & 0xffffffu)) >> 24);
-      int at = 0;
-      for (int base = 0; base < runs; base += 32) {
-        const u64 mine = base + lane < runs ? run[base + lane] : 0;
-        const u64 up = warp_scan(mine);
+      left -= __shfl_sync(0xffffffffu, up, 31);
+    }
+    typename W::Held h;
+    u64 x[W::VEC];
+    w.request(first + at, h);
+    w.weigh(first + at, h, x);
+    if (kWide) {
+      u64 s = 0;
+#pragma unroll
+      for (int e = 0; e < W::VEC; ++e) s += x[e];
+      u64 up = warp_scan(s) - s;
+      int token = -1;
+#pragma unroll
+      for (int e = 0; e < W::VEC; ++e) {
+        up += x[e];
+        if (token < 0 && up > left) token = w.token(first + at, e);
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, token >= 0);
+      if (past && lane == __ffs(past) - 1) tokens[kept] = token;
+    } else {
+#pragma unroll
+      for (int e = 0; e < W::VEC; ++e) {
+        const u64 up = warp_scan(x[e]);
         const unsigned past = __ballot_sync(0xffffffffu, up > left);
         if (past) {
-          const int i = __ffs(past) - 1;
-          at = base + i;
-          left -= __shfl_sync(0xffffffffu, up - mine, i);
+          if (lane == __ffs(past) - 1) tokens[kept] = w.token(first + at, e);
           break;
         }
         left -= __shfl_sync(0xffffffffu, up, 31);
       }
-      for (int e = 0; e < kRun / 32; ++e) {
-        const int i = at * kRun + e * 32 + lane;
-        const u64 up = warp_scan(i < a.V ? w.at(i) : 0);
-        const unsigned past = __ballot_sync(0xffffffffu, up > left);
-        if (past) {
-          if (lane == 0) tokens[kept] = at * kRun + e * 32 + __ffs(past) - 1;
-          return;
-        }
-        left -= __shfl_sync(0xffffffffu, up, 31);
-      }
     }
-    return;
+    break;
   }
+  cluster.sync();  // nobody leaves while its total may be read; the place's -1 came before the token
+}
+
+template <typename T, bool kWide>
+cudaError_t launch(const VerifyArgs& a) {
+  using W = Weights<T, kWide>;
+  // blocks per sequence: as many as fill the device four times, with 16 runs to a block at least
+  const int runs = (a.V + W::kRun - 1) / W::kRun;
+  int blocks = 1;
+  while (blocks < 8 && (int64_t)a.B * blocks < 4 * a.sms && runs >= 32 * blocks) blocks *= 2;
+  const int per = (runs + blocks - 1) / blocks;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)a.B * blocks);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = per * sizeof(u64);
+  c.stream = a.stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = blocks;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, verify_kernel<T, kWide>, a, per);
+}
+template <typename T>
+cudaError_t by_alignment(const VerifyArgs& a) {
+  const bool wide = (uintptr_t)a.p % 16 == 0 && (uintptr_t)a.q % 16 == 0 && a.V % (16 / (int)sizeof(T)) == 0;
+  return wide ? launch<T, true>(a) : launch<T, false>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs& a) {
   if (a.B == 0) return cudaSuccess;
-  if (a.bf16) verify_kernel<__nv_bfloat16><<<a.B, kThreads, 0, a.stream>>>(a);
-  else verify_kernel<float><<<a.B, kThreads, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  return a.bf16 ? by_alignment<__nv_bfloat16>(a) : by_alignment<float>(a);
 }
 
 }  // namespace attn
