@@ -15,7 +15,7 @@ namespace {
 
 using namespace layer;
 
-constexpr int kThreads = 128, kRows = 16;
+constexpr int kThreads = 128, kRows = 16, kTile = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <typename TC> __device__ __forceinline__ void load4(const TC* p, float (&x)[4]);
@@ -58,7 +58,10 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a, Split s) {
   extern __shared__ __align__(16) char raw[];
   Shared<D>& sh = *reinterpret_cast<Shared<D>*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) sh.bad = 0;
+  if (tid == 0) {
+    sh.bad = 0;
+    s.cut[blockIdx.x] = -1;
+  }
   Start st;
   const bool work = find_start<kThreads>(a, s, sh.scratch, st);
   const int64_t each = (int64_t)a.hk * s.chunks;
@@ -66,7 +69,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a, Split s) {
   int n = work ? st.n : 0;
   int64_t before = work ? st.before : 0;
   for (int64_t at = work ? st.at : 0; work && at < st.end;) {
-    const Keys keys = keys_of(a, n);
+    const Keys keys = keys_of(a, s.tile, n);
     const int64_t j = (at - before * each) / keys.tiles;       // head and chunk
     const int64_t item_at = before * each + j * keys.tiles;    // the item's first tile
     const int64_t t0 = at - item_at, t1 = min(keys.tiles, st.end - item_at);
@@ -74,10 +77,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a, Split s) {
     const int rows = min(kRows, a.T * a.rep - row0);
     const int64_t len = a.t.lens[n];
     __syncthreads();
-    if (tid == 0) {
-      if (len > cap) sh.bad = 1;
-      if (t0 == 0) s.first[(int64_t)n * each + j] = item_at;
-    }
+    if (tid == 0 && len > cap) sh.bad = 1;
     for (int i = tid; i < kRows * D; i += kThreads) {
       const int r = i / D, c = i % D, row = row0 + r;
       float x = 0.f;
@@ -204,6 +204,10 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a, Split s) {
       }
     } else {
       float* part = part_of(s, blockIdx.x, t0 == 0 ? 1 : 0);
+      if (t0 == 0 && tid == 0) {
+        s.cut[blockIdx.x] = (int64_t)n * each + j;
+        s.cut_at[blockIdx.x] = item_at;
+      }
       if (tid < kRows) {
         part[tid] = sh.m[tid];
         part[kRows + tid] = sh.l[tid];
@@ -221,42 +225,75 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a, Split s) {
   if (tid == 0) s.verdict[blockIdx.x] = sh.bad ? KDA_ERR_INVALID_ARG : KDA_OK;
 }
 
-// A block per item that several blocks worked on: the parts' outputs weighted by 2^(m - the
-// largest m), over the sum of their sums.
+// One block per cut item and row: the parts' outputs weighted by 2^(m - the largest m), over the
+// sum of their sums.  A lane has four channels, each warp every fourth part.
+constexpr int kJoinWarps = 4;
 template <typename T, int D>
-__global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, Split s) {
-  if (blockIdx.x == 0) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, Split s) {
+  __shared__ float4 fold[kJoinWarps][32];
+  __shared__ float sums[kJoinWarps], tops[kJoinWarps];
+  cudaGridDependencySynchronize();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
     unsigned int bad = 0;
-    for (int64_t b = threadIdx.x; b < s.blocks; b += blockDim.x) bad |= s.verdict[b];
+    for (int64_t b = tid; b < s.blocks; b += blockDim.x) bad |= s.verdict[b];
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *s.status = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
+    if (tid == 0) *s.status = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
   }
-  const int64_t each = (int64_t)a.hk * s.chunks, share = *s.share;
-  for (int64_t item = blockIdx.x; item < s.items; item += gridDim.x) {
-    const int n = (int)(item / each);
-    const int64_t j = item % each;
-    const int64_t first = s.first[item], last = first + keys_of(a, n).tiles - 1;
-    const int64_t b0 = first / share, b1 = last / share;
-    if (b0 == b1) continue;
-    const int head = (int)(j / s.chunks), row0 = (int)(j % s.chunks) * s.rows;
-    const int rows = min(s.rows, a.T * a.rep - row0);
-    for (int i = threadIdx.x; i < rows * D; i += blockDim.x) {
-      const int r = i / D, c = i % D, row = row0 + r;
-      float m = -INFINITY;
-      for (int64_t b = b0; b <= b1; ++b) m = fmaxf(m, part_of(s, b, b == b0 ? 1 : 0)[r]);
-      const float base = m == -INFINITY ? 0.f : m;
-      float l = 0.f, o = 0.f;
-      for (int64_t b = b0; b <= b1; ++b) {
-        const float* p = part_of(s, b, b == b0 ? 1 : 0);
-        const float w = exp2f(p[r] - base);
-        l = fmaf(p[s.rows + r], w, l);
-        o = fmaf(p[2 * s.rows + r * D + c], w, o);
-      }
-      const int64_t to = ((int64_t)n * a.T + row / a.rep) * a.hq + head * a.rep + row % a.rep;
-      static_cast<T*>(a.out)[to * D + c] = from_f32<T>(l == 0.f ? 0.f : o / l);
-      if (c == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  const int64_t item = s.cut[blockIdx.x];
+  if (item < 0) return;
+  const int64_t each = (int64_t)a.hk * s.chunks;
+  const int n = (int)(item / each), head = (int)(item % each) / s.chunks;
+  const int r = blockIdx.y, row = (int)(item % s.chunks) * s.rows + r;
+  if (row >= a.T * a.rep) return;
+  const int64_t b0 = blockIdx.x, b1 = (s.cut_at[b0] + keys_of(a, s.tile, n).tiles - 1) / *s.share;
+  float m = -INFINITY;
+  for (int64_t b = b0 + tid; b <= b1; b += blockDim.x) m = fmaxf(m, part_of(s, b, b == b0)[r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) tops[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) m = fmaxf(m, tops[i]);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int64_t b = b0 + warp; b <= b1; b += kJoinWarps) {
+    const float* p = part_of(s, b, b == b0);
+    const float w = exp2f(p[r] - base);
+    l = fmaf(p[s.rows + r], w, l);
+    if (lane * 4 < D) {
+      const float4 x = *reinterpret_cast<const float4*>(p + 2 * s.rows + r * D + lane * 4);
+      o.x = fmaf(x.x, w, o.x);
+      o.y = fmaf(x.y, w, o.y);
+      o.z = fmaf(x.z, w, o.z);
+      o.w = fmaf(x.w, w, o.w);
     }
   }
+  fold[warp][lane] = o;
+  if (lane == 0) sums[warp] = l;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int i = 1; i < kJoinWarps; ++i) {
+    const float4 x = fold[i][lane];
+    o.x += x.x;
+    o.y += x.y;
+    o.z += x.z;
+    o.w += x.w;
+    l += sums[i];
+  }
+  const int64_t to = ((int64_t)n * a.T + row / a.rep) * a.hq + head * a.rep + row % a.rep;
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  if (lane * 4 < D) {
+    T* out = static_cast<T*>(a.out) + to * D + lane * 4;
+    out[0] = from_f32<T>(o.x * f);
+    out[1] = from_f32<T>(o.y * f);
+    out[2] = from_f32<T>(o.z * f);
+    out[3] = from_f32<T>(o.w * f);
+  }
+  if (lane == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <typename TC, int D>
@@ -278,19 +315,27 @@ cudaError_t by_cache(const AttnArgs& a, const Split& s) {
 
 }  // namespace
 
-Split attn_general_split(const AttnArgs& a) { return split_of(a, kRows, 2); }
+Split attn_general_split(const AttnArgs& a) { return split_of(a, kRows, kTile, 2); }
 
+// The join's blocks may be placed while the last of the main kernel's still run.
+template <typename T, int D>
+static cudaError_t join(const AttnArgs& a, const Split& s) {
+  const int rows = a.T * a.rep;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)s.blocks, rows < s.rows ? rows : s.rows);
+  c.blockDim = dim3(32 * kJoinWarps);
+  c.stream = a.stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, attn_join_kernel<T, D>, a, s);
+}
 cudaError_t launch_attn_join(const AttnArgs& a, const Split& s) {
-  const unsigned grid = (unsigned)(s.items < 8 * a.sms ? s.items : 8 * a.sms);
   using bf = __nv_bfloat16;
-  if (a.d == 128) {
-    a.bf16 ? attn_join_kernel<bf, 128><<<grid, 128, 0, a.stream>>>(a, s)
-           : attn_join_kernel<float, 128><<<grid, 128, 0, a.stream>>>(a, s);
-  } else {
-    a.bf16 ? attn_join_kernel<bf, 64><<<grid, 128, 0, a.stream>>>(a, s)
-           : attn_join_kernel<float, 64><<<grid, 128, 0, a.stream>>>(a, s);
-  }
-  return cudaGetLastError();
+  if (a.d == 128) return a.bf16 ? join<bf, 128>(a, s) : join<float, 128>(a, s);
+  return a.bf16 ? join<bf, 64>(a, s) : join<float, 64>(a, s);
 }
 
 cudaError_t launch_attn_general(const AttnArgs& a) {

@@ -1,31 +1,32 @@
 // Attention of new tokens over the paged cache, bf16 queries: products on the tensor cores.
 //
-// Bound by the bytes of keys and values: 8 to 64 query rows per key are few operations, so the
-// products are warp-level ones (m16n8k16, 16 query rows), and everything else serves a steady
-// stream of loads.  Each of a block's four key groups takes 16 of a tile's 64 places: its warps
-// copy them into a ring of stages of their own (cp.async, 16 bytes a lane, swizzled by row) and
-// wait for nobody else; a running maximum, sum and output per warp are joined when an item ends.
-// The next items' tiles are requested while the present one is worked on.
+// Bound by the bytes of keys and values: 1 to 64 query rows per key are few operations, so the
+// products are warp-level ones (m16n8k16), with the keys as rows and 8 queries as columns, and
+// everything else serves a steady stream of loads.  Each of a block's four key groups takes 16 or
+// 32 of a tile's places: its warps copy them into a ring of stages of their own (cp.async, 16
+// bytes a lane, swizzled by row) and wait for nobody else; a running maximum, sum and output per
+// warp are joined when an item ends.  The next items' tiles are requested while the present one
+// is worked on.
 //
-//     S = Q K^T: A = queries, B = keys (their rows are B's columns: ldmatrix as they lie)
-//     O = P V:   A = the weights, whose accumulator layout is A's; B = values (ldmatrix.trans)
+//     S^T = K Q^T:  A = keys as they lie (ldmatrix), B = queries, kept as fragments
+//     O^T = V^T P^T: A = values (ldmatrix.trans), B = the weights: S^T's accumulators, packed to
+//                    16 bits and transposed 8 x 8 in registers (movmatrix)
 //
 // Types.  bf16 caches: products of bf16, exact in float32; a weight enters as two bf16 parts
 // (16 bits), since one alone would cost as much as the output's own rounding.  Codes become f16,
 // exactly; queries become f16 after a power of two per row has brought their largest to 2^13,
-// which keeps every bit down to 2^-27 of it.  A value's power of two joins the weight in the
-// exponent, 2^(s + e - M) with M the row's own running maximum of s + e, so that f16 holds the
-// largest contributions with 11 bits and smaller ones to 2^-25 of them; the sum of weights
-// stays 2^(s - m) in float32.
+// which keeps every bit down to 2^-27 of it.  A value's power of two joins its weight, relative
+// to the largest power seen by the warp, times 2^15: f16 then holds weights of 2^-29 of the
+// largest with all 11 bits, and what is below to 2^-39 of it; the sum of weights stays float32.
 //
 // Codes lie four to a 32-bit word, and the products' order of channels is free as long as both
 // operands have the same: a word of a key's row is channels 4t .. 4t + 3, used as the two pairs
 // of a k-step; ldmatrix.trans on pairs of bytes gives two channels of two places, which one
-// byte permutation sorts by channel, so that a thread's outputs are four adjacent channels.
+// byte permutation sorts by channel, so that a thread's outputs are pairs of adjacent channels.
 //
-// Places that a row does not see: the tiles at the ends of the seen range replace their scores
-// by -inf, and values that are not finite by zeros, whose rows get them added afterwards if they
-// do see them (0 times infinity would reach the others).
+// Places that a row does not see: the tiles at the ends of the seen range give them the weight 0,
+// and values that are not finite become zeros, whose rows get them added afterwards if they do
+// see them (0 times infinity would reach the others).
 #include "kda_attn_split.cuh"
 
 namespace kda {
@@ -105,60 +106,68 @@ __device__ __forceinline__ bool clear_wild(uint32_t& w) {
   return wild;
 }
 
+__device__ __forceinline__ uint32_t transposed(uint32_t w) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+  return r;
+}
+
 // Places of tiles in the block's share, item by item.
 struct Cursor {
-  int64_t left;  // tiles of the share from here on
-  int n, j;      // sequence; head and chunk
-  int t, tiles;  // tile of the item, the item's number
-  int lo, hi;    // the sequence's places
-  __device__ __forceinline__ void enter(const AttnArgs& a) {
-    const Keys k = keys_of(a, n);
+  int64_t left;     // tiles of the share from here on
+  int n, head, chunk;
+  int t, tiles;     // tile of the item, the item's number
+  int lo, hi;       // the sequence's places
+  __device__ __forceinline__ void enter(const AttnArgs& a, const Split& s) {
+    const Keys k = keys_of(a, s.tile, n);
     lo = (int)k.lo;
     hi = (int)k.hi;
     tiles = (int)k.tiles;
   }
-  __device__ __forceinline__ void next(const AttnArgs& a, int each) {
-    --left;
-    if (++t < tiles) return;
+  // past `by` tiles of the item
+  __device__ __forceinline__ void pass(const AttnArgs& a, const Split& s, int by) {
+    left -= by;
+    t += by;
+    if (t < tiles) return;
     t = 0;
-    if (++j < each) return;
-    j = 0;
+    if (++chunk < s.chunks) return;
+    chunk = 0;
+    if (++head < a.hk) return;
+    head = 0;
     ++n;
-    if (left > 0) enter(a);
+    if (left > 0) enter(a, s);
   }
 };
 
-template <int CACHE, int D, int MT, int WM>
+// NT: query rows of a warp in eights; WM: warps with rows of their own; KT: places of a key group
+// in a tile; PER: blocks to an SM
+template <int CACHE, int D, int NT, int WM, int KT, int PER>
 struct Shape {
   static constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
-  static constexpr int kThreads = kGroups * WM * 32;
-  static constexpr int kRows = 16 * MT * WM;
-  static constexpr int kRowBytes = D * (kCoded ? 1 : 2);
-  static constexpr int kChunks = kRowBytes / 16;           // 16-byte pieces of a row
-  static constexpr int kHalf = 16 * kRowBytes;             // a group's keys (or values) of a tile
+  static constexpr int kThreads = kGroups * WM * 32, kPerSm = PER;
+  static constexpr int kRows = 8 * NT * WM, kTile = kGroups * KT;
+  static constexpr int kElem = kCoded ? 1 : 2;
+  static constexpr int kChunks = D * kElem / 16;           // 16-byte pieces of a row
+  static constexpr int kHalf = KT * D * kElem;             // a group's keys (or values) of a tile
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kMergeWarp = 16 * MT * (D + 2) * 4;  // a warp's output, maxima and sums
-  static constexpr int kQBytes = WM * MT * (D / 16) * 32 * 16;
+  static constexpr int kMergeWarp = 8 * NT * (D + 2) * 4;  // a warp's output, maxima and sums
+  static constexpr int kQBytes = kRows * D * 2;
   static constexpr int bytes(int stages) {
-    return kGroups * stages * (kStage + 32 + 4) + kQBytes + (kRows * 4 + 15) / 16 * 16 + WM * kMergeWarp;
+    return kGroups * stages * (kStage + 2 * KT + 4) + kQBytes + 8 * kRows + WM * kMergeWarp;
   }
-  // two blocks to an SM where three stages of each fit (228 KB, of which a block takes 1.5 KB
-  // for itself), with up to five stages; otherwise one block with up to six
-  static constexpr int kRoom = 228 * 1024;
-  static constexpr bool kTwo = WM == 1 && 2 * (bytes(3) + 1536) <= kRoom;
+  // as many stages as the SM's 228 KB hold for its blocks (each takes 1.5 KB for itself), up to six
   static constexpr int fit() {
     int n = 2;
-    while (n < (kTwo ? 5 : 6) && (kTwo ? 2 : 1) * (bytes(n + 1) + 1536) <= kRoom) ++n;
+    while (n < 6 && PER * (bytes(n + 1) + 1536) <= 228 * 1024) ++n;
     return n;
   }
   static constexpr int kStages = fit();
-  static constexpr int kPerSm = kTwo ? 2 : 1;
-  // shared memory
+  static_assert(PER * (bytes(kStages) + 1536) <= 228 * 1024, "shared memory");
   static constexpr int oQ = kGroups * kStages * kStage;
   static constexpr int oScale = oQ + kQBytes;
-  static constexpr int oSeen = oScale + kGroups * kStages * 32;
+  static constexpr int oSeen = oScale + kGroups * kStages * 2 * KT;
   static constexpr int oRow = oSeen + kGroups * kStages * 4;
-  static constexpr int oMerge = oRow + (kRows * 4 + 15) / 16 * 16;
+  static constexpr int oMerge = oRow + 8 * kRows;
   static constexpr int kBytes = bytes(kStages);
   static_assert(oMerge % 16 == 0 && kMergeWarp % 16 == 0 && oMerge + WM * kMergeWarp == kBytes, "layout");
 };
@@ -169,92 +178,119 @@ __device__ __forceinline__ int piece(int row, int c) {
   else return row * CHUNKS + (c ^ ((row >> 1) & 3));
 }
 
-template <int CACHE, int D, int MT, int WM>
-__global__ void __launch_bounds__(Shape<CACHE, D, MT, WM>::kThreads, Shape<CACHE, D, MT, WM>::kPerSm)
+template <int CACHE, int D, int NT, int WM, int KT, int PER>
+__global__ void __launch_bounds__(Shape<CACHE, D, NT, WM, KT, PER>::kThreads, PER)
 attn_mma_kernel(AttnArgs a, Split s, bool words) {
-  using S = Shape<CACHE, D, MT, WM>;
-  constexpr int KS = D / 16;
+  using S = Shape<CACHE, D, NT, WM, KT, PER>;
+  constexpr bool kCoded = S::kCoded;
+  constexpr int KS = D / 16, KM = KT / 16, CH = S::kChunks;
+  constexpr bool kHoldQ = NT * KS <= 8;  // queries stay in registers
+  constexpr unsigned kAll = KT == 32 ? 0xffffffffu : 0xffffu;
   extern __shared__ __align__(128) char raw[];
   __shared__ int64_t scratch[34];
   __shared__ int bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grp = warp % kGroups, wm = warp / kGroups;  // key group; which query rows
   const int g = lane >> 2, t4 = lane & 3;
-  if (tid == 0) bad = 0;
+  if (tid == 0) {
+    bad = 0;
+    s.cut[blockIdx.x] = -1;
+  }
   Start st;
-  const bool work = find_start<S::kThreads>(a, s, scratch, st);
-  if (!work) {
+  if (!find_start<S::kThreads>(a, s, scratch, st)) {
     if (tid == 0) s.verdict[blockIdx.x] = KDA_OK;
     return;
   }
-  const int each = a.hk * s.chunks;
   const int mask = (1 << a.t.shift) - 1;
   Cursor now;
   {
     now.n = st.n;
     now.left = st.end - st.at;
-    now.enter(a);
-    const int64_t off = st.at - st.before * each;
-    now.j = (int)(off / now.tiles);
+    now.enter(a, s);
+    const int64_t off = st.at - st.before * (a.hk * s.chunks);
+    const int j = (int)(off / now.tiles);
     now.t = (int)(off % now.tiles);
+    now.head = j / s.chunks;
+    now.chunk = j % s.chunks;
   }
   Cursor ahead = now;
   char* const kv = raw + grp * S::kStages * S::kStage;
-  uint8_t* const sc = reinterpret_cast<uint8_t*>(raw + S::oScale) + grp * S::kStages * 32;
-  int* const seen_of = reinterpret_cast<int*>(raw + S::oSeen) + grp * S::kStages;
+  uint8_t* const sc = reinterpret_cast<uint8_t*>(raw + S::oScale) + grp * S::kStages * 2 * KT;
+  unsigned* const seen_of = reinterpret_cast<unsigned*>(raw + S::oSeen) + grp * S::kStages;
   float* const row_factor = reinterpret_cast<float*>(raw + S::oRow);
-  uint4* const qs = reinterpret_cast<uint4*>(raw + S::oQ);
+  int* const row_end = reinterpret_cast<int*>(raw + S::oRow) + S::kRows;
+  uint2* const qs = reinterpret_cast<uint2*>(raw + S::oQ) + wm * NT * KS * 32;
 
-  // The group's 16 places of the tile at `ahead` into a stage (its WM warps take a share each).
+  // The table's entries of the next request are read one request early.
+  int ids[KM];
+  auto look = [&]() {
+    if (a.t.shift < 4 || ahead.left <= 0) return;
+#pragma unroll
+    for (int u = 0; u < KM; ++u) {
+      const unsigned pos = (unsigned)ahead.lo + (unsigned)ahead.t * S::kTile + grp * KT + u * 16;
+      const int64_t col = pos >> a.t.shift;
+      ids[u] = pos < (unsigned)ahead.hi && col < a.t.max_pages ? a.t.pages[(int64_t)ahead.n * a.t.max_pages + col] : -1;
+    }
+  };
+  // The group's places of the tile at `ahead` into a stage (its WM warps take a share each).
   auto request = [&](int stage) {
     if (ahead.left > 0) {
-      const int head = ahead.j / s.chunks;
-      const int64_t pos = (int64_t)ahead.lo + (int64_t)ahead.t * kTile + grp * 16;
+      const unsigned pos = (unsigned)ahead.lo + (unsigned)ahead.t * S::kTile + grp * KT;
       const uint32_t dst = smem_at(kv + stage * S::kStage);
       unsigned seen = 0;
-      if (a.t.shift >= 4) {  // a page holds all 16
-        const int id = pos < ahead.hi ? page_of(a.t, ahead.n, pos) : -1;
-        const int have = pos < ahead.hi ? (int)min((int64_t)16, ahead.hi - pos) : 0;
-        if (id >= 0) seen = (1u << have) - 1;
-        else if (have > 0) bad = 1;
-        const int64_t row = ((int64_t)head << a.t.shift) + (pos & mask);
-        const int64_t from = id >= 0 ? (id * a.ldpage + row * D) * (S::kCoded ? 1 : 2) : 0;
-        const char* k = static_cast<const char*>(a.kc) + from;
-        const char* v = static_cast<const char*>(a.vc) + from;
+      if (a.t.shift >= 4) {  // a page holds 16 places in a row
+        const char *k[KM], *v[KM];
+        int have[KM];
 #pragma unroll
-        for (int i = 0; i < 16 * S::kChunks / 32 / WM; ++i) {
-          const int x = (i * WM + wm) * 32 + lane, r = x / S::kChunks, c = x % S::kChunks;
-          const bool ok = id >= 0 && r < have;
-          const int to = piece<S::kChunks>(r, c) * 16;
-          copy16(dst + to, ok ? k + x * 16 : k, ok);
-          copy16(dst + S::kHalf + to, ok ? v + x * 16 : v, ok);
+        for (int u = 0; u < KM; ++u) {
+          const unsigned p = pos + u * 16;
+          const bool some = p < (unsigned)ahead.hi;
+          const bool ok = some && (unsigned)ids[u] < (unsigned)a.t.num_pages;
+          have[u] = ok ? (int)min(16u, (unsigned)ahead.hi - p) : 0;
+          if (some && !ok) bad = 1;
+          seen |= ((1u << have[u]) - 1) << (u * 16);
+          const int64_t row = ((int64_t)ahead.head << a.t.shift) + (p & mask);
+          const int64_t from = ok ? (ids[u] * a.ldpage + row * D) * S::kElem : 0;
+          k[u] = static_cast<const char*>(a.kc) + from;
+          v[u] = static_cast<const char*>(a.vc) + from;
+          if (kCoded && wm == 0 && ok && (lane >> 1) == u) {
+            const int64_t b = (((int64_t)ids[u] * a.hk) << a.t.shift) + row;
+            copy16(smem_at(sc + stage * 2 * KT + (lane & 1) * KT + u * 16), (lane & 1 ? a.vs : a.ks) + b, true);
+          }
         }
-        if (S::kCoded && wm == 0 && lane < 2 && id >= 0) {
-          const int64_t b = (((int64_t)id * a.hk) << a.t.shift) + row;
-          copy16(smem_at(sc + stage * 32 + lane * 16), (lane ? a.vs : a.ks) + b, true);
+#pragma unroll
+        for (int i = 0; i < KT * CH / 32 / WM; ++i) {
+          const int x = (i * WM + wm) * 32 + lane, r = x / CH, c = x % CH;
+          constexpr int rows_of = 32 / CH;
+          const int u = i * WM * rows_of / 16;
+          const bool ok = (r & 15) < have[u];
+          const int to = piece<CH>(r, c) * 16, from = ok ? (x % (16 * CH)) * 16 : 0;
+          copy16(dst + to, k[u] + from, ok);
+          copy16(dst + S::kHalf + to, v[u] + from, ok);
         }
       } else {
-        for (int i = 0; i < 16 * S::kChunks / 32 / WM; ++i) {
-          const int x = (i * WM + wm) * 32 + lane, r = x / S::kChunks, c = x % S::kChunks;
-          const int id = pos + r < ahead.hi ? page_of(a.t, ahead.n, pos + r) : -1;
-          const int64_t row = ((int64_t)head << a.t.shift) + ((pos + r) & mask);
-          const int64_t from = id >= 0 ? (id * a.ldpage + row * D) * (S::kCoded ? 1 : 2) + c * 16 : 0;
-          const int to = piece<S::kChunks>(r, c) * 16;
+        for (int i = 0; i < KT * CH / 32 / WM; ++i) {
+          const int x = (i * WM + wm) * 32 + lane, r = x / CH, c = x % CH;
+          const int id = pos + r < (unsigned)ahead.hi ? page_of(a.t, ahead.n, pos + r) : -1;
+          const int64_t row = ((int64_t)ahead.head << a.t.shift) + ((pos + r) & mask);
+          const int64_t from = id >= 0 ? (id * a.ldpage + row * D) * S::kElem + c * 16 : 0;
+          const int to = piece<CH>(r, c) * 16;
           copy16(dst + to, static_cast<const char*>(a.kc) + from, id >= 0);
           copy16(dst + S::kHalf + to, static_cast<const char*>(a.vc) + from, id >= 0);
         }
-        const int r = lane & 15;
-        const int id = pos + r < ahead.hi ? page_of(a.t, ahead.n, pos + r) : -1;
-        if (id < 0 && pos + r < ahead.hi) bad = 1;
-        seen = __ballot_sync(0xffffffffu, id >= 0) & 0xffffu;
-        if (S::kCoded && wm == 0 && id >= 0) {
-          const int64_t row = ((int64_t)head << a.t.shift) + ((pos + r) & mask);
-          const int64_t b = (((int64_t)id * a.hk) << a.t.shift) + row;
-          sc[stage * 32 + lane] = (lane < 16 ? a.ks : a.vs)[b];
+        const bool some = lane < KT && pos + lane < (unsigned)ahead.hi;
+        const int id = some ? page_of(a.t, ahead.n, pos + lane) : -1;
+        if (some && id < 0) bad = 1;
+        seen = __ballot_sync(0xffffffffu, id >= 0);
+        if (kCoded && wm == 0 && id >= 0) {
+          const int64_t b = (((int64_t)id * a.hk + ahead.head) << a.t.shift) + ((pos + lane) & mask);
+          sc[stage * 2 * KT + lane] = a.ks[b];
+          sc[stage * 2 * KT + KT + lane] = a.vs[b];
         }
       }
-      if (wm == 0 && lane == 0) seen_of[stage] = (int)seen;
-      ahead.next(a, each);
+      if (wm == 0 && lane == 0) seen_of[stage] = seen;
+      ahead.pass(a, s, 1);
+      look();
     }
     copy_commit();
   };
@@ -264,26 +300,35 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * WM) : "memory");
   };
 
+  look();
 #pragma unroll
   for (int i = 0; i < S::kStages - 1; ++i) request(i);
   int stage = 0;
+  // ldmatrix: the lane's row of 16 places and piece of two, (places, pieces) = 0 0, 1 0, 0 1, 1 1
+  // by eights of lanes; bf16 values take 0 0, 0 1, 1 0, 1 1
+  const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mcol = lane >> 4;
+  const int vrow = kCoded ? mrow : (lane & 7) + (lane >> 4) * 8, vcol = kCoded ? mcol : (lane >> 3) & 1;
 
   while (now.left > 0) {
-    // ---- an item begins: its queries as fragments of A, one row per warp and turn
-    const int n = now.n, head = now.j / s.chunks, row0 = now.j % s.chunks * S::kRows;
+    // ---- an item begins: its queries as fragments of B, one row per warp and turn
+    const int n = now.n, head = now.head, row0 = now.chunk * S::kRows;
     const int rows = min(S::kRows, a.T * a.rep - row0);
     const int len = max(a.t.lens[n], -8);  // nothing is seen at 0 and below
     const int t0 = now.t, t1 = (int)min((int64_t)now.tiles, now.t + now.left);
     if (tid == 0) {
       if ((int64_t)len > (int64_t)a.t.max_pages << a.t.shift) bad = 1;
-      if (t0 == 0) s.first[(int64_t)n * each + now.j] = st.end - now.left;
+      if (t0 == 0 && t1 < now.tiles) {
+        s.cut[blockIdx.x] = ((int64_t)n * a.hk + head) * s.chunks + now.chunk;
+        s.cut_at[blockIdx.x] = st.end - now.left;
+      }
     }
     __syncthreads();
+#pragma unroll 2
     for (int r = warp; r < S::kRows; r += S::kThreads / 32) {
-      const int row = row0 + r;
+      const int row = row0 + r, tok = row / a.rep;
       __nv_bfloat162 x[D / 64];
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-          ((int64_t)n * a.T + row / a.rep) * a.ldq + (int64_t)(head * a.rep + row % a.rep) * D;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)n * a.T + tok) * a.ldq +
+                               (int64_t)(head * a.rep + row - tok * a.rep) * D;
       uint32_t most = 0;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
@@ -296,47 +341,54 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         most = max(most, max(__float_as_uint(__bfloat162float(x[i].x)) & 0x7fffffffu,
                              __float_as_uint(__bfloat162float(x[i].y)) & 0x7fffffffu));
       }
-      float up = 1.f;
-      if constexpr (S::kCoded) {
+      // the sign of the scale goes into the query, so that factors are positive; no scale: no query
+      float up = a.scale < 0.f ? -1.f : a.scale > 0.f ? 1.f : 0.f, f = fabsf(a.scale) * kLog2e;
+      if constexpr (kCoded) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
         // 2^13 over the largest's power of two, kept a normal number
         const int e = (int)(most >> 23);
         const int k = e == 0 || e == 255 ? 0 : min(max(127 + 13 - e, -120), 120);
-        up = __uint_as_float((uint32_t)(127 + k) << 23);
-        if (lane == 0) row_factor[r] = a.scale * kLog2e * __uint_as_float((uint32_t)(127 - k) << 23);
+        up *= __uint_as_float((uint32_t)(127 + k) << 23);
+        f *= __uint_as_float((uint32_t)(127 - k) << 23);
+      }
+      if (lane == 0) {
+        row_factor[r] = f > 1e-37f ? f : 1e-37f;
+        row_end[r] = len - a.T + tok + 1;  // the row sees places below this
       }
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         const int p = lane + 32 * i, ks = p / 8, w = p % 8;
-        const int t = S::kCoded ? w / 2 : w % 4, hi = S::kCoded ? w & 1 : w / 4;
-        uint32_t v;
-        if constexpr (S::kCoded) v = pack_half(__bfloat162float(x[i].x) * up, __bfloat162float(x[i].y) * up);
-        else v = *reinterpret_cast<const uint32_t*>(&x[i]);
-        uint32_t* to = reinterpret_cast<uint32_t*>(&qs[((r / 16) * KS + ks) * 32 + (r & 7) * 4 + t]);
-        to[hi * 2 + ((r >> 3) & 1)] = v;
+        const int t = kCoded ? w / 2 : w % 4, hi = kCoded ? w & 1 : w / 4;
+        const float x0 = __bfloat162float(x[i].x) * up, x1 = __bfloat162float(x[i].y) * up;
+        uint32_t* to = reinterpret_cast<uint32_t*>(raw + S::oQ) + ((r / 8) * KS + ks) * 64 + ((r & 7) * 4 + t) * 2 + hi;
+        *to = kCoded ? pack_half(x0, x1) : layer::pack_bf16(x0, x1);
       }
     }
     __syncthreads();
-    float m[MT][2], M[MT][2], l[MT][2], rf[MT][2];
-    float o[MT][D / 8][4];
-    int hi_of[MT][2];
+    float y[NT][2], l[NT][2], rf[NT][2];  // maxima (without the row's factor), sums, factors
+    float o[D / 16][NT][4];
+    uint2 qh[kHoldQ ? NT * KS : 1];
+    int top = 0;  // the largest byte of a value seen
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = (wm * MT + mt) * 16 + h * 8 + g;
-        m[mt][h] = M[mt][h] = -INFINITY;
-        l[mt][h] = 0.f;
-        rf[mt][h] = S::kCoded ? row_factor[r] : a.scale * kLog2e;
-        hi_of[mt][h] = len - a.T + (row0 + r) / a.rep + 1;  // the row sees places below this
+      for (int e = 0; e < 2; ++e) {
+        y[i][e] = -INFINITY;
+        l[i][e] = 0.f;
+        rf[i][e] = row_factor[(wm * NT + i) * 8 + 2 * t4 + e];
       }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+    if (kHoldQ) {
+#pragma unroll
+      for (int i = 0; i < NT * KS; ++i) qh[i] = qs[i * 32 + lane];
+    }
+    auto query = [&](int nt, int ks) { return kHoldQ ? qh[nt * KS + ks] : qs[(nt * KS + ks) * 32 + lane]; };
     const int hi_min = len - a.T + row0 / a.rep + 1;
     const int lo_max = a.window > 0 ? len - a.T + (row0 + rows - 1) / a.rep + 1 - a.window : INT_MIN;
 
@@ -344,356 +396,365 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       copy_wait<S::kStages - 2>();
       meet();
       request(stage == 0 ? S::kStages - 1 : stage - 1);
-      const int pos = now.lo + t * kTile + grp * 16;
-      const unsigned seen = (unsigned)seen_of[stage];
-      const bool edge = seen != 0xffffu || pos > hi_min - 16 || pos < lo_max;
-      const uint32_t kbase = smem_at(kv + stage * S::kStage), vbase = kbase + S::kHalf;
-      // ---- scores of 16 places: c[mt][places 0-7, 8-15]
-      float c[MT][2][4];
+      const char* const here = kv + stage * S::kStage;
+      const uint8_t* const bytes = sc + stage * 2 * KT;
+      const unsigned seen = seen_of[stage];
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
+      if (seen == 0) continue;
+      const int pos = (int)((unsigned)now.lo + (unsigned)t * S::kTile + grp * KT);
+      const bool edge = seen != kAll || pos > hi_min - KT || pos < lo_max;
+      const uint32_t kbase = smem_at(here), vbase = kbase + S::kHalf;
+      // ---- scores: c[places][queries]
+      float c[KM][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int u = 0; u < KM; ++u)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c[mt][i][e] = 0.f;
-      if constexpr (!S::kCoded) {
+          for (int e = 0; e < 4; ++e) c[u][j][e] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          // matrices: places 0-7 and 8-15 by channels 0-7 and 8-15 of the step
+      for (int i = 0; i < CH / 2; ++i)
+#pragma unroll
+        for (int u = 0; u < KM; ++u) {
           uint32_t b[4];
-          const int r = (lane & 7) + (lane >> 4) * 8;
-          matrix4(b, kbase + piece<S::kChunks>(r, 2 * ks + ((lane >> 3) & 1)) * 16);
+          matrix4(b, kbase + piece<CH>(u * 16 + mrow, 2 * i + mcol) * 16);
+          if constexpr (!kCoded) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const uint4 q = qs[((wm * MT + mt) * KS + ks) * 32 + lane];
-            product<true>(c[mt][0], q, b[0], b[1]);
-            product<true>(c[mt][1], q, b[2], b[3]);
-          }
-        }
-      } else {
+            for (int j = 0; j < NT; ++j) {
+              const uint2 q = query(j, i);
+              product<true>(c[u][j], make_uint4(b[0], b[1], b[2], b[3]), q.x, q.y);
+            }
+          } else {
 #pragma unroll
-        for (int k2 = 0; k2 < KS / 2; ++k2) {
-          // matrices: places 0-7 and 8-15 by steps 2 k2 and 2 k2 + 1 (16 bytes each)
-          uint32_t b[4];
-          const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
-          matrix4(b, kbase + piece<S::kChunks>(r, 2 * k2 + (lane >> 4)) * 16);
+            for (int k = 0; k < 2; ++k) {
+              uint4 w;
+              open4<CACHE>(b[2 * k], w.x, w.z);
+              open4<CACHE>(b[2 * k + 1], w.y, w.w);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t x0, x1, y0, y1;
-            open4<CACHE>(b[2 * k], x0, x1);
-            open4<CACHE>(b[2 * k + 1], y0, y1);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const uint4 q = qs[((wm * MT + mt) * KS + 2 * k2 + k) * 32 + lane];
-              product<false>(c[mt][0], q, x0, x1);
-              product<false>(c[mt][1], q, y0, y1);
+              for (int j = 0; j < NT; ++j) {
+                const uint2 q = query(j, 2 * i + k);
+                product<false>(c[u][j], w, q.x, q.y);
+              }
             }
           }
         }
-      }
-      float kf[2][2], ev[2][2];  // a key's power of two; a value's exponent
-      if constexpr (S::kCoded) {
+      float kf[KM][2], vf[KM][2];  // of places g and g + 8
+      bool moved = false;
+      float rise = 1.f;
+      if constexpr (kCoded) {
+        const int mine = lane < KT && (seen >> lane & 1) ? bytes[KT + lane] : 0;
+        const int most = max(top, (int)__reduce_max_sync(0xffffffffu, mine == 255 ? 0 : mine));
+        moved = most != top;
+        rise = __uint_as_float((uint32_t)max(127 + top - most, 0) << 23);
+        top = most;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int u = 0; u < KM; ++u)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int at = stage * 32 + i * 8 + 2 * t4 + e;
-            const int b = sc[at + 16];
-            kf[i][e] = power(sc[at]);
-            ev[i][e] = b == 255 ? INFINITY : (float)(b - 127);
+            const int at = u * 16 + e * 8 + g, b = bytes[KT + at];
+            kf[u][e] = power(bytes[at]);
+            vf[u][e] = __uint_as_float(b == 255 ? 0x7f800000u : (uint32_t)max(min(b - top, 0) + 142, 0) << 23);
           }
       }
       // ---- weights
-      bool moved = false;
-      float al[MT][2];  // the output's factor
-      uint4 ph[MT], pl[MT];
+      unsigned on[NT][2];  // edge: the places that the query sees
+      if (edge) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float p[2][4];
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float mx = -INFINITY, Mx = -INFINITY;
+          for (int e = 0; e < 2; ++e) {
+            const int64_t end = (int64_t)row_end[(wm * NT + j) * 8 + 2 * t4 + e] - pos;
+            const int64_t from = a.window > 0 ? end - a.window : 0;
+            unsigned m = end >= KT ? kAll : end <= 0 ? 0u : (1u << end) - 1;
+            if (from > 0) m = from >= KT ? 0u : m & ~((1u << from) - 1);
+            on[j][e] = m & seen;
+          }
+      }
+      float al[NT][2];  // the outputs' factors
+      uint32_t ph[KM][NT][2], pl[KM][NT][2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < NT; ++j) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& x = c[mt][i][2 * h + e];
-              x *= rf[mt][h];
-              if (S::kCoded) x *= kf[i][e];
-              if (edge) {
-                const int key = i * 8 + 2 * t4 + e;
-                const bool ok = ((seen >> key) & 1) && pos + key < hi_of[mt][h] &&
-                                (a.window == 0 || pos + key >= hi_of[mt][h] - a.window);
-                if (!ok) x = -INFINITY;
-              }
+        for (int e = 0; e < 2; ++e) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < KM; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float& x = c[u][j][2 * h + e];
+              if (kCoded) x *= kf[u][h];
+              if (edge && !(on[j][e] >> (u * 16 + h * 8 + g) & 1)) x = -INFINITY;
               mx = fmaxf(mx, x);
-              if (S::kCoded) Mx = fmaxf(Mx, edge && x == -INFINITY ? x : x + ev[i][e]);
             }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[mt][h], mx);
-          const float mb = mn == -INFINITY ? 0.f : mn;
-          const float am = exp2_of(m[mt][h] - mb);
-          l[mt][h] *= am;
-          al[mt][h] = am;
-          moved |= mn != m[mt][h];
-          m[mt][h] = mn;
-          float Mb = 0.f;
-          if (S::kCoded) {
-            Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, 1));
-            Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, 2));
-            const float Mn = fmaxf(M[mt][h], Mx);
-            Mb = Mn == -INFINITY ? 0.f : Mn;
-            al[mt][h] = exp2_of(M[mt][h] - Mb);
-            moved |= Mn != M[mt][h];
-            M[mt][h] = Mn;
-          }
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+          const float yn = fmaxf(y[j][e], mx), base = yn == -INFINITY ? 0.f : yn * rf[j][e];
+          const float f = exp2_of(fmaf(y[j][e], rf[j][e], -base));
+          moved |= yn != y[j][e];
+          y[j][e] = yn;
+          l[j][e] *= f;
+          al[j][e] = kCoded ? f * rise : f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float x = c[mt][i][2 * h + e];
-              const float w = exp2_of(x - mb);
-              l[mt][h] += w;
-              p[i][2 * h + e] = w;
-              if (S::kCoded) p[i][2 * h + e] = edge && x == -INFINITY ? 0.f : exp2_of(x + ev[i][e] - Mb);
+          for (int u = 0; u < KM; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float& x = c[u][j][2 * h + e];
+              const bool off = edge && !(on[j][e] >> (u * 16 + h * 8 + g) & 1);
+              x = exp2_of(fmaf(x, rf[j][e], -base));
+              if (off) x = 0.f;
+              l[j][e] += x;
+              if (kCoded) {
+                x *= vf[u][h];
+                if (off) x = 0.f;
+              }
             }
         }
-        uint32_t w[4], v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // A's words: rows g, g + 8 of places 0-7, then of 8-15
-          const float x = p[k >> 1][(k & 1) * 2], y = p[k >> 1][(k & 1) * 2 + 1];
-          if constexpr (S::kCoded) {
-            w[k] = pack_half(x, y);
-          } else {
-            w[k] = layer::pack_bf16(x, y);
-            float xh, yh;
-            layer::unpack2(w[k], xh, yh);
-            v[k] = layer::pack_bf16(x - xh, y - yh);
+        for (int u = 0; u < KM; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float x = c[u][j][2 * h], z = c[u][j][2 * h + 1];
+            if constexpr (kCoded) {
+              ph[u][j][h] = transposed(pack_half(x, z));
+            } else {
+              const uint32_t w = layer::pack_bf16(x, z);
+              float xh, zh;
+              layer::unpack2(w, xh, zh);
+              ph[u][j][h] = transposed(w);
+              pl[u][j][h] = transposed(layer::pack_bf16(x - xh, z - zh));
+            }
           }
-        }
-        ph[mt] = make_uint4(w[0], w[1], w[2], w[3]);
-        if constexpr (!S::kCoded) pl[mt] = make_uint4(v[0], v[1], v[2], v[3]);
       }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[mt][i][0] *= al[mt][0];
-            o[mt][i][1] *= al[mt][0];
-            o[mt][i][2] *= al[mt][1];
-            o[mt][i][3] *= al[mt][1];
-          }
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][j][e] *= al[j][e & 1];
       }
-      // ---- outputs; each ldmatrix gives 16 bytes of channels twice
+      // ---- outputs
       bool wild = false;
 #pragma unroll
-      for (int i = 0; i < S::kChunks / 2; ++i) {
-        uint32_t b[4];
-        const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
-        matrix4_trans(b, vbase + piece<S::kChunks>(r, 2 * i + (lane >> 4)) * 16);
-        if constexpr (!S::kCoded) {
-          if (edge) {
+      for (int u = 0; u < KM; ++u)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) wild |= clear_wild<true>(b[k]);
-          }
+        for (int i = 0; i < CH / 2; ++i) {
+          uint32_t b[4];
+          matrix4_trans(b, vbase + piece<CH>(u * 16 + vrow, 2 * i + vcol) * 16);
+          if constexpr (!kCoded) {
+            if (edge) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+              for (int k = 0; k < 4; ++k) wild |= clear_wild<true>(b[k]);
+            }
+            const uint4 w = make_uint4(b[0], b[1], b[2], b[3]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              product<true>(o[i][j], w, ph[u][j][0], ph[u][j][1]);
+              product<true>(o[i][j], w, pl[u][j][0], pl[u][j][1]);
+            }
+          } else {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              product<true>(o[mt][2 * i + k], ph[mt], b[2 * k], b[2 * k + 1]);
-              product<true>(o[mt][2 * i + k], pl[mt], b[2 * k], b[2 * k + 1]);
-            }
-        } else {
+              uint4 w;  // even channels of places 0-7, odd ones, the same of 8-15
+              open4<CACHE>(__byte_perm(b[2 * k], 0u, 0x3120), w.x, w.y);
+              open4<CACHE>(__byte_perm(b[2 * k + 1], 0u, 0x3120), w.z, w.w);
+              if (CACHE == KDA_CACHE_E4M3 && edge) {
+                wild |= clear_wild<false>(w.x);
+                wild |= clear_wild<false>(w.y);
+                wild |= clear_wild<false>(w.z);
+                wild |= clear_wild<false>(w.w);
+              }
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t x0, x1, y0, y1;  // even channels of places 0-7 (8-15), odd channels
-            open4<CACHE>(__byte_perm(b[2 * k], 0u, 0x3120), x0, x1);
-            open4<CACHE>(__byte_perm(b[2 * k + 1], 0u, 0x3120), y0, y1);
-            if (CACHE == KDA_CACHE_E4M3 && edge) {
-              wild |= clear_wild<false>(x0);
-              wild |= clear_wild<false>(x1);
-              wild |= clear_wild<false>(y0);
-              wild |= clear_wild<false>(y1);
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              product<false>(o[mt][2 * (2 * i + k)], ph[mt], x0, y0);
-              product<false>(o[mt][2 * (2 * i + k) + 1], ph[mt], x1, y1);
+              for (int j = 0; j < NT; ++j) product<false>(o[2 * i + k][j], w, ph[u][j][0], ph[u][j][1]);
             }
           }
         }
-      }
       if (edge && CACHE != KDA_CACHE_INT8 && __any_sync(0xffffffffu, wild)) {
         // the rows that do see such a value take it
-        const char* v = kv + stage * S::kStage + S::kHalf;
-        for (int key = 0; key < 16; ++key)
+        const char* v = here + S::kHalf;
+#pragma unroll 1
+        for (int key = 0; key < KT; ++key)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
+            for (int h = 0; h < 2; ++h) {
+              const int byte = (kCoded ? i * 16 + 2 * g + h : i * 16 + h * 8 + g) * S::kElem;
+              const char* at = v + piece<CH>(key, byte / 16) * 16 + byte % 16;
+              float x;
+              if constexpr (kCoded) x = (*reinterpret_cast<const uint8_t*>(at) & 0x7f) == 0x7f ? NAN : 0.f;
+              else x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at));
+              if (!isfinite(x)) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int h = e >> 1, lim = hi_of[mt][h];
-                const int ch = S::kCoded ? (i / 2) * 16 + 4 * t4 + 2 * (e & 1) + (i & 1) : i * 8 + 2 * t4 + (e & 1);
-                const int byte = ch * (S::kCoded ? 1 : 2);
-                const char* at = v + piece<S::kChunks>(key, byte / 16) * 16 + byte % 16;
-                float x;
-                if constexpr (S::kCoded) x = (*reinterpret_cast<const uint8_t*>(at) & 0x7f) == 0x7f ? NAN : 0.f;
-                else x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at));
-                const bool ok = ((seen >> key) & 1) && pos + key < lim && (a.window == 0 || pos + key >= lim - a.window);
-                if (ok && !isfinite(x)) o[mt][i][e] += x;
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (on[j][e] >> key & 1) o[i][j][2 * h + e] += x;
               }
+            }
       }
-      stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
 
     // ---- the item's end: the groups' outputs of the same rows join, one after the other
+    float* const buf = reinterpret_cast<float*>(raw + S::oMerge + wm * S::kMergeWarp);
+    constexpr int kM = 8 * NT * D, kL = kM + 8 * NT;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 1);
-        l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 2);
-        if (S::kCoded) {  // from the outputs' own base to the weights'
-          const float f = m[mt][h] == -INFINITY ? 1.f : exp2_of(M[mt][h] - m[mt][h]);
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[mt][i][2 * h] *= f;
-            o[mt][i][2 * h + 1] *= f;
-          }
-        }
-      }
+        for (int i = 4; i < 32; i <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], i);
+    if (kCoded) {
+      const float f = power(top) * 0x1p-15f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][j][e] *= f;
+    }
 #pragma unroll
     for (int up = kGroups - 1; up > 0; --up) {
-      float* buf = reinterpret_cast<float*>(raw + S::oMerge + wm * S::kMergeWarp);
       __syncthreads();
       if (grp == up) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float4*>(buf + ((mt * (D / 8) + i) * 32 + lane) * 4) =
-                make_float4(o[mt][i][0], o[mt][i][1], o[mt][i][2], o[mt][i][3]);
+          for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<float4*>(buf + ((i * NT + j) * 32 + lane) * 4) =
+                make_float4(o[i][j][0], o[i][j][1], o[i][j][2], o[i][j][3]);
+        if (g == 0) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (t4 == 0) {
-              buf[16 * MT * D + mt * 16 + h * 8 + g] = m[mt][h];
-              buf[16 * MT * (D + 1) + mt * 16 + h * 8 + g] = l[mt][h];
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              buf[kM + j * 8 + 2 * t4 + e] = y[j][e];
+              buf[kL + j * 8 + 2 * t4 + e] = l[j][e];
             }
         }
       }
       __syncthreads();
       if (grp == 0) {
+        float fa[NT][2], fb[NT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          float fa[2], fb[2];
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float mo = buf[16 * MT * D + mt * 16 + h * 8 + g], lo = buf[16 * MT * (D + 1) + mt * 16 + h * 8 + g];
-            const float mn = fmaxf(m[mt][h], mo), base = mn == -INFINITY ? 0.f : mn;
-            fa[h] = exp2_of(m[mt][h] - base);
-            fb[h] = exp2_of(mo - base);
-            l[mt][h] = l[mt][h] * fa[h] + lo * fb[h];
-            m[mt][h] = mn;
+          for (int e = 0; e < 2; ++e) {
+            const float yo = buf[kM + j * 8 + 2 * t4 + e], lo = buf[kL + j * 8 + 2 * t4 + e];
+            const float yn = fmaxf(y[j][e], yo), base = yn == -INFINITY ? 0.f : yn * rf[j][e];
+            fa[j][e] = exp2_of(fmaf(y[j][e], rf[j][e], -base));
+            fb[j][e] = exp2_of(fmaf(yo, rf[j][e], -base));
+            l[j][e] = l[j][e] * fa[j][e] + lo * fb[j][e];
+            y[j][e] = yn;
           }
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const float4 x = *reinterpret_cast<const float4*>(buf + ((mt * (D / 8) + i) * 32 + lane) * 4);
-            o[mt][i][0] = o[mt][i][0] * fa[0] + x.x * fb[0];
-            o[mt][i][1] = o[mt][i][1] * fa[0] + x.y * fb[0];
-            o[mt][i][2] = o[mt][i][2] * fa[1] + x.z * fb[1];
-            o[mt][i][3] = o[mt][i][3] * fa[1] + x.w * fb[1];
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const float4 x = *reinterpret_cast<const float4*>(buf + ((i * NT + j) * 32 + lane) * 4);
+            o[i][j][0] = o[i][j][0] * fa[j][0] + x.x * fb[j][0];
+            o[i][j][1] = o[i][j][1] * fa[j][1] + x.y * fb[j][1];
+            o[i][j][2] = o[i][j][2] * fa[j][0] + x.z * fb[j][0];
+            o[i][j][3] = o[i][j][3] * fa[j][1] + x.w * fb[j][1];
           }
-        }
       }
     }
+    // rows of channels, then out: whole items divided by their sums, parts as they are
+    const bool whole = t0 == 0 && t1 == now.tiles;
     if (grp == 0) {
-      const bool whole = t0 == 0 && t1 == now.tiles;
-      float* part = whole ? nullptr : part_of(s, blockIdx.x, t0 == 0 ? 1 : 0);
+      __syncwarp();
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = (wm * MT + mt) * 16 + h * 8 + g, row = row0 + r;
-          if (r >= rows) continue;
-          const float lr = l[mt][h];
-          if (!whole) {
-            if (t4 == 0) {
-              part[r] = m[mt][h];
-              part[S::kRows + r] = lr;
-            }
-            float* to = part + 2 * S::kRows + r * D;
-            if constexpr (S::kCoded) {
+        for (int e = 0; e < 2; ++e) {
+          const int r = j * 8 + 2 * t4 + e;
+          const float f = !whole ? 1.f : l[j][e] == 0.f ? 0.f : 1.f / l[j][e];
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i)
-                *reinterpret_cast<float4*>(to + i * 16 + 4 * t4) =
-                    make_float4(o[mt][2 * i][2 * h], o[mt][2 * i + 1][2 * h], o[mt][2 * i][2 * h + 1], o[mt][2 * i + 1][2 * h + 1]);
-            } else {
+          for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-              for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<float2*>(to + i * 8 + 2 * t4) = make_float2(o[mt][i][2 * h], o[mt][i][2 * h + 1]);
-            }
-            continue;
-          }
-          const int64_t at = ((int64_t)n * a.T + row / a.rep) * a.hq + head * a.rep + row % a.rep;
-          const float f = lr == 0.f ? 0.f : 1.f / lr;
-          if (t4 == 0 && a.lse) a.lse[at] = lr == 0.f ? -INFINITY : (m[mt][h] + log2f(lr)) * kLn2;
-          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at * D;
-          auto put = [&](int ch, float x, float y) {
-            if (words) {
-              *reinterpret_cast<uint32_t*>(to + ch) = layer::pack_bf16(x, y);
-            } else {
-              to[ch] = __float2bfloat16_rn(x);
-              to[ch + 1] = __float2bfloat16_rn(y);
-            }
-          };
-          if constexpr (S::kCoded) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              put(i * 16 + 4 * t4, o[mt][2 * i][2 * h] * f, o[mt][2 * i + 1][2 * h] * f);
-              put(i * 16 + 4 * t4 + 2, o[mt][2 * i][2 * h + 1] * f, o[mt][2 * i + 1][2 * h + 1] * f);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) put(i * 8 + 2 * t4, o[mt][i][2 * h] * f, o[mt][i][2 * h + 1] * f);
+            for (int h = 0; h < 2; ++h)
+              buf[r * D + (kCoded ? i * 16 + 2 * g + h : i * 16 + h * 8 + g)] = o[i][j][2 * h + e] * f;
+          if (g == 0) {
+            buf[kM + r] = y[j][e] == -INFINITY ? -INFINITY : y[j][e] * rf[j][e];
+            buf[kL + r] = l[j][e];
           }
         }
     }
-    // on to the next item
-    now.left -= t1 - t0;
-    if (t1 == now.tiles) {
-      now.t = 0;
-      if (++now.j == each) {
-        now.j = 0;
-        ++now.n;
-        if (now.left > 0) now.enter(a);
+    __syncthreads();
+    {
+      const float* const from = reinterpret_cast<const float*>(raw + S::oMerge);
+      constexpr int kWarpFloats = S::kMergeWarp / 4;
+      float* const part = part_of(s, blockIdx.x, t0 == 0 ? 1 : 0);
+      for (int i = tid; i < rows * (D / 2); i += S::kThreads) {
+        const int r = i / (D / 2), ch = i % (D / 2) * 2, row = row0 + r, tok = row / a.rep;
+        const float2 x = *reinterpret_cast<const float2*>(from + r / (8 * NT) * kWarpFloats + r % (8 * NT) * D + ch);
+        if (whole) {
+          const int64_t at = ((int64_t)n * a.T + tok) * a.hq + head * a.rep + row - tok * a.rep;
+          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at * D + ch;
+          if (words) {
+            *reinterpret_cast<uint32_t*>(to) = layer::pack_bf16(x.x, x.y);
+          } else {
+            to[0] = __float2bfloat16_rn(x.x);
+            to[1] = __float2bfloat16_rn(x.y);
+          }
+        } else {
+          *reinterpret_cast<float2*>(part + 2 * S::kRows + r * D + ch) = x;
+        }
+      }
+      if (tid < rows) {
+        const float* w = from + tid / (8 * NT) * kWarpFloats + tid % (8 * NT);
+        const float m = w[kM], sum = w[kL];
+        const int row = row0 + tid, tok = row / a.rep;
+        if (!whole) {
+          part[tid] = m;
+          part[S::kRows + tid] = sum;
+        } else if (a.lse) {
+          a.lse[((int64_t)n * a.T + tok) * a.hq + head * a.rep + row - tok * a.rep] =
+              sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        }
       }
     }
+    now.pass(a, s, t1 - t0);
   }
   copy_wait<0>();
   __syncthreads();
   if (tid == 0) s.verdict[blockIdx.x] = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
 }
 
-template <int CACHE, int D, int MT, int WM>
-cudaError_t launch(const AttnArgs& a, const Split& s) {
-  using S = Shape<CACHE, D, MT, WM>;
-  cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<CACHE, D, MT, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+template <int CACHE, int D, int NT, int WM, int KT, int PER>
+cudaError_t launch(Shape<CACHE, D, NT, WM, KT, PER>, const AttnArgs& a, const Split& s) {
+  using S = Shape<CACHE, D, NT, WM, KT, PER>;
+  auto* kernel = attn_mma_kernel<CACHE, D, NT, WM, KT, PER>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
   const bool words = (uintptr_t)a.q % 4 == 0 && (uintptr_t)a.out % 4 == 0 && a.ldq % 2 == 0;
-  attn_mma_kernel<CACHE, D, MT, WM><<<(unsigned)s.blocks, S::kThreads, S::kBytes, a.stream>>>(a, s, words);
+  kernel<<<(unsigned)s.blocks, S::kThreads, S::kBytes, a.stream>>>(a, s, words);
   return cudaGetLastError();
 }
 
-// f(Shape) for the rows of a call: 16, 32 or 64 to a block
+// f(Shape) for the rows of a call: 8, 16, 32 or 64 to a block
+#ifndef KT1
+#define KT1 16
+#endif
+#ifndef PER1
+#define PER1 4
+#endif
+#ifndef PERB
+#define PERB 2
+#endif
+#ifndef PER2
+#define PER2 2
+#endif
+#ifndef KT2
+#define KT2 32
+#endif
 template <int CACHE, int D, class F>
 auto by_rows(const AttnArgs& a, F f) {
+  constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
   const int rows = a.T * a.rep;
-  if (rows <= 16) return f(Shape<CACHE, D, 1, 1>());
-  if (rows <= 32) return f(Shape<CACHE, D, 2, 1>());
-  return f(Shape<CACHE, D, 2, 2>());
+  if (rows <= 8) return f(Shape<CACHE, D, 1, 1, kCoded ? KT1 : 16, kCoded ? PER1 : PERB>());
+  if (rows <= 16) return f(Shape<CACHE, D, 2, 1, kCoded ? KT2 : 16, PER2>());
+  if (rows <= 32) return f(Shape<CACHE, D, 4, 1, 16, kCoded ? 2 : 1>());
+  return f(Shape<CACHE, D, 4, 2, 16, 1>());
 }
 template <class F>
 auto by_type(const AttnArgs& a, F f) {
@@ -706,21 +767,17 @@ auto by_type(const AttnArgs& a, F f) {
   if (a.cache == KDA_CACHE_INT8) return by_rows<KDA_CACHE_INT8, 64>(a, f);
   return by_rows<KDA_CACHE_BF16, 64>(a, f);
 }
-template <int CACHE, int D, int MT, int WM>
-cudaError_t launch_of(Shape<CACHE, D, MT, WM>, const AttnArgs& a, const Split& s) {
-  return launch<CACHE, D, MT, WM>(a, s);
-}
 
 }  // namespace
 
 Split attn_mma_split(const AttnArgs& a) {
-  return by_type(a, [&](auto shape) { return split_of(a, shape.kRows, shape.kPerSm); });
+  return by_type(a, [&](auto shape) { return split_of(a, shape.kRows, shape.kTile, shape.kPerSm); });
 }
 
 cudaError_t launch_attn_mma(const AttnArgs& a) {
   Split s = attn_mma_split(a);
   split_place(s, a.ws);
-  cudaError_t e = by_type(a, [&](auto shape) { return launch_of(shape, a, s); });
+  cudaError_t e = by_type(a, [&](auto shape) { return launch(shape, a, s); });
   return e != cudaSuccess ? e : launch_attn_join(a, s);
 }
 

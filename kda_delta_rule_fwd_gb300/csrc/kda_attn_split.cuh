@@ -1,13 +1,14 @@
 // How the keys of a call are split over the device, and what the parts leave for the join.
 //
 // An item is a sequence, a key-value head and a chunk of up to `rows` query rows (tokens x query
-// heads of the group); its keys are tiles of kTile places.  All items' tiles in a row, sequence
+// heads of the group); its keys are tiles of `tile` places.  All items' tiles in a row, sequence
 // by sequence, are cut into equal shares, one per block: the lengths are on the device, so every
 // block counts the tiles by itself and finds its share.  A block walks the items of its share; an
 // item that lies in it whole is written out, a part goes to the workspace as (maximum, sum,
 // unnormalised output) per row: a block has at most two parts, the rest of an item that begins in
 // an earlier block (slot 0) and the beginning of one that goes on in the next (slot 1).  The join
-// kernel adds an item's parts in the order of the blocks.
+// kernel looks at each block that cut an item at its end, and adds that item's parts in the order
+// of the blocks.
 #pragma once
 
 #include "kda_attn.cuh"
@@ -15,35 +16,38 @@
 namespace kda {
 namespace attn {
 
-constexpr int kTile = 64;          // places of a tile
-constexpr int64_t kMinShare = 4;   // tiles of a block, where there are as many
+constexpr int kMinPlaces = 256;  // of a block's share, where there are as many
 
 struct Split {
   unsigned int* status;   // workspace header
   unsigned int* verdict;  // [blocks]: what each block found
   int64_t* share;         // tiles per block
-  int64_t* first;         // [items]: position of the item's first tile
+  int64_t* cut;           // [blocks]: the item that begins in the block and goes on in the next, or -1
+  int64_t* cut_at;        // [blocks]: position of its first tile
   float* part;            // [blocks][2][rows (d + 2)]
   int64_t blocks, items;
-  int rows, chunks, part_floats;
+  int rows, tile, chunks, part_floats;
+  int64_t least;  // tiles of a share
 };
 inline int64_t pad256(int64_t b) { return (b + 255) / 256 * 256; }
 
-inline Split split_of(const AttnArgs& a, int rows, int per_sm) {
+inline Split split_of(const AttnArgs& a, int rows, int tile, int per_sm) {
   Split s{};
   s.rows = rows;
+  s.tile = tile;
+  s.least = kMinPlaces / tile;
   s.chunks = (a.T * a.rep + rows - 1) / rows;
   s.items = (int64_t)a.B * a.hk * s.chunks;
   s.blocks = a.sms * per_sm;
   // no more blocks than the table has tiles for
-  const int64_t tiles = ((((int64_t)a.t.max_pages << a.t.shift) + kTile - 1) / kTile + 1);
-  const int64_t most = s.items * ((tiles + kMinShare - 1) / kMinShare);
+  const int64_t tiles = ((((int64_t)a.t.max_pages << a.t.shift) + tile - 1) / tile + 1);
+  const int64_t most = s.items * ((tiles + s.least - 1) / s.least);
   if (most < s.blocks) s.blocks = most;
   s.part_floats = rows * (a.d + 2);
   return s;
 }
 inline size_t split_bytes(const Split& s) {
-  return kWsHeader + pad256(4 * s.blocks) + pad256(8) + pad256(8 * s.items) +
+  return kWsHeader + pad256(4 * s.blocks) + pad256(8) + 2 * pad256(8 * s.blocks) +
          pad256(s.blocks * 2 * s.part_floats * (int64_t)sizeof(float));
 }
 inline void split_place(Split& s, void* ws) {
@@ -54,8 +58,10 @@ inline void split_place(Split& s, void* ws) {
   p += pad256(4 * s.blocks);
   s.share = reinterpret_cast<int64_t*>(p);
   p += pad256(8);
-  s.first = reinterpret_cast<int64_t*>(p);
-  p += pad256(8 * s.items);
+  s.cut = reinterpret_cast<int64_t*>(p);
+  p += pad256(8 * s.blocks);
+  s.cut_at = reinterpret_cast<int64_t*>(p);
+  p += pad256(8 * s.blocks);
   s.part = reinterpret_cast<float*>(p);
 }
 
@@ -64,7 +70,7 @@ struct Keys {
   int64_t lo, hi;
   int64_t tiles;  // at least 1, so that an empty item has a block that writes its zeros
 };
-__device__ __forceinline__ Keys keys_of(const AttnArgs& a, int n) {
+__device__ __forceinline__ Keys keys_of(const AttnArgs& a, int tile, int n) {
   const int64_t cap = (int64_t)a.t.max_pages << a.t.shift, len = a.t.lens[n];
   Keys k;
   k.hi = len < 0 ? 0 : len < cap ? len : cap;
@@ -72,9 +78,9 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs& a, int n) {
   if (a.window > 0) {
     k.lo = len - a.T + 1 - a.window;
     k.lo = k.lo < 0 ? 0 : k.lo > k.hi ? k.hi : k.lo;
-    k.lo -= k.lo % kTile;
+    k.lo -= k.lo % tile;
   }
-  k.tiles = (k.hi - k.lo + kTile - 1) / kTile;
+  k.tiles = (k.hi - k.lo + tile - 1) / tile;
   if (k.tiles < 1) k.tiles = 1;
   return k;
 }
@@ -92,7 +98,7 @@ __device__ __forceinline__ bool find_start(const AttnArgs& a, const Split& s, in
   const int per = (a.B + NT - 1) / NT, n0 = min(tid * per, a.B), n1 = min(n0 + per, a.B);
   const int64_t each = (int64_t)a.hk * s.chunks;
   int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += keys_of(a, n).tiles;
+  for (int n = n0; n < n1; ++n) mine += keys_of(a, s.tile, n).tiles;
   int64_t up = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -108,7 +114,7 @@ __device__ __forceinline__ bool find_start(const AttnArgs& a, const Split& s, in
     total += scratch[w];
   }
   int64_t share = (total * each + s.blocks - 1) / s.blocks;
-  if (share < kMinShare) share = kMinShare;
+  if (share < s.least) share = s.least;
   if (blockIdx.x == 0 && tid == 0) *s.share = share;
   out.at = blockIdx.x * share;
   out.end = min(out.at + share, total * each);
@@ -116,7 +122,7 @@ __device__ __forceinline__ bool find_start(const AttnArgs& a, const Split& s, in
   if (before * each <= out.at && out.at < (before + mine) * each) {
     int n = n0;
     for (;; ++n) {
-      const int64_t t = keys_of(a, n).tiles;
+      const int64_t t = keys_of(a, s.tile, n).tiles;
       if (out.at < (before + t) * each) break;
       before += t;
     }
