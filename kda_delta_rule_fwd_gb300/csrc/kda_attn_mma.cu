@@ -25,8 +25,8 @@
 // byte permutation sorts by channel, so that a thread's outputs are pairs of adjacent channels.
 //
 // Places that a row does not see: the tiles at the ends of the seen range give them the weight 0,
-// and values that are not finite become zeros, whose rows get them added afterwards if they do
-// see them (0 times infinity would reach the others).
+// and values that are not finite become zeros there once the rows that do see them have got them
+// (0 times infinity would reach the others).
 #include "kda_attn_split.cuh"
 
 namespace kda {
@@ -38,6 +38,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // 16 bytes, or zeros when `have` is false
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool have) {
@@ -96,16 +99,23 @@ __device__ __forceinline__ void open4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     hi = *reinterpret_cast<const uint32_t*>(&y);
   }
 }
-// whether a half of the pair is an infinity or NaN; such halves are cleared
-template <bool kBf16>
-__device__ __forceinline__ bool clear_wild(uint32_t& w) {
-  constexpr uint32_t m = kBf16 ? 0x7f80u : 0x7c00u;
-  bool wild = false;
-  if ((w & m) == m) { w &= 0xffff0000u; wild = true; }
-  if (((w >> 16) & m) == m) { w &= 0xffffu; wild = true; }
-  return wild;
+// whether a 32-bit word of values (two bf16, or four e4m3 codes) holds one that is not finite
+template <int CACHE>
+__device__ __forceinline__ bool wild(uint32_t w) {
+  if constexpr (CACHE == KDA_CACHE_BF16) return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+  else if constexpr (CACHE == KDA_CACHE_E4M3) return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+  else return false;
 }
-
+template <int CACHE>
+__device__ __forceinline__ uint32_t tamed(uint32_t w) {  // such values as zeros
+  if constexpr (CACHE == KDA_CACHE_BF16) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+    return w;
+  } else {
+    return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+}
 __device__ __forceinline__ uint32_t transposed(uint32_t w) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
@@ -255,20 +265,30 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
           v[u] = static_cast<const char*>(a.vc) + from;
           if (kCoded && wm == 0 && ok && (lane >> 1) == u) {
             const int64_t b = (((int64_t)ids[u] * a.hk) << a.t.shift) + row;
-            copy16(smem_at(sc + stage * 2 * KT + (lane & 1) * KT + u * 16), (lane & 1 ? a.vs : a.ks) + b, true);
+            copy16(smem_at(sc + stage * 2 * KT + (lane & 1) * KT + u * 16), (lane & 1 ? a.vs : a.ks) + b);
           }
         }
+        constexpr int kTurns = KT * CH / 32 / WM, kRowsOf = 32 / CH;
+        if (seen == kAll) {
 #pragma unroll
-        for (int i = 0; i < KT * CH / 32 / WM; ++i) {
-          const int x = (i * WM + wm) * 32 + lane, r = x / CH, c = x % CH;
-          constexpr int rows_of = 32 / CH;
-          const int u = i * WM * rows_of / 16;
-          const bool ok = (r & 15) < have[u];
-          const int to = piece<CH>(r, c) * 16, from = ok ? (x % (16 * CH)) * 16 : 0;
-          copy16(dst + to, k[u] + from, ok);
-          copy16(dst + S::kHalf + to, v[u] + from, ok);
+          for (int i = 0; i < kTurns; ++i) {
+            const int x = (i * WM + wm) * 32 + lane, u = i * WM * kRowsOf / 16;
+            const int to = piece<CH>(x / CH, x % CH) * 16, from = (x % (16 * CH)) * 16;
+            copy16(dst + to, k[u] + from);
+            copy16(dst + S::kHalf + to, v[u] + from);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kTurns; ++i) {
+            const int x = (i * WM + wm) * 32 + lane, r = x / CH, u = r / 16;
+            const bool ok = (r & 15) < (KM == 2 && u ? have[KM - 1] : have[0]);
+            const int to = piece<CH>(r, x % CH) * 16, from = ok ? (x % (16 * CH)) * 16 : 0;
+            copy16(dst + to, (KM == 2 && u ? k[KM - 1] : k[0]) + from, ok);
+            copy16(dst + S::kHalf + to, (KM == 2 && u ? v[KM - 1] : v[0]) + from, ok);
+          }
         }
       } else {
+#pragma unroll 1
         for (int i = 0; i < KT * CH / 32 / WM; ++i) {
           const int x = (i * WM + wm) * 32 + lane, r = x / CH, c = x % CH;
           const int id = pos + r < (unsigned)ahead.hi ? page_of(a.t, ahead.n, pos + r) : -1;
@@ -301,7 +321,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
   };
 
   look();
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < S::kStages - 1; ++i) request(i);
   int stage = 0;
   // ldmatrix: the lane's row of 16 places and piece of two, (places, pieces) = 0 0, 1 0, 0 1, 1 1
@@ -396,7 +416,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       copy_wait<S::kStages - 2>();
       meet();
       request(stage == 0 ? S::kStages - 1 : stage - 1);
-      const char* const here = kv + stage * S::kStage;
+      char* const here = kv + stage * S::kStage;
       const uint8_t* const bytes = sc + stage * 2 * KT;
       const unsigned seen = seen_of[stage];
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
@@ -438,27 +458,42 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             }
           }
         }
-      float kf[KM][2], vf[KM][2];  // of places g and g + 8
+      // powers of two of places g and g + 8, each worked out by one lane; a value's relative to the
+      // largest so far, 0 for a row that is not finite (its readers become NaN through their sums)
+      float kf[KM][2], vf[KM][2];
       bool moved = false;
       float rise = 1.f;
+      unsigned nan_rows = 0;
       if constexpr (kCoded) {
-        const int mine = lane < KT && (seen >> lane & 1) ? bytes[KT + lane] : 0;
-        const int most = max(top, (int)__reduce_max_sync(0xffffffffu, mine == 255 ? 0 : mine));
+        const int kb = bytes[lane], vb = KT == 16 ? kb : bytes[KT + lane];
+        const bool mine = KT == 16 ? lane >= 16 && (seen >> (lane & 15) & 1) : seen >> lane & 1;
+        nan_rows = __ballot_sync(0xffffffffu, mine && vb == 255);
+        if (KT == 16) nan_rows >>= 16;
+        const int most = max(top, (int)__reduce_max_sync(0xffffffffu, mine && vb != 255 ? vb : 0));
         moved = most != top;
         rise = __uint_as_float((uint32_t)max(127 + top - most, 0) << 23);
         top = most;
+        const float vfac = vb == 255 ? 0.f : __uint_as_float((uint32_t)max(min(vb - top, 0) + 142, 0) << 23);
+        const float kfac = KT == 16 && lane >= 16 ? vfac : power(kb);
 #pragma unroll
         for (int u = 0; u < KM; ++u)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int at = u * 16 + e * 8 + g, b = bytes[KT + at];
-            kf[u][e] = power(bytes[at]);
-            vf[u][e] = __uint_as_float(b == 255 ? 0x7f800000u : (uint32_t)max(min(b - top, 0) + 142, 0) << 23);
+            kf[u][e] = __shfl_sync(0xffffffffu, kfac, u * 16 + e * 8 + g);
+            vf[u][e] = __shfl_sync(0xffffffffu, KT == 16 ? kfac : vfac, (KT == 16 ? 16 : u * 16) + e * 8 + g);
           }
       }
+      if constexpr (kCoded) {
+#pragma unroll
+        for (int u = 0; u < KM; ++u)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[u][j][e] *= kf[u][e >> 1];
+      }
       // ---- weights
-      unsigned on[NT][2];  // edge: the places that the query sees
       if (edge) {
+        unsigned on[NT][2];  // the places that a query sees
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -468,7 +503,54 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             unsigned m = end >= KT ? kAll : end <= 0 ? 0u : (1u << end) - 1;
             if (from > 0) m = from >= KT ? 0u : m & ~((1u << from) - 1);
             on[j][e] = m & seen;
+            if (on[j][e] & nan_rows) l[j][e] = NAN;
+#pragma unroll
+            for (int u = 0; u < KM; ++u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (!(on[j][e] >> (u * 16 + h * 8 + g) & 1)) c[u][j][2 * h + e] = -INFINITY;
           }
+        if (CACHE != KDA_CACHE_INT8) {
+          bool found = false;
+          for (int i = lane; i < S::kHalf / 16; i += 32) {
+            const uint4 w = reinterpret_cast<const uint4*>(here + S::kHalf)[i];
+            found |= wild<CACHE>(w.x) || wild<CACHE>(w.y) || wild<CACHE>(w.z) || wild<CACHE>(w.w);
+          }
+          if (__any_sync(0xffffffffu, found)) {
+            // the rows that do see such a value take it (their output stays so), then it is 0
+#pragma unroll 1
+            for (int key = 0; key < KT; ++key)
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int byte = (kCoded ? i * 16 + 2 * g + h : i * 16 + h * 8 + g) * S::kElem;
+                  const char* at = here + S::kHalf + piece<CH>(key, byte / 16) * 16 + byte % 16;
+                  float x;
+                  if constexpr (kCoded) x = (*reinterpret_cast<const uint8_t*>(at) & 0x7f) == 0x7f ? NAN : 0.f;
+                  else x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at));
+                  if (!isfinite(x)) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                      for (int e = 0; e < 2; ++e)
+                        if (on[j][e] >> key & 1) o[i][j][2 * h + e] += x;
+                  }
+                }
+            meet();
+            if (wm == 0)
+              for (int i = lane; i < S::kHalf / 4; i += 32) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(here + S::kHalf) + i;
+                *w = tamed<CACHE>(*w);
+              }
+            meet();
+          }
+        }
+      } else if (nan_rows) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) l[j][e] = NAN;
       }
       float al[NT][2];  // the outputs' factors
       uint32_t ph[KM][NT][2], pl[KM][NT][2];
@@ -482,8 +564,6 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float& x = c[u][j][2 * h + e];
-              if (kCoded) x *= kf[u][h];
-              if (edge && !(on[j][e] >> (u * 16 + h * 8 + g) & 1)) x = -INFINITY;
               mx = fmaxf(mx, x);
             }
 #pragma unroll
@@ -499,14 +579,9 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float& x = c[u][j][2 * h + e];
-              const bool off = edge && !(on[j][e] >> (u * 16 + h * 8 + g) & 1);
               x = exp2_of(fmaf(x, rf[j][e], -base));
-              if (off) x = 0.f;
               l[j][e] += x;
-              if (kCoded) {
-                x *= vf[u][h];
-                if (off) x = 0.f;
-              }
+              if (kCoded) x *= vf[u][h];
             }
         }
 #pragma unroll
@@ -534,7 +609,6 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             for (int e = 0; e < 4; ++e) o[i][j][e] *= al[j][e & 1];
       }
       // ---- outputs
-      bool wild = false;
 #pragma unroll
       for (int u = 0; u < KM; ++u)
 #pragma unroll
@@ -542,10 +616,6 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
           uint32_t b[4];
           matrix4_trans(b, vbase + piece<CH>(u * 16 + vrow, 2 * i + vcol) * 16);
           if constexpr (!kCoded) {
-            if (edge) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) wild |= clear_wild<true>(b[k]);
-            }
             const uint4 w = make_uint4(b[0], b[1], b[2], b[3]);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -558,40 +628,11 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
               uint4 w;  // even channels of places 0-7, odd ones, the same of 8-15
               open4<CACHE>(__byte_perm(b[2 * k], 0u, 0x3120), w.x, w.y);
               open4<CACHE>(__byte_perm(b[2 * k + 1], 0u, 0x3120), w.z, w.w);
-              if (CACHE == KDA_CACHE_E4M3 && edge) {
-                wild |= clear_wild<false>(w.x);
-                wild |= clear_wild<false>(w.y);
-                wild |= clear_wild<false>(w.z);
-                wild |= clear_wild<false>(w.w);
-              }
 #pragma unroll
               for (int j = 0; j < NT; ++j) product<false>(o[2 * i + k][j], w, ph[u][j][0], ph[u][j][1]);
             }
           }
         }
-      if (edge && CACHE != KDA_CACHE_INT8 && __any_sync(0xffffffffu, wild)) {
-        // the rows that do see such a value take it
-        const char* v = here + S::kHalf;
-#pragma unroll 1
-        for (int key = 0; key < KT; ++key)
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int byte = (kCoded ? i * 16 + 2 * g + h : i * 16 + h * 8 + g) * S::kElem;
-              const char* at = v + piece<CH>(key, byte / 16) * 16 + byte % 16;
-              float x;
-              if constexpr (kCoded) x = (*reinterpret_cast<const uint8_t*>(at) & 0x7f) == 0x7f ? NAN : 0.f;
-              else x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at));
-              if (!isfinite(x)) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    if (on[j][e] >> key & 1) o[i][j][2 * h + e] += x;
-              }
-            }
-      }
     }
 
     // ---- the item's end: the groups' outputs of the same rows join, one after the other
@@ -744,6 +785,15 @@ cudaError_t launch(Shape<CACHE, D, NT, WM, KT, PER>, const AttnArgs& a, const Sp
 #ifndef PER2
 #define PER2 2
 #endif
+#ifndef KT4
+#define KT4 16
+#endif
+#ifndef PER4
+#define PER4 2
+#endif
+#ifndef PERB4
+#define PERB4 1
+#endif
 #ifndef KT2
 #define KT2 32
 #endif
@@ -753,7 +803,7 @@ auto by_rows(const AttnArgs& a, F f) {
   const int rows = a.T * a.rep;
   if (rows <= 8) return f(Shape<CACHE, D, 1, 1, kCoded ? KT1 : 16, kCoded ? PER1 : PERB>());
   if (rows <= 16) return f(Shape<CACHE, D, 2, 1, kCoded ? KT2 : 16, PER2>());
-  if (rows <= 32) return f(Shape<CACHE, D, 4, 1, 16, kCoded ? 2 : 1>());
+  if (rows <= 32) return f(Shape<CACHE, D, 4, 1, kCoded ? KT4 : 16, kCoded ? PER4 : PERB4>());
   return f(Shape<CACHE, D, 4, 2, 16, 1>());
 }
 template <class F>
