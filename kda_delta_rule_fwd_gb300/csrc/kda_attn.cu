@@ -70,9 +70,11 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a, Split s) {
   int64_t before = work ? st.before : 0;
   for (int64_t at = work ? st.at : 0; work && at < st.end;) {
     const Keys keys = keys_of(a, s.tile, n);
-    const int64_t j = (at - before * each) / keys.tiles;       // head and chunk
-    const int64_t item_at = before * each + j * keys.tiles;    // the item's first tile
-    const int64_t t0 = at - item_at, t1 = min(keys.tiles, st.end - item_at);
+    const int64_t j = (at - before * each) / (keys.tiles + s.cost);       // head and chunk
+    const int64_t item_at = before * each + j * (keys.tiles + s.cost);
+    const int64_t tile_at = item_at + s.cost;                             // the item's first tile
+    if (tile_at >= st.end) break;
+    const int64_t t0 = max(at - tile_at, (int64_t)0), t1 = min(keys.tiles, st.end - tile_at);
     const int head = (int)(j / s.chunks), row0 = (int)(j % s.chunks) * kRows;
     const int rows = min(kRows, a.T * a.rep - row0);
     const int64_t len = a.t.lens[n];
@@ -215,9 +217,9 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a, Split s) {
 #pragma unroll
       for (int r = 0; r < kOwn; ++r) part[2 * kRows + (r0 + r) * D + c] = acc[r];
     }
-    at = item_at + t1;
+    at = tile_at + t1;
     if (t1 == keys.tiles && j == each - 1) {
-      before += keys.tiles;
+      before += keys.tiles + s.cost;
       ++n;
     }
   }
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
   const int n = (int)(item / each), head = (int)(item % each) / s.chunks;
   const int r = blockIdx.y, row = (int)(item % s.chunks) * s.rows + r;
   if (row >= a.T * a.rep) return;
-  const int64_t b0 = blockIdx.x, b1 = (s.cut_at[b0] + keys_of(a, s.tile, n).tiles - 1) / *s.share;
+  const int64_t b0 = blockIdx.x, b1 = (s.cut_at[b0] + s.cost + keys_of(a, s.tile, n).tiles - 1) / *s.share;
   float m = -INFINITY;
   for (int64_t b = b0 + tid; b <= b1; b += blockDim.x) m = fmaxf(m, part_of(s, b, b == b0)[r]);
 #pragma unroll
@@ -315,7 +317,7 @@ cudaError_t by_cache(const AttnArgs& a, const Split& s) {
 
 }  // namespace
 
-Split attn_general_split(const AttnArgs& a) { return split_of(a, kRows, kTile, 2); }
+Split attn_general_split(const AttnArgs& a) { return split_of(a, kRows, kTile, 1, 2); }
 
 // The join's blocks may be placed while the last of the main kernel's still run.
 template <typename T, int D>

@@ -33,7 +33,10 @@ namespace kda {
 namespace attn {
 namespace {
 
-constexpr int kGroups = 4;  // key groups of a block
+constexpr int kGroups = 4;    // key groups of a block
+// tiles that an item's beginning and end take the time of: the calls named at by_rows take 368, 334
+// and 342 us, and 249, 185 and 184, with 0, 4 and 8
+constexpr int kItemCost = 4;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
@@ -124,7 +127,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t w) {
 
 // Places of tiles in the block's share, item by item.
 struct Cursor {
-  int64_t left;     // tiles of the share from here on
+  int64_t left;     // of the share from here on
   int n, head, chunk;
   int t, tiles;     // tile of the item, the item's number
   int lo, hi;       // the sequence's places
@@ -140,6 +143,7 @@ struct Cursor {
     t += by;
     if (t < tiles) return;
     t = 0;
+    left -= s.cost;
     if (++chunk < s.chunks) return;
     chunk = 0;
     if (++head < a.hk) return;
@@ -160,10 +164,11 @@ struct Shape {
   static constexpr int kChunks = D * kElem / 16;           // 16-byte pieces of a row
   static constexpr int kHalf = KT * D * kElem;             // a group's keys (or values) of a tile
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kMergeWarp = 8 * NT * (D + 2) * 4;  // a warp's output, maxima and sums
+  static constexpr int kSlice = NT == 1 ? 16 : 32, kPitch = kSlice + 2;     // channels of all groups' rows that meet at once
+  static constexpr int kMerge = kGroups * kRows * kPitch * 4;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int bytes(int stages) {
-    return kGroups * stages * (kStage + 2 * KT + 4) + kQBytes + 8 * kRows + WM * kMergeWarp;
+    return kGroups * stages * (kStage + 2 * KT + 4) + kQBytes + 8 * kRows + kGroups * kRows * 8 + 2 * kMerge;
   }
   // as many stages as the SM's 228 KB hold for its blocks (each takes 1.5 KB for itself), up to six
   static constexpr int fit() {
@@ -177,9 +182,10 @@ struct Shape {
   static constexpr int oScale = oQ + kQBytes;
   static constexpr int oSeen = oScale + kGroups * kStages * 2 * KT;
   static constexpr int oRow = oSeen + kGroups * kStages * 4;
-  static constexpr int oMerge = oRow + 8 * kRows;
+  static constexpr int oStats = oRow + 8 * kRows;
+  static constexpr int oMerge = oStats + kGroups * kRows * 8;
   static constexpr int kBytes = bytes(kStages);
-  static_assert(oMerge % 16 == 0 && kMergeWarp % 16 == 0 && oMerge + WM * kMergeWarp == kBytes, "layout");
+  static_assert(oMerge % 16 == 0 && oMerge + 2 * kMerge == kBytes, "layout");
 };
 // a row's 16-byte piece c, moved so that 8 rows' pieces c lie in different banks
 template <int CHUNKS>
@@ -218,8 +224,12 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
     now.left = st.end - st.at;
     now.enter(a, s);
     const int64_t off = st.at - st.before * (a.hk * s.chunks);
-    const int j = (int)(off / now.tiles);
-    now.t = (int)(off % now.tiles);
+    const int all = now.tiles + s.cost, j = (int)(off / all);
+    now.t = (int)(off % all) - s.cost;
+    if (now.t < 0) {
+      now.left += now.t;
+      now.t = 0;
+    }
     now.head = j / s.chunks;
     now.chunk = j % s.chunks;
   }
@@ -339,25 +349,34 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       if ((int64_t)len > (int64_t)a.t.max_pages << a.t.shift) bad = 1;
       if (t0 == 0 && t1 < now.tiles) {
         s.cut[blockIdx.x] = ((int64_t)n * a.hk + head) * s.chunks + now.chunk;
-        s.cut_at[blockIdx.x] = st.end - now.left;
+        s.cut_at[blockIdx.x] = st.end - now.left - s.cost;
       }
     }
     __syncthreads();
-#pragma unroll 2
-    for (int r = warp; r < S::kRows; r += S::kThreads / 32) {
-      const int row = row0 + r, tok = row / a.rep;
-      __nv_bfloat162 x[D / 64];
+    constexpr int kTurns = S::kRows / (S::kThreads / 32);  // rows of a warp, all loaded before the first is used
+    __nv_bfloat162 held[kTurns][D / 64];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+      const int r = warp + k * (S::kThreads / 32), row = row0 + r, tok = row / a.rep;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)n * a.T + tok) * a.ldq +
                                (int64_t)(head * a.rep + row - tok * a.rep) * D;
-      uint32_t most = 0;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         const int p = lane + 32 * i;
-        x[i] = __floats2bfloat162_rn(0.f, 0.f);
+        held[k][i] = __floats2bfloat162_rn(0.f, 0.f);
         if (r < rows) {
-          if (words) x[i] = reinterpret_cast<const __nv_bfloat162*>(q)[p];
-          else { x[i].x = q[2 * p]; x[i].y = q[2 * p + 1]; }
+          if (words) held[k][i] = reinterpret_cast<const __nv_bfloat162*>(q)[p];
+          else { held[k][i].x = q[2 * p]; held[k][i].y = q[2 * p + 1]; }
         }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+      const int r = warp + k * (S::kThreads / 32), tok = (row0 + r) / a.rep;
+      const __nv_bfloat162 (&x)[D / 64] = held[k];
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
         most = max(most, max(__float_as_uint(__bfloat162float(x[i].x)) & 0x7fffffffu,
                              __float_as_uint(__bfloat162float(x[i].y)) & 0x7fffffffu));
       }
@@ -635,122 +654,111 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         }
     }
 
-    // ---- the item's end: the groups' outputs of the same rows join, one after the other
-    float* const buf = reinterpret_cast<float*>(raw + S::oMerge + wm * S::kMergeWarp);
-    constexpr int kM = 8 * NT * D, kL = kM + 8 * NT;
+    // ---- the item's end: the groups' outputs of the same rows, weighted by 2^(m - the largest m),
+    // add up through shared memory, kSlice channels at a time in two buffers by turns
+    const bool whole = t0 == 0 && t1 == now.tiles;
+    float2* const stats = reinterpret_cast<float2*>(raw + S::oStats);  // [groups][rows]: maximum, sum
+    float scale_by[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], i);
-    if (kCoded) {
-      const float f = power(top) * 0x1p-15f;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][j][e] *= f;
-    }
-#pragma unroll
-    for (int up = kGroups - 1; up > 0; --up) {
-      __syncthreads();
-      if (grp == up) {
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<float4*>(buf + ((i * NT + j) * 32 + lane) * 4) =
-                make_float4(o[i][j][0], o[i][j][1], o[i][j][2], o[i][j][3]);
-        if (g == 0) {
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              buf[kM + j * 8 + 2 * t4 + e] = y[j][e];
-              buf[kL + j * 8 + 2 * t4 + e] = l[j][e];
-            }
-        }
+        const float m = y[j][e] == -INFINITY ? -INFINITY : y[j][e] * rf[j][e];
+        if (g == 0) stats[grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e] = make_float2(m, l[j][e]);
       }
-      __syncthreads();
-      if (grp == 0) {
-        float fa[NT][2], fb[NT][2];
+    __syncthreads();
+    const float up = kCoded ? power(top) * 0x1p-15f : 1.f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float yo = buf[kM + j * 8 + 2 * t4 + e], lo = buf[kL + j * 8 + 2 * t4 + e];
-            const float yn = fmaxf(y[j][e], yo), base = yn == -INFINITY ? 0.f : yn * rf[j][e];
-            fa[j][e] = exp2_of(fmaf(y[j][e], rf[j][e], -base));
-            fb[j][e] = exp2_of(fmaf(yo, rf[j][e], -base));
-            l[j][e] = l[j][e] * fa[j][e] + lo * fb[j][e];
-            y[j][e] = yn;
-          }
+      for (int e = 0; e < 2; ++e) {
+        const int r = (wm * NT + j) * 8 + 2 * t4 + e;
+        float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
+        for (int i = 0; i < kGroups; ++i) m = fmaxf(m, stats[i * S::kRows + r].x);
+        scale_by[j][e] = exp2_of(stats[grp * S::kRows + r].x - (m == -INFINITY ? 0.f : m));
+      }
+    float* const part = part_of(s, blockIdx.x, t0 == 0 ? 1 : 0);
+    // the sum of a row, and its maximum
+    auto row_sum = [&](int r, float& m) {
+      m = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const float4 x = *reinterpret_cast<const float4*>(buf + ((i * NT + j) * 32 + lane) * 4);
-            o[i][j][0] = o[i][j][0] * fa[j][0] + x.x * fb[j][0];
-            o[i][j][1] = o[i][j][1] * fa[j][1] + x.y * fb[j][1];
-            o[i][j][2] = o[i][j][2] * fa[j][0] + x.z * fb[j][0];
-            o[i][j][3] = o[i][j][3] * fa[j][1] + x.w * fb[j][1];
-          }
+      for (int i = 0; i < kGroups; ++i) m = fmaxf(m, stats[i * S::kRows + r].x);
+      const float base = m == -INFINITY ? 0.f : m;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) sum += stats[i * S::kRows + r].y * exp2_of(stats[i * S::kRows + r].x - base);
+      return sum;
+    };
+    auto place_of = [&](int r) {  // the row's place in the output
+      const int row = row0 + r, tok = row / a.rep;
+      return ((int64_t)n * a.T + tok) * a.hq + head * a.rep + row - tok * a.rep;
+    };
+    if (tid < rows) {
+      float m;
+      const float sum = row_sum(tid, m);
+      if (!whole) {
+        part[tid] = m;
+        part[S::kRows + tid] = sum;
+      } else if (a.lse) {
+        a.lse[place_of(tid)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
       }
     }
-    // rows of channels, then out: whole items divided by their sums, parts as they are
-    const bool whole = t0 == 0 && t1 == now.tiles;
-    if (grp == 0) {
-      __syncwarp();
+    constexpr int kSlice = S::kSlice, kPairs = kSlice / 2;
+    // a thread's rows and channels of a slice are the same in every turn
+    constexpr int kPer = (S::kRows * kPairs + S::kThreads - 1) / S::kThreads;
+    float inverse[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = (i * S::kThreads + tid) / kPairs;
+      float m, sum = 1.f;
+      if (r < rows && whole) sum = row_sum(r, m);
+      inverse[i] = sum == 0.f ? 0.f : 1.f / sum;
+    }
+#pragma unroll
+    for (int q = 0; q < D / kSlice; ++q) {
+      float* const buf = reinterpret_cast<float*>(raw + S::oMerge + (q & 1) * S::kMerge);  // [groups][rows][kPitch]
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = j * 8 + 2 * t4 + e;
-          const float f = !whole ? 1.f : l[j][e] == 0.f ? 0.f : 1.f / l[j][e];
+          float* const to = buf + (grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e) * S::kPitch;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              buf[r * D + (kCoded ? i * 16 + 2 * g + h : i * 16 + h * 8 + g)] = o[i][j][2 * h + e] * f;
-          if (g == 0) {
-            buf[kM + r] = y[j][e] == -INFINITY ? -INFINITY : y[j][e] * rf[j][e];
-            buf[kL + r] = l[j][e];
+          for (int i = 0; i < kSlice / 16; ++i) {
+            const float x = o[q * (kSlice / 16) + i][j][e] * up * scale_by[j][e];
+            const float z = o[q * (kSlice / 16) + i][j][2 + e] * up * scale_by[j][e];
+            if constexpr (kCoded) {
+              *reinterpret_cast<float2*>(to + i * 16 + 2 * g) = make_float2(x, z);
+            } else {
+              to[i * 16 + g] = x;
+              to[i * 16 + 8 + g] = z;
+            }
           }
         }
-    }
-    __syncthreads();
-    {
-      const float* const from = reinterpret_cast<const float*>(raw + S::oMerge);
-      constexpr int kWarpFloats = S::kMergeWarp / 4;
-      float* const part = part_of(s, blockIdx.x, t0 == 0 ? 1 : 0);
-      for (int i = tid; i < rows * (D / 2); i += S::kThreads) {
-        const int r = i / (D / 2), ch = i % (D / 2) * 2, row = row0 + r, tok = row / a.rep;
-        const float2 x = *reinterpret_cast<const float2*>(from + r / (8 * NT) * kWarpFloats + r % (8 * NT) * D + ch);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int x = i * S::kThreads + tid, r = x / kPairs, ch = x % kPairs * 2;
+        if (r >= rows) break;
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+          const float2 w = *reinterpret_cast<const float2*>(buf + (k * S::kRows + r) * S::kPitch + ch);
+          v.x += w.x;
+          v.y += w.y;
+        }
         if (whole) {
-          const int64_t at = ((int64_t)n * a.T + tok) * a.hq + head * a.rep + row - tok * a.rep;
-          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at * D + ch;
+          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + place_of(r) * D + q * kSlice + ch;
           if (words) {
-            *reinterpret_cast<uint32_t*>(to) = layer::pack_bf16(x.x, x.y);
+            *reinterpret_cast<uint32_t*>(to) = layer::pack_bf16(v.x * inverse[i], v.y * inverse[i]);
           } else {
-            to[0] = __float2bfloat16_rn(x.x);
-            to[1] = __float2bfloat16_rn(x.y);
+            to[0] = __float2bfloat16_rn(v.x * inverse[i]);
+            to[1] = __float2bfloat16_rn(v.y * inverse[i]);
           }
         } else {
-          *reinterpret_cast<float2*>(part + 2 * S::kRows + r * D + ch) = x;
-        }
-      }
-      if (tid < rows) {
-        const float* w = from + tid / (8 * NT) * kWarpFloats + tid % (8 * NT);
-        const float m = w[kM], sum = w[kL];
-        const int row = row0 + tid, tok = row / a.rep;
-        if (!whole) {
-          part[tid] = m;
-          part[S::kRows + tid] = sum;
-        } else if (a.lse) {
-          a.lse[((int64_t)n * a.T + tok) * a.hq + head * a.rep + row - tok * a.rep] =
-              sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+          *reinterpret_cast<float2*>(part + 2 * S::kRows + r * D + q * kSlice + ch) = v;
         }
       }
     }
@@ -772,38 +780,19 @@ cudaError_t launch(Shape<CACHE, D, NT, WM, KT, PER>, const AttnArgs& a, const Sp
   return cudaGetLastError();
 }
 
-// f(Shape) for the rows of a call: 8, 16, 32 or 64 to a block
-#ifndef KT1
-#define KT1 16
-#endif
-#ifndef PER1
-#define PER1 4
-#endif
-#ifndef PERB
-#define PERB 2
-#endif
-#ifndef PER2
-#define PER2 2
-#endif
-#ifndef KT4
-#define KT4 16
-#endif
-#ifndef PER4
-#define PER4 2
-#endif
-#ifndef PERB4
-#define PERB4 1
-#endif
-#ifndef KT2
-#define KT2 32
-#endif
+// f(Shape) for the rows of a call: 8, 16, 32 or 64 to a block.  One GB300, us: 256 sequences of up
+// to 8192 e4m3 places, 4 rows: 32 places a group and 3 blocks to an SM 334, 16 and 4 blocks 389, 32
+// and 2 blocks 488 (before the ends were weighed in); 131071 bf16 places: 3 blocks 92, 2 blocks 94;
+// 16 sequences of up to 32768 int8 places, 32 rows: four eights to a warp 185, two 224 to 234 (codes
+// opened twice), four with 32 places a group 300 (one block to an SM).
 template <int CACHE, int D, class F>
 auto by_rows(const AttnArgs& a, F f) {
   constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
+  constexpr int kPlaces = kCoded ? 32 : 16;
   const int rows = a.T * a.rep;
-  if (rows <= 8) return f(Shape<CACHE, D, 1, 1, kCoded ? KT1 : 16, kCoded ? PER1 : PERB>());
-  if (rows <= 16) return f(Shape<CACHE, D, 2, 1, kCoded ? KT2 : 16, PER2>());
-  if (rows <= 32) return f(Shape<CACHE, D, 4, 1, kCoded ? KT4 : 16, kCoded ? PER4 : PERB4>());
+  if (rows <= 8) return f(Shape<CACHE, D, 1, 1, kPlaces, 3>());
+  if (rows <= 16) return f(Shape<CACHE, D, 2, 1, kPlaces, 2>());
+  if (rows <= 32) return f(Shape<CACHE, D, 4, 1, 16, kCoded ? 2 : 1>());
   return f(Shape<CACHE, D, 4, 2, 16, 1>());
 }
 template <class F>
@@ -821,7 +810,7 @@ auto by_type(const AttnArgs& a, F f) {
 }  // namespace
 
 Split attn_mma_split(const AttnArgs& a) {
-  return by_type(a, [&](auto shape) { return split_of(a, shape.kRows, shape.kTile, shape.kPerSm); });
+  return by_type(a, [&](auto shape) { return split_of(a, shape.kRows, shape.kTile, kItemCost, shape.kPerSm); });
 }
 
 cudaError_t launch_attn_mma(const AttnArgs& a) {

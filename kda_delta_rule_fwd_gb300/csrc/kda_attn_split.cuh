@@ -3,7 +3,8 @@
 // An item is a sequence, a key-value head and a chunk of up to `rows` query rows (tokens x query
 // heads of the group); its keys are tiles of `tile` places.  All items' tiles in a row, sequence
 // by sequence, are cut into equal shares, one per block: the lengths are on the device, so every
-// block counts the tiles by itself and finds its share.  A block walks the items of its share; an
+// block counts the tiles by itself and finds its share.  An item begins with `cost` places in the
+// row that stand for its own beginning and end, so that blocks with many short items get fewer tiles.  A block walks the items of its share; an
 // item that lies in it whole is written out, a part goes to the workspace as (maximum, sum,
 // unnormalised output) per row: a block has at most two parts, the rest of an item that begins in
 // an earlier block (slot 0) and the beginning of one that goes on in the next (slot 1).  The join
@@ -23,24 +24,25 @@ struct Split {
   unsigned int* verdict;  // [blocks]: what each block found
   int64_t* share;         // tiles per block
   int64_t* cut;           // [blocks]: the item that begins in the block and goes on in the next, or -1
-  int64_t* cut_at;        // [blocks]: position of its first tile
+  int64_t* cut_at;        // [blocks]: its position
   float* part;            // [blocks][2][rows (d + 2)]
   int64_t blocks, items;
-  int rows, tile, chunks, part_floats;
+  int rows, tile, cost, chunks, part_floats;
   int64_t least;  // tiles of a share
 };
 inline int64_t pad256(int64_t b) { return (b + 255) / 256 * 256; }
 
-inline Split split_of(const AttnArgs& a, int rows, int tile, int per_sm) {
+inline Split split_of(const AttnArgs& a, int rows, int tile, int cost, int per_sm) {
   Split s{};
   s.rows = rows;
   s.tile = tile;
+  s.cost = cost;
   s.least = kMinPlaces / tile;
   s.chunks = (a.T * a.rep + rows - 1) / rows;
   s.items = (int64_t)a.B * a.hk * s.chunks;
   s.blocks = a.sms * per_sm;
   // no more blocks than the table has tiles for
-  const int64_t tiles = ((((int64_t)a.t.max_pages << a.t.shift) + tile - 1) / tile + 1);
+  const int64_t tiles = ((((int64_t)a.t.max_pages << a.t.shift) + tile - 1) / tile + 1 + cost);
   const int64_t most = s.items * ((tiles + s.least - 1) / s.least);
   if (most < s.blocks) s.blocks = most;
   s.part_floats = rows * (a.d + 2);
@@ -88,7 +90,7 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs& a, int tile, int n) {
 // Where a block starts: item (n, j) with j = head and chunk, tile t of it; its tiles.
 struct Start {
   int64_t at, end;  // positions [at, end)
-  int64_t before;   // tiles of one (head, chunk) of the sequences before n
+  int64_t before;   // places in the row of one (head, chunk) of the sequences before n
   int n;
 };
 // All threads of the block take part (NT of them); `scratch` holds 34 values.
@@ -98,7 +100,7 @@ __device__ __forceinline__ bool find_start(const AttnArgs& a, const Split& s, in
   const int per = (a.B + NT - 1) / NT, n0 = min(tid * per, a.B), n1 = min(n0 + per, a.B);
   const int64_t each = (int64_t)a.hk * s.chunks;
   int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += keys_of(a, s.tile, n).tiles;
+  for (int n = n0; n < n1; ++n) mine += keys_of(a, s.tile, n).tiles + s.cost;
   int64_t up = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -122,7 +124,7 @@ __device__ __forceinline__ bool find_start(const AttnArgs& a, const Split& s, in
   if (before * each <= out.at && out.at < (before + mine) * each) {
     int n = n0;
     for (;; ++n) {
-      const int64_t t = keys_of(a, s.tile, n).tiles;
+      const int64_t t = keys_of(a, s.tile, n).tiles + s.cost;
       if (out.at < (before + t) * each) break;
       before += t;
     }
