@@ -91,15 +91,6 @@ __device__ __forceinline__ void decode8(uint2 v, float scale, float (&x)[8]) {
 }
 
 template <typename T, bool kWide>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  if constexpr (kWide) {
-    load<8>(p, x);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = to_f32(p[e]);
-  }
-}
-template <typename T, bool kWide>
 __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   if constexpr (kWide) {
     store<8>(p, x);
@@ -109,85 +100,145 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   }
 }
 
+// 8 values of a row as they lie in memory, held while in flight
+template <typename T, bool kWide> struct Held { layer::Raw<T, 8> v; };
+template <typename T> struct Held<T, false> { T v[8]; };
+template <typename T, bool kWide>
+__device__ __forceinline__ void fetch8(const T* p, Held<T, kWide>& h) {
+  if constexpr (kWide) {
+    h.v = fetch<T, 8>(p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h.v[e] = p[e];
+  }
+}
+template <typename T, bool kWide>
+__device__ __forceinline__ void open8(const Held<T, kWide>& h, float (&x)[8]) {
+  if constexpr (kWide) {
+    open<T, 8>(h.v, x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = to_f32(h.v[e]);
+  }
+}
+
+// A group of L = D / 8 lanes takes one head (of keys or of values) of the tile's tokens, kAhead of
+// them in flight; groups that outnumber the heads share a head's tokens.
+template <int D, class F>
+__device__ __forceinline__ void each_head(const CacheArgs& a, F f) {
+  constexpr int kGroups = kThreads / (D / 8);
+  const int group = threadIdx.x / (D / 8), heads = 2 * a.heads;
+  if (heads >= kGroups) {
+    for (int r = group; r < heads; r += kGroups) f(r >= a.heads, r >= a.heads ? r - a.heads : r, 0, 1);
+  } else {
+    const int ways = kGroups / heads, r = group % heads, way = group / heads;
+    if (way < ways) f(r >= a.heads, r >= a.heads ? r - a.heads : r, way, ways);
+  }
+}
+constexpr int kAhead = 4;
+
 template <typename T, int CACHE, int D, bool kWide>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a, int tile) {
   constexpr int L = D / 8;  // lanes of a row
-  constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
   __shared__ int2 place[kMaxTile];
   const int64_t t0 = (int64_t)blockIdx.x * tile;
   find_places(a, t0, tile, place);
-  const int lane = threadIdx.x % L, rows = tile * a.heads * 2;
-  for (int base = 0; base < rows; base += kThreads / L) {
-    const int r = base + threadIdx.x / L;
-    const int kv = r / (tile * a.heads), i = (r / a.heads) % tile, h = r % a.heads;
-    const int2 at = r < rows ? place[i] : make_int2(-2, 0);
-    float x[8];
+  const int lane = threadIdx.x % L;
+  // the lanes of a row leave and stay together
+  const unsigned mask = L == 32 ? 0xffffffffu : ((1u << L) - 1) << (threadIdx.x & 31 & ~(L - 1));
+  each_head<D>(a, [&](bool kv, int h, int first, int step) {
+    const int64_t ld = kv ? a.ldv : a.ldk;
+    const T* src = static_cast<const T*>(kv ? a.v : a.k) + t0 * ld + (int64_t)h * D + lane * 8;
+    void* const pool = kv ? a.vc : a.kc;
+    for (int base = first; base < tile; base += step * kAhead) {
+      Held<T, kWide> held[kAhead];
+      int2 at[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (at.x >= 0) {
-      const T* src = static_cast<const T*>(kv ? a.v : a.k) + (t0 + i) * (kv ? a.ldv : a.ldk) + h * D;
-      load8<T, kWide>(src + lane * 8, x);
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = base + k * step;
+        at[k] = i < tile ? place[i] : make_int2(-2, 0);
+        if (at[k].x >= 0) fetch8<T, kWide>(src + i * ld, held[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (at[k].x < 0) continue;  // the same for all lanes of the row
+        float x[8];
+        open8<T, kWide>(held[k], x);
+        const int64_t row = ((int64_t)h << a.t.shift) + at[k].y;
+        const int64_t to = at[k].x * a.ldpage + row * D + lane * 8;
+        if constexpr (CACHE == KDA_CACHE_F32) {
+          store<8>(static_cast<float*>(pool) + to, x);
+        } else if constexpr (CACHE == KDA_CACHE_BF16) {
+          store<8>(static_cast<__nv_bfloat16*>(pool) + to, x);
+        } else {
+          uint32_t m = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+          for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
+          // 448 = 1.75 2^8, 127 = 1.984375 2^6
+          constexpr uint32_t top = CACHE == KDA_CACHE_E4M3 ? 0x600000u : 0x7e0000u;
+          int e = (int)(m >> 23) - 127 - (CACHE == KDA_CACHE_E4M3 ? 8 : 6) + ((m & 0x7fffffu) > top);
+          e = max(e, -126);
+          const bool finite = m < 0x7f800000u;
+          uint2 code = encode8<CACHE>(x, __uint_as_float((uint32_t)(127 - e) << 23));
+          if (!finite) code = make_uint2(0u, 0u);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + to) = code;
+          if (lane == 0)
+            (kv ? a.vs : a.ks)[(((int64_t)at[k].x * a.heads) << a.t.shift) + row] = finite ? (uint8_t)(e + 127) : 255;
+        }
+      }
     }
-    const int64_t row = ((int64_t)h << a.t.shift) + at.y;
-    const int64_t to = at.x * a.ldpage + row * D + lane * 8;
-    void* pool = kv ? a.vc : a.kc;
-    if constexpr (!kCoded) {
-      if (at.x < 0) continue;
-      if constexpr (CACHE == KDA_CACHE_F32) store<8>(static_cast<float*>(pool) + to, x);
-      else store<8>(static_cast<__nv_bfloat16*>(pool) + to, x);
-    } else {
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (at.x < 0) continue;
-      // 448 = 1.75 2^8, 127 = 1.984375 2^6
-      constexpr uint32_t top = CACHE == KDA_CACHE_E4M3 ? 0x600000u : 0x7e0000u;
-      int e = (int)(m >> 23) - 127 - (CACHE == KDA_CACHE_E4M3 ? 8 : 6) + ((m & 0x7fffffu) > top);
-      e = max(e, -126);
-      const bool finite = m < 0x7f800000u;
-      uint2 code = encode8<CACHE>(x, __uint_as_float((uint32_t)(127 - e) << 23));
-      if (!finite) code = make_uint2(0u, 0u);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + to) = code;
-      if (lane == 0)
-        (kv ? a.vs : a.ks)[(((int64_t)at.x * a.heads) << a.t.shift) + row] = finite ? (uint8_t)(e + 127) : 255;
-    }
-  }
+  });
 }
+
+// 8 codes or values of a cache row
+template <int CACHE> struct Row8 { uint2 v; };
+template <> struct Row8<KDA_CACHE_F32> { layer::Raw<float, 8> v; };
+template <> struct Row8<KDA_CACHE_BF16> { layer::Raw<__nv_bfloat16, 8> v; };
 
 template <typename T, int CACHE, int D, bool kWide>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs a, int tile) {
   constexpr int L = D / 8;
   constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
+  constexpr int kElem = CACHE == KDA_CACHE_F32 ? 4 : CACHE == KDA_CACHE_BF16 ? 2 : 1;
   __shared__ int2 place[kMaxTile];
   const int64_t t0 = (int64_t)blockIdx.x * tile;
   find_places(a, t0, tile, place);
-  const int lane = threadIdx.x % L, rows = tile * a.heads * 2;
-  for (int base = 0; base < rows; base += kThreads / L) {
-    const int r = base + threadIdx.x / L;
-    const int kv = r / (tile * a.heads), i = (r / a.heads) % tile, h = r % a.heads;
-    const int2 at = r < rows ? place[i] : make_int2(-2, 0);
-    T* out = static_cast<T*>(kv ? a.vo : a.ko);
-    if (at.x == -2 || !out) continue;
-    float x[8];
+  const int lane = threadIdx.x % L;
+  each_head<D>(a, [&](bool kv, int h, int first, int step) {
+    T* const out = static_cast<T*>(kv ? a.vo : a.ko);
+    if (!out) return;
+    const char* const pool = static_cast<const char*>(kv ? a.vc : a.kc);
+    for (int base = first; base < tile; base += step * kAhead) {
+      Row8<CACHE> held[kAhead];
+      uint8_t byte[kAhead];
+      int2 at[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (at.x >= 0) {
-      const int64_t row = ((int64_t)h << a.t.shift) + at.y;
-      const int64_t from = at.x * a.ldpage + row * D + lane * 8;
-      const void* pool = kv ? a.vc : a.kc;
-      if constexpr (CACHE == KDA_CACHE_F32) {
-        load<8>(static_cast<const float*>(pool) + from, x);
-      } else if constexpr (CACHE == KDA_CACHE_BF16) {
-        load<8>(static_cast<const __nv_bfloat16*>(pool) + from, x);
-      } else {
-        const float s = power((kv ? a.vs : a.ks)[(((int64_t)at.x * a.heads) << a.t.shift) + row]);
-        decode8<CACHE>(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) + from), s, x);
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = base + k * step;
+        at[k] = i < tile ? place[i] : make_int2(-2, 0);
+        if (at[k].x >= 0) {
+          const int64_t row = ((int64_t)h << a.t.shift) + at[k].y;
+          held[k] = *reinterpret_cast<const Row8<CACHE>*>(pool + (at[k].x * a.ldpage + row * D + lane * 8) * kElem);
+          if (kCoded) byte[k] = (kv ? a.vs : a.ks)[(((int64_t)at[k].x * a.heads) << a.t.shift) + row];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (at[k].x == -2) continue;
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        if (at[k].x >= 0) {
+          if constexpr (CACHE == KDA_CACHE_F32) open<float, 8>(held[k].v, x);
+          else if constexpr (CACHE == KDA_CACHE_BF16) open<__nv_bfloat16, 8>(held[k].v, x);
+          else decode8<CACHE>(held[k].v, power(byte[k]), x);
+        }
+        store8<T, kWide>(out + ((t0 + base + k * step) * a.heads + h) * D + lane * 8, x);
       }
     }
-    store8<T, kWide>(out + ((t0 + i) * a.heads + h) * D + lane * 8, x);
-  }
+  });
 }
 
 template <typename T, int CACHE, int D, bool kWide>

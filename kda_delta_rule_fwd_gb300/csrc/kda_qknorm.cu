@@ -190,37 +190,52 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
   int64_t item = (int64_t)block * kGroups + group;
   int64_t first = (int64_t)block * kGroups + threadIdx.x / 32 * (32 / TPR);
   Raw<T, VEC> x[2], dy[2];
-  const auto fetch_row = [&](int64_t it, int h) {
-    const int64_t tok = it / parts;
-    const int head = (int)(it - tok * parts) * per + h;
-    const bool on = it < items && head < p.heads;
+  struct Place {
+    const T *x, *dy;  // the item's first row
+    int64_t row;      // its place among the dense rows
+    int rows, tok_pos;
+  };
+  const auto locate = [&](int64_t it) {
+    Place l{nullptr, nullptr, 0, 0, 0};
+    if (it < items) {
+      const int64_t tok = parts == 1 ? it : it / parts;
+      const int head = (int)(it - tok * parts) * per;
+      l.row = tok * p.heads + head;
+      l.x = static_cast<const T*>(p.x) + tok * p.ld + head * a.d;
+      if (kBwd) l.dy = static_cast<const T*>(p.dy) + l.row * a.d;
+      l.rows = min(per, p.heads - head);
+      l.tok_pos = half ? a.pos[tok] : 0;
+    }
+    return l;
+  };
+  const auto fetch_row = [&](const Place& l, int h) {
+    const bool on = h < l.rows;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       x[i] = Raw<T, VEC>{};
       if (kBwd) dy[i] = Raw<T, VEC>{};
       if (on && at[i] >= 0) {
-        x[i] = fetch<T, VEC>(static_cast<const T*>(p.x) + tok * p.ld + head * a.d + at[i]);
-        if (kBwd) dy[i] = fetch<T, VEC>(static_cast<const T*>(p.dy) + (tok * p.heads + head) * a.d + at[i]);
+        x[i] = fetch<T, VEC>(l.x + h * a.d + at[i]);
+        if (kBwd) dy[i] = fetch<T, VEC>(l.dy + h * a.d + at[i]);
       }
     }
     return on;
   };
-  bool on = fetch_row(item, 0);
-  int pos = half && item < items ? a.pos[item / parts] : 0;
-  for (; first < items; first += step, item += step) {
+  Place now = locate(item);
+  bool on = fetch_row(now, 0);
+  for (; first < items; first += step) {
     float cs[VEC], sn[VEC];  // halves: of the thread's pairs; adjacent: of the two chunks' pairs in a row
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const int c = e < VEC / 2 ? at[0] + 2 * e : at[1] + 2 * e - VEC;
       const int j = kInter ? c >> 1 : at[0] + e;
       const bool turn = kInter ? (e < VEC / 2 ? at[0] : at[1]) >= 0 && j < half : turned && j < half;
-      const float2 r = turn ? angle(turns[j], pos) : make_float2(1.f, 0.f);
+      const float2 r = turn ? angle(turns[j], now.tok_pos) : make_float2(1.f, 0.f);
       cs[e] = r.x;
       sn[e] = r.y;
     }
-    if (half && item + step < items) pos = a.pos[(item + step) / parts];
-    const int64_t tok = item / parts;
-    const int head0 = (int)(item - tok * parts) * per;
+    item += step;
+    const Place next = locate(item);
     for (int h = 0; h < per; ++h) {
       float v[2][VEC], g[2][VEC];
       const bool here = on;
@@ -229,7 +244,7 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
         open<T, VEC>(x[i], v[i]);
         if (kBwd) open<T, VEC>(dy[i], g[i]);
       }
-      on = h + 1 < per ? fetch_row(item, h + 1) : fetch_row(item + step, 0);
+      on = h + 1 < per ? fetch_row(now, h + 1) : fetch_row(next, 0);
       float k = 1.f;
       if (p.w) {
         float2 ss = make_float2(0.f, 0.f);
@@ -256,10 +271,14 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
             }
         } else {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float d = sign * sn[e], u = y[0][e], t = y[1][e];
-            y[0][e] = u * cs[e] - t * d;
-            y[1][e] = u * d + t * cs[e];
+          for (int e = 0; e < VEC; e += 2) {
+            const float2 c = make_float2(cs[e], cs[e + 1]), d = make_float2(sign * sn[e], sign * sn[e + 1]);
+            const float2 u = make_float2(y[0][e], y[0][e + 1]), t = make_float2(y[1][e], y[1][e + 1]);
+            const float2 f = fma2(u, c, mul2(t, make_float2(-d.x, -d.y))), q = fma2(t, c, mul2(u, d));
+            y[0][e] = f.x;
+            y[0][e + 1] = f.y;
+            y[1][e] = q.x;
+            y[1][e + 1] = q.y;
           }
         }
       };
@@ -288,12 +307,13 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
         }
       }
       if (here) {
-        T* y = static_cast<T*>(kBwd ? p.dx : p.y) + (tok * p.heads + head0 + h) * a.d;
+        T* y = static_cast<T*>(kBwd ? p.dx : p.y) + (now.row + h) * a.d;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if (at[i] >= 0) store<VEC>(y + at[i], kBwd ? g[i] : v[i]);
       }
     }
+    now = next;
   }
   if (!kBwd || !p.dw) return;
   __shared__ float fold[kBwd ? kGroups * 2 * TPR * VEC : 1];

@@ -24,9 +24,17 @@ using layer::open;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 using u64 = unsigned long long;
 
-__device__ __forceinline__ long long fixed(float p) {
-  p = p > 0.f ? fminf(p, 1.f) : 0.f;  // NaN: 0
-  return __float2ll_rn(p * 17592186044416.f);
+// A probability as hi 2^22 + lo: hi = p 2^22 to the nearest, lo = what is left to the nearest 2^-44,
+// both read off the mantissas of sums with a number so large that its last bit counts one (hi 2^22
+// is even, so ties of lo go to the even whole; a conversion to 64 bits issues at a quarter of this).
+struct Fixed {
+  int hi, lo;  // with the large numbers' own bits, which differences lose
+};
+__device__ __forceinline__ Fixed fixed(float p) {
+  const float x = __saturatef(p) * 4194304.f;  // NaN and below 0: 0
+  const float h = x + 8388608.f;
+  const float l = fmaf(x - (h - 8388608.f), 4194304.f, 12582912.f);
+  return {__float_as_int(h), __float_as_int(l)};
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
@@ -45,7 +53,9 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {
   return v;
 }
 
-// Weights of a lane's tokens in a run: VEC in a row (aligned rows), else lane, lane + 32, ...
+// Weights of a lane's tokens in a batch: VEC in a row (aligned rows), else lane, lane + 32, ...
+// A run is kBatches of them, requested together and added up before the warp's sum.
+constexpr int kBatches = 4;
 template <typename T, bool kWide>
 struct Weights {
   static constexpr int VEC = 16 / sizeof(T), kRun = 32 * VEC;
@@ -78,13 +88,17 @@ struct Weights {
   __device__ __forceinline__ void weigh(int r, const Held& h, u64 (&w)[VEC]) const {
     float x[VEC], y[VEC];
     open<T, VEC>(h.p, x);
-    open<T, VEC>(h.q, y);
+    open<T, VEC>(h.q, y);  // zeros without q
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      long long d = fixed(x[e]);
-      if (q) d -= fixed(y[e]);
-      if (token(r, e) == certain) d -= 1ll << 44;
+      const Fixed f = fixed(x[e]), g = fixed(y[e]);
+      const long long d = (long long)(f.hi - g.hi) * (1 << 22) + (f.lo - g.lo);
       w[e] = d > 0 ? (u64)d : 0;
+    }
+    if (certain >= 0 && certain / kRun == r) {  // q = 1 there, p at most that
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (token(r, e) == certain) w[e] = 0;
     }
   }
 };
@@ -137,27 +151,25 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyArgs a, int p
     if (q) w.q = q + (int64_t)kept * a.V;
     else w.certain = drafts[kept];
   }
-  const int first = rank * per, runs = min(per, (a.V + W::kRun - 1) / W::kRun - first);  // may be below 0
+  const int first = rank * per, runs = min(per, (a.V + W::kRun * kBatches - 1) / (W::kRun * kBatches) - first);  // may be below 0
   const u64 m = (u64)(fminf(fmaxf(u[a.K], 0.f), 0.99999994f) * 16777216.f);
   for (int turn = 0;; ++turn) {
     u64 sum = 0;
-    constexpr int kAhead = 4;  // runs in flight
-    for (int r = warp; r < runs; r += kWarps * kAhead) {
-      typename W::Held h[kAhead];
+    for (int r = warp; r < runs; r += kWarps) {
+      typename W::Held h[kBatches];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (r + i * kWarps < runs) w.request(first + r + i * kWarps, h[i]);
+      for (int i = 0; i < kBatches; ++i) w.request((first + r) * kBatches + i, h[i]);
+      u64 s = 0;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (r + i * kWarps >= runs) break;
-        u64 x[W::VEC], s = 0;
-        w.weigh(first + r + i * kWarps, h[i], x);
+      for (int i = 0; i < kBatches; ++i) {
+        u64 x[W::VEC];
+        w.weigh((first + r) * kBatches + i, h[i], x);
 #pragma unroll
         for (int e = 0; e < W::VEC; ++e) s += x[e];
-        s = warp_sum(s);
-        if (lane == 0) run[r + i * kWarps] = s;
-        sum += s;
       }
+      s = warp_sum(s);
+      if (lane == 0) run[r] = s;
+      sum += s;
     }
     if (lane == 0) total_of[warp] = sum;
     __syncthreads();
@@ -200,33 +212,39 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyArgs a, int p
       }
       left -= __shfl_sync(0xffffffffu, up, 31);
     }
-    typename W::Held h;
-    u64 x[W::VEC];
-    w.request(first + at, h);
-    w.weigh(first + at, h, x);
-    if (kWide) {
-      u64 s = 0;
+    bool found = false;
+    for (int k = 0; k < kBatches && !found; ++k) {
+      const int batch = (first + at) * kBatches + k;
+      typename W::Held h;
+      u64 x[W::VEC];
+      w.request(batch, h);
+      w.weigh(batch, h, x);
+      if (kWide) {
+        u64 s = 0;
 #pragma unroll
-      for (int e = 0; e < W::VEC; ++e) s += x[e];
-      u64 up = warp_scan(s) - s;
-      int token = -1;
+        for (int e = 0; e < W::VEC; ++e) s += x[e];
+        const u64 up = warp_scan(s);
+        u64 past = up - s;
+        int token = -1;
 #pragma unroll
-      for (int e = 0; e < W::VEC; ++e) {
-        up += x[e];
-        if (token < 0 && up > left) token = w.token(first + at, e);
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, token >= 0);
-      if (past && lane == __ffs(past) - 1) tokens[kept] = token;
-    } else {
-#pragma unroll
-      for (int e = 0; e < W::VEC; ++e) {
-        const u64 up = warp_scan(x[e]);
-        const unsigned past = __ballot_sync(0xffffffffu, up > left);
-        if (past) {
-          if (lane == __ffs(past) - 1) tokens[kept] = w.token(first + at, e);
-          break;
+        for (int e = 0; e < W::VEC; ++e) {
+          past += x[e];
+          if (token < 0 && past > left) token = w.token(batch, e);
         }
+        const unsigned who = __ballot_sync(0xffffffffu, token >= 0);
+        if (who && lane == __ffs(who) - 1) tokens[kept] = token;
+        found = who != 0;
         left -= __shfl_sync(0xffffffffu, up, 31);
+      } else {
+#pragma unroll
+        for (int e = 0; e < W::VEC; ++e) {
+          const u64 up = warp_scan(x[e]);
+          const unsigned past = __ballot_sync(0xffffffffu, up > left);
+          if (!found && past && lane == __ffs(past) - 1) tokens[kept] = w.token(batch, e);
+          found |= past != 0;
+          if (found) break;
+          left -= __shfl_sync(0xffffffffu, up, 31);
+        }
       }
     }
     break;
@@ -237,10 +255,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyArgs a, int p
 template <typename T, bool kWide>
 cudaError_t launch(const VerifyArgs& a) {
   using W = Weights<T, kWide>;
-  // blocks per sequence: as many as fill the device four times, with 16 runs to a block at least
-  const int runs = (a.V + W::kRun - 1) / W::kRun;
+  // blocks per sequence: as many as fill the device four times, with a run for half of the warps
+  const int runs = (a.V + W::kRun * kBatches - 1) / (W::kRun * kBatches);
   int blocks = 1;
-  while (blocks < 8 && (int64_t)a.B * blocks < 4 * a.sms && runs >= 32 * blocks) blocks *= 2;
+  while (blocks < 8 && (int64_t)a.B * blocks < 4 * a.sms && runs >= kWarps * blocks) blocks *= 2;
   const int per = (runs + blocks - 1) / blocks;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)a.B * blocks);
