@@ -17,17 +17,36 @@ namespace {
 
 using namespace layer;
 
-constexpr int kThreads = 256, kMaxTile = 16;
+#ifndef MT_
+#define MT_ 16
+#endif
+constexpr int kThreads = 256, kMaxTile = MT_;
 
 // Places of the tile's tokens: the page and the row in it, page -1 for a token without a place
 // and -2 for one of no sequence (behind the last).
+// (One warp: each step of the search for the first token's sequence looks at 32 offsets at once.)
+__device__ __forceinline__ int find_seq(const Seqs& q, int64_t t) {
+  if (!q.cu) return (int)(t / q.T);
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = q.N;  // the last of [lo, lo + n) that begins at t or before (or lo)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, lane * step < n && (int64_t)q.cu[at] <= t);
+    const int i = le ? 31 - __clz(le) : 0;
+    n = min(step, n - i * step);
+    lo += i * step;
+  }
+  return lo;
+}
 __device__ __forceinline__ void find_places(const CacheArgs& a, int64_t t0, int tile, int2* place) {
   const int i = threadIdx.x;
-  if (i < tile) {
+  if (i < 32) {
+    int n = find_seq(a.q, t0);
     int2 r = make_int2(-2, 0);
     const int64_t t = t0 + i;
-    if (t < a.q.total) {
-      const int n = a.q.find(t);
+    if (i < tile && t < a.q.total) {
+      if (!a.q.cu) n = (int)(t / a.q.T);
+      else while (n + 1 < a.q.N && (int64_t)a.q.cu[n + 1] <= t) ++n;
       int64_t start, end;
       a.q.range(n, start, end);
       if (t >= start && t < end) {
@@ -40,7 +59,7 @@ __device__ __forceinline__ void find_places(const CacheArgs& a, int64_t t0, int 
         }
       }
     }
-    place[i] = r;
+    if (i < tile) place[i] = r;
   }
   // one block looks over the offsets
   if (blockIdx.x == 0 && a.status && a.q.cu)
@@ -135,10 +154,16 @@ __device__ __forceinline__ void each_head(const CacheArgs& a, F f) {
     if (way < ways) f(r >= a.heads, r >= a.heads ? r - a.heads : r, way, ways);
   }
 }
-constexpr int kAhead = 4;
+#ifndef CAHEAD
+#define CAHEAD 4
+#endif
+#ifndef CPER
+#define CPER 4
+#endif
+constexpr int kAhead = CAHEAD;
 
 template <typename T, int CACHE, int D, bool kWide>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a, int tile) {
+__global__ void __launch_bounds__(kThreads, CPER) cache_write_kernel(CacheArgs a, int tile) {
   constexpr int L = D / 8;  // lanes of a row
   __shared__ int2 place[kMaxTile];
   const int64_t t0 = (int64_t)blockIdx.x * tile;
@@ -198,7 +223,7 @@ template <> struct Row8<KDA_CACHE_F32> { layer::Raw<float, 8> v; };
 template <> struct Row8<KDA_CACHE_BF16> { layer::Raw<__nv_bfloat16, 8> v; };
 
 template <typename T, int CACHE, int D, bool kWide>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs a, int tile) {
+__global__ void __launch_bounds__(kThreads, CPER) cache_read_kernel(CacheArgs a, int tile) {
   constexpr int L = D / 8;
   constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
   constexpr int kElem = CACHE == KDA_CACHE_F32 ? 4 : CACHE == KDA_CACHE_BF16 ? 2 : 1;

@@ -15,7 +15,6 @@ namespace {
 
 using layer::Raw;
 using layer::dot_v;
-using layer::fetch;
 using layer::fma_v;
 using layer::mul_v;
 using layer::open;
@@ -141,6 +140,12 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) qknorm_narrow_kernel(QKArgs
   }
 }
 
+// 16 bytes into shared memory, or zeros
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(have ? 16 : 0) : "memory");
+}
+
 // Aligned rows: TPR threads hold a row in two chunks of 16 bytes each, chosen so that both members
 // of a pair are in one thread (chunk c and c + rot / 2 of halves, adjacent channels of one chunk),
 // and nothing but the row's sum leaves a thread.  A group of TPR threads takes a token's heads (or
@@ -148,11 +153,24 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) qknorm_narrow_kernel(QKArgs
 // and request the next row before they work on the present one; a block serves q or k, in
 // proportion to their heads, so that its weights and its sums for their gradient stay in registers.
 constexpr int kWide = 256;  // threads of a block
-template <bool kBwd> constexpr int wide_blocks() { return kBwd ? 2 : 3; }
+#ifndef QF
+#define QF 3
+#endif
+#ifndef QD
+#define QD 4
+#endif
+#ifndef QDB
+#define QDB 4
+#endif
+template <bool kBwd> constexpr int wide_blocks() { return kBwd ? 2 : QF; }
+// rows in flight
+template <bool kBwd> constexpr int wide_ahead() { return kBwd ? QDB : QD; }
 
 template <typename T, int TPR, bool kInter, bool kBwd>
 __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel(QKArgs a, int2 per_of) {
   constexpr int VEC = 16 / sizeof(T), kGroups = kWide / TPR;
+  constexpr int kAhead = wide_ahead<kBwd>(), kWords = kBwd ? 4 : 2;  // 16-byte words of a thread's row
+  extern __shared__ uint4 ring[];  // [kAhead][kWords][kWide]: each thread copies what it reads itself
   __shared__ u64 turns[128];
   const bool second = (int)blockIdx.x >= a.p[0].ctas;
   const QKPart& p = a.p[second];
@@ -189,7 +207,6 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
   const int64_t items = a.tokens * parts, step = (int64_t)p.ctas * kGroups;
   int64_t item = (int64_t)block * kGroups + group;
   int64_t first = (int64_t)block * kGroups + threadIdx.x / 32 * (32 / TPR);
-  Raw<T, VEC> x[2], dy[2];
   struct Place {
     const T *x, *dy;  // the item's first row
     int64_t row;      // its place among the dense rows
@@ -208,43 +225,55 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
     }
     return l;
   };
-  const auto fetch_row = [&](const Place& l, int h) {
-    const bool on = h < l.rows;
+  // the next row to request: head `req_h` of the item at `req`
+  Place req = locate(item);
+  int64_t req_item = item;
+  int req_h = 0;
+  const auto request = [&](int slot) {
+    const bool on = req_h < req.rows;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      x[i] = Raw<T, VEC>{};
-      if (kBwd) dy[i] = Raw<T, VEC>{};
-      if (on && at[i] >= 0) {
-        x[i] = fetch<T, VEC>(l.x + h * a.d + at[i]);
-        if (kBwd) dy[i] = fetch<T, VEC>(l.dy + h * a.d + at[i]);
-      }
+      uint4* const to = ring + (slot * kWords + i) * kWide + threadIdx.x;
+      const bool have = on && at[i] >= 0;
+      copy16(to, have ? req.x + req_h * a.d + at[i] : static_cast<const T*>(p.x), have);
+      if (kBwd) copy16(to + 2 * kWide, have ? req.dy + req_h * a.d + at[i] : static_cast<const T*>(p.dy), have);
     }
-    return on;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++req_h == per) {
+      req_h = 0;
+      req_item += step;
+      req = locate(req_item);
+    }
   };
-  Place now = locate(item);
-  bool on = fetch_row(now, 0);
-  for (; first < items; first += step) {
-    float cs[VEC], sn[VEC];  // halves: of the thread's pairs; adjacent: of the two chunks' pairs in a row
+  Place now = req;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int c = e < VEC / 2 ? at[0] + 2 * e : at[1] + 2 * e - VEC;
-      const int j = kInter ? c >> 1 : at[0] + e;
-      const bool turn = kInter ? (e < VEC / 2 ? at[0] : at[1]) >= 0 && j < half : turned && j < half;
-      const float2 r = turn ? angle(turns[j], now.tok_pos) : make_float2(1.f, 0.f);
-      cs[e] = r.x;
-      sn[e] = r.y;
-    }
-    item += step;
-    const Place next = locate(item);
-    for (int h = 0; h < per; ++h) {
+  for (int d = 0; d < kAhead; ++d) request(d);
+  int h = 0, slot = 0;
+  float cs[VEC], sn[VEC];  // halves: of the thread's pairs; adjacent: of the two chunks' pairs in a row
+  while (first < items) {
+    {
+      if (h == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const int c = e < VEC / 2 ? at[0] + 2 * e : at[1] + 2 * e - VEC;
+          const int j = kInter ? c >> 1 : at[0] + e;
+          const bool turn = kInter ? (e < VEC / 2 ? at[0] : at[1]) >= 0 && j < half : turned && j < half;
+          const float2 r = turn ? angle(turns[j], now.tok_pos) : make_float2(1.f, 0.f);
+          cs[e] = r.x;
+          sn[e] = r.y;
+        }
+      }
       float v[2][VEC], g[2][VEC];
-      const bool here = on;
+      const bool here = h < now.rows;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        open<T, VEC>(x[i], v[i]);
-        if (kBwd) open<T, VEC>(dy[i], g[i]);
+        const uint4* const from = ring + (slot * kWords + i) * kWide + threadIdx.x;
+        open<T, VEC>(*reinterpret_cast<const Raw<T, VEC>*>(from), v[i]);
+        if (kBwd) open<T, VEC>(*reinterpret_cast<const Raw<T, VEC>*>(from + 2 * kWide), g[i]);
       }
-      on = h + 1 < per ? fetch_row(now, h + 1) : fetch_row(next, 0);
+      request(slot);
+      slot = slot + 1 == kAhead ? 0 : slot + 1;
       float k = 1.f;
       if (p.w) {
         float2 ss = make_float2(0.f, 0.f);
@@ -312,11 +341,19 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
         for (int i = 0; i < 2; ++i)
           if (at[i] >= 0) store<VEC>(y + at[i], kBwd ? g[i] : v[i]);
       }
+      if (++h == per) {
+        h = 0;
+        first += step;
+        item += step;
+        now = locate(item);
+      }
     }
-    now = next;
   }
   if (!kBwd || !p.dw) return;
-  __shared__ float fold[kBwd ? kGroups * 2 * TPR * VEC : 1];
+  static_assert(kAhead * kWords * 16 >= 2 * VEC * 4, "room for the sums");
+  float* const fold = reinterpret_cast<float*>(ring);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     if (at[i] >= 0) {
@@ -386,7 +423,10 @@ void launch_wide(QKArgs& a) {
   }
   const int grid = a.p[0].ctas + a.p[1].ctas;
   if (grid == 0) return;
-  qknorm_wide_kernel<T, TPR, kInter, kBwd><<<grid, kWide, 0, a.stream>>>(a, make_int2(per[0], per[1]));
+  constexpr int bytes = wide_ahead<kBwd>() * (kBwd ? 4 : 2) * kWide * 16;
+  if (bytes > 40 * 1024)  // with the table more than a block gets unasked
+    cudaFuncSetAttribute(qknorm_wide_kernel<T, TPR, kInter, kBwd>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  qknorm_wide_kernel<T, TPR, kInter, kBwd><<<grid, kWide, bytes, a.stream>>>(a, make_int2(per[0], per[1]));
 }
 template <typename T, int TPR>
 void by_kind(QKArgs& a, bool bwd) {

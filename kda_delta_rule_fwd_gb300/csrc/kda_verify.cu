@@ -21,7 +21,12 @@ using layer::Raw;
 using layer::fetch;
 using layer::open;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+#ifndef VTH
+#define VTH 128
+#define VPER 8
+#define VFILL 4
+#endif
+constexpr int kThreads = VTH, kWarps = kThreads / 32;
 using u64 = unsigned long long;
 
 // A probability as hi 2^22 + lo: hi = p 2^22 to the nearest, lo = what is left to the nearest 2^-44,
@@ -104,7 +109,7 @@ struct Weights {
 };
 
 template <typename T, bool kWide>
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyArgs a, int per) {
+__global__ void __launch_bounds__(kThreads, VPER) verify_kernel(VerifyArgs a, int per) {
   using W = Weights<T, kWide>;
   extern __shared__ u64 run[];  // sums of this block's runs [0, per)
   __shared__ u64 total_of[kWarps], total_here[2];
@@ -258,7 +263,7 @@ cudaError_t launch(const VerifyArgs& a) {
   // blocks per sequence: as many as fill the device four times, with a run for half of the warps
   const int runs = (a.V + W::kRun * kBatches - 1) / (W::kRun * kBatches);
   int blocks = 1;
-  while (blocks < 8 && (int64_t)a.B * blocks < 4 * a.sms && runs >= kWarps * blocks) blocks *= 2;
+  while (blocks < 8 && (int64_t)a.B * blocks < VFILL * a.sms && runs >= kWarps * blocks) blocks *= 2;
   const int per = (runs + blocks - 1) / blocks;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)a.B * blocks);
