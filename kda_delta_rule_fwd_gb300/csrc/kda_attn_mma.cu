@@ -16,8 +16,8 @@
 // (16 bits), since one alone would cost as much as the output's own rounding.  Codes become f16,
 // exactly; queries become f16 after a power of two per row has brought their largest to 2^13,
 // which keeps every bit down to 2^-27 of it.  A value's power of two joins its weight, relative
-// to the largest power seen by the warp, times 2^15: f16 then holds weights of 2^-29 of the
-// largest with all 11 bits, and what is below to 2^-39 of it; the sum of weights stays float32.
+// to the largest power seen by the warp, times 2^7: f16 then holds weights down to 2^-21 with all
+// 11 bits, and what is below to 2^-31; the sum of weights stays float32.
 //
 // Codes lie four to a 32-bit word, and the products' order of channels is free as long as both
 // operands have the same: a word of a key's row is channels 4t .. 4t + 3, used as the two pairs
@@ -37,6 +37,7 @@ constexpr int kGroups = 4;    // key groups of a block
 // tiles that an item's beginning and end take the time of: the calls named at by_rows take 368, 334
 // and 342 us, and 249, 185 and 184, with 0, 4 and 8
 constexpr int kItemCost = 4;
+constexpr int kLazy = 8, kShift = 7;  // 2^15 is the largest weight in f16
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
@@ -492,7 +493,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         moved = most != top;
         rise = __uint_as_float((uint32_t)max(127 + top - most, 0) << 23);
         top = most;
-        const float vfac = vb == 255 ? 0.f : __uint_as_float((uint32_t)max(min(vb - top, 0) + 142, 0) << 23);
+        const float vfac = vb == 255 ? 0.f : __uint_as_float((uint32_t)max(min(vb - top, 0) + 127 + kShift, 0) << 23);
         const float kfac = KT == 16 && lane >= 16 ? vfac : power(kb);
 #pragma unroll
         for (int u = 0; u < KM; ++u)
@@ -571,28 +572,47 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) l[j][e] = NAN;
       }
-      float al[NT][2];  // the outputs' factors
-      uint32_t ph[KM][NT][2], pl[KM][NT][2];
+      // The base of a row's weights follows its maximum only where that rises by more than 2^kLazy:
+      // the outputs are then rarely scaled again, and a weight is 2^kLazy at most.
+      float yn[NT][2];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float mx = -INFINITY;
 #pragma unroll
           for (int u = 0; u < KM; ++u)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float& x = c[u][j][2 * h + e];
-              mx = fmaxf(mx, x);
-            }
+            for (int h = 0; h < 2; ++h) mx = fmaxf(mx, c[u][j][2 * h + e]);
 #pragma unroll
           for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
-          const float yn = fmaxf(y[j][e], mx), base = yn == -INFINITY ? 0.f : yn * rf[j][e];
-          const float f = exp2_of(fmaf(y[j][e], rf[j][e], -base));
-          moved |= yn != y[j][e];
-          y[j][e] = yn;
-          l[j][e] *= f;
-          al[j][e] = kCoded ? f * rise : f;
+          const bool more = (mx - y[j][e]) * rf[j][e] > (float)kLazy;
+          yn[j][e] = more ? mx : y[j][e];
+          moved |= more;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float base = yn[j][e] == -INFINITY ? 0.f : yn[j][e] * rf[j][e];
+            const float f = exp2_of(fmaf(y[j][e], rf[j][e], -base));
+            y[j][e] = yn[j][e];
+            l[j][e] *= f;
+            const float al = kCoded ? f * rise : f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[i][j][e] *= al;
+              o[i][j][2 + e] *= al;
+            }
+          }
+      }
+      uint32_t ph[KM][NT][2], pl[KM][NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float base = y[j][e] == -INFINITY ? 0.f : y[j][e] * rf[j][e];
 #pragma unroll
           for (int u = 0; u < KM; ++u)
 #pragma unroll
@@ -618,14 +638,6 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
               pl[u][j][h] = transposed(layer::pack_bf16(x - xh, z - zh));
             }
           }
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][j][e] *= al[j][e & 1];
       }
       // ---- outputs
 #pragma unroll
@@ -669,7 +681,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         if (g == 0) stats[grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e] = make_float2(m, l[j][e]);
       }
     __syncthreads();
-    const float up = kCoded ? power(top) * 0x1p-15f : 1.f;
+    const float up = kCoded ? power(top) * __uint_as_float((127u - kShift) << 23) : 1.f;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll

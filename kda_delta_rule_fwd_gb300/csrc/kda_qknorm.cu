@@ -157,7 +157,7 @@ constexpr int kWide = 256;  // threads of a block
 #define QF 3
 #endif
 #ifndef QD
-#define QD 4
+#define QD 3
 #endif
 #ifndef QDB
 #define QDB 4
@@ -193,12 +193,13 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
     at[0] = c < chunks ? c * VEC : -1;
     at[1] = turned ? (lane + both) * VEC : c + 1 < chunks ? (c + 1) * VEC : -1;
   }
-  float w[2][VEC], sum[2][VEC];
+  const auto weight = [&](int i, int e) { return p.w && at[i] >= 0 ? p.w[at[i] + e] : 1.f; };
+  float w[2][VEC], sum[2][VEC];  // the backward's
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      w[i][e] = p.w && at[i] >= 0 ? p.w[at[i] + e] : 1.f;
+      w[i][e] = kBwd ? weight(i, e) : 1.f;
       sum[i][e] = 0.f;
     }
   // items (token, heads [c per, c per + per)) of this group; all groups of a warp run as often as
@@ -249,7 +250,9 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
 #pragma unroll
   for (int d = 0; d < kAhead; ++d) request(d);
   int h = 0, slot = 0;
-  float cs[VEC], sn[VEC];  // halves: of the thread's pairs; adjacent: of the two chunks' pairs in a row
+  // A pair's rotation (a, b) -> (f0 a + f1 b, f2 a + f3 b), with the weights in it forwards and turned
+  // back backwards; halves: pair e of the thread, adjacent: of the two chunks' pairs in a row.
+  float f0[VEC], f1[VEC], f2[VEC], f3[VEC];
   while (first < items) {
     {
       if (h == 0) {
@@ -259,8 +262,14 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
           const int j = kInter ? c >> 1 : at[0] + e;
           const bool turn = kInter ? (e < VEC / 2 ? at[0] : at[1]) >= 0 && j < half : turned && j < half;
           const float2 r = turn ? angle(turns[j], now.tok_pos) : make_float2(1.f, 0.f);
-          cs[e] = r.x;
-          sn[e] = r.y;
+          const int ia = kInter ? e / (VEC / 2) : 0, ea = kInter ? e % (VEC / 2) * 2 : e;
+          const int ib = kInter ? ia : 1, eb = kInter ? ea + 1 : e;
+          const float wa = kBwd ? 1.f : weight(ia, ea), wb = kBwd ? 1.f : weight(ib, eb);
+          const float sine = kBwd ? -r.y : r.y;
+          f0[e] = wa * r.x;
+          f1[e] = -wb * sine;
+          f2[e] = wa * sine;
+          f3[e] = wb * r.x;
         }
       }
       float v[2][VEC], g[2][VEC];
@@ -283,43 +292,40 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
 #pragma unroll
         for (int o = TPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         k = here ? rsqrtf(fmaf(s, a.inv_d, a.eps)) : 0.f;
-        mul_v(v[0], k);
-        mul_v(v[1], k);
       }
-      // (a, b) -> (a cos - b sin, a sin + b cos); back with the other sine
-      const auto turn_pairs = [&](float (&y)[2][VEC], float sign) {
+      const auto turn_pairs = [&](float (&y)[2][VEC]) {
         if constexpr (kInter) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC / 2; ++e) {
-              const float c = cs[i * (VEC / 2) + e], d = sign * sn[i * (VEC / 2) + e];
-              const float u = y[i][2 * e], t = y[i][2 * e + 1];
-              y[i][2 * e] = u * c - t * d;
-              y[i][2 * e + 1] = u * d + t * c;
-            }
+          for (int e = 0; e < VEC; ++e) {
+            float &u = y[e / (VEC / 2)][e % (VEC / 2) * 2], &t = y[e / (VEC / 2)][e % (VEC / 2) * 2 + 1];
+            const float x0 = fmaf(t, f1[e], u * f0[e]), x1 = fmaf(t, f3[e], u * f2[e]);
+            u = x0;
+            t = x1;
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < VEC; e += 2) {
-            const float2 c = make_float2(cs[e], cs[e + 1]), d = make_float2(sign * sn[e], sign * sn[e + 1]);
             const float2 u = make_float2(y[0][e], y[0][e + 1]), t = make_float2(y[1][e], y[1][e + 1]);
-            const float2 f = fma2(u, c, mul2(t, make_float2(-d.x, -d.y))), q = fma2(t, c, mul2(u, d));
-            y[0][e] = f.x;
-            y[0][e + 1] = f.y;
-            y[1][e] = q.x;
-            y[1][e + 1] = q.y;
+            const float2 x0 = fma2(t, make_float2(f1[e], f1[e + 1]), mul2(u, make_float2(f0[e], f0[e + 1])));
+            const float2 x1 = fma2(t, make_float2(f3[e], f3[e + 1]), mul2(u, make_float2(f2[e], f2[e + 1])));
+            y[0][e] = x0.x;
+            y[0][e + 1] = x0.y;
+            y[1][e] = x1.x;
+            y[1][e + 1] = x1.y;
           }
         }
       };
       if constexpr (!kBwd) {
-        mul_v(v[0], w[0]);
-        mul_v(v[1], w[1]);
-        turn_pairs(v, 1.f);
+        turn_pairs(v);
+        mul_v(v[0], k);
+        mul_v(v[1], k);
       } else {
-        turn_pairs(g, -1.f);
-        fma_v(g[0], v[0], sum[0]);
-        fma_v(g[1], v[1], sum[1]);
-        if (p.w) {
+        turn_pairs(g);
+        if (p.w) {  // with g k for g: the weights' sums, then dx = g k w - x k^2 mean(g k w x)
+          mul_v(g[0], k);
+          mul_v(g[1], k);
+          fma_v(g[0], v[0], sum[0]);
+          fma_v(g[1], v[1], sum[1]);
           mul_v(g[0], w[0]);
           mul_v(g[1], w[1]);
           float2 pn = make_float2(0.f, 0.f);
@@ -328,11 +334,9 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
           float s = pn.x + pn.y;
 #pragma unroll
           for (int o = TPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          const float mean = -s * a.inv_d;
-          fma_v(v[0], mean, g[0]);
-          fma_v(v[1], mean, g[1]);
-          mul_v(g[0], k);
-          mul_v(g[1], k);
+          const float back = -s * a.inv_d * k * k;
+          fma_v(v[0], back, g[0]);
+          fma_v(v[1], back, g[1]);
         }
       }
       if (here) {

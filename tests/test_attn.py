@@ -5,9 +5,11 @@ Tolerances.  A rounding to a type of p bits is off by at most eps / 2 of the val
 products and sum stay within 16 roundings (2^-20) of the pair's size, the angle within 2^-22; written
 values are rounded once more.  Attention: scores are sums of up to 128 products in float32, at most
 about 128 / 2 roundings of sum |q k| scale, which moves a weight by that much relatively; the weights'
-own rounding is 2^-17 at most where they enter 16-bit products, and the sums of weights add 2^-20:
-taken together 2^-13 of the largest value in bf16 (sum |q k| scale up to 8) and 2^-15 in float32,
-and the output's rounding.  Cache rows and drawn tokens are exact.
+own rounding is 2^-17 at most where they enter 16-bit products (bf16 caches), and the sums of weights
+add 2^-20: taken together 2^-13 of the largest value in bf16 (sum |q k| scale up to 8) and 2^-15 in
+float32, and the output's rounding.  Over 8-bit caches a bf16 query's weights are f16, 11 bits: each is
+off by 2^-12 of itself at most, the sum of p v by 2^-12 of the sum of p |v| (computed beside the
+reference).  Cache rows and drawn tokens are exact.
 """
 import math
 
@@ -310,7 +312,12 @@ def attn_check(kda, q, cache, pages, lens, window=0, scale=None, status=0):
     top = want.abs().nan_to_num().max().clamp(min=1e-3)
     assert torch.equal(torch.isnan(got.cpu()), torch.isnan(want))
     err = (got.cpu().to(F64) - want).abs().nan_to_num()
-    assert (err <= want.abs().nan_to_num() * ROUND[q.dtype] + tol * top).all(), err.max()
+    spread = 0.0
+    if cache[2] is not None and q.dtype is torch.bfloat16:
+        sizes = cache[1].float().abs().to(cache[1].dtype)
+        spread = ref.attn(q, (cache[0], sizes, *cache[2:]), pages, lens,
+                          q.shape[-1] ** -0.5 if scale is None else scale, window)[0].nan_to_num()
+    assert (err <= want.abs().nan_to_num() * ROUND[q.dtype] + tol * top + 2.0 ** -12 * spread).all(), err.max()
     gone = want_lse == -math.inf
     assert torch.equal(lse.cpu() == -math.inf, gone)
     assert not got.cpu()[gone].any()
@@ -414,7 +421,11 @@ def test_attn_long_splits_repeat(kda, dtype, kind):
             # sharp scores: up to 128 roundings of |q k| scale, about 2^-17 x 100 x 3
             tol = (2.0 ** -13 if q.dtype is torch.bfloat16 else 2.0 ** -15) * (4 if abs(scale) >= 1 else 1)
             err = (a[0, t].double() - want).abs()
-            assert (err <= want.abs() * ROUND[q.dtype] + tol * want.abs().max().clamp(min=0.1)).all(), (scale, err.max())
+            spread = 0.0
+            if cache[2] is not None and q.dtype is torch.bfloat16:
+                spread = torch.einsum("grk,gkd->grd", torch.softmax(s, -1), v[:, :m].abs()).reshape(hq, d)
+            assert (err <= want.abs() * ROUND[q.dtype] + tol * want.abs().max().clamp(min=0.1)
+                    + 2.0 ** -12 * spread).all(), (scale, err.max())
             assert ((la[0, t].double() - torch.logsumexp(s, -1).flatten()).abs() <= 1e-3).all()
 
 
