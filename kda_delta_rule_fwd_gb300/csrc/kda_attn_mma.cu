@@ -38,6 +38,7 @@ constexpr int kGroups = 4;    // key groups of a block
 // and 342 us, and 249, 185 and 184, with 0, 4 and 8
 constexpr int kItemCost = 4;
 constexpr int kLazy = 8, kShift = 7;  // 2^15 is the largest weight in f16
+constexpr float kNone = -3e38f;           // the base of a row that has seen nothing: every score passes it
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
@@ -65,11 +66,11 @@ __device__ __forceinline__ void matrix4_trans(uint32_t (&r)[4], uint32_t at) {
 template <bool kBf16>
 __device__ __forceinline__ void product(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   if constexpr (kBf16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
@@ -406,7 +407,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       }
     }
     __syncthreads();
-    float y[NT][2], l[NT][2], rf[NT][2];  // maxima (without the row's factor), sums, factors
+    float base[NT][2], l[NT][2], rf[NT][2];  // the weights' bases and sums, the scores' factors
     float o[D / 16][NT][4];
     uint2 qh[kHoldQ ? NT * KS : 1];
     int top = 0;  // the largest byte of a value seen
@@ -414,7 +415,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        y[i][e] = -INFINITY;
+        base[i][e] = kNone;
         l[i][e] = 0.f;
         rf[i][e] = row_factor[(wm * NT + i) * 8 + 2 * t4 + e];
       }
@@ -572,34 +573,38 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) l[j][e] = NAN;
       }
-      // The base of a row's weights follows its maximum only where that rises by more than 2^kLazy:
-      // the outputs are then rarely scaled again, and a weight is 2^kLazy at most.
-      float yn[NT][2];
+      // The base of a row's weights follows its maximum only where a score passes it by more than
+      // 2^kLazy: the outputs are then rarely scaled again, the rows' maxima rarely looked for across
+      // the warp, and a weight is 2^kLazy at most.
+      float high = -INFINITY;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = -INFINITY;
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int u = 0; u < KM; ++u)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) mx = fmaxf(mx, c[u][j][2 * h + e]);
-#pragma unroll
-          for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
-          const bool more = (mx - y[j][e]) * rf[j][e] > (float)kLazy;
-          yn[j][e] = more ? mx : y[j][e];
-          moved |= more;
-        }
-      if (__any_sync(0xffffffffu, moved)) {
+            for (int h = 0; h < 2; ++h) high = fmaxf(high, fmaf(c[u][j][2 * h + e], rf[j][e], -base[j][e]));
+      if (__any_sync(0xffffffffu, moved || high > (float)kLazy)) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float base = yn[j][e] == -INFINITY ? 0.f : yn[j][e] * rf[j][e];
-            const float f = exp2_of(fmaf(y[j][e], rf[j][e], -base));
-            y[j][e] = yn[j][e];
-            l[j][e] *= f;
-            const float al = kCoded ? f * rise : f;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < KM; ++u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) mx = fmaxf(mx, c[u][j][2 * h + e]);
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+            mx *= rf[j][e];
+            float al = rise;
+            if (mx - base[j][e] > (float)kLazy) {
+              const float f = exp2_of(base[j][e] - mx);
+              base[j][e] = mx;
+              l[j][e] *= f;
+              al *= f;
+            }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               o[i][j][e] *= al;
@@ -612,13 +617,12 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float base = y[j][e] == -INFINITY ? 0.f : y[j][e] * rf[j][e];
 #pragma unroll
           for (int u = 0; u < KM; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float& x = c[u][j][2 * h + e];
-              x = exp2_of(fmaf(x, rf[j][e], -base));
+              x = exp2_of(fmaf(x, rf[j][e], -base[j][e]));
               l[j][e] += x;
               if (kCoded) x *= vf[u][h];
             }
@@ -677,7 +681,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], i);
-        const float m = y[j][e] == -INFINITY ? -INFINITY : y[j][e] * rf[j][e];
+        const float m = base[j][e] == kNone ? -INFINITY : base[j][e];
         if (g == 0) stats[grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e] = make_float2(m, l[j][e]);
       }
     __syncthreads();
