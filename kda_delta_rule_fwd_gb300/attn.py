@@ -94,38 +94,45 @@ def _row_stride(t, name):
     return ld
 
 
+def _ints(t, name, what, n, x):
+    """A contiguous int32 tensor of n values beside x."""
+    if t.dtype is not _I32 or t.numel() != n or not t.is_contiguous() \
+            or t.get_device() != x.get_device():
+        raise ValueError(f"{name} must be int32 with one {what}, beside the others")
+
+
 def _qknorm_shape(q, k, positions, freqs, q_weight, k_weight, interleaved, eps):
-    if q.dtype not in _DT:
+    dtype = q.dtype
+    if dtype not in _DT:
         raise TypeError("q must be float32 or bfloat16")
     if q.dim() < 3:
         raise ValueError("q must be [..., heads, d]")
-    lead, (heads, d) = q.shape[:-2], q.shape[-2:]
-    kh = 0
+    *lead, heads, d = q.shape
+    kh = ldk = 0
     if k is not None:
-        if k.dim() != q.dim():
+        *also, kh, dk = k.shape
+        if len(also) != len(lead):
             raise ValueError("k must have q's shape but for its heads")
-        kh = k.shape[-2]
-        _activation(k, "k", q, lead + (kh, d))
-    tokens = 1
-    for n in lead:
-        tokens *= n
-    if freqs is None:
-        rot = 0
-    else:
+        if also != lead or dk != d or k.dtype is not dtype or k.get_device() != q.get_device():
+            _activation(k, "k", q, q.shape[:-2] + (kh, d))
+        ldk = _row_stride(k, "k")
+    tokens = lead[0] if len(lead) == 1 else q.numel() // (heads * d) if heads * d else 0
+    rot = 0
+    if freqs is not None:
         if freqs.dim() != 1:
             raise ValueError("freqs must be [rot / 2]")
-        rot = 2 * freqs.shape[0]
+        rot = 2 * freqs.numel()
         _dense(freqs, "freqs", torch.float64, freqs.shape, q)
     if rot:
         if positions is None:
             raise ValueError("a rotation needs positions")
-        if positions.dtype is not _I32 or positions.numel() != tokens \
-                or not positions.is_contiguous() or positions.get_device() != q.get_device():
-            raise ValueError("positions must be int32 with one place per token, beside q")
-    _dense(q_weight, "q_weight", _F32, (d,), q)
-    _dense(k_weight, "k_weight", _F32, (d,), q)
-    return _qknorm_struct(tokens, heads, kh, d, rot, _DT[q.dtype], bool(interleaved), float(eps),
-                          _row_stride(q, "q"), 0 if k is None else _row_stride(k, "k"))
+        _ints(positions, "positions", "place per token", tokens, q)
+    if q_weight is not None:
+        _dense(q_weight, "q_weight", _F32, (d,), q)
+    if k_weight is not None:
+        _dense(k_weight, "k_weight", _F32, (d,), q)
+    return _qknorm_struct(tokens, heads, kh, d, rot, _DT[dtype], bool(interleaved), float(eps),
+                          _row_stride(q, "q"), ldk)
 
 
 def qknorm_fwd(q, k, positions, freqs, *, q_weight=None, k_weight=None, interleaved=False,
@@ -220,7 +227,8 @@ def _pools(cache, x, pages, lens, N):
     if kind is None or v.dtype is not k.dtype:
         raise TypeError("a cache holds float32, bfloat16, float8_e4m3fn or int8, k as v")
     at = x.get_device()
-    if k.dim() != 4 or v.shape != k.shape:
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape:
         raise ValueError("k and v of a cache must be [num_pages, heads, page, d]")
     ld = 0
     if not (k.is_contiguous() and v.is_contiguous()):
@@ -232,16 +240,14 @@ def _pools(cache, x, pages, lens, N):
     if kind > 1:
         if ks is None or vs is None:
             raise ValueError("an 8-bit cache has k_scale and v_scale")
-        _dense(ks, "k_scale", torch.uint8, k.shape[:3], x)
-        _dense(vs, "v_scale", torch.uint8, k.shape[:3], x)
+        _dense(ks, "k_scale", torch.uint8, shape[:3], x)
+        _dense(vs, "v_scale", torch.uint8, shape[:3], x)
     elif ks is not None or vs is not None:
         raise ValueError("only an 8-bit cache has scales")
     if pages.dtype is not _I32 or pages.dim() != 2 or pages.shape[0] != N \
             or not pages.is_contiguous() or pages.get_device() != at:
         raise ValueError("pages must be a contiguous int32 tensor [num_seqs, max_pages], beside the cache")
-    if lens.dtype is not _I32 or lens.numel() != N or not lens.is_contiguous() \
-            or lens.get_device() != at:
-        raise ValueError("lens must be int32 with one length per sequence, beside the cache")
+    _ints(lens, "lens", "length per sequence", N, x)
     return kind, ld
 
 
@@ -256,13 +262,13 @@ def cache_write(k, v, cache, pages, lens, *, cu_seqlens=None, workspace=None, st
     if k.dim() != 4:
         raise ValueError("k and v must be [B, T, heads, d]")
     B, T, H, d = k.shape
-    _activation(k, "k", k)
     _activation(v, "v", k)
     packed, N = _seqs(cu_seqlens, B, k)
     kind, ldpage = _pools(cache, k, pages, lens, N)
-    if cache[0].shape[1] != H or cache[0].shape[3] != d:
-        raise ValueError(f"the cache has heads of {tuple(cache[0].shape[1::2])}, k of {(H, d)}")
-    shape = _cache_struct(B, T, packed, H, d, cache[0].shape[2], pages.shape[1], cache[0].shape[0],
+    num_pages, heads, page, width = cache[0].shape
+    if heads != H or width != d:
+        raise ValueError(f"the cache has heads of {(heads, width)}, k of {(H, d)}")
+    shape = _cache_struct(B, T, packed, H, d, page, pages.shape[1], num_pages,
                           _DT[k.dtype], kind, _token_stride(k, "k"), _token_stride(v, "v"), ldpage)
     _check(load().kda_cache_write(shape, k.data_ptr(), v.data_ptr(), _ptr(cu_seqlens),
                                   pages.data_ptr(), lens.data_ptr(), cache[0].data_ptr(),
@@ -287,14 +293,16 @@ def cache_read(cache, pages, lens, T, *, cu_seqlens=None, dtype=torch.bfloat16, 
     kind, ldpage = _pools(cache, x, pages, lens, N)
     num_pages, H, page, d = x.shape
     out = (B, T, H, d)
-    _dense(k, "k", dtype, out, x)
-    _dense(v, "v", dtype, out, x)
+    if k is not None:
+        _dense(k, "k", dtype, out, x)
+    if v is not None:
+        _dense(v, "v", dtype, out, x)
     shape = _cache_struct(B, T, packed, H, d, page, pages.shape[1], num_pages, _DT[dtype], kind, 0,
                           0, ldpage)
     if k is None:
         k = torch.empty(out, dtype=dtype, device=x.device)
     if v is None:
-        v = torch.empty(out, dtype=dtype, device=x.device)
+        v = torch.empty_like(k)
     _check(load().kda_cache_read(shape, _ptr(cu_seqlens), pages.data_ptr(), lens.data_ptr(),
                                  x.data_ptr(), cache[1].data_ptr(), _ptr(cache[2]), _ptr(cache[3]),
                                  k.data_ptr(), v.data_ptr(), *_ws(workspace, x),
@@ -339,17 +347,18 @@ def attn_step(q, cache, pages, lens, *, scale=None, window=0, out=None, lse=None
             return attn_step(q, cache, pages, lens, scale=scale, window=window, out=out, lse=lse,
                              want_lse=want_lse, workspace=workspace)
     shape = _attn_shape(q, cache, pages, lens, scale, window)
-    want_lse = want_lse or lse is not None
-    _dense(out, "out", q.dtype, q.shape, q)
-    _dense(lse, "lse", _F32, q.shape[:3], q)
     lib = load()
     if out is None:
         out = _new(q, q.dtype)
-    if lse is None and want_lse:
+    else:
+        _dense(out, "out", q.dtype, q.shape, q)
+    if lse is not None:
+        _dense(lse, "lse", _F32, q.shape[:3], q)
+        want_lse = True
+    elif want_lse:
         lse = torch.empty(q.shape[:3], dtype=_F32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(lib.kda_attn_workspace_size(shape), dtype=torch.uint8,
-                                device=q.device)
+    if workspace is None:  # whole 256-byte units
+        workspace = lens.new_empty(lib.kda_attn_workspace_size(shape) // 4)
     _check(lib.kda_attn_step(shape, q.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(),
                              _ptr(cache[2]), _ptr(cache[3]), pages.data_ptr(), lens.data_ptr(),
                              out.data_ptr(), _ptr(lse), *_ws(workspace, q),
@@ -377,18 +386,23 @@ def draft_verify(p, q, drafts, u, *, num_draft=None, tokens=None, num_commit=Non
         raise ValueError("p must be [B, K + 1, V]")
     if p.dtype not in _DT:
         raise TypeError("p must be float32 or bfloat16")
-    B, K, V = p.shape[0], p.shape[1] - 1, p.shape[2]
+    B, rows, V = p.shape
+    K = rows - 1
     _dense(p, "p", p.dtype, p.shape, p)
-    _dense(q, "q", p.dtype, (B, K, V), p)
+    if q is not None:
+        _dense(q, "q", p.dtype, (B, K, V), p)
     _dense(drafts, "drafts", _I32, (B, K), p)
-    _dense(u, "u", _F32, (B, K + 1), p)
-    _dense(num_draft, "num_draft", _I32, (B,), p)
-    _dense(tokens, "tokens", _I32, (B, K + 1), p)
-    _dense(num_commit, "num_commit", _I32, (B,), p)
+    _dense(u, "u", _F32, (B, rows), p)
+    if num_draft is not None:
+        _dense(num_draft, "num_draft", _I32, (B,), p)
     if tokens is None:
-        tokens = torch.empty((B, K + 1), dtype=_I32, device=p.device)
+        tokens = drafts.new_empty(B, rows)
+    else:
+        _dense(tokens, "tokens", _I32, (B, rows), p)
     if num_commit is None:
-        num_commit = torch.empty((B,), dtype=_I32, device=p.device)
+        num_commit = drafts.new_empty(B)
+    else:
+        _dense(num_commit, "num_commit", _I32, (B,), p)
     _check(load().kda_draft_verify(_verify_struct(B, K, V, _DT[p.dtype]), p.data_ptr(), _ptr(q),
                                    drafts.data_ptr(), _ptr(num_draft), u.data_ptr(),
                                    tokens.data_ptr(), num_commit.data_ptr(), *_ws(workspace, p),
