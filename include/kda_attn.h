@@ -155,9 +155,10 @@ typedef struct {
  * (KDA_ERR_INVALID_ARG), as is a lens past the table (the places that it has
  * are seen).  The keys are split over the device by equal numbers of tiles and
  * the parts joined in a fixed order: results repeat bit for bit on one device.
- * Sums and statistics are float32; with bf16 the scores are exact products in
+ * Sums and statistics are float32.  With bf16 the scores are exact products in
  * float32, and the weights enter the second product with 16 bits over a bf16
- * cache and with 11 over one of 8 bits.  workspace:
+ * cache and with 11 over one of 8 bits; with float32 products keep 22 bits
+ * over an 8-bit cache and 24 over a float32 one.  workspace:
  * required, 256-byte aligned, kda_attn_workspace_size(s) bytes. */
 size_t kda_attn_workspace_size(const kda_attn_shape* s);
 kda_status kda_attn_step(const kda_attn_shape* s, const void* q, const void* k_cache,

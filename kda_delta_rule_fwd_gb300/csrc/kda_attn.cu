@@ -1,359 +1,948 @@
-// Attention of new tokens over the paged cache, float32 queries: float32 arithmetic on the CUDA
-// cores; and the join of the parts.
+// Attention of new tokens over the paged cache: products on the tensor cores.
 //
-// One pass over the keys with the running maximum and sum: a tile of 64 places is brought to
-// shared memory as float32, each thread forms the scores of one place with 8 query rows, a warp
-// takes 4 rows' maxima and weights, then each thread adds up one channel of all rows.  Scores
-// count in units of log 2.  The power of two of a key's codes multiplies its score, that of a
-// value its weight.  A place that a row does not see has no part in its sums: its score is
-// replaced (not added to), and where its weight is 0 its value is not multiplied.
+// Bound by the bytes of keys and values: 1 to 64 query rows per key are few operations, so the
+// products are warp-level ones (m16n8k16), with the keys as rows and 8 queries as columns, and
+// everything else serves a steady stream of loads.  Each of a block's four key groups takes 16 or
+// 32 of a tile's places: its warps copy them into a ring of stages of their own (cp.async, 16
+// bytes a lane, swizzled by row) and wait for nobody else; a running maximum, sum and output per
+// warp are joined when an item ends.  The next items' tiles are requested while the present one
+// is worked on.
+//
+//     S^T = K Q^T:  A = keys as they lie (ldmatrix), B = queries, kept as fragments
+//     O^T = V^T P^T: A = values (ldmatrix.trans), B = the weights: S^T's accumulators, packed to
+//                    16 bits and transposed 8 x 8 in registers (movmatrix)
+//
+// Types.  bf16 caches: products of bf16, exact in float32; a weight enters as two bf16 parts
+// (16 bits), since one alone would cost as much as the output's own rounding.  Codes become f16,
+// exactly; queries become f16 after a power of two per row has brought their largest to 2^13,
+// which keeps every bit down to 2^-27 of it.  A value's power of two joins its weight, relative
+// to the largest power seen by the warp, times 2^7: f16 then holds weights down to 2^-21 with all
+// 11 bits, and what is below to 2^-31; the sum of weights stays float32.
+//
+// float32 queries over codes are two f16 parts (22 bits), as are their weights; over a float32 cache
+// keys, values, queries and weights are three bf16 parts each (all 24 bits), whose six largest products
+// leave out 2^-24.
+//
+// Codes lie four to a 32-bit word, and the products' order of channels is free as long as both
+// operands have the same: a word of a key's row is channels 4t .. 4t + 3, used as the two pairs
+// of a k-step; ldmatrix.trans on pairs of bytes gives two channels of two places, which one
+// byte permutation sorts by channel, so that a thread's outputs are pairs of adjacent channels.
+//
+// Places that a row does not see: the tiles at the ends of the seen range give them the weight 0,
+// and values that are not finite become zeros there once the rows that do see them have got them
+// (0 times infinity would reach the others).
+#include <type_traits>
+
 #include "kda_attn_split.cuh"
 
 namespace kda {
 namespace attn {
 namespace {
 
-using namespace layer;
-
-constexpr int kThreads = 128, kRows = 16, kTile = 64;
+constexpr int kGroups = 4;    // key groups of a block
+// tiles that an item's beginning and end take the time of: the calls named at by_rows take 368, 334
+// and 342 us, and 249, 185 and 184, with 0, 4 and 8
+constexpr int kItemCost = 4;
+constexpr int kLazy = 8, kShift = 7;  // 2^15 is the largest weight in f16
+constexpr float kNone = -3e38f;           // the base of a row that has seen nothing: every score passes it
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <typename TC> __device__ __forceinline__ void load4(const TC* p, float (&x)[4]);
-template <> __device__ __forceinline__ void load4(const float* p, float (&x)[4]) { load<4>(p, x); }
-struct E4M3 { uint8_t v; };
-struct Int8 { int8_t v; };
-template <> __device__ __forceinline__ void load4(const E4M3* p, float (&x)[4]) {
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+__device__ __forceinline__ uint32_t smem_at(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes, or zeros when `have` is false
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void matrix4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void matrix4_trans(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+template <bool kBf16>
+__device__ __forceinline__ void product(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  if constexpr (kBf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two numbers as N parts of 16 bits each, their sum the number: bf16 or f16 to the nearest, each part of
+// what the ones before it left; three bf16 parts are cut off a float32's 24 bits, exactly.
+template <bool kBf16, int N, bool kCut = N == 3>
+__device__ __forceinline__ void split(float x, float y, uint32_t (&part)[N]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t f;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"((uint16_t)(u >> (16 * i))));
-    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&f));
-    x[2 * i] = g.x;
-    x[2 * i + 1] = g.y;
+  for (int i = 0; i < N; ++i) {
+    float xh, yh;
+    if constexpr (kCut) {
+      part[i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+      xh = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+      yh = __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+    } else if constexpr (kBf16) {
+      part[i] = layer::pack_bf16(x, y);
+      layer::unpack2(part[i], xh, yh);
+    } else {
+      part[i] = pack_half(x, y);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&part[i]));
+      xh = f.x;
+      yh = f.y;
+    }
+    if (i + 1 < N) {
+      x -= xh;
+      y -= yh;
+    }
   }
 }
-template <> __device__ __forceinline__ void load4(const Int8* p, float (&x)[4]) {
-  const char4 u = *reinterpret_cast<const char4*>(p);
-  x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+// two codes as f16
+__device__ __forceinline__ uint32_t open2(uint16_t two) {
+  uint32_t f;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(two));
+  return f;
+}
+// four codes as two pairs of f16
+template <int CACHE>
+__device__ __forceinline__ void open4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (CACHE == KDA_CACHE_E4M3) {
+    lo = open2((uint16_t)w);
+    hi = open2((uint16_t)(w >> 16));
+  } else {  // 1024 + 128 + code in f16's mantissa, less 1152
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off), y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+// whether a 32-bit word of values (a float32, two bf16 or four e4m3 codes) holds one that is not finite
+template <int CACHE>
+__device__ __forceinline__ bool wild(uint32_t w) {
+  if constexpr (CACHE == KDA_CACHE_BF16) return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+  else if constexpr (CACHE == KDA_CACHE_F32) return (w & 0x7f800000u) == 0x7f800000u;
+  else if constexpr (CACHE == KDA_CACHE_E4M3) return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+  else return false;
+}
+template <int CACHE>
+__device__ __forceinline__ uint32_t tamed(uint32_t w) {  // such values as zeros
+  if constexpr (CACHE == KDA_CACHE_BF16) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+    return w;
+  } else if constexpr (CACHE == KDA_CACHE_F32) {
+    return wild<CACHE>(w) ? 0u : w;
+  } else {
+    return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t w) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+  return r;
 }
 
-template <int D> struct Shared {
-  float q[kRows][D];
-  float k[kTile][D + 4];
-  float v[kTile][D];
-  float p[kRows][kTile];
-  float ks[kTile], vs[kTile];
-  float m[kRows], l[kRows], alpha[kRows];
-  int64_t scratch[34];
-  int seen[kTile];  // the place lies in the sequence and on a page of the pool
-  int bad;
+// Places of tiles in the block's share, item by item.
+struct Cursor {
+  int64_t left;     // of the share from here on
+  int n, head, chunk;
+  int t, tiles;     // tile of the item, the item's number
+  int lo, hi;       // the sequence's places
+  __device__ __forceinline__ void enter(const AttnArgs& a, const Split& s) {
+    const Keys k = keys_of(a, s.tile, n);
+    lo = (int)k.lo;
+    hi = (int)k.hi;
+    tiles = (int)k.tiles;
+  }
+  // past `by` tiles of the item
+  __device__ __forceinline__ void pass(const AttnArgs& a, const Split& s, int by) {
+    left -= by;
+    t += by;
+    if (t < tiles) return;
+    t = 0;
+    left -= s.cost;
+    if (++chunk < s.chunks) return;
+    chunk = 0;
+    if (++head < a.hk) return;
+    head = 0;
+    ++n;
+    if (left > 0) enter(a, s);
+  }
 };
 
-template <typename TC, int D>
-__global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a, Split s) {
-  constexpr bool kCoded = sizeof(TC) == 1;
-  constexpr int kGroups = kThreads / D;       // threads of a channel
-  constexpr int kOwn = kRows / kGroups;       // rows of a thread in the second product
-  extern __shared__ __align__(16) char raw[];
-  Shared<D>& sh = *reinterpret_cast<Shared<D>*>(raw);
+// NT: query rows of a warp in eights; WM: warps with rows of their own; KT: places of a key group
+// in a tile; PER: blocks to an SM
+template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER>
+struct Shape {
+  static constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8, kF32 = CACHE == KDA_CACHE_F32;
+  // 16-bit parts of a key or value, of a query, of a weight
+  static constexpr int kParts = kF32 ? 3 : 1, kQParts = kF32 ? 3 : FQ ? 2 : 1, kWParts = kF32 ? 3 : kCoded && !FQ ? 1 : 2;
+  static constexpr int kThreads = kGroups * WM * 32, kPerSm = PER;
+  static constexpr int kRows = 8 * NT * WM, kTile = kGroups * KT;
+  static constexpr int kElem = kCoded ? 1 : kF32 ? 4 : 2;
+  static constexpr int kChunks = D * kElem / 16;           // 16-byte pieces of a row
+  static constexpr int kHalf = KT * D * kElem;             // a group's keys (or values) of a tile
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kSlice = NT == 1 ? 16 : 32, kPitch = kSlice + 2;     // channels of all groups' rows that meet at once
+  static constexpr int kMerge = kGroups * kRows * kPitch * 4;
+  static constexpr int kQBytes = kRows * D * 2 * kQParts;
+  static constexpr int bytes(int stages) {
+    return kGroups * stages * (kStage + 2 * KT + 4) + kQBytes + 8 * kRows + kGroups * kRows * 8 + 2 * kMerge;
+  }
+  // as many stages as the SM's 228 KB hold for its blocks (each takes 1.5 KB for itself), up to six
+  static constexpr int fit() {
+    int n = 2;
+    while (n < 6 && PER * (bytes(n + 1) + 1536) <= 228 * 1024) ++n;
+    return n;
+  }
+  static constexpr int kStages = fit();
+  static_assert(PER * (bytes(kStages) + 1536) <= 228 * 1024, "shared memory");
+  static constexpr int oQ = kGroups * kStages * kStage;
+  static constexpr int oScale = oQ + kQBytes;
+  static constexpr int oSeen = oScale + kGroups * kStages * 2 * KT;
+  static constexpr int oRow = oSeen + kGroups * kStages * 4;
+  static constexpr int oStats = oRow + 8 * kRows;
+  static constexpr int oMerge = oStats + kGroups * kRows * 8;
+  static constexpr int kBytes = bytes(kStages);
+  static_assert(oMerge % 16 == 0 && oMerge + 2 * kMerge == kBytes, "layout");
+};
+// a row's 16-byte piece c, moved so that 8 rows' pieces c lie in different banks
+template <int CHUNKS>
+__device__ __forceinline__ int piece(int row, int c) {
+  if constexpr (CHUNKS >= 8) return row * CHUNKS + (c ^ (row & 7));
+  else return row * CHUNKS + (c ^ ((row >> 1) & 3));
+}
+
+// float32 keys are read 16 bytes a lane, 4 pieces of 2 rows at once: adjacent rows in other halves
+template <int CHUNKS, bool kF32>
+__device__ __forceinline__ int key_piece(int row, int c) {
+  if constexpr (kF32) return row * CHUNKS + (c ^ ((row & 1) << 2 | (row >> 1 & 3)));
+  else return piece<CHUNKS>(row, c);
+}
+
+template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER>
+__global__ void __launch_bounds__(Shape<FQ, CACHE, D, NT, WM, KT, PER>::kThreads, PER)
+attn_mma_kernel(AttnArgs a, Split s, bool words) {
+  using S = Shape<FQ, CACHE, D, NT, WM, KT, PER>;
+  using TQ = std::conditional_t<FQ, float, __nv_bfloat16>;
+  constexpr bool kCoded = S::kCoded, kF32 = S::kF32;
+  constexpr int AP = S::kParts, QP = S::kQParts, PP = S::kWParts;
+  // a thread's outputs are channels 16 i + 2 g + (0, 1), or 16 i + g and 8 behind it
+  constexpr bool kNext = kCoded || kF32;
+  constexpr int KS = D / 16, KM = KT / 16, CH = S::kChunks;
+  constexpr bool kHoldQ = NT * KS * QP <= 8;  // queries stay in registers
+  constexpr unsigned kAll = KT == 32 ? 0xffffffffu : 0xffffu;
+  extern __shared__ __align__(128) char raw[];
+  __shared__ int64_t scratch[34];
+  __shared__ int bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int grp = warp % kGroups, wm = warp / kGroups;  // key group; which query rows
+  const int g = lane >> 2, t4 = lane & 3;
   if (tid == 0) {
-    sh.bad = 0;
+    bad = 0;
     s.cut[blockIdx.x] = -1;
   }
   Start st;
-  const bool work = find_start<kThreads>(a, s, sh.scratch, st);
-  const int64_t each = (int64_t)a.hk * s.chunks;
-  const int64_t cap = (int64_t)a.t.max_pages << a.t.shift;
-  int n = work ? st.n : 0;
-  int64_t before = work ? st.before : 0;
-  for (int64_t at = work ? st.at : 0; work && at < st.end;) {
-    const Keys keys = keys_of(a, s.tile, n);
-    const int64_t j = (at - before * each) / (keys.tiles + s.cost);       // head and chunk
-    const int64_t item_at = before * each + j * (keys.tiles + s.cost);
-    const int64_t tile_at = item_at + s.cost;                             // the item's first tile
-    if (tile_at >= st.end) break;
-    const int64_t t0 = max(at - tile_at, (int64_t)0), t1 = min(keys.tiles, st.end - tile_at);
-    const int head = (int)(j / s.chunks), row0 = (int)(j % s.chunks) * kRows;
-    const int rows = min(kRows, a.T * a.rep - row0);
-    const int64_t len = a.t.lens[n];
-    __syncthreads();
-    if (tid == 0 && len > cap) sh.bad = 1;
-    for (int i = tid; i < kRows * D; i += kThreads) {
-      const int r = i / D, c = i % D, row = row0 + r;
-      float x = 0.f;
-      if (r < rows) {
-        const float* q = static_cast<const float*>(a.q) + ((int64_t)n * a.T + row / a.rep) * a.ldq;
-        x = q[(int64_t)(head * a.rep + row % a.rep) * D + c] * a.scale * kLog2e;
-      }
-      sh.q[r][c] = x;
-    }
-    if (tid < kRows) {
-      sh.m[tid] = -INFINITY;
-      sh.l[tid] = 0.f;
-    }
-    float acc[kOwn];
-#pragma unroll
-    for (int r = 0; r < kOwn; ++r) acc[r] = 0.f;
-    for (int64_t t = t0; t < t1; ++t) {
-      const int64_t k0 = keys.lo + t * kTile;
-      __syncthreads();
-      // the tile, two halves of the block for keys and values; places unseen are zeros
-      for (int i = tid; i < kTile * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), c = i % (D / 4) * 4;
-        const int64_t pos = k0 + r;
-        float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-        int id = -1;
-        if (pos < keys.hi) {
-          id = page_of(a.t, n, pos);
-          if (id < 0) sh.bad = 1;
-        }
-        float sk = 1.f, sv = 1.f;
-        if (id >= 0) {
-          const int64_t row = ((int64_t)head << a.t.shift) + (pos & ((1 << a.t.shift) - 1));
-          load4<TC>(static_cast<const TC*>(a.kc) + id * a.ldpage + row * D + c, x);
-          load4<TC>(static_cast<const TC*>(a.vc) + id * a.ldpage + row * D + c, y);
-          if (kCoded && c == 0) {
-            const int64_t b = (((int64_t)id * a.hk) << a.t.shift) + row;
-            sk = power(a.ks[b]);
-            sv = power(a.vs[b]);
-          }
-        }
-        *reinterpret_cast<float4*>(&sh.k[r][c]) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4*>(&sh.v[r][c]) = make_float4(y[0], y[1], y[2], y[3]);
-        if (c == 0) {
-          sh.seen[r] = id >= 0;
-          sh.ks[r] = sk;
-          sh.vs[r] = sv;
-        }
-      }
-      __syncthreads();
-      {
-        const int key = tid % kTile, r0 = tid / kTile * (kRows / 2);
-        float dot[kRows / 2];
-#pragma unroll
-        for (int r = 0; r < kRows / 2; ++r) dot[r] = 0.f;
-        for (int c = 0; c < D; c += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(&sh.k[key][c]);
-#pragma unroll
-          for (int r = 0; r < kRows / 2; ++r) {
-            const float4 y = *reinterpret_cast<const float4*>(&sh.q[r0 + r][c]);
-            dot[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot[r]))));
-          }
-        }
-        const int64_t pos = k0 + key;
-#pragma unroll
-        for (int r = 0; r < kRows / 2; ++r) {
-          const int64_t hi = len - a.T + (row0 + r0 + r) / a.rep + 1;
-          const bool seen = sh.seen[key] && r0 + r < rows && pos < hi && (a.window == 0 || pos >= hi - a.window);
-          sh.p[r0 + r][key] = seen ? dot[r] * sh.ks[key] : -INFINITY;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kRows / 4; ++i) {
-        const int r = warp * (kRows / 4) + i;
-        const float x = sh.p[r][lane], y = sh.p[r][lane + 32];
-        // a score that is NaN makes the row NaN through its sum
-        float m = fmaxf(x, y);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float old = sh.m[r];
-        m = fmaxf(m, old);
-        const float base = m == -INFINITY ? 0.f : m;
-        const float px = exp2f(x - base), py = exp2f(y - base);
-        float l = px + py;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        // a weight of 0 stays 0, whatever its value's power
-        sh.p[r][lane] = px == 0.f ? 0.f : px * sh.vs[lane];
-        sh.p[r][lane + 32] = py == 0.f ? 0.f : py * sh.vs[lane + 32];
-        __syncwarp();
-        if (lane == 0) {
-          const float alpha = exp2f(old - base);
-          sh.alpha[r] = alpha;
-          sh.l[r] = fmaf(sh.l[r], alpha, l);
-          sh.m[r] = m;
-        }
-      }
-      __syncthreads();
-      {
-        const int c = tid % D, r0 = tid / D * kOwn;
-#pragma unroll
-        for (int r = 0; r < kOwn; ++r) acc[r] *= sh.alpha[r0 + r];
-        for (int key = 0; key < kTile; ++key) {
-          const float v = sh.v[key][c];
-#pragma unroll
-          for (int r = 0; r < kOwn; ++r) {
-            const float p = sh.p[r0 + r][key];
-            if (p != 0.f) acc[r] = fmaf(p, v, acc[r]);
-          }
-        }
-      }
-    }
-    __syncthreads();
-    const int c = tid % D, r0 = tid / D * kOwn;
-    if (t0 == 0 && t1 == keys.tiles) {
-#pragma unroll
-      for (int r = 0; r < kOwn; ++r) {
-        const int row = row0 + r0 + r;
-        if (r0 + r >= rows) break;
-        const int64_t o = ((int64_t)n * a.T + row / a.rep) * a.hq + head * a.rep + row % a.rep;
-        const float l = sh.l[r0 + r];
-        static_cast<float*>(a.out)[o * D + c] = l == 0.f ? 0.f : acc[r] / l;
-        if (c == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (sh.m[r0 + r] + log2f(l)) * kLn2;
-      }
-    } else {
-      float* part = part_of(s, blockIdx.x, t0 == 0 ? 1 : 0);
-      if (t0 == 0 && tid == 0) {
-        s.cut[blockIdx.x] = (int64_t)n * each + j;
-        s.cut_at[blockIdx.x] = item_at;
-      }
-      if (tid < kRows) {
-        part[tid] = sh.m[tid];
-        part[kRows + tid] = sh.l[tid];
-      }
-#pragma unroll
-      for (int r = 0; r < kOwn; ++r) part[2 * kRows + (r0 + r) * D + c] = acc[r];
-    }
-    at = tile_at + t1;
-    if (t1 == keys.tiles && j == each - 1) {
-      before += keys.tiles + s.cost;
-      ++n;
-    }
+  if (!find_start<S::kThreads>(a, s, scratch, st)) {
+    if (tid == 0) s.verdict[blockIdx.x] = KDA_OK;
+    return;
   }
+  const int mask = (1 << a.t.shift) - 1;
+  Cursor now;
+  {
+    now.n = st.n;
+    now.left = st.end - st.at;
+    now.enter(a, s);
+    const int64_t off = st.at - st.before * (a.hk * s.chunks);
+    const int all = now.tiles + s.cost, j = (int)(off / all);
+    now.t = (int)(off % all) - s.cost;
+    if (now.t < 0) {
+      now.left += now.t;
+      now.t = 0;
+    }
+    now.head = j / s.chunks;
+    now.chunk = j % s.chunks;
+  }
+  Cursor ahead = now;
+  char* const kv = raw + grp * S::kStages * S::kStage;
+  uint8_t* const sc = reinterpret_cast<uint8_t*>(raw + S::oScale) + grp * S::kStages * 2 * KT;
+  unsigned* const seen_of = reinterpret_cast<unsigned*>(raw + S::oSeen) + grp * S::kStages;
+  float* const row_factor = reinterpret_cast<float*>(raw + S::oRow);
+  int* const row_end = reinterpret_cast<int*>(raw + S::oRow) + S::kRows;
+  uint2* const qs = reinterpret_cast<uint2*>(raw + S::oQ) + wm * NT * KS * 32;  // [parts][rows / 8][steps][lanes]
+
+  // The table's entries of the next request are read one request early.
+  int ids[KM];
+  auto look = [&]() {
+    if (a.t.shift < 4 || ahead.left <= 0) return;
+#pragma unroll
+    for (int u = 0; u < KM; ++u) {
+      const unsigned pos = (unsigned)ahead.lo + (unsigned)ahead.t * S::kTile + grp * KT + u * 16;
+      const int64_t col = pos >> a.t.shift;
+      ids[u] = pos < (unsigned)ahead.hi && col < a.t.max_pages ? a.t.pages[(int64_t)ahead.n * a.t.max_pages + col] : -1;
+    }
+  };
+  // The group's places of the tile at `ahead` into a stage (its WM warps take a share each).
+  auto request = [&](int stage) {
+    if (ahead.left > 0) {
+      const unsigned pos = (unsigned)ahead.lo + (unsigned)ahead.t * S::kTile + grp * KT;
+      const uint32_t dst = smem_at(kv + stage * S::kStage);
+      unsigned seen = 0;
+      if (a.t.shift >= 4) {  // a page holds 16 places in a row
+        const char *k[KM], *v[KM];
+        int have[KM];
+#pragma unroll
+        for (int u = 0; u < KM; ++u) {
+          const unsigned p = pos + u * 16;
+          const bool some = p < (unsigned)ahead.hi;
+          const bool ok = some && (unsigned)ids[u] < (unsigned)a.t.num_pages;
+          have[u] = ok ? (int)min(16u, (unsigned)ahead.hi - p) : 0;
+          if (some && !ok) bad = 1;
+          seen |= ((1u << have[u]) - 1) << (u * 16);
+          const int64_t row = ((int64_t)ahead.head << a.t.shift) + (p & mask);
+          const int64_t from = ok ? (ids[u] * a.ldpage + row * D) * S::kElem : 0;
+          k[u] = static_cast<const char*>(a.kc) + from;
+          v[u] = static_cast<const char*>(a.vc) + from;
+          if (kCoded && wm == 0 && ok && (lane >> 1) == u) {
+            const int64_t b = (((int64_t)ids[u] * a.hk) << a.t.shift) + row;
+            copy16(smem_at(sc + stage * 2 * KT + (lane & 1) * KT + u * 16), (lane & 1 ? a.vs : a.ks) + b);
+          }
+        }
+        constexpr int kTurns = KT * CH / 32 / WM, kRowsOf = 32 / CH;
+        if (seen == kAll) {
+#pragma unroll
+          for (int i = 0; i < kTurns; ++i) {
+            const int x = (i * WM + wm) * 32 + lane, u = i * WM * kRowsOf / 16;
+            const int r = x / CH, c = x % CH, from = (x % (16 * CH)) * 16;
+            copy16(dst + key_piece<CH, kF32>(r, c) * 16, k[u] + from);
+            copy16(dst + S::kHalf + piece<CH>(r, c) * 16, v[u] + from);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kTurns; ++i) {
+            const int x = (i * WM + wm) * 32 + lane, r = x / CH, u = r / 16;
+            const bool ok = (r & 15) < (KM == 2 && u ? have[KM - 1] : have[0]);
+            const int c = x % CH, from = ok ? (x % (16 * CH)) * 16 : 0;
+            copy16(dst + key_piece<CH, kF32>(r, c) * 16, (KM == 2 && u ? k[KM - 1] : k[0]) + from, ok);
+            copy16(dst + S::kHalf + piece<CH>(r, c) * 16, (KM == 2 && u ? v[KM - 1] : v[0]) + from, ok);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < KT * CH / 32 / WM; ++i) {
+          const int x = (i * WM + wm) * 32 + lane, r = x / CH, c = x % CH;
+          const int id = pos + r < (unsigned)ahead.hi ? page_of(a.t, ahead.n, pos + r) : -1;
+          const int64_t row = ((int64_t)ahead.head << a.t.shift) + ((pos + r) & mask);
+          const int64_t from = id >= 0 ? (id * a.ldpage + row * D) * S::kElem + c * 16 : 0;
+          copy16(dst + key_piece<CH, kF32>(r, c) * 16, static_cast<const char*>(a.kc) + from, id >= 0);
+          copy16(dst + S::kHalf + piece<CH>(r, c) * 16, static_cast<const char*>(a.vc) + from, id >= 0);
+        }
+        const bool some = lane < KT && pos + lane < (unsigned)ahead.hi;
+        const int id = some ? page_of(a.t, ahead.n, pos + lane) : -1;
+        if (some && id < 0) bad = 1;
+        seen = __ballot_sync(0xffffffffu, id >= 0);
+        if (kCoded && wm == 0 && id >= 0) {
+          const int64_t b = (((int64_t)id * a.hk + ahead.head) << a.t.shift) + ((pos + lane) & mask);
+          sc[stage * 2 * KT + lane] = a.ks[b];
+          sc[stage * 2 * KT + KT + lane] = a.vs[b];
+        }
+      }
+      if (wm == 0 && lane == 0) seen_of[stage] = seen;
+      ahead.pass(a, s, 1);
+      look();
+    }
+    copy_commit();
+  };
+  // all that the group's warps wrote of a stage is there, and nobody reads the one before
+  auto meet = [&]() {
+    if constexpr (WM == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * WM) : "memory");
+  };
+
+  look();
+#pragma unroll 1
+  for (int i = 0; i < S::kStages - 1; ++i) request(i);
+  int stage = 0;
+  // ldmatrix: the lane's row of 16 places and piece of two, (places, pieces) = 0 0, 1 0, 0 1, 1 1
+  // by eights of lanes; bf16 values take 0 0, 0 1, 1 0, 1 1
+  const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mcol = lane >> 4;
+  const int vrow = kCoded ? mrow : (lane & 7) + (lane >> 4) * 8, vcol = kCoded ? mcol : (lane >> 3) & 1;
+
+  while (now.left > 0) {
+    // ---- an item begins: its queries as fragments of B, one row per warp and turn
+    const int n = now.n, head = now.head, row0 = now.chunk * S::kRows;
+    const int rows = min(S::kRows, a.T * a.rep - row0);
+    const int len = max(a.t.lens[n], -8);  // nothing is seen at 0 and below
+    const int t0 = now.t, t1 = (int)min((int64_t)now.tiles, now.t + now.left);
+    if (tid == 0) {
+      if ((int64_t)len > (int64_t)a.t.max_pages << a.t.shift) bad = 1;
+      if (t0 == 0 && t1 < now.tiles) {
+        s.cut[blockIdx.x] = ((int64_t)n * a.hk + head) * s.chunks + now.chunk;
+        s.cut_at[blockIdx.x] = st.end - now.left - s.cost;
+      }
+    }
+    __syncthreads();
+    constexpr int kTurns = S::kRows / (S::kThreads / 32);  // rows of a warp, all loaded before the first is used
+    using Pair = std::conditional_t<FQ, float2, __nv_bfloat162>;
+    Pair held[kTurns][D / 64];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+      const int r = warp + k * (S::kThreads / 32), row = row0 + r, tok = row / a.rep;
+      const TQ* q = static_cast<const TQ*>(a.q) + ((int64_t)n * a.T + tok) * a.ldq +
+                    (int64_t)(head * a.rep + row - tok * a.rep) * D;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const int p = lane + 32 * i;
+        held[k][i].x = held[k][i].y = from_f32<TQ>(0.f);
+        if (r < rows) {
+          if (words) held[k][i] = reinterpret_cast<const Pair*>(q)[p];
+          else { held[k][i].x = q[2 * p]; held[k][i].y = q[2 * p + 1]; }
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+      const int r = warp + k * (S::kThreads / 32), tok = (row0 + r) / a.rep;
+      const Pair (&x)[D / 64] = held[k];
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        most = max(most, max(__float_as_uint(to_f32(x[i].x)) & 0x7fffffffu, __float_as_uint(to_f32(x[i].y)) & 0x7fffffffu));
+      // the sign of the scale goes into the query, so that factors are positive; no scale: no query
+      float up = a.scale < 0.f ? -1.f : a.scale > 0.f ? 1.f : 0.f, f = fabsf(a.scale) * kLog2e;
+      if constexpr (kCoded) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        // 2^13 over the largest's power of two, kept a normal number
+        const int e = (int)(most >> 23);
+        const int k = e == 0 || e == 255 ? 0 : min(max(127 + 13 - e, -120), 120);
+        up *= __uint_as_float((uint32_t)(127 + k) << 23);
+        f *= __uint_as_float((uint32_t)(127 - k) << 23);
+      }
+      if (lane == 0) {
+        row_factor[r] = f > 1e-37f ? f : 1e-37f;
+        row_end[r] = len - a.T + tok + 1;  // the row sees places below this
+      }
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const int p = lane + 32 * i, ks = p / 8, w = p % 8;
+        const int t = kNext ? w / 2 : w % 4, hi = kNext ? w & 1 : w / 4;
+        uint32_t* to = reinterpret_cast<uint32_t*>(raw + S::oQ) + ((r / 8) * KS + ks) * 64 + ((r & 7) * 4 + t) * 2 + hi;
+        uint32_t part[QP];
+        split<!kCoded, QP>(to_f32(x[i].x) * up, to_f32(x[i].y) * up, part);
+#pragma unroll
+        for (int j = 0; j < QP; ++j) to[j * (S::kRows / 8) * KS * 64] = part[j];
+      }
+    }
+    __syncthreads();
+    float base[NT][2], l[NT][2], rf[NT][2];  // the weights' bases and sums, the scores' factors
+    float o[D / 16][NT][4];
+    uint2 qh[kHoldQ ? QP * NT * KS : 1];
+    int top = 0;  // the largest byte of a value seen
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        base[i][e] = kNone;
+        l[i][e] = 0.f;
+        rf[i][e] = row_factor[(wm * NT + i) * 8 + 2 * t4 + e];
+      }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+    if (kHoldQ) {
+#pragma unroll
+      for (int i = 0; i < QP * NT * KS; ++i) qh[i] = qs[(i / (NT * KS) * (S::kRows / 8) * KS + i % (NT * KS)) * 32 + lane];
+    }
+    auto query = [&](int part, int nt, int ks) {
+      return kHoldQ ? qh[(part * NT + nt) * KS + ks] : qs[(part * (S::kRows / 8) * KS + nt * KS + ks) * 32 + lane];
+    };
+    // c += A's parts times B's, down to the smallest that count
+    auto scores = [&](float (&c)[NT][4], const uint4 (&w)[AP], int ks) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int b = 0; b < QP; ++b) {
+          const uint2 q = query(b, j, ks);
+#pragma unroll
+          for (int i = 0; i < AP; ++i)
+            if (i + b < (AP > QP ? AP : QP)) product<!kCoded>(c[j], w[i], q.x, q.y);
+        }
+    };
+    const int hi_min = len - a.T + row0 / a.rep + 1;
+    const int lo_max = a.window > 0 ? len - a.T + (row0 + rows - 1) / a.rep + 1 - a.window : INT_MIN;
+
+    for (int t = t0; t < t1; ++t) {
+      copy_wait<S::kStages - 2>();
+      meet();
+      request(stage == 0 ? S::kStages - 1 : stage - 1);
+      char* const here = kv + stage * S::kStage;
+      const uint8_t* const bytes = sc + stage * 2 * KT;
+      const unsigned seen = seen_of[stage];
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
+      if (seen == 0) continue;
+      const int pos = (int)((unsigned)now.lo + (unsigned)t * S::kTile + grp * KT);
+      const bool edge = seen != kAll || pos > hi_min - KT || pos < lo_max;
+      const uint32_t kbase = smem_at(here), vbase = kbase + S::kHalf;
+      // ---- scores: c[places][queries]
+      float c[KM][NT][4];
+#pragma unroll
+      for (int u = 0; u < KM; ++u)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[u][j][e] = 0.f;
+      if constexpr (kF32) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int u = 0; u < KM; ++u) {  // channels 4 t .. 4 t + 3 of the step, places g and g + 8
+            const float4 x = *reinterpret_cast<const float4*>(here + key_piece<CH, true>(u * 16 + g, 4 * ks + t4) * 16);
+            const float4 y = *reinterpret_cast<const float4*>(here + key_piece<CH, true>(u * 16 + 8 + g, 4 * ks + t4) * 16);
+            uint32_t p[4][3];
+            split<true, 3>(x.x, x.y, p[0]);
+            split<true, 3>(y.x, y.y, p[1]);
+            split<true, 3>(x.z, x.w, p[2]);
+            split<true, 3>(y.z, y.w, p[3]);
+            uint4 w[AP];
+#pragma unroll
+            for (int k = 0; k < AP; ++k) w[k] = make_uint4(p[0][k], p[1][k], p[2][k], p[3][k]);
+            scores(c[u], w, ks);
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i)
+#pragma unroll
+          for (int u = 0; u < KM; ++u) {
+            uint32_t b[4];
+            matrix4(b, kbase + piece<CH>(u * 16 + mrow, 2 * i + mcol) * 16);
+            if constexpr (!kCoded) {
+              const uint4 w[1] = {make_uint4(b[0], b[1], b[2], b[3])};
+              scores(c[u], w, i);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint4 w[1];
+                open4<CACHE>(b[2 * k], w[0].x, w[0].z);
+                open4<CACHE>(b[2 * k + 1], w[0].y, w[0].w);
+                scores(c[u], w, 2 * i + k);
+              }
+            }
+          }
+      }
+      // powers of two of places g and g + 8, each worked out by one lane; a value's relative to the
+      // largest so far, 0 for a row that is not finite (its readers become NaN through their sums)
+      float kf[KM][2], vf[KM][2];
+      bool moved = false;
+      float rise = 1.f;
+      unsigned nan_rows = 0;
+      if constexpr (kCoded) {
+        const int kb = bytes[lane], vb = KT == 16 ? kb : bytes[KT + lane];
+        const bool mine = KT == 16 ? lane >= 16 && (seen >> (lane & 15) & 1) : seen >> lane & 1;
+        nan_rows = __ballot_sync(0xffffffffu, mine && vb == 255);
+        if (KT == 16) nan_rows >>= 16;
+        const int most = max(top, (int)__reduce_max_sync(0xffffffffu, mine && vb != 255 ? vb : 0));
+        moved = most != top;
+        rise = __uint_as_float((uint32_t)max(127 + top - most, 0) << 23);
+        top = most;
+        const float vfac = vb == 255 ? 0.f : __uint_as_float((uint32_t)max(min(vb - top, 0) + 127 + kShift, 0) << 23);
+        const float kfac = KT == 16 && lane >= 16 ? vfac : power(kb);
+#pragma unroll
+        for (int u = 0; u < KM; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            kf[u][e] = __shfl_sync(0xffffffffu, kfac, u * 16 + e * 8 + g);
+            vf[u][e] = __shfl_sync(0xffffffffu, KT == 16 ? kfac : vfac, (KT == 16 ? 16 : u * 16) + e * 8 + g);
+          }
+      }
+      if constexpr (kCoded) {
+#pragma unroll
+        for (int u = 0; u < KM; ++u)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[u][j][e] *= kf[u][e >> 1];
+      }
+      // ---- weights
+      if (edge) {
+        unsigned on[NT][2];  // the places that a query sees
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int64_t end = (int64_t)row_end[(wm * NT + j) * 8 + 2 * t4 + e] - pos;
+            const int64_t from = a.window > 0 ? end - a.window : 0;
+            unsigned m = end >= KT ? kAll : end <= 0 ? 0u : (1u << end) - 1;
+            if (from > 0) m = from >= KT ? 0u : m & ~((1u << from) - 1);
+            on[j][e] = m & seen;
+            if (on[j][e] & nan_rows) l[j][e] = NAN;
+#pragma unroll
+            for (int u = 0; u < KM; ++u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (!(on[j][e] >> (u * 16 + h * 8 + g) & 1)) c[u][j][2 * h + e] = -INFINITY;
+          }
+        if (CACHE != KDA_CACHE_INT8) {
+          bool found = false;
+          for (int i = lane; i < S::kHalf / 16; i += 32) {
+            const uint4 w = reinterpret_cast<const uint4*>(here + S::kHalf)[i];
+            found |= wild<CACHE>(w.x) || wild<CACHE>(w.y) || wild<CACHE>(w.z) || wild<CACHE>(w.w);
+          }
+          if (__any_sync(0xffffffffu, found)) {
+            // the rows that do see such a value take it (their output stays so), then it is 0
+#pragma unroll 1
+            for (int key = 0; key < KT; ++key)
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int byte = (kNext ? i * 16 + 2 * g + h : i * 16 + h * 8 + g) * S::kElem;
+                  const char* at = here + S::kHalf + piece<CH>(key, byte / 16) * 16 + byte % 16;
+                  float x;
+                  if constexpr (kCoded) x = (*reinterpret_cast<const uint8_t*>(at) & 0x7f) == 0x7f ? NAN : 0.f;
+                  else if constexpr (kF32) x = *reinterpret_cast<const float*>(at);
+                  else x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at));
+                  if (!isfinite(x)) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                      for (int e = 0; e < 2; ++e)
+                        if (on[j][e] >> key & 1) o[i][j][2 * h + e] += x;
+                  }
+                }
+            meet();
+            if (wm == 0)
+              for (int i = lane; i < S::kHalf / 4; i += 32) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(here + S::kHalf) + i;
+                *w = tamed<CACHE>(*w);
+              }
+            meet();
+          }
+        }
+      } else if (nan_rows) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) l[j][e] = NAN;
+      }
+      // The base of a row's weights follows its maximum only where a score passes it by more than
+      // 2^kLazy: the outputs are then rarely scaled again, the rows' maxima rarely looked for across
+      // the warp, and a weight is 2^kLazy at most.
+      float high = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int u = 0; u < KM; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) high = fmaxf(high, fmaf(c[u][j][2 * h + e], rf[j][e], -base[j][e]));
+      if (__any_sync(0xffffffffu, moved || high > (float)kLazy)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < KM; ++u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) mx = fmaxf(mx, c[u][j][2 * h + e]);
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+            mx *= rf[j][e];
+            float al = rise;
+            if (mx - base[j][e] > (float)kLazy) {
+              const float f = exp2_of(base[j][e] - mx);
+              base[j][e] = mx;
+              l[j][e] *= f;
+              al *= f;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[i][j][e] *= al;
+              o[i][j][2 + e] *= al;
+            }
+          }
+      }
+      uint32_t pw[PP][KM][NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int u = 0; u < KM; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float& x = c[u][j][2 * h + e];
+              x = exp2_of(fmaf(x, rf[j][e], -base[j][e]));
+              l[j][e] += x;
+              if (kCoded) x *= vf[u][h];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < KM; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t part[PP];
+            split<!kCoded, PP, kF32>(c[u][j][2 * h], c[u][j][2 * h + 1], part);
+#pragma unroll
+            for (int k = 0; k < PP; ++k) pw[k][u][j][h] = transposed(part[k]);
+          }
+      }
+      // ---- outputs
+      auto outputs = [&](float (&o)[NT][4], const uint4 (&w)[AP], int u) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int b = 0; b < PP; ++b)
+#pragma unroll
+            for (int i = 0; i < AP; ++i)
+              if (i + b < (AP > PP ? AP : PP)) product<!kCoded>(o[j], w[i], pw[b][u][j][0], pw[b][u][j][1]);
+      };
+#pragma unroll
+      for (int u = 0; u < KM; ++u) {
+        if constexpr (kF32) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {  // channels 2 g and 2 g + 1, places 2 t, 2 t + 1 and 8 behind them
+            float2 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = u * 16 + 2 * t4 + (k & 1) + (k >> 1) * 8;
+              x[k] = *reinterpret_cast<const float2*>(here + S::kHalf + piece<CH>(r, 4 * i + (g >> 1)) * 16 + (g & 1) * 8);
+            }
+            uint32_t p[4][3];
+            split<true, 3>(x[0].x, x[1].x, p[0]);
+            split<true, 3>(x[0].y, x[1].y, p[1]);
+            split<true, 3>(x[2].x, x[3].x, p[2]);
+            split<true, 3>(x[2].y, x[3].y, p[3]);
+            uint4 w[AP];
+#pragma unroll
+            for (int k = 0; k < AP; ++k) w[k] = make_uint4(p[0][k], p[1][k], p[2][k], p[3][k]);
+            outputs(o[i], w, u);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < CH / 2; ++i) {
+            uint32_t b[4];
+            matrix4_trans(b, vbase + piece<CH>(u * 16 + vrow, 2 * i + vcol) * 16);
+            if constexpr (!kCoded) {
+              const uint4 w[1] = {make_uint4(b[0], b[1], b[2], b[3])};
+              outputs(o[i], w, u);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint4 w[1];  // even channels of places 0-7, odd ones, the same of 8-15
+                open4<CACHE>(__byte_perm(b[2 * k], 0u, 0x3120), w[0].x, w[0].y);
+                open4<CACHE>(__byte_perm(b[2 * k + 1], 0u, 0x3120), w[0].z, w[0].w);
+                outputs(o[2 * i + k], w, u);
+              }
+            }
+          }
+        }
+      }
+    }
+
+    // ---- the item's end: the groups' outputs of the same rows, weighted by 2^(m - the largest m),
+    // add up through shared memory, kSlice channels at a time in two buffers by turns
+    const bool whole = t0 == 0 && t1 == now.tiles;
+    float2* const stats = reinterpret_cast<float2*>(raw + S::oStats);  // [groups][rows]: maximum, sum
+    float scale_by[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], i);
+        const float m = base[j][e] == kNone ? -INFINITY : base[j][e];
+        if (g == 0) stats[grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e] = make_float2(m, l[j][e]);
+      }
+    __syncthreads();
+    const float up = kCoded ? power(top) * __uint_as_float((127u - kShift) << 23) : 1.f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = (wm * NT + j) * 8 + 2 * t4 + e;
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) m = fmaxf(m, stats[i * S::kRows + r].x);
+        scale_by[j][e] = exp2_of(stats[grp * S::kRows + r].x - (m == -INFINITY ? 0.f : m));
+      }
+    float* const part = part_of(s, blockIdx.x, t0 == 0 ? 1 : 0);
+    // the sum of a row, and its maximum
+    auto row_sum = [&](int r, float& m) {
+      m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) m = fmaxf(m, stats[i * S::kRows + r].x);
+      const float base = m == -INFINITY ? 0.f : m;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) sum += stats[i * S::kRows + r].y * exp2_of(stats[i * S::kRows + r].x - base);
+      return sum;
+    };
+    auto place_of = [&](int r) {  // the row's place in the output
+      const int row = row0 + r, tok = row / a.rep;
+      return ((int64_t)n * a.T + tok) * a.hq + head * a.rep + row - tok * a.rep;
+    };
+    if (tid < rows) {
+      float m;
+      const float sum = row_sum(tid, m);
+      if (!whole) {
+        part[tid] = m;
+        part[S::kRows + tid] = sum;
+      } else if (a.lse) {
+        a.lse[place_of(tid)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+      }
+    }
+    constexpr int kSlice = S::kSlice, kPairs = kSlice / 2;
+    // a thread's rows and channels of a slice are the same in every turn
+    constexpr int kPer = (S::kRows * kPairs + S::kThreads - 1) / S::kThreads;
+    float inverse[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = (i * S::kThreads + tid) / kPairs;
+      float m, sum = 1.f;
+      if (r < rows && whole) sum = row_sum(r, m);
+      inverse[i] = sum == 0.f ? 0.f : 1.f / sum;
+    }
+#pragma unroll
+    for (int q = 0; q < D / kSlice; ++q) {
+      float* const buf = reinterpret_cast<float*>(raw + S::oMerge + (q & 1) * S::kMerge);  // [groups][rows][kPitch]
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float* const to = buf + (grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e) * S::kPitch;
+#pragma unroll
+          for (int i = 0; i < kSlice / 16; ++i) {
+            const float x = o[q * (kSlice / 16) + i][j][e] * up * scale_by[j][e];
+            const float z = o[q * (kSlice / 16) + i][j][2 + e] * up * scale_by[j][e];
+            if constexpr (kNext) {
+              *reinterpret_cast<float2*>(to + i * 16 + 2 * g) = make_float2(x, z);
+            } else {
+              to[i * 16 + g] = x;
+              to[i * 16 + 8 + g] = z;
+            }
+          }
+        }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int x = i * S::kThreads + tid, r = x / kPairs, ch = x % kPairs * 2;
+        if (r >= rows) break;
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+          const float2 w = *reinterpret_cast<const float2*>(buf + (k * S::kRows + r) * S::kPitch + ch);
+          v.x += w.x;
+          v.y += w.y;
+        }
+        if (whole) {
+          TQ* to = static_cast<TQ*>(a.out) + place_of(r) * D + q * kSlice + ch;
+          if (words && FQ) {
+            *reinterpret_cast<float2*>(to) = make_float2(v.x * inverse[i], v.y * inverse[i]);
+          } else if (words) {
+            *reinterpret_cast<uint32_t*>(to) = layer::pack_bf16(v.x * inverse[i], v.y * inverse[i]);
+          } else {
+            to[0] = from_f32<TQ>(v.x * inverse[i]);
+            to[1] = from_f32<TQ>(v.y * inverse[i]);
+          }
+        } else {
+          *reinterpret_cast<float2*>(part + 2 * S::kRows + r * D + q * kSlice + ch) = v;
+        }
+      }
+    }
+    now.pass(a, s, t1 - t0);
+  }
+  copy_wait<0>();
   __syncthreads();
-  if (tid == 0) s.verdict[blockIdx.x] = sh.bad ? KDA_ERR_INVALID_ARG : KDA_OK;
+  if (tid == 0) s.verdict[blockIdx.x] = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
 }
 
-// One block per cut item and row: the parts' outputs weighted by 2^(m - the largest m), over the
-// sum of their sums.  A lane has four channels, each warp every fourth part.
-constexpr int kJoinWarps = 4;
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, Split s) {
-  __shared__ float4 fold[kJoinWarps][32];
-  __shared__ float sums[kJoinWarps], tops[kJoinWarps];
-  cudaGridDependencySynchronize();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    unsigned int bad = 0;
-    for (int64_t b = tid; b < s.blocks; b += blockDim.x) bad |= s.verdict[b];
-    bad = __syncthreads_or(bad);
-    if (tid == 0) *s.status = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
-  }
-  const int64_t item = s.cut[blockIdx.x];
-  if (item < 0) return;
-  const int64_t each = (int64_t)a.hk * s.chunks;
-  const int n = (int)(item / each), head = (int)(item % each) / s.chunks;
-  const int r = blockIdx.y, row = (int)(item % s.chunks) * s.rows + r;
-  if (row >= a.T * a.rep) return;
-  const int64_t b0 = blockIdx.x, b1 = (s.cut_at[b0] + s.cost + keys_of(a, s.tile, n).tiles - 1) / *s.share;
-  float m = -INFINITY;
-  for (int64_t b = b0 + tid; b <= b1; b += blockDim.x) m = fmaxf(m, part_of(s, b, b == b0)[r]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) tops[warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) m = fmaxf(m, tops[i]);
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int64_t b = b0 + warp; b <= b1; b += kJoinWarps) {
-    const float* p = part_of(s, b, b == b0);
-    const float w = exp2f(p[r] - base);
-    l = fmaf(p[s.rows + r], w, l);
-    if (lane * 4 < D) {
-      const float4 x = *reinterpret_cast<const float4*>(p + 2 * s.rows + r * D + lane * 4);
-      o.x = fmaf(x.x, w, o.x);
-      o.y = fmaf(x.y, w, o.y);
-      o.z = fmaf(x.z, w, o.z);
-      o.w = fmaf(x.w, w, o.w);
-    }
-  }
-  fold[warp][lane] = o;
-  if (lane == 0) sums[warp] = l;
-  __syncthreads();
-  if (warp != 0) return;
-#pragma unroll
-  for (int i = 1; i < kJoinWarps; ++i) {
-    const float4 x = fold[i][lane];
-    o.x += x.x;
-    o.y += x.y;
-    o.z += x.z;
-    o.w += x.w;
-    l += sums[i];
-  }
-  const int64_t to = ((int64_t)n * a.T + row / a.rep) * a.hq + head * a.rep + row % a.rep;
-  const float f = l == 0.f ? 0.f : 1.f / l;
-  if (lane * 4 < D) {
-    T* out = static_cast<T*>(a.out) + to * D + lane * 4;
-    out[0] = from_f32<T>(o.x * f);
-    out[1] = from_f32<T>(o.y * f);
-    out[2] = from_f32<T>(o.z * f);
-    out[3] = from_f32<T>(o.w * f);
-  }
-  if (lane == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
-template <typename TC, int D>
-cudaError_t launch(const AttnArgs& a, const Split& s) {
-  constexpr int bytes = sizeof(Shared<D>);
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<TC, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER>
+cudaError_t launch(Shape<FQ, CACHE, D, NT, WM, KT, PER>, const AttnArgs& a, const Split& s) {
+  using S = Shape<FQ, CACHE, D, NT, WM, KT, PER>;
+  auto* kernel = attn_mma_kernel<FQ, CACHE, D, NT, WM, KT, PER>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
-  attn_kernel<TC, D><<<(unsigned)s.blocks, kThreads, bytes, a.stream>>>(a, s);
+  constexpr uintptr_t two = FQ ? 8 : 4;  // whole pairs of q and out
+  const bool words = (uintptr_t)a.q % two == 0 && (uintptr_t)a.out % two == 0 && a.ldq % 2 == 0;
+  kernel<<<(unsigned)s.blocks, S::kThreads, S::kBytes, a.stream>>>(a, s, words);
   return cudaGetLastError();
 }
-template <int D>
-cudaError_t by_cache(const AttnArgs& a, const Split& s) {
-  switch (a.cache) {
-    case KDA_CACHE_E4M3: return launch<E4M3, D>(a, s);
-    case KDA_CACHE_INT8: return launch<Int8, D>(a, s);
-    default: return launch<float, D>(a, s);
-  }
+
+// f(Shape) for the rows of a call: 8, 16, 32 or 64 to a block.  One GB300, us: 256 sequences of up
+// to 8192 e4m3 places, 4 rows: 32 places a group and 3 blocks to an SM 334, 16 and 4 blocks 389, 32
+// and 2 blocks 488 (before the ends were weighed in); 131071 bf16 places: 3 blocks 92, 2 blocks 94;
+// 16 sequences of up to 32768 int8 places, 32 rows: four eights to a warp 185, two 224 to 234 (codes
+// opened twice), four with 32 places a group 300 (one block to an SM).
+template <int CACHE, int D, class F>
+auto by_rows(const AttnArgs& a, F f) {
+  constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
+  constexpr int kPlaces = kCoded ? 32 : 16;
+  const int rows = a.T * a.rep;
+  if (rows <= 8) return f(Shape<false, CACHE, D, 1, 1, kPlaces, 3>());
+  if (rows <= 16) return f(Shape<false, CACHE, D, 2, 1, kPlaces, 2>());
+  if (rows <= 32) return f(Shape<false, CACHE, D, 4, 1, 16, kCoded ? 2 : 1>());
+  return f(Shape<false, CACHE, D, 4, 2, 16, 1>());
+}
+// float32 queries: their parts take room, so 32 rows at most
+template <int CACHE, int D, class F>
+auto by_rows_f32(const AttnArgs& a, F f) {
+  constexpr int kPer = CACHE == KDA_CACHE_F32 && D == 128 ? 1 : 2;
+  const int rows = a.T * a.rep;
+  if (rows <= 8) return f(Shape<true, CACHE, D, 1, 1, 16, kPer>());
+  if (rows <= 16) return f(Shape<true, CACHE, D, 2, 1, 16, kPer>());
+  return f(Shape<true, CACHE, D, 2, 2, 16, 1>());
+}
+template <int D, class F>
+auto by_cache(const AttnArgs& a, F f) {
+  if (a.cache == KDA_CACHE_E4M3) return a.bf16 ? by_rows<KDA_CACHE_E4M3, D>(a, f) : by_rows_f32<KDA_CACHE_E4M3, D>(a, f);
+  if (a.cache == KDA_CACHE_INT8) return a.bf16 ? by_rows<KDA_CACHE_INT8, D>(a, f) : by_rows_f32<KDA_CACHE_INT8, D>(a, f);
+  return a.bf16 ? by_rows<KDA_CACHE_BF16, D>(a, f) : by_rows_f32<KDA_CACHE_F32, D>(a, f);  // of q's type
+}
+template <class F>
+auto by_type(const AttnArgs& a, F f) {
+  return a.d == 128 ? by_cache<128>(a, f) : by_cache<64>(a, f);
+}
+
+Split split_for(const AttnArgs& a) {
+  return by_type(a, [&](auto shape) { return split_of(a, shape.kRows, shape.kTile, kItemCost, shape.kPerSm); });
 }
 
 }  // namespace
 
-Split attn_general_split(const AttnArgs& a) { return split_of(a, kRows, kTile, 1, 2); }
-
-// The join's blocks may be placed while the last of the main kernel's still run.
-template <typename T, int D>
-static cudaError_t join(const AttnArgs& a, const Split& s) {
-  const int rows = a.T * a.rep;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)s.blocks, rows < s.rows ? rows : s.rows);
-  c.blockDim = dim3(32 * kJoinWarps);
-  c.stream = a.stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &attr;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, attn_join_kernel<T, D>, a, s);
-}
-cudaError_t launch_attn_join(const AttnArgs& a, const Split& s) {
-  using bf = __nv_bfloat16;
-  if (a.d == 128) return a.bf16 ? join<bf, 128>(a, s) : join<float, 128>(a, s);
-  return a.bf16 ? join<bf, 64>(a, s) : join<float, 64>(a, s);
-}
-
-cudaError_t launch_attn_general(const AttnArgs& a) {
-  Split s = attn_general_split(a);
-  split_place(s, a.ws);
-  cudaError_t e = a.d == 128 ? by_cache<128>(a, s) : by_cache<64>(a, s);
-  return e != cudaSuccess ? e : launch_attn_join(a, s);
-}
-
-size_t attn_workspace(const AttnArgs& a) {
-  return split_bytes(a.bf16 ? attn_mma_split(a) : attn_general_split(a));
-}
+size_t attn_workspace(const AttnArgs& a) { return split_bytes(split_for(a)); }
 
 cudaError_t launch_attn(const AttnArgs& a) {
   if (a.B == 0) return cudaMemsetAsync(a.ws, 0, 4, a.stream);
-  return a.bf16 ? launch_attn_mma(a) : launch_attn_general(a);
+  Split s = split_for(a);
+  split_place(s, a.ws);
+  cudaError_t e = by_type(a, [&](auto shape) { return launch(shape, a, s); });
+  return e != cudaSuccess ? e : launch_attn_join(a, s);
 }
 
 }  // namespace attn

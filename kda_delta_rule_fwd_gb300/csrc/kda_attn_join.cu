@@ -1,0 +1,105 @@
+// Attention of new tokens: the join of the parts that the main kernel's blocks leave of an item.
+#include "kda_attn_split.cuh"
+
+namespace kda {
+namespace attn {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// One block per cut item and row: the parts' outputs weighted by 2^(m - the largest m), over the
+// sum of their sums.  A lane has four channels, each warp every fourth part.
+constexpr int kJoinWarps = 4;
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, Split s) {
+  __shared__ float4 fold[kJoinWarps][32];
+  __shared__ float sums[kJoinWarps], tops[kJoinWarps];
+  cudaGridDependencySynchronize();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    unsigned int bad = 0;
+    for (int64_t b = tid; b < s.blocks; b += blockDim.x) bad |= s.verdict[b];
+    bad = __syncthreads_or(bad);
+    if (tid == 0) *s.status = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
+  }
+  const int64_t item = s.cut[blockIdx.x];
+  if (item < 0) return;
+  const int64_t each = (int64_t)a.hk * s.chunks;
+  const int n = (int)(item / each), head = (int)(item % each) / s.chunks;
+  const int r = blockIdx.y, row = (int)(item % s.chunks) * s.rows + r;
+  if (row >= a.T * a.rep) return;
+  const int64_t b0 = blockIdx.x, b1 = (s.cut_at[b0] + s.cost + keys_of(a, s.tile, n).tiles - 1) / *s.share;
+  float m = -INFINITY;
+  for (int64_t b = b0 + tid; b <= b1; b += blockDim.x) m = fmaxf(m, part_of(s, b, b == b0)[r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) tops[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) m = fmaxf(m, tops[i]);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int64_t b = b0 + warp; b <= b1; b += kJoinWarps) {
+    const float* p = part_of(s, b, b == b0);
+    const float w = exp2f(p[r] - base);
+    l = fmaf(p[s.rows + r], w, l);
+    if (lane * 4 < D) {
+      const float4 x = *reinterpret_cast<const float4*>(p + 2 * s.rows + r * D + lane * 4);
+      o.x = fmaf(x.x, w, o.x);
+      o.y = fmaf(x.y, w, o.y);
+      o.z = fmaf(x.z, w, o.z);
+      o.w = fmaf(x.w, w, o.w);
+    }
+  }
+  fold[warp][lane] = o;
+  if (lane == 0) sums[warp] = l;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int i = 1; i < kJoinWarps; ++i) {
+    const float4 x = fold[i][lane];
+    o.x += x.x;
+    o.y += x.y;
+    o.z += x.z;
+    o.w += x.w;
+    l += sums[i];
+  }
+  const int64_t to = ((int64_t)n * a.T + row / a.rep) * a.hq + head * a.rep + row % a.rep;
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  if (lane * 4 < D) {
+    T* out = static_cast<T*>(a.out) + to * D + lane * 4;
+    out[0] = from_f32<T>(o.x * f);
+    out[1] = from_f32<T>(o.y * f);
+    out[2] = from_f32<T>(o.z * f);
+    out[3] = from_f32<T>(o.w * f);
+  }
+  if (lane == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+}  // namespace
+
+// The join's blocks may be placed while the last of the main kernel's still run.
+template <typename T, int D>
+static cudaError_t join(const AttnArgs& a, const Split& s) {
+  const int rows = a.T * a.rep;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)s.blocks, rows < s.rows ? rows : s.rows);
+  c.blockDim = dim3(32 * kJoinWarps);
+  c.stream = a.stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, attn_join_kernel<T, D>, a, s);
+}
+cudaError_t launch_attn_join(const AttnArgs& a, const Split& s) {
+  using bf = __nv_bfloat16;
+  if (a.d == 128) return a.bf16 ? join<bf, 128>(a, s) : join<float, 128>(a, s);
+  return a.bf16 ? join<bf, 64>(a, s) : join<float, 64>(a, s);
+}
+
+}  // namespace attn
+}  // namespace kda

@@ -144,11 +144,5 @@ __device__ __forceinline__ float* part_of(const Split& s, int64_t block, int slo
 
 cudaError_t launch_attn_join(const AttnArgs& a, const Split& s);
 
-// float32 queries; bf16 queries (on the tensor cores)
-Split attn_general_split(const AttnArgs& a);
-cudaError_t launch_attn_general(const AttnArgs& a);
-Split attn_mma_split(const AttnArgs& a);
-cudaError_t launch_attn_mma(const AttnArgs& a);
-
 }  // namespace attn
 }  // namespace kda
