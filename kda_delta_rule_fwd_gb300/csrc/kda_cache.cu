@@ -8,7 +8,9 @@
 //
 // Both directions move each value once and are bound by memory traffic.  A block takes the rows
 // (heads, keys and values) of a few consecutive tokens: their places are looked up once, then
-// d / 8 lanes move a row, 8 channels each.
+// d / 16 lanes move a row, twice 8 channels each.
+#include <type_traits>
+
 #include "kda_attn.cuh"
 
 namespace kda {
@@ -17,10 +19,7 @@ namespace {
 
 using namespace layer;
 
-#ifndef MT_
-#define MT_ 16
-#endif
-constexpr int kThreads = 256, kMaxTile = MT_;
+constexpr int kThreads = 256, kMaxTile = 16;  // kMaxTile: tokens of a block
 
 // Places of the tile's tokens: the page and the row in it, page -1 for a token without a place
 // and -2 for one of no sequence (behind the last).
@@ -119,34 +118,67 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   }
 }
 
-// 8 values of a row as they lie in memory, held while in flight
-template <typename T, bool kWide> struct Held { layer::Raw<T, 8> v; };
-template <typename T> struct Held<T, false> { T v[8]; };
+// A lane's two runs of 8 values of a row (of 8 L channels each) as they lie in memory, held while in
+// flight
+template <typename T, bool kWide> struct Held { layer::Raw<T, 8> v[2]; };
+template <typename T> struct Held<T, false> { T v[2][8]; };
 template <typename T, bool kWide>
-__device__ __forceinline__ void fetch8(const T* p, Held<T, kWide>& h) {
-  if constexpr (kWide) {
-    h.v = fetch<T, 8>(p);
-  } else {
+__device__ __forceinline__ void fetch16(const T* p, int apart, Held<T, kWide>& h) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h.v[e] = p[e];
+  for (int k = 0; k < 2; ++k) {
+    if constexpr (kWide) {
+      h.v[k] = fetch<T, 8>(p + k * apart);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h.v[k][e] = p[k * apart + e];
+    }
   }
 }
 template <typename T, bool kWide>
-__device__ __forceinline__ void open8(const Held<T, kWide>& h, float (&x)[8]) {
+__device__ __forceinline__ void open8(const Held<T, kWide>& h, int k, float (&x)[8]) {
   if constexpr (kWide) {
-    open<T, 8>(h.v, x);
+    open<T, 8>(h.v[k], x);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = to_f32(h.v[e]);
+    for (int e = 0; e < 8; ++e) x[e] = to_f32(h.v[k][e]);
+  }
+}
+// the largest magnitude of a row's L lanes as float32 bits; of bf16 pairs two to an instruction
+template <int L, typename T, bool kWide>
+__device__ __forceinline__ uint32_t peak(const Held<T, kWide>& h, unsigned mask) {
+  uint32_t m = 0;
+  if constexpr (kWide && sizeof(T) == 2) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 w = h.v[k].v;
+      m = __vmaxu2(m, w.x & 0x7fff7fffu);
+      m = __vmaxu2(m, w.y & 0x7fff7fffu);
+      m = __vmaxu2(m, w.z & 0x7fff7fffu);
+      m = __vmaxu2(m, w.w & 0x7fff7fffu);
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(mask, m, o));
+    return max(m << 16, m & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float x[8];
+      open8<T, kWide>(h, k, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
+    return m;
   }
 }
 
-// A group of L = D / 8 lanes takes one head (of keys or of values) of the tile's tokens, kAhead of
+// A group of L = D / 16 lanes takes one head (of keys or of values) of the tile's tokens, some of
 // them in flight; groups that outnumber the heads share a head's tokens.
 template <int D, class F>
 __device__ __forceinline__ void each_head(const CacheArgs& a, F f) {
-  constexpr int kGroups = kThreads / (D / 8);
-  const int group = threadIdx.x / (D / 8), heads = 2 * a.heads;
+  constexpr int kGroups = kThreads / (D / 16);
+  const int group = threadIdx.x / (D / 16), heads = 2 * a.heads;
   if (heads >= kGroups) {
     for (int r = group; r < heads; r += kGroups) f(r >= a.heads, r >= a.heads ? r - a.heads : r, 0, 1);
   } else {
@@ -154,17 +186,14 @@ __device__ __forceinline__ void each_head(const CacheArgs& a, F f) {
     if (way < ways) f(r >= a.heads, r >= a.heads ? r - a.heads : r, way, ways);
   }
 }
-#ifndef CAHEAD
-#define CAHEAD 4
-#endif
-#ifndef CPER
-#define CPER 4
-#endif
-constexpr int kAhead = CAHEAD;
+// Rows in flight of values of `size` bytes, and blocks to an SM.  58511 tokens of 8 heads of 128 in
+// e4m3, written and read back, take 122 us with 4 rows and 3 blocks, 131 with 2 and 4, 122 with 2 and 6.
+constexpr int ahead(int size) { return size == 4 ? 2 : 4; }
+constexpr int kPerSm = 3;
 
 template <typename T, int CACHE, int D, bool kWide>
-__global__ void __launch_bounds__(kThreads, CPER) cache_write_kernel(CacheArgs a, int tile) {
-  constexpr int L = D / 8;  // lanes of a row
+__global__ void __launch_bounds__(kThreads, kPerSm) cache_write_kernel(CacheArgs a, int tile) {
+  constexpr int L = D / 16, kAhead = ahead(sizeof(T));  // L: lanes of a row
   __shared__ int2 place[kMaxTile];
   const int64_t t0 = (int64_t)blockIdx.x * tile;
   find_places(a, t0, tile, place);
@@ -182,33 +211,37 @@ __global__ void __launch_bounds__(kThreads, CPER) cache_write_kernel(CacheArgs a
       for (int k = 0; k < kAhead; ++k) {
         const int i = base + k * step;
         at[k] = i < tile ? place[i] : make_int2(-2, 0);
-        if (at[k].x >= 0) fetch8<T, kWide>(src + i * ld, held[k]);
+        if (at[k].x >= 0) fetch16<T, kWide>(src + i * ld, 8 * L, held[k]);
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (at[k].x < 0) continue;  // the same for all lanes of the row
-        float x[8];
-        open8<T, kWide>(held[k], x);
         const int64_t row = ((int64_t)h << a.t.shift) + at[k].y;
         const int64_t to = at[k].x * a.ldpage + row * D + lane * 8;
-        if constexpr (CACHE == KDA_CACHE_F32) {
-          store<8>(static_cast<float*>(pool) + to, x);
-        } else if constexpr (CACHE == KDA_CACHE_BF16) {
-          store<8>(static_cast<__nv_bfloat16*>(pool) + to, x);
+        if constexpr (CACHE == KDA_CACHE_F32 || CACHE == KDA_CACHE_BF16) {
+          using TC = std::conditional_t<CACHE == KDA_CACHE_F32, float, __nv_bfloat16>;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float x[8];
+            open8<T, kWide>(held[k], r, x);
+            store<8>(static_cast<TC*>(pool) + to + r * 8 * L, x);
+          }
         } else {
-          uint32_t m = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
-#pragma unroll
-          for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
+          const uint32_t m = peak<L, T, kWide>(held[k], mask);
           // 448 = 1.75 2^8, 127 = 1.984375 2^6
           constexpr uint32_t top = CACHE == KDA_CACHE_E4M3 ? 0x600000u : 0x7e0000u;
           int e = (int)(m >> 23) - 127 - (CACHE == KDA_CACHE_E4M3 ? 8 : 6) + ((m & 0x7fffffu) > top);
           e = max(e, -126);
           const bool finite = m < 0x7f800000u;
-          uint2 code = encode8<CACHE>(x, __uint_as_float((uint32_t)(127 - e) << 23));
-          if (!finite) code = make_uint2(0u, 0u);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + to) = code;
+          const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float x[8];
+            open8<T, kWide>(held[k], r, x);
+            uint2 code = encode8<CACHE>(x, inv);
+            if (!finite) code = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + to + r * 8 * L) = code;
+          }
           if (lane == 0)
             (kv ? a.vs : a.ks)[(((int64_t)at[k].x * a.heads) << a.t.shift) + row] = finite ? (uint8_t)(e + 127) : 255;
         }
@@ -223,10 +256,10 @@ template <> struct Row8<KDA_CACHE_F32> { layer::Raw<float, 8> v; };
 template <> struct Row8<KDA_CACHE_BF16> { layer::Raw<__nv_bfloat16, 8> v; };
 
 template <typename T, int CACHE, int D, bool kWide>
-__global__ void __launch_bounds__(kThreads, CPER) cache_read_kernel(CacheArgs a, int tile) {
-  constexpr int L = D / 8;
+__global__ void __launch_bounds__(kThreads, kPerSm) cache_read_kernel(CacheArgs a, int tile) {
+  constexpr int L = D / 16;
   constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
-  constexpr int kElem = CACHE == KDA_CACHE_F32 ? 4 : CACHE == KDA_CACHE_BF16 ? 2 : 1;
+  constexpr int kElem = CACHE == KDA_CACHE_F32 ? 4 : CACHE == KDA_CACHE_BF16 ? 2 : 1, kAhead = ahead(kElem);
   __shared__ int2 place[kMaxTile];
   const int64_t t0 = (int64_t)blockIdx.x * tile;
   find_places(a, t0, tile, place);
@@ -236,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, CPER) cache_read_kernel(CacheArgs a,
     if (!out) return;
     const char* const pool = static_cast<const char*>(kv ? a.vc : a.kc);
     for (int base = first; base < tile; base += step * kAhead) {
-      Row8<CACHE> held[kAhead];
+      Row8<CACHE> held[kAhead][2];
       uint8_t byte[kAhead];
       int2 at[kAhead];
 #pragma unroll
@@ -245,22 +278,28 @@ __global__ void __launch_bounds__(kThreads, CPER) cache_read_kernel(CacheArgs a,
         at[k] = i < tile ? place[i] : make_int2(-2, 0);
         if (at[k].x >= 0) {
           const int64_t row = ((int64_t)h << a.t.shift) + at[k].y;
-          held[k] = *reinterpret_cast<const Row8<CACHE>*>(pool + (at[k].x * a.ldpage + row * D + lane * 8) * kElem);
+          const char* from = pool + (at[k].x * a.ldpage + row * D + lane * 8) * kElem;
+          held[k][0] = *reinterpret_cast<const Row8<CACHE>*>(from);
+          held[k][1] = *reinterpret_cast<const Row8<CACHE>*>(from + 8 * L * kElem);
           if (kCoded) byte[k] = (kv ? a.vs : a.ks)[(((int64_t)at[k].x * a.heads) << a.t.shift) + row];
         }
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (at[k].x == -2) continue;
-        float x[8];
+        const float p = kCoded && at[k].x >= 0 ? power(byte[k]) : 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        if (at[k].x >= 0) {
-          if constexpr (CACHE == KDA_CACHE_F32) open<float, 8>(held[k].v, x);
-          else if constexpr (CACHE == KDA_CACHE_BF16) open<__nv_bfloat16, 8>(held[k].v, x);
-          else decode8<CACHE>(held[k].v, power(byte[k]), x);
+        for (int r = 0; r < 2; ++r) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = 0.f;
+          if (at[k].x >= 0) {
+            if constexpr (CACHE == KDA_CACHE_F32) open<float, 8>(held[k][r].v, x);
+            else if constexpr (CACHE == KDA_CACHE_BF16) open<__nv_bfloat16, 8>(held[k][r].v, x);
+            else decode8<CACHE>(held[k][r].v, p, x);
+          }
+          store8<T, kWide>(out + ((t0 + base + k * step) * a.heads + h) * D + lane * 8 + r * 8 * L, x);
         }
-        store8<T, kWide>(out + ((t0 + base + k * step) * a.heads + h) * D + lane * 8, x);
       }
     }
   });

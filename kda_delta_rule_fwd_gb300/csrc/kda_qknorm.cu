@@ -153,18 +153,10 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool have) {
 // and request the next row before they work on the present one; a block serves q or k, in
 // proportion to their heads, so that its weights and its sums for their gradient stay in registers.
 constexpr int kWide = 256;  // threads of a block
-#ifndef QF
-#define QF 3
-#endif
-#ifndef QD
-#define QD 3
-#endif
-#ifndef QDB
-#define QDB 4
-#endif
-template <bool kBwd> constexpr int wide_blocks() { return kBwd ? 2 : QF; }
-// rows in flight
-template <bool kBwd> constexpr int wide_ahead() { return kBwd ? QDB : QD; }
+// Blocks to an SM and rows in flight.  16384 tokens of 40 heads of 128 in bf16 take 66 us forwards (with
+// four rows 70, with four blocks 99: too few registers), their gradient 97 (two or three rows 99).
+template <bool kBwd> constexpr int wide_blocks() { return kBwd ? 2 : 3; }
+template <bool kBwd> constexpr int wide_ahead() { return kBwd ? 4 : 3; }
 
 template <typename T, int TPR, bool kInter, bool kBwd>
 __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel(QKArgs a, int2 per_of) {
@@ -254,103 +246,102 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
   // back backwards; halves: pair e of the thread, adjacent: of the two chunks' pairs in a row.
   float f0[VEC], f1[VEC], f2[VEC], f3[VEC];
   while (first < items) {
-    {
-      if (h == 0) {
+    if (h == 0) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int c = e < VEC / 2 ? at[0] + 2 * e : at[1] + 2 * e - VEC;
+        const int j = kInter ? c >> 1 : at[0] + e;
+        const bool turn = kInter ? (e < VEC / 2 ? at[0] : at[1]) >= 0 && j < half : turned && j < half;
+        const float2 r = turn ? angle(turns[j], now.tok_pos) : make_float2(1.f, 0.f);
+        const int ia = kInter ? e / (VEC / 2) : 0, ea = kInter ? e % (VEC / 2) * 2 : e;
+        const int ib = kInter ? ia : 1, eb = kInter ? ea + 1 : e;
+        const float wa = kBwd ? 1.f : weight(ia, ea), wb = kBwd ? 1.f : weight(ib, eb);
+        const float sine = kBwd ? -r.y : r.y;
+        f0[e] = wa * r.x;
+        f1[e] = -wb * sine;
+        f2[e] = wa * sine;
+        if (!kBwd) f3[e] = wb * r.x;  // backwards it is f0
+      }
+    }
+    float v[2][VEC], g[2][VEC];
+    const bool here = h < now.rows;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4* const from = ring + (slot * kWords + i) * kWide + threadIdx.x;
+      open<T, VEC>(*reinterpret_cast<const Raw<T, VEC>*>(from), v[i]);
+      if (kBwd) open<T, VEC>(*reinterpret_cast<const Raw<T, VEC>*>(from + 2 * kWide), g[i]);
+    }
+    request(slot);
+    slot = slot + 1 == kAhead ? 0 : slot + 1;
+    float k = 1.f;
+    if (p.w) {
+      float2 ss = make_float2(0.f, 0.f);
+      dot_v(v[0], v[0], ss);
+      dot_v(v[1], v[1], ss);
+      float s = ss.x + ss.y;
+#pragma unroll
+      for (int o = TPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      k = here ? rsqrtf(fmaf(s, a.inv_d, a.eps)) : 0.f;
+    }
+    const auto turn_pairs = [&](float (&y)[2][VEC]) {
+      if constexpr (kInter) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const int c = e < VEC / 2 ? at[0] + 2 * e : at[1] + 2 * e - VEC;
-          const int j = kInter ? c >> 1 : at[0] + e;
-          const bool turn = kInter ? (e < VEC / 2 ? at[0] : at[1]) >= 0 && j < half : turned && j < half;
-          const float2 r = turn ? angle(turns[j], now.tok_pos) : make_float2(1.f, 0.f);
-          const int ia = kInter ? e / (VEC / 2) : 0, ea = kInter ? e % (VEC / 2) * 2 : e;
-          const int ib = kInter ? ia : 1, eb = kInter ? ea + 1 : e;
-          const float wa = kBwd ? 1.f : weight(ia, ea), wb = kBwd ? 1.f : weight(ib, eb);
-          const float sine = kBwd ? -r.y : r.y;
-          f0[e] = wa * r.x;
-          f1[e] = -wb * sine;
-          f2[e] = wa * sine;
-          f3[e] = wb * r.x;
+          float &u = y[e / (VEC / 2)][e % (VEC / 2) * 2], &t = y[e / (VEC / 2)][e % (VEC / 2) * 2 + 1];
+          const float x0 = fmaf(t, f1[e], u * f0[e]), x1 = fmaf(t, kBwd ? f0[e] : f3[e], u * f2[e]);
+          u = x0;
+          t = x1;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          const float2 u = make_float2(y[0][e], y[0][e + 1]), t = make_float2(y[1][e], y[1][e + 1]);
+          const float2 x0 = fma2(t, make_float2(f1[e], f1[e + 1]), mul2(u, make_float2(f0[e], f0[e + 1])));
+          const float2 last = kBwd ? make_float2(f0[e], f0[e + 1]) : make_float2(f3[e], f3[e + 1]);
+          const float2 x1 = fma2(t, last, mul2(u, make_float2(f2[e], f2[e + 1])));
+          y[0][e] = x0.x;
+          y[0][e + 1] = x0.y;
+          y[1][e] = x1.x;
+          y[1][e + 1] = x1.y;
         }
       }
-      float v[2][VEC], g[2][VEC];
-      const bool here = h < now.rows;
-      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4* const from = ring + (slot * kWords + i) * kWide + threadIdx.x;
-        open<T, VEC>(*reinterpret_cast<const Raw<T, VEC>*>(from), v[i]);
-        if (kBwd) open<T, VEC>(*reinterpret_cast<const Raw<T, VEC>*>(from + 2 * kWide), g[i]);
-      }
-      request(slot);
-      slot = slot + 1 == kAhead ? 0 : slot + 1;
-      float k = 1.f;
-      if (p.w) {
-        float2 ss = make_float2(0.f, 0.f);
-        dot_v(v[0], v[0], ss);
-        dot_v(v[1], v[1], ss);
-        float s = ss.x + ss.y;
+    };
+    if constexpr (!kBwd) {
+      turn_pairs(v);
+      mul_v(v[0], k);
+      mul_v(v[1], k);
+    } else {
+      turn_pairs(g);
+      if (p.w) {  // with g k for g: the weights' sums, then dx = g k w - x k^2 mean(g k w x)
+        mul_v(g[0], k);
+        mul_v(g[1], k);
+        fma_v(g[0], v[0], sum[0]);
+        fma_v(g[1], v[1], sum[1]);
+        mul_v(g[0], w[0]);
+        mul_v(g[1], w[1]);
+        float2 pn = make_float2(0.f, 0.f);
+        dot_v(g[0], v[0], pn);
+        dot_v(g[1], v[1], pn);
+        float s = pn.x + pn.y;
 #pragma unroll
         for (int o = TPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        k = here ? rsqrtf(fmaf(s, a.inv_d, a.eps)) : 0.f;
+        const float back = -s * a.inv_d * k * k;
+        fma_v(v[0], back, g[0]);
+        fma_v(v[1], back, g[1]);
       }
-      const auto turn_pairs = [&](float (&y)[2][VEC]) {
-        if constexpr (kInter) {
+    }
+    if (here) {
+      T* y = static_cast<T*>(kBwd ? p.dx : p.y) + (now.row + h) * a.d;
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            float &u = y[e / (VEC / 2)][e % (VEC / 2) * 2], &t = y[e / (VEC / 2)][e % (VEC / 2) * 2 + 1];
-            const float x0 = fmaf(t, f1[e], u * f0[e]), x1 = fmaf(t, f3[e], u * f2[e]);
-            u = x0;
-            t = x1;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; e += 2) {
-            const float2 u = make_float2(y[0][e], y[0][e + 1]), t = make_float2(y[1][e], y[1][e + 1]);
-            const float2 x0 = fma2(t, make_float2(f1[e], f1[e + 1]), mul2(u, make_float2(f0[e], f0[e + 1])));
-            const float2 x1 = fma2(t, make_float2(f3[e], f3[e + 1]), mul2(u, make_float2(f2[e], f2[e + 1])));
-            y[0][e] = x0.x;
-            y[0][e + 1] = x0.y;
-            y[1][e] = x1.x;
-            y[1][e + 1] = x1.y;
-          }
-        }
-      };
-      if constexpr (!kBwd) {
-        turn_pairs(v);
-        mul_v(v[0], k);
-        mul_v(v[1], k);
-      } else {
-        turn_pairs(g);
-        if (p.w) {  // with g k for g: the weights' sums, then dx = g k w - x k^2 mean(g k w x)
-          mul_v(g[0], k);
-          mul_v(g[1], k);
-          fma_v(g[0], v[0], sum[0]);
-          fma_v(g[1], v[1], sum[1]);
-          mul_v(g[0], w[0]);
-          mul_v(g[1], w[1]);
-          float2 pn = make_float2(0.f, 0.f);
-          dot_v(g[0], v[0], pn);
-          dot_v(g[1], v[1], pn);
-          float s = pn.x + pn.y;
-#pragma unroll
-          for (int o = TPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          const float back = -s * a.inv_d * k * k;
-          fma_v(v[0], back, g[0]);
-          fma_v(v[1], back, g[1]);
-        }
-      }
-      if (here) {
-        T* y = static_cast<T*>(kBwd ? p.dx : p.y) + (now.row + h) * a.d;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (at[i] >= 0) store<VEC>(y + at[i], kBwd ? g[i] : v[i]);
-      }
-      if (++h == per) {
-        h = 0;
-        first += step;
-        item += step;
-        now = locate(item);
-      }
+      for (int i = 0; i < 2; ++i)
+        if (at[i] >= 0) store<VEC>(y + at[i], kBwd ? g[i] : v[i]);
+    }
+    if (++h == per) {
+      h = 0;
+      first += step;
+      item += step;
+      now = locate(item);
     }
   }
   if (!kBwd || !p.dw) return;
@@ -407,19 +398,29 @@ template <typename T, int TPR, bool kInter, bool kBwd>
 void launch_wide(QKArgs& a) {
   constexpr int kGroups = kWide / TPR;
   const int64_t most = a.sms * wide_blocks<kBwd>();
-  const int heads = a.p[0].heads + a.p[1].heads;
+  // a token's angles take about as long as two of its heads
+  const int heads = a.p[0].heads + (a.p[1].heads ? a.p[1].heads + 4 : 2);
   int per[2] = {1, 1};
   for (int i = 0; i < 2; ++i) {
     QKPart& p = a.p[i];
     p.ctas = 0;
     if (p.heads == 0) continue;
-    int64_t share = most * p.heads / heads;
-    if (i == 1) share = most - a.p[0].ctas < share + 1 ? share : share + 1;
+    int64_t share = (most * (p.heads + 2) + heads / 2) / heads;
     if (share < 1) share = 1;
-    // a token's heads in as few items as still give every group one
-    const int64_t rows = a.tokens * p.heads, each = rows / (share * kGroups);
-    per[i] = (int)(each < 1 ? 1 : each < p.heads ? each : p.heads);
-    const int64_t items = a.tokens * ((p.heads + per[i] - 1) / per[i]);
+    // A token's heads in equal items: many even the groups' work out (a group takes whole ones),
+    // each makes the angles again.
+    const int64_t groups = share * kGroups;
+    int64_t best = INT64_MAX, items = a.tokens * p.heads;  // a head each where the groups suffice
+    const bool few = items <= groups;
+    for (int parts = 1; !few && parts <= p.heads && parts <= 64; ++parts) {
+      const int n = (p.heads + parts - 1) / parts;
+      const int64_t all = a.tokens * ((p.heads + n - 1) / n), cost = (all + groups - 1) / groups * (n + 2);
+      if (cost < best) {
+        best = cost;
+        per[i] = n;
+        items = all;
+      }
+    }
     const int64_t need = (items + kGroups - 1) / kGroups;
     const int64_t limit = qknorm_bwd_ctas(a.tokens, p.heads, a.sms);
     p.ctas = (int)(need < share ? need : share);

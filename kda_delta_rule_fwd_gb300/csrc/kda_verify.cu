@@ -21,12 +21,10 @@ using layer::Raw;
 using layer::fetch;
 using layer::open;
 
-#ifndef VTH
-#define VTH 128
-#define VPER 8
-#define VFILL 4
-#endif
-constexpr int kThreads = VTH, kWarps = kThreads / 32;
+// 256 sequences of 131072 tokens take 46 us with 8 blocks of 128 threads to an SM, 51 to 56 with 4 of
+// 256 and 59 with 2 of 512: a block waits three times for loads before its row's, so many small ones
+// hide it.
+constexpr int kThreads = 128, kPerSm = 8, kWarps = kThreads / 32;
 using u64 = unsigned long long;
 
 // A probability as hi 2^22 + lo: hi = p 2^22 to the nearest, lo = what is left to the nearest 2^-44,
@@ -109,7 +107,7 @@ struct Weights {
 };
 
 template <typename T, bool kWide>
-__global__ void __launch_bounds__(kThreads, VPER) verify_kernel(VerifyArgs a, int per) {
+__global__ void __launch_bounds__(kThreads, kPerSm) verify_kernel(VerifyArgs a, int per) {
   using W = Weights<T, kWide>;
   extern __shared__ u64 run[];  // sums of this block's runs [0, per)
   __shared__ u64 total_of[kWarps], total_here[2];
@@ -260,10 +258,11 @@ __global__ void __launch_bounds__(kThreads, VPER) verify_kernel(VerifyArgs a, in
 template <typename T, bool kWide>
 cudaError_t launch(const VerifyArgs& a) {
   using W = Weights<T, kWide>;
-  // blocks per sequence: as many as fill the device four times, with a run for half of the warps
+  // Blocks per sequence: half as many as are resident on the device, with a run for every warp (the
+  // same 256 sequences: 46 us, 49 with twice as many, 57 with half)
   const int runs = (a.V + W::kRun * kBatches - 1) / (W::kRun * kBatches);
   int blocks = 1;
-  while (blocks < 8 && (int64_t)a.B * blocks < VFILL * a.sms && runs >= kWarps * blocks) blocks *= 2;
+  while (blocks < 8 && (int64_t)a.B * blocks < 4 * a.sms && runs >= kWarps * blocks) blocks *= 2;
   const int per = (runs + blocks - 1) / blocks;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)a.B * blocks);
