@@ -480,16 +480,27 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
     auto query = [&](int part, int nt, int ks) {
       return kHoldQ ? qh[(part * NT + nt) * KS + ks] : qs[(part * (S::kRows / 8) * KS + nt * KS + ks) * 32 + lane];
     };
-    // c += A's parts times B's, down to the smallest that count
-    auto scores = [&](float (&c)[NT][4], const uint4 (&w)[AP], int ks) {
+    // c += A's parts times B's, down to the smallest that count.  The tensor cores cut what they add to a
+    // sum off instead of rounding it, which over many steps is a drift: with float32 queries the
+    // largest product of a step starts from 0 and is added in float32, the small ones add up in `rest`.
+    auto scores = [&](float (&c)[NT][4], float (&rest)[NT][4], const uint4 (&w)[AP], int ks) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int b = 0; b < QP; ++b) {
           const uint2 q = query(b, j, ks);
 #pragma unroll
-          for (int i = 0; i < AP; ++i)
-            if (i + b < (AP > QP ? AP : QP)) product<!kCoded>(c[j], w[i], q.x, q.y);
+          for (int i = 0; i < AP; ++i) {
+            if (i + b >= (AP > QP ? AP : QP)) continue;
+            if (FQ && i + b == 0) {
+              float one[4] = {0.f, 0.f, 0.f, 0.f};
+              product<!kCoded>(one, w[i], q.x, q.y);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) c[j][e] += one[e];
+            } else {
+              product<!kCoded>(FQ ? rest[j] : c[j], w[i], q.x, q.y);
+            }
+          }
         }
     };
     const int hi_min = len - a.T + row0 / a.rep + 1;
@@ -508,13 +519,13 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       const bool edge = seen != kAll || pos > hi_min - KT || pos < lo_max;
       const uint32_t kbase = smem_at(here), vbase = kbase + S::kHalf;
       // ---- scores: c[places][queries]
-      float c[KM][NT][4];
+      float c[KM][NT][4], rest[KM][NT][4];
 #pragma unroll
       for (int u = 0; u < KM; ++u)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c[u][j][e] = 0.f;
+          for (int e = 0; e < 4; ++e) c[u][j][e] = rest[u][j][e] = 0.f;
       if constexpr (kF32) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
@@ -530,7 +541,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             uint4 w[AP];
 #pragma unroll
             for (int k = 0; k < AP; ++k) w[k] = make_uint4(p[0][k], p[1][k], p[2][k], p[3][k]);
-            scores(c[u], w, ks);
+            scores(c[u], rest[u], w, ks);
           }
       } else {
 #pragma unroll
@@ -541,17 +552,25 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             matrix4(b, kbase + piece<CH>(u * 16 + mrow, 2 * i + mcol) * 16);
             if constexpr (!kCoded) {
               const uint4 w[1] = {make_uint4(b[0], b[1], b[2], b[3])};
-              scores(c[u], w, i);
+              scores(c[u], rest[u], w, i);
             } else {
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 uint4 w[1];
                 open4<CACHE>(b[2 * k], w[0].x, w[0].z);
                 open4<CACHE>(b[2 * k + 1], w[0].y, w[0].w);
-                scores(c[u], w, 2 * i + k);
+                scores(c[u], rest[u], w, 2 * i + k);
               }
             }
           }
+      }
+      if (FQ) {
+#pragma unroll
+        for (int u = 0; u < KM; ++u)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[u][j][e] += rest[u][j][e];
       }
       // powers of two of places g and g + 8, each worked out by one lane; a value's relative to the
       // largest so far, 0 for a row that is not finite (its readers become NaN through their sums)
@@ -715,12 +734,19 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       // ---- outputs
       auto outputs = [&](float (&o)[NT][4], const uint4 (&w)[AP], int u) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j) {
+          float large[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int b = 0; b < PP; ++b)
 #pragma unroll
             for (int i = 0; i < AP; ++i)
-              if (i + b < (AP > PP ? AP : PP)) product<!kCoded>(o[j], w[i], pw[b][u][j][0], pw[b][u][j][1]);
+              if (i + b < (AP > PP ? AP : PP))
+                product<!kCoded>(!FQ ? o[j] : i + b ? small : large, w[i], pw[b][u][j][0], pw[b][u][j][1]);
+          if (FQ) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] += large[e] + small[e];
+          }
+        }
       };
 #pragma unroll
       for (int u = 0; u < KM; ++u) {
