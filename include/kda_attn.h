@@ -37,8 +37,8 @@ extern "C" {
  * ---------------------------------------------------------------------- */
 typedef struct {
   int64_t tokens;       /* >= 0 */
-  int32_t q_heads;      /* heads of q per token, >= 1 */
-  int32_t k_heads;      /* heads of k per token, >= 0 (0: no k) */
+  int32_t q_heads;      /* heads of q per token, 1 .. 65536 */
+  int32_t k_heads;      /* heads of k per token, 0 .. 65536 (0: no k) */
   int32_t d;            /* channels per head, even, 2 .. 256 */
   int32_t rot;          /* rotated channels, even, 0 .. d */
   kda_dtype dtype;      /* q, k, their outputs and gradients */
@@ -90,7 +90,7 @@ typedef struct {
   int32_t B;            /* fixed length: sequences.  Packed: must be 1. */
   int32_t T;            /* tokens per sequence (fixed) or in total (packed), >= 0 */
   int32_t num_seqs;     /* packed: number of sequences; ignored when cu_seqlens is NULL */
-  int32_t heads, d;     /* key-value heads >= 1; channels 64 or 128 */
+  int32_t heads, d;     /* key-value heads, 1 .. 65536; channels 64 or 128 */
   int32_t page;         /* tokens per page, a power of two up to 65536 */
   int32_t max_pages;    /* columns of the page table, >= 1 */
   int32_t num_pages;    /* pages in the pools, >= 1 */
@@ -106,8 +106,8 @@ typedef struct {
  * Tokens whose place is below 0 (an idle row of a padded batch has lens 0) are
  * left out; a place past the table or a page that is not in the pool is left
  * out and reported (KDA_ERR_INVALID_ARG), malformed cu_seqlens are reported
- * (KDA_ERR_BAD_SEQLENS); every access stays inside the buffers.  Two tokens of
- * one call that meet in one row leave either's.  k_cache, v_cache, k_scale and
+ * (KDA_ERR_BAD_SEQLENS); every access stays inside the buffers.  A row in which
+ * two tokens of one call meet is undefined.  k_cache, v_cache, k_scale and
  * v_scale are 16-byte aligned; the scales are given exactly with 8-bit caches.
  * workspace: optional, >= 256 bytes, 256-byte aligned. */
 kda_status kda_cache_write(const kda_cache_shape* s, const void* k, const void* v,
@@ -139,7 +139,7 @@ kda_status kda_cache_read(const kda_cache_shape* s, const int32_t* cu_seqlens,
  * ---------------------------------------------------------------------- */
 typedef struct {
   int32_t B, T;         /* sequences >= 0; tokens 1 .. 8 */
-  int32_t q_heads, kv_heads; /* q_heads a multiple of kv_heads */
+  int32_t q_heads, kv_heads; /* q_heads a multiple of kv_heads, at most 65536 */
   int32_t d;            /* 64 or 128 */
   int32_t page, max_pages, num_pages; /* as kda_cache_shape */
   kda_dtype dtype;      /* q and out */

@@ -41,7 +41,7 @@ cudaError_t clear_status(void* ws, void* stream) {
 
 kda_status check_qknorm(const kda_qknorm_shape* s, QKArgs& a) {
   if (!s) return KDA_ERR_INVALID_ARG;
-  if (s->tokens < 0 || s->q_heads < 1 || s->k_heads < 0 || s->d < 2 || s->d % 2 || s->rot < 0 ||
+  if (s->tokens < 0 || s->q_heads < 1 || s->k_heads < 0 || s->q_heads > 65536 || s->k_heads > 65536 || s->d < 2 || s->d % 2 || s->rot < 0 ||
       s->rot % 2 || s->rot > s->d || !dtype_ok(s->dtype) || !(s->eps >= 0.f))
     return KDA_ERR_INVALID_ARG;
   if (s->d > 256) return KDA_ERR_UNSUPPORTED;

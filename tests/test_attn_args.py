@@ -34,7 +34,7 @@ def test_qknorm_arguments(lib):
     for s, want in ((dict(tokens=-1), bad), (dict(q_heads=0), bad), (dict(k_heads=-1), bad), (dict(d=63), bad),
                     (dict(d=0), bad), (dict(d=258), odd), (dict(rot=3), bad), (dict(rot=66), bad), (dict(rot=-2), bad),
                     (dict(dtype=7), bad), (dict(eps=-1.0), bad), (dict(eps=float("nan")), bad), (dict(ldq=255), bad),
-                    (dict(ldk=127), bad), (dict(tokens=1 << 40), bad)):
+                    (dict(ldk=127), bad), (dict(tokens=1 << 40), bad), (dict(q_heads=65537), bad), (dict(k_heads=65537), bad)):
         assert fwd(shape(**s)) == want, s
     assert fwd(None) == bad
     for i in (0, 1, 2, 3, 6, 7):
