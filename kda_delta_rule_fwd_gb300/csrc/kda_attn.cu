@@ -40,9 +40,10 @@ namespace attn {
 namespace {
 
 constexpr int kGroups = 4;    // key groups of a block
-// tiles that an item's beginning and end take the time of: the calls named at by_rows take 368, 334
-// and 342 us, and 249, 185 and 184, with 0, 4 and 8
-constexpr int kItemCost = 4;
+// Places that an item's beginning and end take the time of, from the blocks' own times: 256 sequences of
+// up to 8192 e4m3 places, 3.4 us an item and 2 us for 128 places of 4 rows; 16 sequences of up to 32768
+// int8 places, 8.7 us and 1.5 us for 64 of 32 rows.  (Without: 368 us for 334, 249 for 185.)
+constexpr int item_cost(int eights) { return eights == 4 ? 384 : 256; }
 constexpr int kLazy = 8, kShift = 7;  // 2^15 is the largest weight in f16
 constexpr float kNone = -3e38f;           // the base of a row that has seen nothing: every score passes it
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -198,7 +199,7 @@ struct Shape {
   // 16-bit parts of a key or value, of a query, of a weight
   static constexpr int kParts = kF32 ? 3 : 1, kQParts = kF32 ? 3 : FQ ? 2 : 1, kWParts = kF32 ? 3 : kCoded && !FQ ? 1 : 2;
   static constexpr int kThreads = kGroups * WM * 32, kPerSm = PER;
-  static constexpr int kRows = 8 * NT * WM, kTile = kGroups * KT;
+  static constexpr int kRows = 8 * NT * WM, kTile = kGroups * KT, kCost = item_cost(NT) / kTile;
   static constexpr int kElem = kCoded ? 1 : kF32 ? 4 : 2;
   static constexpr int kChunks = D * kElem / 16;           // 16-byte pieces of a row
   static constexpr int kHalf = KT * D * kElem;             // a group's keys (or values) of a tile
@@ -398,7 +399,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       if ((int64_t)len > (int64_t)a.t.max_pages << a.t.shift) bad = 1;
       if (t0 == 0 && t1 < now.tiles) {
         s.cut[blockIdx.x] = ((int64_t)n * a.hk + head) * s.chunks + now.chunk;
-        s.cut_at[blockIdx.x] = st.end - now.left - s.cost;
+        s.last[blockIdx.x] = (st.end - now.left + now.tiles - 1) / st.share;
       }
     }
     __syncthreads();
@@ -956,7 +957,7 @@ auto by_type(const AttnArgs& a, F f) {
 }
 
 Split split_for(const AttnArgs& a) {
-  return by_type(a, [&](auto shape) { return split_of(a, shape.kRows, shape.kTile, kItemCost, shape.kPerSm); });
+  return by_type(a, [&](auto shape) { return split_of(a, shape.kRows, shape.kTile, shape.kCost, shape.kPerSm); });
 }
 
 }  // namespace

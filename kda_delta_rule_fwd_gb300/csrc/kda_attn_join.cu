@@ -22,13 +22,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
     bad = __syncthreads_or(bad);
     if (tid == 0) *s.status = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
   }
-  const int64_t item = s.cut[blockIdx.x];
+  const int64_t item = s.cut[blockIdx.x], b1 = s.last[blockIdx.x];
   if (item < 0) return;
   const int64_t each = (int64_t)a.hk * s.chunks;
   const int n = (int)(item / each), head = (int)(item % each) / s.chunks;
   const int r = blockIdx.y, row = (int)(item % s.chunks) * s.rows + r;
   if (row >= a.T * a.rep) return;
-  const int64_t b0 = blockIdx.x, b1 = (s.cut_at[b0] + s.cost + keys_of(a, s.tile, n).tiles - 1) / *s.share;
+  const int64_t b0 = blockIdx.x;
   float m = -INFINITY;
   for (int64_t b = b0 + tid; b <= b1; b += blockDim.x) m = fmaxf(m, part_of(s, b, b == b0)[r]);
 #pragma unroll

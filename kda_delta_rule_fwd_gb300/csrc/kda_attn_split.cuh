@@ -22,9 +22,8 @@ constexpr int kMinPlaces = 256;  // of a block's share, where there are as many
 struct Split {
   unsigned int* status;   // workspace header
   unsigned int* verdict;  // [blocks]: what each block found
-  int64_t* share;         // tiles per block
   int64_t* cut;           // [blocks]: the item that begins in the block and goes on in the next, or -1
-  int64_t* cut_at;        // [blocks]: its position
+  int64_t* last;          // [blocks]: the block in which that item ends
   float* part;            // [blocks][2][rows (d + 2)]
   int64_t blocks, items;
   int rows, tile, cost, chunks, part_floats;
@@ -49,7 +48,7 @@ inline Split split_of(const AttnArgs& a, int rows, int tile, int cost, int per_s
   return s;
 }
 inline size_t split_bytes(const Split& s) {
-  return kWsHeader + pad256(4 * s.blocks) + pad256(8) + 2 * pad256(8 * s.blocks) +
+  return kWsHeader + pad256(4 * s.blocks) + 2 * pad256(8 * s.blocks) +
          pad256(s.blocks * 2 * s.part_floats * (int64_t)sizeof(float));
 }
 inline void split_place(Split& s, void* ws) {
@@ -58,11 +57,9 @@ inline void split_place(Split& s, void* ws) {
   p += kWsHeader;
   s.verdict = reinterpret_cast<unsigned int*>(p);
   p += pad256(4 * s.blocks);
-  s.share = reinterpret_cast<int64_t*>(p);
-  p += pad256(8);
   s.cut = reinterpret_cast<int64_t*>(p);
   p += pad256(8 * s.blocks);
-  s.cut_at = reinterpret_cast<int64_t*>(p);
+  s.last = reinterpret_cast<int64_t*>(p);
   p += pad256(8 * s.blocks);
   s.part = reinterpret_cast<float*>(p);
 }
@@ -90,6 +87,7 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs& a, int tile, int n) {
 // Where a block starts: item (n, j) with j = head and chunk, tile t of it; its tiles.
 struct Start {
   int64_t at, end;  // positions [at, end)
+  int64_t share;    // of a block
   int64_t before;   // places in the row of one (head, chunk) of the sequences before n
   int n;
 };
@@ -117,7 +115,7 @@ __device__ __forceinline__ bool find_start(const AttnArgs& a, const Split& s, in
   }
   int64_t share = (total * each + s.blocks - 1) / s.blocks;
   if (share < s.least) share = s.least;
-  if (blockIdx.x == 0 && tid == 0) *s.share = share;
+  out.share = share;
   out.at = blockIdx.x * share;
   out.end = min(out.at + share, total * each);
   if (out.at >= out.end) return false;
