@@ -193,7 +193,7 @@ struct Cursor {
 
 // NT: query rows of a warp in eights; WM: warps with rows of their own; KT: places of a key group
 // in a tile; PER: blocks to an SM
-template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER>
+template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER, bool SHARE = false>
 struct Shape {
   static constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8, kF32 = CACHE == KDA_CACHE_F32;
   // 16-bit parts of a key or value, of a query, of a weight
@@ -206,9 +206,12 @@ struct Shape {
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kSlice = NT == 1 ? 16 : 32, kPitch = kSlice + 2;     // channels of all groups' rows that meet at once
   static constexpr int kMerge = kGroups * kRows * kPitch * 4;
+  // shared weights: fragments of all groups' weights; maxima and largest powers
+  static constexpr int kWBytes = kGroups * kWParts * NT * 32 * 8, kTops = kGroups * kRows * 4 + 16;
+  static constexpr int kTail = SHARE ? kWBytes + kTops : 2 * kMerge;
   static constexpr int kQBytes = kRows * D * 2 * kQParts;
   static constexpr int bytes(int stages) {
-    return kGroups * stages * (kStage + 2 * KT + 4) + kQBytes + 8 * kRows + kGroups * kRows * 8 + 2 * kMerge;
+    return kGroups * stages * (kStage + 2 * KT + 4) + kQBytes + 12 * kRows + kGroups * kRows * 8 + kTail;
   }
   // as many stages as the SM's 228 KB hold for its blocks (each takes 1.5 KB for itself), up to six
   static constexpr int fit() {
@@ -222,10 +225,10 @@ struct Shape {
   static constexpr int oScale = oQ + kQBytes;
   static constexpr int oSeen = oScale + kGroups * kStages * 2 * KT;
   static constexpr int oRow = oSeen + kGroups * kStages * 4;
-  static constexpr int oStats = oRow + 8 * kRows;
+  static constexpr int oStats = oRow + 12 * kRows;
   static constexpr int oMerge = oStats + kGroups * kRows * 8;
   static constexpr int kBytes = bytes(kStages);
-  static_assert(oMerge % 16 == 0 && oMerge + 2 * kMerge == kBytes, "layout");
+  static_assert(oMerge % 16 == 0 && oMerge + kTail == kBytes, "layout");
 };
 // a row's 16-byte piece c, moved so that 8 rows' pieces c lie in different banks
 template <int CHUNKS>
@@ -241,10 +244,10 @@ __device__ __forceinline__ int key_piece(int row, int c) {
   else return piece<CHUNKS>(row, c);
 }
 
-template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER>
-__global__ void __launch_bounds__(Shape<FQ, CACHE, D, NT, WM, KT, PER>::kThreads, PER)
+template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER, bool SHARE>
+__global__ void __launch_bounds__(Shape<FQ, CACHE, D, NT, WM, KT, PER, SHARE>::kThreads, PER)
 attn_mma_kernel(AttnArgs a, Split s, bool words) {
-  using S = Shape<FQ, CACHE, D, NT, WM, KT, PER>;
+  using S = Shape<FQ, CACHE, D, NT, WM, KT, PER, SHARE>;
   using TQ = std::conditional_t<FQ, float, __nv_bfloat16>;
   constexpr bool kCoded = S::kCoded, kF32 = S::kF32;
   constexpr int AP = S::kParts, QP = S::kQParts, PP = S::kWParts;
@@ -252,6 +255,8 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
   constexpr bool kNext = kCoded || kF32;
   constexpr int KS = D / 16, KM = KT / 16, CH = S::kChunks;
   constexpr bool kHoldQ = NT * KS * QP <= 8;  // queries stay in registers
+  constexpr int OB = SHARE ? D / 16 / kGroups : D / 16;  // blocks of 16 channels that a warp adds up
+  static_assert(!SHARE || (!FQ && WM == 1 && KT == 16), "shared weights");
   constexpr unsigned kAll = KT == 32 ? 0xffffffffu : 0xffffu;
   extern __shared__ __align__(128) char raw[];
   __shared__ int64_t scratch[34];
@@ -290,6 +295,9 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
   unsigned* const seen_of = reinterpret_cast<unsigned*>(raw + S::oSeen) + grp * S::kStages;
   float* const row_factor = reinterpret_cast<float*>(raw + S::oRow);
   int* const row_end = reinterpret_cast<int*>(raw + S::oRow) + S::kRows;
+  int* const row_place = row_end + S::kRows;  // the row among a sequence's rows of the output
+  uint2* const shared_w = reinterpret_cast<uint2*>(raw + S::oMerge);  // [parts][groups][rows / 8][lanes]
+  float* const shared_top = reinterpret_cast<float*>(raw + S::oMerge + S::kWBytes);  // [groups][rows], then powers
   uint2* const qs = reinterpret_cast<uint2*>(raw + S::oQ) + wm * NT * KS * 32;  // [parts][rows / 8][steps][lanes]
 
   // The table's entries of the next request are read one request early.
@@ -376,7 +384,8 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
   };
   // all that the group's warps wrote of a stage is there, and nobody reads the one before
   auto meet = [&]() {
-    if constexpr (WM == 1) __syncwarp();
+    if constexpr (SHARE) __syncthreads();
+    else if constexpr (WM == 1) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * WM) : "memory");
   };
 
@@ -443,6 +452,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       if (lane == 0) {
         row_factor[r] = f > 1e-37f ? f : 1e-37f;
         row_end[r] = len - a.T + tok + 1;  // the row sees places below this
+        row_place[r] = tok * a.hq + row0 + r - tok * a.rep;
       }
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
@@ -457,7 +467,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
     }
     __syncthreads();
     float base[NT][2], l[NT][2], rf[NT][2];  // the weights' bases and sums, the scores' factors
-    float o[D / 16][NT][4];
+    float o[OB][NT][4];
     uint2 qh[kHoldQ ? QP * NT * KS : 1];
     int top = 0;  // the largest byte of a value seen
 #pragma unroll
@@ -469,7 +479,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         rf[i][e] = row_factor[(wm * NT + i) * 8 + 2 * t4 + e];
       }
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
+    for (int i = 0; i < OB; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -514,10 +524,22 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       char* const here = kv + stage * S::kStage;
       const uint8_t* const bytes = sc + stage * 2 * KT;
       const unsigned seen = seen_of[stage];
+      // what the decisions go by that the sharing warps take alike: the group's places, or the tile's
+      unsigned some = seen, all = seen;
+      if constexpr (SHARE) {
+#pragma unroll
+        for (int i = 1; i < kGroups; ++i) {
+          const unsigned x = seen_of[((grp + i) % kGroups - grp) * S::kStages + stage];
+          some |= x;
+          all &= x;
+        }
+      }
+      const int here_at = stage * S::kStage;
+      const int now_stage = stage;
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
-      if (seen == 0) continue;
-      const int pos = (int)((unsigned)now.lo + (unsigned)t * S::kTile + grp * KT);
-      const bool edge = seen != kAll || pos > hi_min - KT || pos < lo_max;
+      if (some == 0) continue;
+      const int first = (int)((unsigned)now.lo + (unsigned)t * S::kTile), pos = (int)((unsigned)first + grp * KT);
+      const bool edge = all != kAll || (SHARE ? first > hi_min - S::kTile || first < lo_max : pos > hi_min - KT || pos < lo_max);
       const uint32_t kbase = smem_at(here), vbase = kbase + S::kHalf;
       // ---- scores: c[places][queries]
       float c[KM][NT][4], rest[KM][NT][4];
@@ -573,30 +595,25 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) c[u][j][e] += rest[u][j][e];
       }
-      // powers of two of places g and g + 8, each worked out by one lane; a value's relative to the
-      // largest so far, 0 for a row that is not finite (its readers become NaN through their sums)
+      // powers of two of places g and g + 8, each worked out by one lane; a value's (below) relative to
+      // the largest so far.  The readers of a row that is not finite become NaN through their sums.
       float kf[KM][2], vf[KM][2];
       bool moved = false;
-      float rise = 1.f;
       unsigned nan_rows = 0;
+      int vb = 0, most = top;
       if constexpr (kCoded) {
-        const int kb = bytes[lane], vb = KT == 16 ? kb : bytes[KT + lane];
+        const int kb = bytes[lane];
+        vb = KT == 16 ? kb : bytes[KT + lane];
         const bool mine = KT == 16 ? lane >= 16 && (seen >> (lane & 15) & 1) : seen >> lane & 1;
         nan_rows = __ballot_sync(0xffffffffu, mine && vb == 255);
         if (KT == 16) nan_rows >>= 16;
-        const int most = max(top, (int)__reduce_max_sync(0xffffffffu, mine && vb != 255 ? vb : 0));
+        most = max(top, (int)__reduce_max_sync(0xffffffffu, mine && vb != 255 ? vb : 0));
         moved = most != top;
-        rise = __uint_as_float((uint32_t)max(127 + top - most, 0) << 23);
-        top = most;
-        const float vfac = vb == 255 ? 0.f : __uint_as_float((uint32_t)max(min(vb - top, 0) + 127 + kShift, 0) << 23);
-        const float kfac = KT == 16 && lane >= 16 ? vfac : power(kb);
+        const float kfac = power(kb);
 #pragma unroll
         for (int u = 0; u < KM; ++u)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            kf[u][e] = __shfl_sync(0xffffffffu, kfac, u * 16 + e * 8 + g);
-            vf[u][e] = __shfl_sync(0xffffffffu, KT == 16 ? kfac : vfac, (KT == 16 ? 16 : u * 16) + e * 8 + g);
-          }
+          for (int e = 0; e < 2; ++e) kf[u][e] = __shfl_sync(0xffffffffu, kfac, u * 16 + e * 8 + g);
       }
       if constexpr (kCoded) {
 #pragma unroll
@@ -631,28 +648,35 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             const uint4 w = reinterpret_cast<const uint4*>(here + S::kHalf)[i];
             found |= wild<CACHE>(w.x) || wild<CACHE>(w.y) || wild<CACHE>(w.z) || wild<CACHE>(w.w);
           }
-          if (__any_sync(0xffffffffu, found)) {
+          if (SHARE ? __syncthreads_or(found) : __any_sync(0xffffffffu, found)) {
             // the rows that do see such a value take it (their output stays so), then it is 0
 #pragma unroll 1
-            for (int key = 0; key < KT; ++key)
+            for (int key = 0; key < (SHARE ? S::kTile : KT); ++key) {
+              const int from = SHARE ? key / KT : grp, k = key % KT, place = first + from * KT + k;
+              const bool there = seen_of[(from - grp) * S::kStages + now_stage] >> k & 1;
+              const char* const row = raw + from * S::kStages * S::kStage + here_at + S::kHalf;
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i)
+              for (int i = 0; i < OB; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const int byte = (kNext ? i * 16 + 2 * g + h : i * 16 + h * 8 + g) * S::kElem;
-                  const char* at = here + S::kHalf + piece<CH>(key, byte / 16) * 16 + byte % 16;
+                  const int ch = (SHARE ? grp * OB * 16 : 0) + (kNext ? i * 16 + 2 * g + h : i * 16 + h * 8 + g);
+                  const int byte = ch * S::kElem;
+                  const char* at = row + piece<CH>(k, byte / 16) * 16 + byte % 16;
                   float x;
                   if constexpr (kCoded) x = (*reinterpret_cast<const uint8_t*>(at) & 0x7f) == 0x7f ? NAN : 0.f;
                   else if constexpr (kF32) x = *reinterpret_cast<const float*>(at);
                   else x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at));
-                  if (!isfinite(x)) {
+                  if (there && !isfinite(x)) {
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
-                      for (int e = 0; e < 2; ++e)
-                        if (on[j][e] >> key & 1) o[i][j][2 * h + e] += x;
+                      for (int e = 0; e < 2; ++e) {
+                        const int end = row_end[(wm * NT + j) * 8 + 2 * t4 + e];
+                        if (place < end && (a.window == 0 || place >= end - a.window)) o[i][j][2 * h + e] += x;
+                      }
                   }
                 }
+            }
             meet();
             if (wm == 0)
               for (int i = lane; i < S::kHalf / 4; i += 32) {
@@ -680,32 +704,63 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
           for (int u = 0; u < KM; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) high = fmaxf(high, fmaf(c[u][j][2 * h + e], rf[j][e], -base[j][e]));
-      if (__any_sync(0xffffffffu, moved || high > (float)kLazy)) {
+      const bool past = moved || high > (float)kLazy;
+      if (SHARE ? __syncthreads_or(past) : __any_sync(0xffffffffu, past)) {
+        float mx[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = -INFINITY;
+            float x = -INFINITY;
 #pragma unroll
             for (int u = 0; u < KM; ++u)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) mx = fmaxf(mx, c[u][j][2 * h + e]);
+              for (int h = 0; h < 2; ++h) x = fmaxf(x, c[u][j][2 * h + e]);
 #pragma unroll
-            for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
-            mx *= rf[j][e];
-            float al = rise;
-            if (mx - base[j][e] > (float)kLazy) {
-              const float f = exp2_of(base[j][e] - mx);
-              base[j][e] = mx;
+            for (int i = 4; i < 32; i <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
+            mx[j][e] = x;
+            if (SHARE && g == 0) shared_top[grp * S::kRows + j * 8 + 2 * t4 + e] = x;
+          }
+        if constexpr (SHARE) {  // the largest of the tile
+          int* const powers = reinterpret_cast<int*>(shared_top + kGroups * S::kRows);
+          if (lane == 0) powers[grp] = most;
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < kGroups; ++i) {
+            most = max(most, powers[i]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) mx[j][e] = fmaxf(mx[j][e], shared_top[i * S::kRows + j * 8 + 2 * t4 + e]);
+          }
+        }
+        const float rise = __uint_as_float((uint32_t)max(127 + top - most, 0) << 23);
+        top = most;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = mx[j][e] * rf[j][e];
+            float al = kCoded ? rise : 1.f;
+            if (x - base[j][e] > (float)kLazy) {
+              const float f = exp2_of(base[j][e] - x);
+              base[j][e] = x;
               l[j][e] *= f;
               al *= f;
             }
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
+            for (int i = 0; i < OB; ++i) {
               o[i][j][e] *= al;
               o[i][j][2 + e] *= al;
             }
           }
+      }
+      if constexpr (kCoded) {  // a value's power, 0 for a row that is not finite
+        const float vfac = vb == 255 ? 0.f : __uint_as_float((uint32_t)max(min(vb - top, 0) + 127 + kShift, 0) << 23);
+#pragma unroll
+        for (int u = 0; u < KM; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) vf[u][e] = __shfl_sync(0xffffffffu, vfac, (KT == 16 ? 16 : u * 16) + e * 8 + g);
       }
       uint32_t pw[PP][KM][NT][2];
 #pragma unroll
@@ -749,6 +804,49 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
           }
         }
       };
+      if constexpr (SHARE) {
+        // all groups' weights through shared memory; each warp adds up a quarter of the channels
+#pragma unroll
+        for (int b = 0; b < PP; ++b)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            shared_w[((b * kGroups + grp) * NT + j) * 32 + lane] = make_uint2(pw[b][0][j][0], pw[b][0][j][1]);
+        __syncthreads();
+        const uint32_t values = smem_at(raw + here_at + S::kHalf);  // of group 0
+        constexpr uint32_t kApart = S::kStages * S::kStage;         // to the next group's
+        auto add = [&](float (&o)[NT][4], const uint4& w, int u) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int b = 0; b < PP; ++b) {
+              const uint2 p = shared_w[((b * kGroups + u) * NT + j) * 32 + lane];
+              product<!kCoded>(o[j], w, p.x, p.y);
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+          uint32_t b[4];
+          if constexpr (!kCoded) {
+#pragma unroll
+            for (int i = 0; i < OB; ++i) {
+              matrix4_trans(b, values + u * kApart + piece<CH>(vrow, (grp * OB + i) * 2 + vcol) * 16);
+              add(o[i], make_uint4(b[0], b[1], b[2], b[3]), u);
+            }
+          } else {
+            // two blocks of a group's values, or one block of two groups'
+            if (OB == 1 && (u & 1)) continue;
+            const uint32_t at = OB == 2 ? piece<CH>(mrow, grp * 2 + mcol) * 16 : mcol * kApart + piece<CH>(mrow, grp) * 16;
+            matrix4_trans(b, values + u * kApart + at);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint4 w;
+              open4<CACHE>(__byte_perm(b[2 * k], 0u, 0x3120), w.x, w.y);
+              open4<CACHE>(__byte_perm(b[2 * k + 1], 0u, 0x3120), w.z, w.w);
+              add(o[OB == 2 ? k : 0], w, OB == 2 ? u : u + k);
+            }
+          }
+        }
+      } else {
 #pragma unroll
       for (int u = 0; u < KM; ++u) {
         if constexpr (kF32) {
@@ -789,6 +887,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             }
           }
         }
+      }
       }
     }
 
@@ -844,6 +943,35 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         a.lse[place_of(tid)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
       }
     }
+    if constexpr (SHARE) {  // each warp has the sums of its channels
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = j * 8 + 2 * t4 + e;
+          if (r >= rows) continue;
+          float m, f = up;
+          if (whole) {
+            const float sum = row_sum(r, m);
+            f = sum == 0.f ? 0.f : up / sum;
+          }
+          TQ* const to = static_cast<TQ*>(a.out) + ((int64_t)n * a.T * a.hq + head * a.rep + row_place[r]) * D;
+#pragma unroll
+          for (int i = 0; i < OB; ++i) {
+            const float x = o[i][j][e] * f, z = o[i][j][2 + e] * f;
+            const int ch = (grp * OB + i) * 16 + (kNext ? 2 * g : g), next = kNext ? 1 : 8;
+            if (!whole) {
+              part[2 * S::kRows + r * D + ch] = x;
+              part[2 * S::kRows + r * D + ch + next] = z;
+            } else if (kNext && words) {
+              *reinterpret_cast<uint32_t*>(to + ch) = layer::pack_bf16(x, z);
+            } else {
+              to[ch] = from_f32<TQ>(x);
+              to[ch + next] = from_f32<TQ>(z);
+            }
+          }
+        }
+    } else {
     constexpr int kSlice = S::kSlice, kPairs = kSlice / 2;
     // a thread's rows and channels of a slice are the same in every turn
     constexpr int kPer = (S::kRows * kPairs + S::kThreads - 1) / S::kThreads;
@@ -902,6 +1030,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         }
       }
     }
+    }
     now.pass(a, s, t1 - t0);
   }
   copy_wait<0>();
@@ -909,10 +1038,10 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
   if (tid == 0) s.verdict[blockIdx.x] = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
 }
 
-template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER>
-cudaError_t launch(Shape<FQ, CACHE, D, NT, WM, KT, PER>, const AttnArgs& a, const Split& s) {
-  using S = Shape<FQ, CACHE, D, NT, WM, KT, PER>;
-  auto* kernel = attn_mma_kernel<FQ, CACHE, D, NT, WM, KT, PER>;
+template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER, bool SHARE>
+cudaError_t launch(Shape<FQ, CACHE, D, NT, WM, KT, PER, SHARE>, const AttnArgs& a, const Split& s) {
+  using S = Shape<FQ, CACHE, D, NT, WM, KT, PER, SHARE>;
+  auto* kernel = attn_mma_kernel<FQ, CACHE, D, NT, WM, KT, PER, SHARE>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
   constexpr uintptr_t two = FQ ? 8 : 4;  // whole pairs of q and out
@@ -933,8 +1062,14 @@ auto by_rows(const AttnArgs& a, F f) {
   const int rows = a.T * a.rep;
   if (rows <= 8) return f(Shape<false, CACHE, D, 1, 1, kPlaces, 3>());
   if (rows <= 16) return f(Shape<false, CACHE, D, 2, 1, kPlaces, 2>());
-  if (rows <= 32) return f(Shape<false, CACHE, D, 4, 1, 16, kCoded ? 2 : 1>());
-  return f(Shape<false, CACHE, D, 4, 2, 16, 1>());
+#ifndef SP4
+#define SP4 4
+#define SP8 2
+#define SB4 2
+#define SB8 2
+#endif
+  if (rows <= 32) return f(Shape<false, CACHE, D, 4, 1, 16, kCoded ? SP4 : SB4, true>());
+  return f(Shape<false, CACHE, D, 8, 1, 16, kCoded ? SP8 : SB8, true>());
 }
 // float32 queries: their parts take room, so 32 rows at most
 template <int CACHE, int D, class F>
