@@ -358,11 +358,15 @@ def attn_step(q, cache, pages, lens, *, scale=None, window=0, out=None, lse=None
     elif want_lse:
         lse = torch.empty(q.shape[:3], dtype=_F32, device=q.device)
     if workspace is None:  # whole 256-byte units
-        workspace = lens.new_empty(lib.kda_attn_workspace_size(shape) // 4)
-    _check(lib.kda_attn_step(shape, q.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(),
-                             _ptr(cache[2]), _ptr(cache[3]), pages.data_ptr(), lens.data_ptr(),
-                             out.data_ptr(), _ptr(lse), *_ws(workspace, q),
-                             _stream(q.get_device())), "kda_attn_step")
+        size = lib.kda_attn_workspace_size(shape)
+        workspace = lens.new_empty(size // 4)
+        ws = workspace.data_ptr()
+    else:
+        ws, size = _ws(workspace, q)
+    k, v, ks, vs = cache
+    _check(lib.kda_attn_step(shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(ks), _ptr(vs),
+                             pages.data_ptr(), lens.data_ptr(), out.data_ptr(), _ptr(lse), ws,
+                             size, _stream(q.get_device())), "kda_attn_step")
     return (out, lse) if want_lse else out
 
 
@@ -377,7 +381,8 @@ def draft_verify(p, q, drafts, u, *, num_draft=None, tokens=None, num_commit=Non
     certain), ``u [B,K+1]`` float32 in [0, 1), the last for the drawn token; ``num_draft`` int32
     ``[B]`` where sequences have fewer than K (-1: an idle row).  Returns ``tokens [B,K+1]`` (the
     kept drafts, the drawn token, then -1) and ``num_commit [B]``, the kept drafts and the token
-    before them: the step forms' count of tokens whose state is kept."""
+    before them: the step forms' count of tokens whose state is kept.  With K = 0 (``drafts`` may
+    be None) a token is drawn from ``p``."""
     if _elsewhere(p, stream):
         with _under(p, stream):
             return draft_verify(p, q, drafts, u, num_draft=num_draft, tokens=tokens,
@@ -388,6 +393,10 @@ def draft_verify(p, q, drafts, u, *, num_draft=None, tokens=None, num_commit=Non
         raise TypeError("p must be float32 or bfloat16")
     B, rows, V = p.shape
     K = rows - 1
+    if drafts is None:
+        if K:
+            raise ValueError("drafts must be given")
+        drafts = torch.empty((B, 0), dtype=_I32, device=p.device)
     _dense(p, "p", p.dtype, p.shape, p)
     if q is not None:
         _dense(q, "q", p.dtype, (B, K, V), p)

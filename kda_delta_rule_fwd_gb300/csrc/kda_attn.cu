@@ -12,6 +12,11 @@
 //     O^T = V^T P^T: A = values (ldmatrix.trans), B = the weights: S^T's accumulators, packed to
 //                    16 bits and transposed 8 x 8 in registers (movmatrix)
 //
+// Above 16 rows the outputs of all channels no longer leave a warp enough registers for others to
+// run beside it (253 of them: two warps to a scheduler, five cycles to an instruction).  There the four
+// groups share their weights through shared memory and each adds up a quarter of the channels for all
+// places of the tile; the rows' bases are then the block's, three barriers to a tile.
+//
 // Types.  bf16 caches: products of bf16, exact in float32; a weight enters as two bf16 parts
 // (16 bits), since one alone would cost as much as the output's own rounding.  Codes become f16,
 // exactly; queries become f16 after a power of two per row has brought their largest to 2^13,
@@ -40,9 +45,10 @@ namespace attn {
 namespace {
 
 constexpr int kGroups = 4;    // key groups of a block
-// Places that an item's beginning and end take the time of, from the blocks' own times: 256 sequences of
-// up to 8192 e4m3 places, 3.4 us an item and 2 us for 128 places of 4 rows; 16 sequences of up to 32768
-// int8 places, 8.7 us and 1.5 us for 64 of 32 rows.  (Without: 368 us for 334, 249 for 185.)
+// Places that an item's beginning and end take the time of.  256 sequences of up to 8192 e4m3 places, 4
+// rows (3.4 us an item, 2 us for 128 places, from the blocks' own times): 368 us with 0, 334 with 256
+// and with 512.  16 sequences of up to 32768 int8 places, 32 rows: 153, 150, 148 and 152 us with 192,
+// 256, 384 and 640.
 constexpr int item_cost(int eights) { return eights == 4 ? 384 : 256; }
 constexpr int kLazy = 8, kShift = 7;  // 2^15 is the largest weight in f16
 constexpr float kNone = -3e38f;           // the base of a row that has seen nothing: every score passes it
@@ -191,8 +197,8 @@ struct Cursor {
   }
 };
 
-// NT: query rows of a warp in eights; WM: warps with rows of their own; KT: places of a key group
-// in a tile; PER: blocks to an SM
+// FQ: float32 queries; NT: query rows of a warp in eights; WM: warps with rows of their own; KT: places
+// of a key group in a tile; PER: blocks to an SM; SHARE: the groups share their weights
 template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER, bool SHARE = false>
 struct Shape {
   static constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8, kF32 = CACHE == KDA_CACHE_F32;
@@ -204,7 +210,7 @@ struct Shape {
   static constexpr int kChunks = D * kElem / 16;           // 16-byte pieces of a row
   static constexpr int kHalf = KT * D * kElem;             // a group's keys (or values) of a tile
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kSlice = NT == 1 ? 16 : 32, kPitch = kSlice + 2;     // channels of all groups' rows that meet at once
+  static constexpr int kSlice = NT == 1 ? 16 : 32, kPitch = kSlice + 2;  // channels of an item's end that meet at once
   static constexpr int kMerge = kGroups * kRows * kPitch * 4;
   // shared weights: fragments of all groups' weights; maxima and largest powers
   static constexpr int kWBytes = kGroups * kWParts * NT * 32 * 8, kTops = kGroups * kRows * 4 + 16;
@@ -848,46 +854,46 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         }
       } else {
 #pragma unroll
-      for (int u = 0; u < KM; ++u) {
-        if constexpr (kF32) {
+        for (int u = 0; u < KM; ++u) {
+          if constexpr (kF32) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {  // channels 2 g and 2 g + 1, places 2 t, 2 t + 1 and 8 behind them
-            float2 x[4];
+            for (int i = 0; i < D / 16; ++i) {  // channels 2 g and 2 g + 1, places 2 t, 2 t + 1 and 8 behind them
+              float2 x[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = u * 16 + 2 * t4 + (k & 1) + (k >> 1) * 8;
-              x[k] = *reinterpret_cast<const float2*>(here + S::kHalf + piece<CH>(r, 4 * i + (g >> 1)) * 16 + (g & 1) * 8);
-            }
-            uint32_t p[4][3];
-            split<true, 3>(x[0].x, x[1].x, p[0]);
-            split<true, 3>(x[0].y, x[1].y, p[1]);
-            split<true, 3>(x[2].x, x[3].x, p[2]);
-            split<true, 3>(x[2].y, x[3].y, p[3]);
-            uint4 w[AP];
+              for (int k = 0; k < 4; ++k) {
+                const int r = u * 16 + 2 * t4 + (k & 1) + (k >> 1) * 8;
+                x[k] = *reinterpret_cast<const float2*>(here + S::kHalf + piece<CH>(r, 4 * i + (g >> 1)) * 16 + (g & 1) * 8);
+              }
+              uint32_t p[4][3];
+              split<true, 3>(x[0].x, x[1].x, p[0]);
+              split<true, 3>(x[0].y, x[1].y, p[1]);
+              split<true, 3>(x[2].x, x[3].x, p[2]);
+              split<true, 3>(x[2].y, x[3].y, p[3]);
+              uint4 w[AP];
 #pragma unroll
-            for (int k = 0; k < AP; ++k) w[k] = make_uint4(p[0][k], p[1][k], p[2][k], p[3][k]);
-            outputs(o[i], w, u);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < CH / 2; ++i) {
-            uint32_t b[4];
-            matrix4_trans(b, vbase + piece<CH>(u * 16 + vrow, 2 * i + vcol) * 16);
-            if constexpr (!kCoded) {
-              const uint4 w[1] = {make_uint4(b[0], b[1], b[2], b[3])};
+              for (int k = 0; k < AP; ++k) w[k] = make_uint4(p[0][k], p[1][k], p[2][k], p[3][k]);
               outputs(o[i], w, u);
-            } else {
+            }
+          } else {
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                uint4 w[1];  // even channels of places 0-7, odd ones, the same of 8-15
-                open4<CACHE>(__byte_perm(b[2 * k], 0u, 0x3120), w[0].x, w[0].y);
-                open4<CACHE>(__byte_perm(b[2 * k + 1], 0u, 0x3120), w[0].z, w[0].w);
-                outputs(o[2 * i + k], w, u);
+            for (int i = 0; i < CH / 2; ++i) {
+              uint32_t b[4];
+              matrix4_trans(b, vbase + piece<CH>(u * 16 + vrow, 2 * i + vcol) * 16);
+              if constexpr (!kCoded) {
+                const uint4 w[1] = {make_uint4(b[0], b[1], b[2], b[3])};
+                outputs(o[i], w, u);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  uint4 w[1];  // even channels of places 0-7, odd ones, the same of 8-15
+                  open4<CACHE>(__byte_perm(b[2 * k], 0u, 0x3120), w[0].x, w[0].y);
+                  open4<CACHE>(__byte_perm(b[2 * k + 1], 0u, 0x3120), w[0].z, w[0].w);
+                  outputs(o[2 * i + k], w, u);
+                }
               }
             }
           }
         }
-      }
       }
     }
 
@@ -929,10 +935,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       for (int i = 0; i < kGroups; ++i) sum += stats[i * S::kRows + r].y * exp2_of(stats[i * S::kRows + r].x - base);
       return sum;
     };
-    auto place_of = [&](int r) {  // the row's place in the output
-      const int row = row0 + r, tok = row / a.rep;
-      return ((int64_t)n * a.T + tok) * a.hq + head * a.rep + row - tok * a.rep;
-    };
+    const int64_t out0 = (int64_t)n * a.T * a.hq + head * a.rep;  // with row_place the row's place in the output
     if (tid < rows) {
       float m;
       const float sum = row_sum(tid, m);
@@ -940,7 +943,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         part[tid] = m;
         part[S::kRows + tid] = sum;
       } else if (a.lse) {
-        a.lse[place_of(tid)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        a.lse[out0 + row_place[tid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
       }
     }
     if constexpr (SHARE) {  // each warp has the sums of its channels
@@ -955,7 +958,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             const float sum = row_sum(r, m);
             f = sum == 0.f ? 0.f : up / sum;
           }
-          TQ* const to = static_cast<TQ*>(a.out) + ((int64_t)n * a.T * a.hq + head * a.rep + row_place[r]) * D;
+          TQ* const to = static_cast<TQ*>(a.out) + (out0 + row_place[r]) * D;
 #pragma unroll
           for (int i = 0; i < OB; ++i) {
             const float x = o[i][j][e] * f, z = o[i][j][2 + e] * f;
@@ -972,64 +975,64 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
           }
         }
     } else {
-    constexpr int kSlice = S::kSlice, kPairs = kSlice / 2;
-    // a thread's rows and channels of a slice are the same in every turn
-    constexpr int kPer = (S::kRows * kPairs + S::kThreads - 1) / S::kThreads;
-    float inverse[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int r = (i * S::kThreads + tid) / kPairs;
-      float m, sum = 1.f;
-      if (r < rows && whole) sum = row_sum(r, m);
-      inverse[i] = sum == 0.f ? 0.f : 1.f / sum;
-    }
-#pragma unroll
-    for (int q = 0; q < D / kSlice; ++q) {
-      float* const buf = reinterpret_cast<float*>(raw + S::oMerge + (q & 1) * S::kMerge);  // [groups][rows][kPitch]
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float* const to = buf + (grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e) * S::kPitch;
-#pragma unroll
-          for (int i = 0; i < kSlice / 16; ++i) {
-            const float x = o[q * (kSlice / 16) + i][j][e] * up * scale_by[j][e];
-            const float z = o[q * (kSlice / 16) + i][j][2 + e] * up * scale_by[j][e];
-            if constexpr (kNext) {
-              *reinterpret_cast<float2*>(to + i * 16 + 2 * g) = make_float2(x, z);
-            } else {
-              to[i * 16 + g] = x;
-              to[i * 16 + 8 + g] = z;
-            }
-          }
-        }
-      __syncthreads();
+      constexpr int kSlice = S::kSlice, kPairs = kSlice / 2;
+      // a thread's rows and channels of a slice are the same in every turn
+      constexpr int kPer = (S::kRows * kPairs + S::kThreads - 1) / S::kThreads;
+      float inverse[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int x = i * S::kThreads + tid, r = x / kPairs, ch = x % kPairs * 2;
-        if (r >= rows) break;
-        float2 v = make_float2(0.f, 0.f);
+        const int r = (i * S::kThreads + tid) / kPairs;
+        float m, sum = 1.f;
+        if (r < rows && whole) sum = row_sum(r, m);
+        inverse[i] = sum == 0.f ? 0.f : 1.f / sum;
+      }
 #pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-          const float2 w = *reinterpret_cast<const float2*>(buf + (k * S::kRows + r) * S::kPitch + ch);
-          v.x += w.x;
-          v.y += w.y;
-        }
-        if (whole) {
-          TQ* to = static_cast<TQ*>(a.out) + place_of(r) * D + q * kSlice + ch;
-          if (words && FQ) {
-            *reinterpret_cast<float2*>(to) = make_float2(v.x * inverse[i], v.y * inverse[i]);
-          } else if (words) {
-            *reinterpret_cast<uint32_t*>(to) = layer::pack_bf16(v.x * inverse[i], v.y * inverse[i]);
-          } else {
-            to[0] = from_f32<TQ>(v.x * inverse[i]);
-            to[1] = from_f32<TQ>(v.y * inverse[i]);
+      for (int q = 0; q < D / kSlice; ++q) {
+        float* const buf = reinterpret_cast<float*>(raw + S::oMerge + (q & 1) * S::kMerge);  // [groups][rows][kPitch]
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float* const to = buf + (grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e) * S::kPitch;
+#pragma unroll
+            for (int i = 0; i < kSlice / 16; ++i) {
+              const float x = o[q * (kSlice / 16) + i][j][e] * up * scale_by[j][e];
+              const float z = o[q * (kSlice / 16) + i][j][2 + e] * up * scale_by[j][e];
+              if constexpr (kNext) {
+                *reinterpret_cast<float2*>(to + i * 16 + 2 * g) = make_float2(x, z);
+              } else {
+                to[i * 16 + g] = x;
+                to[i * 16 + 8 + g] = z;
+              }
+            }
           }
-        } else {
-          *reinterpret_cast<float2*>(part + 2 * S::kRows + r * D + q * kSlice + ch) = v;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int x = i * S::kThreads + tid, r = x / kPairs, ch = x % kPairs * 2;
+          if (r >= rows) break;
+          float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < kGroups; ++k) {
+            const float2 w = *reinterpret_cast<const float2*>(buf + (k * S::kRows + r) * S::kPitch + ch);
+            v.x += w.x;
+            v.y += w.y;
+          }
+          if (whole) {
+            TQ* to = static_cast<TQ*>(a.out) + (out0 + row_place[r]) * D + q * kSlice + ch;
+            if (words && FQ) {
+              *reinterpret_cast<float2*>(to) = make_float2(v.x * inverse[i], v.y * inverse[i]);
+            } else if (words) {
+              *reinterpret_cast<uint32_t*>(to) = layer::pack_bf16(v.x * inverse[i], v.y * inverse[i]);
+            } else {
+              to[0] = from_f32<TQ>(v.x * inverse[i]);
+              to[1] = from_f32<TQ>(v.y * inverse[i]);
+            }
+          } else {
+            *reinterpret_cast<float2*>(part + 2 * S::kRows + r * D + q * kSlice + ch) = v;
+          }
         }
       }
-    }
     }
     now.pass(a, s, t1 - t0);
   }
@@ -1053,8 +1056,9 @@ cudaError_t launch(Shape<FQ, CACHE, D, NT, WM, KT, PER, SHARE>, const AttnArgs& 
 // f(Shape) for the rows of a call: 8, 16, 32 or 64 to a block.  One GB300, us: 256 sequences of up
 // to 8192 e4m3 places, 4 rows: 32 places a group and 3 blocks to an SM 334, 16 and 4 blocks 389, 32
 // and 2 blocks 488 (before the ends were weighed in); 131071 bf16 places: 3 blocks 92, 2 blocks 94;
-// 16 sequences of up to 32768 int8 places, 32 rows: four eights to a warp 185, two 224 to 234 (codes
-// opened twice), four with 32 places a group 300 (one block to an SM).
+// 16 sequences of up to 32768 int8 places, 32 rows: shared weights with 3 blocks to an SM 148, with 4
+// or 2 blocks 160, all channels in each warp 172; 32 sequences of 8192 bf16 places, 32 and 64 rows:
+// shared 226 and 353, not shared 273 and 385.
 template <int CACHE, int D, class F>
 auto by_rows(const AttnArgs& a, F f) {
   constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
@@ -1062,14 +1066,8 @@ auto by_rows(const AttnArgs& a, F f) {
   const int rows = a.T * a.rep;
   if (rows <= 8) return f(Shape<false, CACHE, D, 1, 1, kPlaces, 3>());
   if (rows <= 16) return f(Shape<false, CACHE, D, 2, 1, kPlaces, 2>());
-#ifndef SP4
-#define SP4 4
-#define SP8 2
-#define SB4 2
-#define SB8 2
-#endif
-  if (rows <= 32) return f(Shape<false, CACHE, D, 4, 1, 16, kCoded ? SP4 : SB4, true>());
-  return f(Shape<false, CACHE, D, 8, 1, 16, kCoded ? SP8 : SB8, true>());
+  if (rows <= 32) return f(Shape<false, CACHE, D, 4, 1, 16, kCoded ? 3 : 2, true>());
+  return f(Shape<false, CACHE, D, 8, 1, 16, 2, true>());
 }
 // float32 queries: their parts take room, so 32 rows at most
 template <int CACHE, int D, class F>

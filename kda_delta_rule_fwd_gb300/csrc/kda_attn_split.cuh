@@ -4,12 +4,12 @@
 // heads of the group); its keys are tiles of `tile` places.  All items' tiles in a row, sequence
 // by sequence, are cut into equal shares, one per block: the lengths are on the device, so every
 // block counts the tiles by itself and finds its share.  An item begins with `cost` places in the
-// row that stand for its own beginning and end, so that blocks with many short items get fewer tiles.  A block walks the items of its share; an
-// item that lies in it whole is written out, a part goes to the workspace as (maximum, sum,
-// unnormalised output) per row: a block has at most two parts, the rest of an item that begins in
-// an earlier block (slot 0) and the beginning of one that goes on in the next (slot 1).  The join
-// kernel looks at each block that cut an item at its end, and adds that item's parts in the order
-// of the blocks.
+// row that stand for its own beginning and end, so that blocks with many short items get fewer
+// tiles.  A block walks the items of its share; an item that lies in it whole is written out, a part
+// goes to the workspace as (maximum, sum, unnormalised output) per row: a block has at most two
+// parts, the rest of an item that begins in an earlier block (slot 0) and the beginning of one that
+// goes on in the next (slot 1).  The join kernel looks at each block that cut an item at its end,
+// and adds that item's parts in the order of the blocks.
 #pragma once
 
 #include "kda_attn.cuh"

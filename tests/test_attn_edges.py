@@ -202,3 +202,33 @@ def test_repeatable_gradients_and_many_sequences(kda):
         one = kda.attn_step(q[i:i + 1].contiguous(), cache, pages[i:i + 1].contiguous(), lens[i:i + 1].contiguous())
         assert ((got[i].float() - one[0].float()).abs() <= 2.0 ** -5).all()
     assert not got[0].any()
+
+
+@pytest.mark.parametrize("dtype,kind", [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.int8), (torch.float32, torch.float32)])
+@pytest.mark.parametrize("T,rep", [(1, 3), (4, 7), (8, 5)])
+def test_odd_bases(kda, dtype, kind, T, rep):
+    """q, out and lse one element off every alignment give the same bits, over whole items and parts."""
+    q, cache, pages, full, _, _ = attn_state(kda, 2, 2 * rep, 2, 64, 16, 3000, kind, 8, T=T)
+    q = q.to(dtype)
+    lens = torch.tensor([3000, 90], dtype=torch.int32, device="cuda")
+    want, wl = kda.attn_step(q, cache, pages, lens, want_lse=True)
+    flat = torch.zeros(q.numel() + 1, dtype=dtype, device="cuda")
+    flat[1:] = q.flatten()
+    out = torch.zeros(q.numel() + 1, dtype=dtype, device="cuda")
+    lse = torch.zeros(wl.numel() + 1, device="cuda")
+    kda.attn_step(flat[1:].view(q.shape), cache, pages, lens, out=out[1:].view(q.shape), lse=lse[1:].view(wl.shape))
+    assert torch.equal(out[1:].view(q.shape), want) and torch.equal(lse[1:].view(wl.shape), wl)
+    wide = torch.zeros(2, T, 2 * rep * 64 + 3, dtype=dtype, device="cuda")
+    wide[..., 1:-2] = q.flatten(2)
+    assert torch.equal(kda.attn_step(wide[..., 1:-2].unflatten(-1, (2 * rep, 64)), cache, pages, lens), want)
+
+
+def test_drawing_without_drafts(kda):
+    """K = 0: a token from p, with drafts left out."""
+    p = torch.softmax(torch.randn(9, 1, 77, device="cuda"), -1)
+    u = torch.rand(9, 1, device="cuda")
+    got, commit = kda.draft_verify(p, None, None, u)
+    want = ref.verify(p.cpu(), None, torch.zeros(9, 0, dtype=torch.int32), u.cpu())
+    assert torch.equal(got.cpu(), want[0]) and (commit == 1).all()
+    with pytest.raises(ValueError, match="drafts"):
+        kda.draft_verify(torch.cat([p, p], 1), None, None, torch.rand(9, 2, device="cuda"))
