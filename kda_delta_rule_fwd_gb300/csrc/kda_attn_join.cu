@@ -7,41 +7,45 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// One block per cut item and row: the parts' outputs weighted by 2^(m - the largest m), over the
-// sum of their sums.  A lane has four channels, each warp every fourth part.
+// For each cut item and row: the parts' outputs weighted by 2^(m - the largest m), over the sum of
+// their sums.  A lane has four channels.  Few rows (long items in many parts): a block per row, whose
+// four warps take every fourth part; many rows: a warp per row (32 rows of 304 cuts, mostly of two
+// parts, take 14 us with a block each).
 constexpr int kJoinWarps = 4;
-template <typename T, int D>
+template <typename T, int D, int WAYS>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, Split s) {
-  __shared__ float4 fold[kJoinWarps][32];
-  __shared__ float sums[kJoinWarps], tops[kJoinWarps];
+  __shared__ float4 fold[WAYS][32];
+  __shared__ float sums[WAYS], tops[WAYS];
   cudaGridDependencySynchronize();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, way = WAYS == 1 ? 0 : warp;
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     unsigned int bad = 0;
     for (int64_t b = tid; b < s.blocks; b += blockDim.x) bad |= s.verdict[b];
     bad = __syncthreads_or(bad);
     if (tid == 0) *s.status = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
   }
-  const int64_t item = s.cut[blockIdx.x], b1 = s.last[blockIdx.x];
+  const int64_t b0 = blockIdx.x, item = s.cut[b0], b1 = s.last[b0];
   if (item < 0) return;
   const int64_t each = (int64_t)a.hk * s.chunks;
   const int n = (int)(item / each), head = (int)(item % each) / s.chunks;
-  const int r = blockIdx.y, row = (int)(item % s.chunks) * s.rows + r;
-  if (row >= a.T * a.rep) return;
-  const int64_t b0 = blockIdx.x;
+  const int r = blockIdx.y * (kJoinWarps / WAYS) + (WAYS == 1 ? warp : 0);
+  const int row = (int)(item % s.chunks) * s.rows + r;
+  if (r >= s.rows || row >= a.T * a.rep) return;  // whole warps, or the whole block
   float m = -INFINITY;
-  for (int64_t b = b0 + tid; b <= b1; b += blockDim.x) m = fmaxf(m, part_of(s, b, b == b0)[r]);
+  for (int64_t b = b0 + lane + 32 * way; b <= b1; b += 32 * WAYS) m = fmaxf(m, part_of(s, b, b == b0)[r]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) tops[warp] = m;
-  __syncthreads();
+  if constexpr (WAYS > 1) {
+    if (lane == 0) tops[way] = m;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) m = fmaxf(m, tops[i]);
+    for (int i = 0; i < WAYS; ++i) m = fmaxf(m, tops[i]);
+  }
   const float base = m == -INFINITY ? 0.f : m;
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int64_t b = b0 + warp; b <= b1; b += kJoinWarps) {
+  for (int64_t b = b0 + way; b <= b1; b += WAYS) {
     const float* p = part_of(s, b, b == b0);
     const float w = exp2f(p[r] - base);
     l = fmaf(p[s.rows + r], w, l);
@@ -53,18 +57,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
       o.w = fmaf(x.w, w, o.w);
     }
   }
-  fold[warp][lane] = o;
-  if (lane == 0) sums[warp] = l;
-  __syncthreads();
-  if (warp != 0) return;
+  if constexpr (WAYS > 1) {
+    fold[way][lane] = o;
+    if (lane == 0) sums[way] = l;
+    __syncthreads();
+    if (warp != 0) return;
 #pragma unroll
-  for (int i = 1; i < kJoinWarps; ++i) {
-    const float4 x = fold[i][lane];
-    o.x += x.x;
-    o.y += x.y;
-    o.z += x.z;
-    o.w += x.w;
-    l += sums[i];
+    for (int i = 1; i < WAYS; ++i) {
+      const float4 x = fold[i][lane];
+      o.x += x.x;
+      o.y += x.y;
+      o.z += x.z;
+      o.w += x.w;
+      l += sums[i];
+    }
   }
   const int64_t to = ((int64_t)n * a.T + row / a.rep) * a.hq + head * a.rep + row % a.rep;
   const float f = l == 0.f ? 0.f : 1.f / l;
@@ -81,11 +87,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
 }  // namespace
 
 // The join's blocks may be placed while the last of the main kernel's still run.
-template <typename T, int D>
-static cudaError_t join(const AttnArgs& a, const Split& s) {
-  const int rows = a.T * a.rep;
+template <typename T, int D, int WAYS>
+static cudaError_t launch(const AttnArgs& a, const Split& s) {
+  const int rows = a.T * a.rep < s.rows ? a.T * a.rep : s.rows, per = kJoinWarps / WAYS;
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)s.blocks, rows < s.rows ? rows : s.rows);
+  c.gridDim = dim3((unsigned)s.blocks, (rows + per - 1) / per);
   c.blockDim = dim3(32 * kJoinWarps);
   c.stream = a.stream;
   cudaLaunchAttribute attr{};
@@ -93,7 +99,11 @@ static cudaError_t join(const AttnArgs& a, const Split& s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &attr;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, attn_join_kernel<T, D>, a, s);
+  return cudaLaunchKernelEx(&c, attn_join_kernel<T, D, WAYS>, a, s);
+}
+template <typename T, int D>
+static cudaError_t join(const AttnArgs& a, const Split& s) {
+  return s.rows > 8 ? launch<T, D, 1>(a, s) : launch<T, D, kJoinWarps>(a, s);
 }
 cudaError_t launch_attn_join(const AttnArgs& a, const Split& s) {
   using bf = __nv_bfloat16;
