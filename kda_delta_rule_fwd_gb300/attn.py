@@ -288,6 +288,8 @@ def cache_read(cache, pages, lens, T, *, cu_seqlens=None, dtype=torch.bfloat16, 
                               workspace=workspace)
     if dtype not in _DT:
         raise TypeError("k and v are read as float32 or bfloat16")
+    if not 0 <= T < 2 ** 31:
+        raise ValueError("T must be a number of tokens below 2^31")
     B = 1 if cu_seqlens is not None else pages.shape[0]
     packed, N = _seqs(cu_seqlens, B, x)
     kind, ldpage = _pools(cache, x, pages, lens, N)
@@ -327,8 +329,11 @@ def _attn_shape(q, cache, pages, lens, scale, window):
         raise TypeError("the cache must be of q's type or of 8 bits")
     if scale is None:
         scale = d ** -0.5
+    window = int(window or 0)
+    if not 0 <= window < 2 ** 31:  # the C side's type would cut it off
+        raise ValueError("window must be 0 (all places) or a number of places below 2^31")
     return _attn_struct(B, T, H, G, d, page, pages.shape[1], num_pages, _DT[q.dtype], kind,
-                        float(scale), int(window or 0), _token_stride(q, "q"), ldpage)
+                        float(scale), window, _token_stride(q, "q"), ldpage)
 
 
 def attn_workspace_size(shape: AttnShape) -> int:

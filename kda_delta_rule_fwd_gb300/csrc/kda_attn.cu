@@ -521,7 +521,8 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         }
     };
     const int hi_min = len - a.T + row0 / a.rep + 1;
-    const int lo_max = a.window > 0 ? len - a.T + (row0 + rows - 1) / a.rep + 1 - a.window : INT_MIN;
+    const int lo_max =
+        a.window > 0 ? (int)max((int64_t)len - a.T + (row0 + rows - 1) / a.rep + 1 - a.window, (int64_t)INT_MIN) : INT_MIN;
 
     for (int t = t0; t < t1; ++t) {
       copy_wait<S::kStages - 2>();

@@ -167,3 +167,19 @@ def test_binding_refuses(lib):
             go(**kw)
     both = torch.zeros(5, 2, 4, 16, 64, dtype=torch.int8)
     assert go(c=m.KVCache(both[:, 0], both[:, 1], cache.k_scale, cache.v_scale)).ldpage == 2 * 4 * 16 * 64
+
+
+def test_numbers_that_the_structs_would_cut_off(lib, monkeypatch):
+    """A window or a length of 2^32 + 5 is refused, not taken as 5."""
+    m, attn, _ = lib
+    cache = m.kv_cache(5, 16, 4, 64, device="cpu")
+    q, pages, lens = torch.zeros(2, 1, 4, 64).bfloat16(), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for w, want in ((None, 0), (0, 0), (5, 5), (2**31 - 1, 2**31 - 1)):
+        assert attn._attn_shape(q, cache, pages, lens, None, w).window == want
+    for w in (-1, 2**31, 2**32 + 5):
+        with pytest.raises(ValueError, match="window"):
+            attn._attn_shape(q, cache, pages, lens, None, w)
+    monkeypatch.setattr(attn, "_elsewhere", lambda x, stream: False)
+    for T in (-1, 2**31, 2**32 + 5):
+        with pytest.raises(ValueError, match="T must"):
+            m.cache_read(cache, pages, lens, T)

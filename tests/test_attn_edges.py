@@ -232,3 +232,15 @@ def test_drawing_without_drafts(kda):
     assert torch.equal(got.cpu(), want[0]) and (commit == 1).all()
     with pytest.raises(ValueError, match="drafts"):
         kda.draft_verify(torch.cat([p, p], 1), None, None, torch.rand(9, 2, device="cuda"))
+
+
+@pytest.mark.parametrize("T,rep", [(1, 3), (8, 4)])
+def test_largest_windows(kda, T, rep):
+    """Windows up to 2^31 - 1 that reach before the first place are no windows; sequences shorter than the
+    new tokens among them."""
+    q, cache, pages, _, _, _ = attn_state(kda, 4, 2 * rep, 2, 64, 16, 600, torch.int8, 7, T=T)
+    lens = torch.tensor([600, 0, 3, 77], dtype=torch.int32, device="cuda")
+    want, lse = kda.attn_step(q, cache, pages, lens, want_lse=True)
+    for w in (600, 2**31 - 600, 2**31 - 1):
+        got, l = kda.attn_step(q, cache, pages, lens, window=w, want_lse=True)
+        assert torch.equal(got, want) and torch.equal(l, lse)
