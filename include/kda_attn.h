@@ -159,7 +159,8 @@ typedef struct {
  * float32, and the weights enter the second product with 16 bits over a bf16
  * cache and with 11 over one of 8 bits; with float32 products keep 22 bits
  * over an 8-bit cache and 24 over a float32 one.  workspace:
- * required, 256-byte aligned, kda_attn_workspace_size(s) bytes. */
+ * 256-byte aligned, kda_attn_workspace_size(s) bytes; where those are 256 they
+ * hold the status alone and may be left out (NULL, 0). */
 size_t kda_attn_workspace_size(const kda_attn_shape* s);
 kda_status kda_attn_step(const kda_attn_shape* s, const void* q, const void* k_cache,
                          const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,

@@ -362,10 +362,13 @@ def attn_step(q, cache, pages, lens, *, scale=None, window=0, out=None, lse=None
         want_lse = True
     elif want_lse:
         lse = torch.empty(q.shape[:3], dtype=_F32, device=q.device)
-    if workspace is None:  # whole 256-byte units
-        size = lib.kda_attn_workspace_size(shape)
-        workspace = lens.new_empty(size // 4)
-        ws = workspace.data_ptr()
+    if workspace is None:  # whole 256-byte units; one of them is the status alone, which nobody would read
+        ws, size = None, lib.kda_attn_workspace_size(shape)
+        if size > 256:
+            workspace = lens.new_empty(size // 4)
+            ws = workspace.data_ptr()
+        else:
+            size = 0
     else:
         ws, size = _ws(workspace, q)
     k, v, ks, vs = cache

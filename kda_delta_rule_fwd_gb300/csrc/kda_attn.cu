@@ -272,11 +272,11 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
   const int g = lane >> 2, t4 = lane & 3;
   if (tid == 0) {
     bad = 0;
-    s.cut[blockIdx.x] = -1;
+    if (!s.one) s.cut[blockIdx.x] = -1;
   }
   Start st;
   if (!find_start<S::kThreads>(a, s, scratch, st)) {
-    if (tid == 0) s.verdict[blockIdx.x] = KDA_OK;
+    if (tid == 0 && !s.one) s.verdict[blockIdx.x] = KDA_OK;
     return;
   }
   const int mask = (1 << a.t.shift) - 1;
@@ -1039,7 +1039,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
   }
   copy_wait<0>();
   __syncthreads();
-  if (tid == 0) s.verdict[blockIdx.x] = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
+  if (tid == 0 && !s.one) s.verdict[blockIdx.x] = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
 }
 
 template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER, bool SHARE>
@@ -1099,11 +1099,13 @@ Split split_for(const AttnArgs& a) {
 size_t attn_workspace(const AttnArgs& a) { return split_bytes(split_for(a)); }
 
 cudaError_t launch_attn(const AttnArgs& a) {
-  if (a.B == 0) return cudaMemsetAsync(a.ws, 0, 4, a.stream);
+  if (a.B == 0) return a.ws ? cudaMemsetAsync(a.ws, 0, 4, a.stream) : cudaSuccess;
   Split s = split_for(a);
   split_place(s, a.ws);
   cudaError_t e = by_type(a, [&](auto shape) { return launch(shape, a, s); });
-  return e != cudaSuccess ? e : launch_attn_join(a, s);
+  if (e != cudaSuccess) return e;
+  if (s.one) return a.ws ? launch_attn_table(a, s) : e;
+  return launch_attn_join(a, s);
 }
 
 }  // namespace attn

@@ -260,7 +260,9 @@ kda_status kda_attn_step(const kda_attn_shape* s, const void* q, const void* k_c
       !all_aligned({(const void*)pages, (const void*)lens, (const void*)lse}, 4) ||
       !all_aligned({k_cache, v_cache, (const void*)k_scale, (const void*)v_scale}, 16))
     return KDA_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < attn_workspace(a))
+  const size_t need = attn_workspace(a);  // the status alone may be left out
+  if ((workspace || workspace_bytes || need > kWsHeader) &&
+      (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
     return KDA_ERR_WORKSPACE;
   a.q = q; a.kc = k_cache; a.vc = v_cache; a.ks = k_scale; a.vs = v_scale;
   a.t.pages = pages; a.t.lens = lens;

@@ -84,26 +84,52 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
   if (lane == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-}  // namespace
+// Short tables: what the main kernel's blocks meet, places past the table and pages not in the pool.
+constexpr int kTableThreads = 512;
+__global__ void __launch_bounds__(kTableThreads) attn_table_kernel(AttnArgs a, Split s) {
+  const int entries = a.B * a.t.max_pages;
+  int bad = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < entries; i += kTableThreads) {
+    const int n = i / a.t.max_pages;
+    const int64_t from = (int64_t)(i - n * a.t.max_pages) << a.t.shift;
+    const Keys k = keys_of(a, s.tile, n);
+    if (from < k.hi && from + (1 << a.t.shift) > k.lo) bad |= (unsigned)a.t.pages[i] >= (unsigned)a.t.num_pages;
+    bad |= a.t.lens[n] > (int64_t)a.t.max_pages << a.t.shift;
+  }
+  bad = __syncthreads_or(bad);
+  cudaGridDependencySynchronize();
+  if (threadIdx.x == 0) *s.status = bad ? KDA_ERR_INVALID_ARG : KDA_OK;
+}
 
-// The join's blocks may be placed while the last of the main kernel's still run.
-template <typename T, int D, int WAYS>
-static cudaError_t launch(const AttnArgs& a, const Split& s) {
-  const int rows = a.T * a.rep < s.rows ? a.T * a.rep : s.rows, per = kJoinWarps / WAYS;
+// Blocks of a kernel behind the main one may be placed while the last of its still run.
+template <class F>
+cudaError_t launch_behind(F kernel, dim3 grid, int threads, const AttnArgs& a, const Split& s) {
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)s.blocks, (rows + per - 1) / per);
-  c.blockDim = dim3(32 * kJoinWarps);
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
   c.stream = a.stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &attr;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, attn_join_kernel<T, D, WAYS>, a, s);
+  return cudaLaunchKernelEx(&c, kernel, a, s);
+}
+template <typename T, int D, int WAYS>
+cudaError_t launch(const AttnArgs& a, const Split& s) {
+  const int rows = a.T * a.rep < s.rows ? a.T * a.rep : s.rows, per = kJoinWarps / WAYS;
+  return launch_behind(attn_join_kernel<T, D, WAYS>, dim3((unsigned)s.blocks, (rows + per - 1) / per), 32 * kJoinWarps, a, s);
 }
 template <typename T, int D>
-static cudaError_t join(const AttnArgs& a, const Split& s) {
+cudaError_t join(const AttnArgs& a, const Split& s) {
   return s.rows > 8 ? launch<T, D, 1>(a, s) : launch<T, D, kJoinWarps>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_table(const AttnArgs& a, const Split& s) {
+  return launch_behind(attn_table_kernel, dim3(1), kTableThreads, a, s);
 }
 cudaError_t launch_attn_join(const AttnArgs& a, const Split& s) {
   using bf = __nv_bfloat16;

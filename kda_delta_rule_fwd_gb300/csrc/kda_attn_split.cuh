@@ -10,6 +10,9 @@
 // parts, the rest of an item that begins in an earlier block (slot 0) and the beginning of one that
 // goes on in the next (slot 1).  The join kernel looks at each block that cut an item at its end,
 // and adds that item's parts in the order of the blocks.
+//
+// Short tables: a block takes one whole item, no lengths are counted and there is no join; where the
+// caller reads the status, a kernel of one block looks through the table for it.
 #pragma once
 
 #include "kda_attn.cuh"
@@ -18,6 +21,15 @@ namespace kda {
 namespace attn {
 
 constexpr int kMinPlaces = 256;  // of a block's share, where there are as many
+// A table of up to 512 places (256 where places take long, with float32 queries or more than 16 rows,
+// and items are fewer than half the SMs) is short.  Split and joined / a block per item, us on the GPU:
+// 8 items of bf16 heads of 128, 4 rows, 64 places 7.3 / 4.9, 256 9.4 / 7.2, 512 10.7 / 9.8, 1024 10.7 / 14.5;
+// float32, 256 14.4 / 11.5, 512 15.6 / 18.1, 128 items of 512 23.1 / 18.6; 32 rows over bf16, 8 items of
+// 256 16.2 / 12.0, 512 15.8 / 16.6, 128 items of 512 23.1 / 17.1; 256 sequences of 1 to 512 bf16 places and
+// 8 heads, cold, 68 / 61.  Many more items than blocks do better in equal shares: 512 sequences of 100 to 300
+// places, 8 heads, 4 tokens over bf16 138 / 150, float32 275 / 301.  A table of more entries would take the
+// kernel that looks through it too long.
+constexpr int kShortPlaces = 512, kShortEntries = 4096;
 
 struct Split {
   unsigned int* status;   // workspace header
@@ -28,6 +40,7 @@ struct Split {
   int64_t blocks, items;
   int rows, tile, cost, chunks, part_floats;
   int64_t least;  // tiles of a share
+  bool one;       // a block per item
 };
 inline int64_t pad256(int64_t b) { return (b + 255) / 256 * 256; }
 
@@ -40,20 +53,30 @@ inline Split split_of(const AttnArgs& a, int rows, int tile, int cost, int per_s
   s.chunks = (a.T * a.rep + rows - 1) / rows;
   s.items = (int64_t)a.B * a.hk * s.chunks;
   s.blocks = a.sms * per_sm;
+  const int64_t cap = (int64_t)a.t.max_pages << a.t.shift;
+  const bool quick = a.bf16 && rows <= 16;
+  s.one = cap <= (quick || s.items >= a.sms / 2 ? kShortPlaces : kShortPlaces / 2) && s.items <= 5 * s.blocks &&
+          (int64_t)a.B * a.t.max_pages <= kShortEntries;
+  if (s.one) {
+    s.blocks = s.items;
+    return s;
+  }
   // no more blocks than the table has tiles for
-  const int64_t tiles = ((((int64_t)a.t.max_pages << a.t.shift) + tile - 1) / tile + 1 + cost);
+  const int64_t tiles = (cap + tile - 1) / tile + 1 + cost;
   const int64_t most = s.items * ((tiles + s.least - 1) / s.least);
   if (most < s.blocks) s.blocks = most;
   s.part_floats = rows * (a.d + 2);
   return s;
 }
 inline size_t split_bytes(const Split& s) {
+  if (s.one) return kWsHeader;
   return kWsHeader + pad256(4 * s.blocks) + 2 * pad256(8 * s.blocks) +
          pad256(s.blocks * 2 * s.part_floats * (int64_t)sizeof(float));
 }
 inline void split_place(Split& s, void* ws) {
   char* p = static_cast<char*>(ws);
   s.status = reinterpret_cast<unsigned int*>(p);
+  if (s.one) return;
   p += kWsHeader;
   s.verdict = reinterpret_cast<unsigned int*>(p);
   p += pad256(4 * s.blocks);
@@ -94,9 +117,18 @@ struct Start {
 // All threads of the block take part (NT of them); `scratch` holds 34 values.
 template <int NT>
 __device__ __forceinline__ bool find_start(const AttnArgs& a, const Split& s, int64_t* scratch, Start& out) {
+  const int64_t each = (int64_t)a.hk * s.chunks;
+  if (s.one) {
+    out.n = blockIdx.x / (unsigned)each;
+    out.share = keys_of(a, s.tile, out.n).tiles + s.cost;
+    out.at = (blockIdx.x - out.n * each) * out.share;
+    out.end = out.at + out.share;
+    out.before = 0;
+    __syncthreads();
+    return true;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.B + NT - 1) / NT, n0 = min(tid * per, a.B), n1 = min(n0 + per, a.B);
-  const int64_t each = (int64_t)a.hk * s.chunks;
   int64_t mine = 0;
   for (int n = n0; n < n1; ++n) mine += keys_of(a, s.tile, n).tiles + s.cost;
   int64_t up = mine;
@@ -141,6 +173,7 @@ __device__ __forceinline__ float* part_of(const Split& s, int64_t block, int slo
 }
 
 cudaError_t launch_attn_join(const AttnArgs& a, const Split& s);
+cudaError_t launch_attn_table(const AttnArgs& a, const Split& s);
 
 }  // namespace attn
 }  // namespace kda

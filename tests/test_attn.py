@@ -543,3 +543,41 @@ def test_graph_replay_and_streams(kda):
         want = step()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,kind", [("f32", "f32"), ("f32", "int8"), ("bf16", "bf16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("T,rep,d,page,copies", [(1, 4, 128, 16, 1), (3, 5, 64, 64, 1), (8, 4, 128, 32, 1), (8, 9, 64, 4, 1), (2, 3, 64, 16, 8)])
+def test_attn_short_tables(kda, dtype, kind, T, rep, d, page, copies):
+    """Tables of up to 512 places take a block per item, longer ones are split: the same inputs under tables of
+    256 and 512 places and of a page more, with pages that are not in the pool behind the lengths."""
+    lens = [256, 0, 1, 255, T - 1, -3, 100, 17] * copies
+    for cap, more in ((256, []), (512, [512, 257]), (512 + page, [512, 511])):
+        q, cache, pages, ln = attn_inputs(kda, lens + more, T, 2 * rep, 2, d, page, dtype, kind, 21, max_pages=cap // page)
+        for b, n in enumerate(ln.tolist()):
+            pages[b, -(-max(n, 0) // page):] = -1 if b % 2 else 2 ** 30
+        attn_check(kda, q, cache, pages, ln)
+        attn_check(kda, q, cache, pages, ln, window=33)
+
+
+@pytest.mark.parametrize("page", [1, 16, 64])
+def test_attn_short_tables_report(kda, page):
+    """With a workspace the status, without one none is kept: places past the table and pages not in the pool
+    that a token sees, and none that it does not; a workspace with no sequences; too small ones refused."""
+    q, cache, pages, ln = attn_inputs(kda, [512, 200, 0], 2, 4, 2, 64, page, "bf16", "int8", 22)
+    q, cache, pages = dev(q), kda.KVCache(*map(dev, cache)), dev(pages)
+    ws = torch.full((64,), -1, dtype=torch.int32, device="cuda")
+    bad = pages.clone()
+    bad[1, 63 // page] = 10 ** 6
+    for lens, table_, window, status in (
+            ([512, 200, 0], pages, 0, 0), ([513, 200, 0], pages, 0, kda.KDA_ERR_INVALID_ARG), ([512, 200, 0], pages, 0, 0),
+            ([512, 200, 0], bad, 0, kda.KDA_ERR_INVALID_ARG), ([512, 0, 200], bad, 0, 0), ([512, 200, -9], bad, 8, 0),
+            ([512, 64, 1], bad, 8, kda.KDA_ERR_INVALID_ARG)):
+        lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        got = kda.attn_step(q, cache, table_, lens, window=window, workspace=ws)
+        assert kda.read_device_status(ws) == status, (lens, window)
+        assert torch.equal(kda.attn_step(q, cache, table_, lens, window=window), got)
+    ws.fill_(-1)
+    assert kda.attn_step(q[:0], cache, pages[:0], lens[:0], workspace=ws).shape == q[:0].shape
+    assert kda.read_device_status(ws) == 0
+    with pytest.raises(RuntimeError):
+        kda.attn_step(q, cache, pages, lens, workspace=ws[:32])

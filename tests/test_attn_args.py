@@ -183,3 +183,21 @@ def test_numbers_that_the_structs_would_cut_off(lib, monkeypatch):
     for T in (-1, 2**31, 2**32 + 5):
         with pytest.raises(ValueError, match="T must"):
             m.cache_read(cache, pages, lens, T)
+
+
+def test_attn_status_left_out(lib):
+    """A short table's workspace holds the status alone: it may be left out, but not be of the wrong size."""
+    m, attn, L = lib
+
+    def shape(max_pages, B=0):
+        return attn.AttnShape(B=B, T=1, q_heads=4, kv_heads=2, d=128, page=64, max_pages=max_pages, num_pages=8,
+                              dtype=m.KDA_BF16, cache=2, scale=0.1, window=0, ldq=0, ldpage=0)
+    for pages, B in ((4, 2), (8, 2), (9, 0)):
+        assert L.kda_attn_workspace_size(shape(pages, B)) == 256
+    assert L.kda_attn_workspace_size(shape(9, 2)) > 256
+    go = lambda s, ws, size: L.kda_attn_step(s, *[FAKE] * 9, ws, size, None)
+    assert go(shape(9, 2), None, 0) == go(shape(4), FAKE, 0) == go(shape(4), FAKE, 255) == go(shape(4), None, 256) \
+        == go(shape(4), FAKE + 8, 256) == m.KDA_ERR_WORKSPACE
+    assert call(L.kda_attn_step, shape(4, 2), 9, p4=None) == m.KDA_ERR_INVALID_ARG
+    # checked, and nothing to launch
+    assert L.kda_attn_step(shape(4), *[FAKE] * 3, None, None, *[FAKE] * 4, None, 0, None) == m.KDA_OK
