@@ -153,8 +153,10 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool have) {
 // and request the next row before they work on the present one; a block serves q or k, in
 // proportion to their heads, so that its weights and its sums for their gradient stay in registers.
 constexpr int kWide = 256;  // threads of a block
-// Blocks to an SM and rows in flight.  16384 tokens of 40 heads of 128 in bf16 take 66 us forwards (with
-// four rows 70, with four blocks 99: too few registers), their gradient 97 (two or three rows 99).
+// Blocks to an SM and rows in flight.  16384 tokens of 40 heads of 128 in bf16 took 66 us forwards (with
+// four rows 70, with four blocks 99: too few registers), their gradient 97 (two or three rows 99), before
+// the items were made equal; they take 64 and 91, bound by memory: a copy of as many bytes takes 60 and
+// 85, and without the rotation, the angles or most of the sum the forward kernel takes 65.
 template <bool kBwd> constexpr int wide_blocks() { return kBwd ? 2 : 3; }
 template <bool kBwd> constexpr int wide_ahead() { return kBwd ? 4 : 3; }
 
