@@ -158,7 +158,11 @@ typedef struct {
  * Sums and statistics are float32.  With bf16 the scores are exact products in
  * float32, and the weights enter the second product with 16 bits over a bf16
  * cache and with 11 over one of 8 bits; with float32 products keep 22 bits
- * over an 8-bit cache and 24 over a float32 one.  workspace:
+ * over an 8-bit cache and 24 over a float32 one.  Over 8 bits what counts for a
+ * query row is its weight times the value row's power of two: 11 (22) bits for
+ * products down to 2^-23 of its largest, 2^-34 of that for those below.  Where all
+ * that it sees has powers below 2^-87 (values below 2^-78), bits are lost.
+ * workspace:
  * 256-byte aligned, kda_attn_workspace_size(s) bytes; where those are 256 they
  * hold the status alone and may be left out (NULL, 0). */
 size_t kda_attn_workspace_size(const kda_attn_shape* s);

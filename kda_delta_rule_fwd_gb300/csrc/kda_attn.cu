@@ -20,9 +20,15 @@
 // Types.  bf16 caches: products of bf16, exact in float32; a weight enters as two bf16 parts
 // (16 bits), since one alone would cost as much as the output's own rounding.  Codes become f16,
 // exactly; queries become f16 after a power of two per row has brought their largest to 2^13,
-// which keeps every bit down to 2^-27 of it.  A value's power of two joins its weight, relative
-// to the largest power seen by the warp, times 2^7: f16 then holds weights down to 2^-21 with all
-// 11 bits, and what is below to 2^-31; the sum of weights stays float32.
+// which keeps every bit down to 2^-27 of it.  A value's power of two joins its weight, and a query
+// row's base follows the largest product of the two that it meets, which f16 gets as 2^9 to 2^15:
+// products down to 2^-23 of the largest keep all 11 bits, what is below is off by 2^-34 of it at most.
+// A row of large power takes nothing from the others where its weight is small or it is not seen.
+// (With 2^11 to 2^15 the bases move more often: 32 and 64 rows over int8 330 and 582 us, now 316 and
+// 528, with 2^7 to 2^15 312 and 517.)  The sum of weights is float32 and counts from the same base: its
+// terms fall with the largest power (2^-112 for 2^121, the largest there is).  A base stays within 2^103
+// of the largest weight, so that sums of weights of rows of zeros (power 2^-126) stay finite: where all
+// that a row sees has powers below 2^-87, they keep fewer bits.
 //
 // float32 queries over codes are two f16 parts (22 bits), as are their weights; over a float32 cache
 // keys, values, queries and weights are three bf16 parts each (all 24 bits), whose six largest products
@@ -50,7 +56,9 @@ constexpr int kGroups = 4;    // key groups of a block
 // and with 512.  16 sequences of up to 32768 int8 places, 32 rows: 153, 150, 148 and 152 us with 192,
 // 256, 384 and 640.
 constexpr int item_cost(int eights) { return eights == 4 ? 384 : 256; }
-constexpr int kLazy = 8, kShift = 7;  // 2^15 is the largest weight in f16
+// The base of a row's weights follows where a weight, times the power of its value's codes, passes it by this much
+template <bool kCoded> constexpr float lazy() { return kCoded ? 6.f : 8.f; }
+constexpr float kFill = 9.f, kDeep = 96.f;  // codes: the largest product in f16 as the base is set; the smallest power that counts
 constexpr float kNone = -3e38f;           // the base of a row that has seen nothing: every score passes it
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -122,6 +130,8 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&part)[N]) {
     }
   }
 }
+// a value's byte as the exponent that a base allows for: its power, less what f16 holds of the product
+__device__ __forceinline__ float ask(int byte) { return fmaxf((float)(byte - 127) - kFill, -kDeep); }
 // two codes as f16
 __device__ __forceinline__ uint32_t open2(uint16_t two) {
   uint32_t f;
@@ -212,8 +222,8 @@ struct Shape {
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kSlice = NT == 1 ? 16 : 32, kPitch = kSlice + 2;  // channels of an item's end that meet at once
   static constexpr int kMerge = kGroups * kRows * kPitch * 4;
-  // shared weights: fragments of all groups' weights; maxima and largest powers
-  static constexpr int kWBytes = kGroups * kWParts * NT * 32 * 8, kTops = kGroups * kRows * 4 + 16;
+  // shared weights: fragments of all groups' weights; bases that the groups ask for
+  static constexpr int kWBytes = kGroups * kWParts * NT * 32 * 8, kTops = kGroups * kRows * 4;
   static constexpr int kTail = SHARE ? kWBytes + kTops : 2 * kMerge;
   static constexpr int kQBytes = kRows * D * 2 * kQParts;
   static constexpr int bytes(int stages) {
@@ -303,7 +313,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
   int* const row_end = reinterpret_cast<int*>(raw + S::oRow) + S::kRows;
   int* const row_place = row_end + S::kRows;  // the row among a sequence's rows of the output
   uint2* const shared_w = reinterpret_cast<uint2*>(raw + S::oMerge);  // [parts][groups][rows / 8][lanes]
-  float* const shared_top = reinterpret_cast<float*>(raw + S::oMerge + S::kWBytes);  // [groups][rows], then powers
+  float* const shared_top = reinterpret_cast<float*>(raw + S::oMerge + S::kWBytes);  // [groups][rows]
   uint2* const qs = reinterpret_cast<uint2*>(raw + S::oQ) + wm * NT * KS * 32;  // [parts][rows / 8][steps][lanes]
 
   // The table's entries of the next request are read one request early.
@@ -475,7 +485,6 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
     float base[NT][2], l[NT][2], rf[NT][2];  // the weights' bases and sums, the scores' factors
     float o[OB][NT][4];
     uint2 qh[kHoldQ ? QP * NT * KS : 1];
-    int top = 0;  // the largest byte of a value seen
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -602,20 +611,19 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) c[u][j][e] += rest[u][j][e];
       }
-      // powers of two of places g and g + 8, each worked out by one lane; a value's (below) relative to
-      // the largest so far.  The readers of a row that is not finite become NaN through their sums.
+      // powers of two of places g and g + 8, each worked out by one lane.  The readers of a value's row that
+      // is not finite become NaN through their sums.
       float kf[KM][2], vf[KM][2];
-      bool moved = false;
       unsigned nan_rows = 0;
-      int vb = 0, most = top;
+      int vb = 0;
+      float most = 0.f;  // the largest power, as an exponent that a base is asked to allow for
       if constexpr (kCoded) {
         const int kb = bytes[lane];
         vb = KT == 16 ? kb : bytes[KT + lane];
         const bool mine = KT == 16 ? lane >= 16 && (seen >> (lane & 15) & 1) : seen >> lane & 1;
         nan_rows = __ballot_sync(0xffffffffu, mine && vb == 255);
         if (KT == 16) nan_rows >>= 16;
-        most = max(top, (int)__reduce_max_sync(0xffffffffu, mine && vb != 255 ? vb : 0));
-        moved = most != top;
+        most = ask((int)__reduce_max_sync(0xffffffffu, mine && vb != 255 ? vb : 0));
         const float kfac = power(kb);
 #pragma unroll
         for (int u = 0; u < KM; ++u)
@@ -699,9 +707,10 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) l[j][e] = NAN;
       }
-      // The base of a row's weights follows its maximum only where a score passes it by more than
-      // 2^kLazy: the outputs are then rarely scaled again, the rows' maxima rarely looked for across
-      // the warp, and a weight is 2^kLazy at most.
+      // The base of a row's weights follows its maximum (over codes the largest of weights times powers) only
+      // where a score passes it by more than 2^lazy: the outputs are then rarely scaled again, the rows' maxima
+      // rarely looked for across the warp, and a weight is 2^lazy at most.  Whether one does is told by the
+      // largest power of all fetched places; by how much, below, from the places that the row sees.
       float high = -INFINITY;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -711,9 +720,14 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
           for (int u = 0; u < KM; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) high = fmaxf(high, fmaf(c[u][j][2 * h + e], rf[j][e], -base[j][e]));
-      const bool past = moved || high > (float)kLazy;
+      const bool past = high > lazy<kCoded>() - most;
       if (SHARE ? __syncthreads_or(past) : __any_sync(0xffffffffu, past)) {
-        float mx[NT][2];
+        float want[NT][2], add[KM][2];
+#pragma unroll
+        for (int u = 0; u < KM; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            add[u][h] = kCoded ? __shfl_sync(0xffffffffu, ask(vb == 255 ? 0 : vb), (KT == 16 ? 16 : u * 16) + h * 8 + g) : 0.f;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -722,38 +736,31 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll
             for (int u = 0; u < KM; ++u)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) x = fmaxf(x, c[u][j][2 * h + e]);
+              for (int h = 0; h < 2; ++h) x = fmaxf(x, fmaf(c[u][j][2 * h + e], rf[j][e], add[u][h]));
 #pragma unroll
             for (int i = 4; i < 32; i <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
-            mx[j][e] = x;
+            want[j][e] = x;
             if (SHARE && g == 0) shared_top[grp * S::kRows + j * 8 + 2 * t4 + e] = x;
           }
         if constexpr (SHARE) {  // the largest of the tile
-          int* const powers = reinterpret_cast<int*>(shared_top + kGroups * S::kRows);
-          if (lane == 0) powers[grp] = most;
           __syncthreads();
 #pragma unroll
-          for (int i = 0; i < kGroups; ++i) {
-            most = max(most, powers[i]);
+          for (int i = 0; i < kGroups; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) mx[j][e] = fmaxf(mx[j][e], shared_top[i * S::kRows + j * 8 + 2 * t4 + e]);
-          }
+              for (int e = 0; e < 2; ++e) want[j][e] = fmaxf(want[j][e], shared_top[i * S::kRows + j * 8 + 2 * t4 + e]);
         }
-        const float rise = __uint_as_float((uint32_t)max(127 + top - most, 0) << 23);
-        top = most;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float x = mx[j][e] * rf[j][e];
-            float al = kCoded ? rise : 1.f;
-            if (x - base[j][e] > (float)kLazy) {
-              const float f = exp2_of(base[j][e] - x);
+            float al = 1.f;
+            if (want[j][e] - base[j][e] > lazy<kCoded>()) {
+              const float x = kCoded ? floorf(want[j][e]) : want[j][e];  // whole: an item's end moves it exactly
+              al = exp2_of(base[j][e] - x);
               base[j][e] = x;
-              l[j][e] *= f;
-              al *= f;
+              l[j][e] *= al;
             }
 #pragma unroll
             for (int i = 0; i < OB; ++i) {
@@ -763,7 +770,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
           }
       }
       if constexpr (kCoded) {  // a value's power, 0 for a row that is not finite
-        const float vfac = vb == 255 ? 0.f : __uint_as_float((uint32_t)max(min(vb - top, 0) + 127 + kShift, 0) << 23);
+        const float vfac = vb == 255 ? 0.f : power(vb);
 #pragma unroll
         for (int u = 0; u < KM; ++u)
 #pragma unroll
@@ -899,7 +906,8 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
     }
 
     // ---- the item's end: the groups' outputs of the same rows, weighted by 2^(m - the largest m),
-    // add up through shared memory, kSlice channels at a time in two buffers by turns
+    // add up through shared memory, kSlice channels at a time in two buffers by turns.  Over codes a base counts
+    // from the largest product of weight and power: the sum's own power goes into the maximum first.
     const bool whole = t0 == 0 && t1 == now.tiles;
     float2* const stats = reinterpret_cast<float2*>(raw + S::oStats);  // [groups][rows]: maximum, sum
     float scale_by[NT][2];
@@ -909,11 +917,16 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], i);
-        const float m = base[j][e] == kNone ? -INFINITY : base[j][e];
-        if (g == 0) stats[grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e] = make_float2(m, l[j][e]);
+        if (base[j][e] == kNone) base[j][e] = -INFINITY;
+        float m = base[j][e], sum = l[j][e];
+        if (kCoded && sum > 0.f) {
+          const int k = min((int)(__float_as_uint(sum) >> 23) - 127, 126);  // 126: an infinity
+          sum *= __uint_as_float((uint32_t)(127 - k) << 23);
+          m += (float)k;
+        }
+        if (g == 0) stats[grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e] = make_float2(m, sum);
       }
     __syncthreads();
-    const float up = kCoded ? power(top) * __uint_as_float((127u - kShift) << 23) : 1.f;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -922,7 +935,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         float m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) m = fmaxf(m, stats[i * S::kRows + r].x);
-        scale_by[j][e] = exp2_of(stats[grp * S::kRows + r].x - (m == -INFINITY ? 0.f : m));
+        scale_by[j][e] = exp2_of(base[j][e] - (m == -INFINITY ? 0.f : m));
       }
     float* const part = part_of(s, blockIdx.x, t0 == 0 ? 1 : 0);
     // the sum of a row, and its maximum
@@ -954,10 +967,10 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         for (int e = 0; e < 2; ++e) {
           const int r = j * 8 + 2 * t4 + e;
           if (r >= rows) continue;
-          float m, f = up;
+          float m, f = kCoded ? scale_by[j][e] : 1.f;  // the base is the same in all groups
           if (whole) {
             const float sum = row_sum(r, m);
-            f = sum == 0.f ? 0.f : up / sum;
+            f = sum == 0.f ? 0.f : f / sum;
           }
           TQ* const to = static_cast<TQ*>(a.out) + (out0 + row_place[r]) * D;
 #pragma unroll
@@ -997,8 +1010,8 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             float* const to = buf + (grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e) * S::kPitch;
 #pragma unroll
             for (int i = 0; i < kSlice / 16; ++i) {
-              const float x = o[q * (kSlice / 16) + i][j][e] * up * scale_by[j][e];
-              const float z = o[q * (kSlice / 16) + i][j][2 + e] * up * scale_by[j][e];
+              const float x = o[q * (kSlice / 16) + i][j][e] * scale_by[j][e];
+              const float z = o[q * (kSlice / 16) + i][j][2 + e] * scale_by[j][e];
               if constexpr (kNext) {
                 *reinterpret_cast<float2*>(to + i * 16 + 2 * g) = make_float2(x, z);
               } else {
