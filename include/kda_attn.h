@@ -151,9 +151,9 @@ typedef struct {
 } kda_attn_shape;
 
 /* q [B,T,q_heads,d], out the same, dense; lse f32 [B,T,q_heads] or NULL.
- * Places whose page is not in the pool count as unseen and are reported
- * (KDA_ERR_INVALID_ARG), as is a lens past the table (the places that it has
- * are seen).  The keys are split over the device by equal numbers of tiles and
+ * Places that a token would see on a page that is not in the pool count as unseen
+ * and are reported (KDA_ERR_INVALID_ARG), as is a lens past the table (the places
+ * that it has are seen); the table's other entries may hold anything.  The keys are split over the device by equal numbers of tiles and
  * the parts joined in a fixed order: results repeat bit for bit on one device.
  * Sums and statistics are float32.  With bf16 the scores are exact products in
  * float32, and the weights enter the second product with 16 bits over a bf16

@@ -184,10 +184,12 @@ struct Cursor {
   int64_t left;     // of the share from here on
   int n, head, chunk;
   int t, tiles;     // tile of the item, the item's number
-  int lo, hi;       // the sequence's places
+  int lo, hi;       // the sequence's places, from a tile's beginning on
+  int first;        // the first of them that a token sees
   __device__ __forceinline__ void enter(const AttnArgs& a, const Split& s) {
     const Keys k = keys_of(a, s.tile, n);
     lo = (int)k.lo;
+    first = (int)k.first;
     hi = (int)k.hi;
     tiles = (int)k.tiles;
   }
@@ -332,18 +334,21 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
     if (ahead.left > 0) {
       const unsigned pos = (unsigned)ahead.lo + (unsigned)ahead.t * S::kTile + grp * KT;
       const uint32_t dst = smem_at(kv + stage * S::kStage);
-      unsigned seen = 0;
+      unsigned seen = 0;  // the places that a token sees, on pages of the pool
       if (a.t.shift >= 4) {  // a page holds 16 places in a row
         const char *k[KM], *v[KM];
         int have[KM];
+        bool full = true;
 #pragma unroll
         for (int u = 0; u < KM; ++u) {
           const unsigned p = pos + u * 16;
-          const bool some = p < (unsigned)ahead.hi;
+          const bool some = p < (unsigned)ahead.hi && p + 16 > (unsigned)ahead.first;
           const bool ok = some && (unsigned)ids[u] < (unsigned)a.t.num_pages;
           have[u] = ok ? (int)min(16u, (unsigned)ahead.hi - p) : 0;
           if (some && !ok) bad = 1;
-          seen |= ((1u << have[u]) - 1) << (u * 16);
+          full &= have[u] == 16;
+          const int before = min(max(ahead.first - (int)p, 0), 15);  // no token sees these
+          seen |= (((1u << have[u]) - 1) >> before << before) << (u * 16);
           const int64_t row = ((int64_t)ahead.head << a.t.shift) + (p & mask);
           const int64_t from = ok ? (ids[u] * a.ldpage + row * D) * S::kElem : 0;
           k[u] = static_cast<const char*>(a.kc) + from;
@@ -354,7 +359,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
           }
         }
         constexpr int kTurns = KT * CH / 32 / WM, kRowsOf = 32 / CH;
-        if (seen == kAll) {
+        if (full) {
 #pragma unroll
           for (int i = 0; i < kTurns; ++i) {
             const int x = (i * WM + wm) * 32 + lane, u = i * WM * kRowsOf / 16;
@@ -376,13 +381,13 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll 1
         for (int i = 0; i < KT * CH / 32 / WM; ++i) {
           const int x = (i * WM + wm) * 32 + lane, r = x / CH, c = x % CH;
-          const int id = pos + r < (unsigned)ahead.hi ? page_of(a.t, ahead.n, pos + r) : -1;
+          const int id = pos + r < (unsigned)ahead.hi && pos + r >= (unsigned)ahead.first ? page_of(a.t, ahead.n, pos + r) : -1;
           const int64_t row = ((int64_t)ahead.head << a.t.shift) + ((pos + r) & mask);
           const int64_t from = id >= 0 ? (id * a.ldpage + row * D) * S::kElem + c * 16 : 0;
           copy16(dst + key_piece<CH, kF32>(r, c) * 16, static_cast<const char*>(a.kc) + from, id >= 0);
           copy16(dst + S::kHalf + piece<CH>(r, c) * 16, static_cast<const char*>(a.vc) + from, id >= 0);
         }
-        const bool some = lane < KT && pos + lane < (unsigned)ahead.hi;
+        const bool some = lane < KT && pos + lane < (unsigned)ahead.hi && pos + lane >= (unsigned)ahead.first;
         const int id = some ? page_of(a.t, ahead.n, pos + lane) : -1;
         if (some && id < 0) bad = 1;
         seen = __ballot_sync(0xffffffffu, id >= 0);

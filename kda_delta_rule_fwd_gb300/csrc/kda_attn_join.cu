@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kTableThreads) attn_table_kernel(AttnArgs a, S
     const int n = i / a.t.max_pages;
     const int64_t from = (int64_t)(i - n * a.t.max_pages) << a.t.shift;
     const Keys k = keys_of(a, s.tile, n);
-    if (from < k.hi && from + (1 << a.t.shift) > k.lo) bad |= (unsigned)a.t.pages[i] >= (unsigned)a.t.num_pages;
+    if (from < k.hi && from + (1 << a.t.shift) > k.first) bad |= (unsigned)a.t.pages[i] >= (unsigned)a.t.num_pages;
     bad |= a.t.lens[n] > (int64_t)a.t.max_pages << a.t.shift;
   }
   bad = __syncthreads_or(bad);

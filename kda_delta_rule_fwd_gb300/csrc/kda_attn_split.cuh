@@ -87,21 +87,21 @@ inline void split_place(Split& s, void* ws) {
   s.part = reinterpret_cast<float*>(p);
 }
 
-// The places of sequence n that any of its tokens sees: [lo, hi), lo rounded down to a tile.
+// The places of sequence n that any of its tokens sees: [first, hi); lo is first rounded down to a tile.
 struct Keys {
-  int64_t lo, hi;
+  int64_t first, lo, hi;
   int64_t tiles;  // at least 1, so that an empty item has a block that writes its zeros
 };
 __device__ __forceinline__ Keys keys_of(const AttnArgs& a, int tile, int n) {
   const int64_t cap = (int64_t)a.t.max_pages << a.t.shift, len = a.t.lens[n];
   Keys k;
   k.hi = len < 0 ? 0 : len < cap ? len : cap;
-  k.lo = 0;
+  k.first = 0;
   if (a.window > 0) {
-    k.lo = len - a.T + 1 - a.window;
-    k.lo = k.lo < 0 ? 0 : k.lo > k.hi ? k.hi : k.lo;
-    k.lo -= k.lo % tile;
+    k.first = len - a.T + 1 - a.window;
+    k.first = k.first < 0 ? 0 : k.first > k.hi ? k.hi : k.first;
   }
+  k.lo = k.first - k.first % tile;
   k.tiles = (k.hi - k.lo + tile - 1) / tile;
   if (k.tiles < 1) k.tiles = 1;
   return k;
