@@ -135,7 +135,10 @@ kda_status kda_cache_read(const kda_cache_shape* s, const int32_t* cu_seqlens,
  *
  * Query head h reads key-value head h / (q_heads / kv_heads).  A token that
  * sees nothing (its place is below 0) gets zeros and lse = -inf.  A row of the
- * cache that a token does not see does not touch it, whatever it holds.
+ * cache that a token does not see does not touch it, whatever it holds.  A value
+ * that it sees and that is infinite gives its channel that infinity (of both
+ * signs: NaN), whatever its weight, and a NaN NaN; a query or a seen key that is
+ * not finite may make the rows of that query, or all that see the key, NaN.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int32_t B, T;         /* sequences >= 0; tokens 1 .. 8 */

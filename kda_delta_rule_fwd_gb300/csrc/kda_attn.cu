@@ -41,7 +41,9 @@
 //
 // Places that a row does not see: the tiles at the ends of the seen range give them the weight 0,
 // and values that are not finite become zeros there once the rows that do see them have got them
-// (0 times infinity would reach the others).
+// (0 times infinity would reach the others).  Such a value, seen, leaves its channel's sum infinite or NaN,
+// whatever the weight's parts; at the item's end those sums are replaced by the sum of the channel's values
+// that are not finite (a weight is above 0, though its parts may be 0).
 #include <type_traits>
 
 #include "kda_attn_split.cuh"
@@ -177,6 +179,21 @@ __device__ __forceinline__ uint32_t transposed(uint32_t w) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
   return r;
+}
+
+// A channel of a row whose sum came out infinite or NaN: the sum of the values [from, to) of sequence n that
+// are not finite, 0 where all are.
+template <typename TC, int D>
+__device__ __noinline__ float sum_of_wild(const AttnArgs& a, int n, int head, int ch, int from, int to) {
+  float sum = 0.f;
+  for (int p = from; p < to && sum == sum; ++p) {
+    const int id = page_of(a.t, n, p);
+    if (id < 0) continue;
+    const int64_t row = ((int64_t)head << a.t.shift) + (p & ((1 << a.t.shift) - 1));
+    const float x = to_f32(static_cast<const TC*>(a.vc)[id * a.ldpage + row * D + ch]);
+    if (!isfinite(x)) sum += x;
+  }
+  return sum;
 }
 
 // Places of tiles in the block's share, item by item.
@@ -432,7 +449,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         s.last[blockIdx.x] = (st.end - now.left + now.tiles - 1) / st.share;
       }
     }
-    __syncthreads();
+    if (kCoded) __syncthreads();  // other caches: behind the item before
     constexpr int kTurns = S::kRows / (S::kThreads / 32);  // rows of a warp, all loaded before the first is used
     using Pair = std::conditional_t<FQ, float2, __nv_bfloat162>;
     Pair held[kTurns][D / 64];
@@ -965,6 +982,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         a.lse[out0 + row_place[tid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
       }
     }
+    float odd = 0.f;  // plus 0 times what is stored: NaN where one is not finite
     if constexpr (SHARE) {  // each warp has the sums of its channels
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -981,6 +999,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll
           for (int i = 0; i < OB; ++i) {
             const float x = o[i][j][e] * f, z = o[i][j][2 + e] * f;
+            if (!kCoded) odd = fmaf(x, 0.f, fmaf(z, 0.f, odd));
             const int ch = (grp * OB + i) * 16 + (kNext ? 2 * g : g), next = kNext ? 1 : 8;
             if (!whole) {
               part[2 * S::kRows + r * D + ch] = x;
@@ -1037,6 +1056,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             v.x += w.x;
             v.y += w.y;
           }
+          if (!kCoded) odd = fmaf(v.x, 0.f, fmaf(v.y, 0.f, odd));
           if (whole) {
             TQ* to = static_cast<TQ*>(a.out) + (out0 + row_place[r]) * D + q * kSlice + ch;
             if (words && FQ) {
@@ -1051,6 +1071,27 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             *reinterpret_cast<float2*>(part + 2 * S::kRows + r * D + q * kSlice + ch) = v;
           }
         }
+      }
+    }
+    if constexpr (!kCoded) {
+      if (__syncthreads_or(odd != odd)) {
+        using TC = std::conditional_t<kF32, float, __nv_bfloat16>;
+        const int from = now.lo + t0 * S::kTile, to = (int)min((int64_t)now.lo + (int64_t)t1 * S::kTile, (int64_t)now.hi);
+#pragma unroll 1
+        for (int i = tid; i < rows * D; i += S::kThreads) {
+          const int r = i / D, end = row_end[r];
+          TQ* const at = static_cast<TQ*>(a.out) + (out0 + row_place[r]) * D + i % D;
+          const float x = whole ? to_f32(*at) : part[2 * S::kRows + i];
+          float m;
+          const float sum = row_sum(r, m);
+          if (isfinite(x) || sum != sum) continue;  // scores that are NaN
+          const int seen = a.window > 0 ? (int)max((int64_t)end - a.window, (int64_t)from) : from;
+          const float wild = sum_of_wild<TC, D>(a, n, head, i % D, seen, min(to, end));
+          if (wild == 0.f) continue;
+          if (whole) *at = from_f32<TQ>(wild);
+          else part[2 * S::kRows + i] = wild;
+        }
+        __syncthreads();
       }
     }
     now.pass(a, s, t1 - t0);

@@ -7,6 +7,9 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
+// A part's sum, weighted; one that is not finite stays so, as its own weights made it, though w may be 0.
+__device__ __forceinline__ float plus(float o, float x, float w) { return isfinite(x) ? fmaf(x, w, o) : o + x; }
+
 // For each cut item and row: the parts' outputs weighted by 2^(m - the largest m), over the sum of
 // their sums.  A lane has four channels.  Few rows (long items in many parts): a block per row, whose
 // four warps take every fourth part; many rows: a warp per row (32 rows of 304 cuts, mostly of two
@@ -51,10 +54,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
     l = fmaf(p[s.rows + r], w, l);
     if (lane * 4 < D) {
       const float4 x = *reinterpret_cast<const float4*>(p + 2 * s.rows + r * D + lane * 4);
-      o.x = fmaf(x.x, w, o.x);
-      o.y = fmaf(x.y, w, o.y);
-      o.z = fmaf(x.z, w, o.z);
-      o.w = fmaf(x.w, w, o.w);
+      o.x = plus(o.x, x.x, w);
+      o.y = plus(o.y, x.y, w);
+      o.z = plus(o.z, x.z, w);
+      o.w = plus(o.w, x.w, w);
     }
   }
   if constexpr (WAYS > 1) {
