@@ -32,8 +32,9 @@ extern "C" {
  *
  * for the rot / 2 pairs of the first rot channels: (i, i + rot / 2), or with
  * `interleaved` (2i, 2i + 1).  The other channels keep n.  Angles are reduced
- * exactly: positions of any size lose nothing.  Evaluated in float32, each
- * output rounded once.
+ * to within 2^-31 of a turn for all frequencies and positions (a frequency over
+ * 2 pi counts in multiples of 2^-64).  Evaluated in float32, each output rounded
+ * once.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int64_t tokens;       /* >= 0 */

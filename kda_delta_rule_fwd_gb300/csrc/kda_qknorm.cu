@@ -6,7 +6,8 @@
 //
 // Angles.  f / 2 pi per position is a fraction of a turn in 64-bit fixed point, and position
 // times it modulo 2^64 is the place on the circle: whole turns fall off the top, exactly, for
-// positions of either sign.  The top 32 bits then go to sincospi.
+// positions of either sign, and half a unit of the fraction times 2^31 is 2^-34 of a turn.  The top 32
+// bits then go to sincospi.
 #include "kda_attn.cuh"
 
 namespace kda {
@@ -22,14 +23,24 @@ using layer::store;
 
 using u64 = unsigned long long;
 
-// freq / 2 pi in 64-bit fixed point, modulo 1: the mantissa times 2^66 / 2 pi in 128 bits, moved by
-// the exponent (whole numbers: 64 float64 operations of every thread would take 10 us).
+// freq / 2 pi in 64-bit fixed point, modulo 1, to the nearest: the mantissa times 2^130 / 2 pi (128 bits) in 192
+// bits, moved by the exponent (whole numbers: 64 float64 operations of every thread would take 10 us).
+// With only the upper 64 bits of 2^130 / 2 pi a frequency of 2^20 was 2^-48 of a turn off.
 __device__ __forceinline__ u64 turn_of(double freq) {
   const u64 bits = (u64)__double_as_longlong(freq), m = (bits & 0xfffffffffffffull) | 1ull << 52;
-  const int s = 54 + 1023 - (int)(bits >> 52 & 0x7ff);
-  constexpr u64 c = 0xa2f9836e4e441529ull;
-  const u64 hi = __umul64hi(m, c), lo = m * c;
-  const u64 t = s <= 0 ? lo : s < 64 ? hi << (64 - s) | lo >> s : s < 128 ? hi >> (s - 64) : 0;
+  constexpr u64 hi = 0xa2f9836e4e441529ull, lo = 0xfc2757d1f534ddc1ull;
+  const u64 p1 = __umul64hi(m, lo) + m * hi;                     // the product's second word
+  const u64 p2 = __umul64hi(m, hi) + (p1 < m * hi ? 1 : 0);      // and its third
+  const int r = max(1077 - (int)(bits >> 52 & 0x7ff), 34);       // whole turns lie above bit 64 + r; 34: 2^20
+  u64 t = 0, half = 0;
+  if (r < 64) {
+    t = p2 << (64 - r) | p1 >> r;
+    half = p1 >> (r - 1) & 1;
+  } else if (r < 128) {
+    t = p2 >> (r - 64);
+    half = (r == 64 ? p1 >> 63 : p2 >> (r - 65)) & 1;
+  }
+  t += half;
   return bits >> 63 ? 0 - t : t;
 }
 __device__ __forceinline__ float2 angle(u64 turn, int pos) {  // (cos, sin)
