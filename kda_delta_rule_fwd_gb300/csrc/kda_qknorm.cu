@@ -339,7 +339,13 @@ __global__ void __launch_bounds__(kWide, wide_blocks<kBwd>()) qknorm_wide_kernel
         float s = pn.x + pn.y;
 #pragma unroll
         for (int o = TPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float back = -s * a.inv_d * k * k;
+        float back = -s * a.inv_d * k;
+        if (k > 0x1p60f) {  // rows near float32's smallest, with eps as small: k^2 would not do
+          mul_v(v[0], k);
+          mul_v(v[1], k);
+        } else {
+          back *= k;
+        }
         fma_v(v[0], back, g[0]);
         fma_v(v[1], back, g[1]);
       }
