@@ -201,15 +201,15 @@ struct Cursor {
   int64_t left;     // of the share from here on
   int n, head, chunk;
   int t, tiles;     // tile of the item, the item's number
-  int lo, hi;       // the sequence's places, from a tile's beginning on
-  int first;        // the first of them that a token sees
+  int first, hi;    // the sequence's places that a token sees
   __device__ __forceinline__ void enter(const AttnArgs& a, const Split& s) {
     const Keys k = keys_of(a, s.tile, n);
-    lo = (int)k.lo;
     first = (int)k.first;
     hi = (int)k.hi;
     tiles = (int)k.tiles;
   }
+  // where its tiles begin
+  template <int TILE> __device__ __forceinline__ int lo() const { return first & ~(TILE - 1); }
   // past `by` tiles of the item
   __device__ __forceinline__ void pass(const AttnArgs& a, const Split& s, int by) {
     left -= by;
@@ -341,7 +341,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
     if (a.t.shift < 4 || ahead.left <= 0) return;
 #pragma unroll
     for (int u = 0; u < KM; ++u) {
-      const unsigned pos = (unsigned)ahead.lo + (unsigned)ahead.t * S::kTile + grp * KT + u * 16;
+      const unsigned pos = (unsigned)ahead.template lo<S::kTile>() + (unsigned)ahead.t * S::kTile + grp * KT + u * 16;
       const int64_t col = pos >> a.t.shift;
       ids[u] = pos < (unsigned)ahead.hi && col < a.t.max_pages ? a.t.pages[(int64_t)ahead.n * a.t.max_pages + col] : -1;
     }
@@ -349,23 +349,20 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
   // The group's places of the tile at `ahead` into a stage (its WM warps take a share each).
   auto request = [&](int stage) {
     if (ahead.left > 0) {
-      const unsigned pos = (unsigned)ahead.lo + (unsigned)ahead.t * S::kTile + grp * KT;
+      const unsigned pos = (unsigned)ahead.template lo<S::kTile>() + (unsigned)ahead.t * S::kTile + grp * KT;
       const uint32_t dst = smem_at(kv + stage * S::kStage);
       unsigned seen = 0;  // the places that a token sees, on pages of the pool
       if (a.t.shift >= 4) {  // a page holds 16 places in a row
         const char *k[KM], *v[KM];
         int have[KM];
-        bool full = true;
 #pragma unroll
         for (int u = 0; u < KM; ++u) {
           const unsigned p = pos + u * 16;
-          const bool some = p < (unsigned)ahead.hi && p + 16 > (unsigned)ahead.first;
+          const bool some = p < (unsigned)ahead.hi;
           const bool ok = some && (unsigned)ids[u] < (unsigned)a.t.num_pages;
           have[u] = ok ? (int)min(16u, (unsigned)ahead.hi - p) : 0;
-          if (some && !ok) bad = 1;
-          full &= have[u] == 16;
-          const int before = min(max(ahead.first - (int)p, 0), 15);  // no token sees these
-          seen |= (((1u << have[u]) - 1) >> before << before) << (u * 16);
+          if (some && !ok && p + 16 > (unsigned)ahead.first) bad = 1;
+          seen |= ((1u << have[u]) - 1) << (u * 16);
           const int64_t row = ((int64_t)ahead.head << a.t.shift) + (p & mask);
           const int64_t from = ok ? (ids[u] * a.ldpage + row * D) * S::kElem : 0;
           k[u] = static_cast<const char*>(a.kc) + from;
@@ -376,6 +373,11 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
           }
         }
         constexpr int kTurns = KT * CH / 32 / WM, kRowsOf = 32 / CH;
+        const bool full = seen == kAll;
+        if (pos < (unsigned)ahead.first) {  // no token sees these
+          const unsigned before = min(ahead.first - pos, 31u);
+          seen = seen >> before << before;
+        }
         if (full) {
 #pragma unroll
           for (int i = 0; i < kTurns; ++i) {
@@ -398,7 +400,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll 1
         for (int i = 0; i < KT * CH / 32 / WM; ++i) {
           const int x = (i * WM + wm) * 32 + lane, r = x / CH, c = x % CH;
-          const int id = pos + r < (unsigned)ahead.hi && pos + r >= (unsigned)ahead.first ? page_of(a.t, ahead.n, pos + r) : -1;
+          const int id = pos + r < (unsigned)ahead.hi ? page_of(a.t, ahead.n, pos + r) : -1;
           const int64_t row = ((int64_t)ahead.head << a.t.shift) + ((pos + r) & mask);
           const int64_t from = id >= 0 ? (id * a.ldpage + row * D) * S::kElem + c * 16 : 0;
           copy16(dst + key_piece<CH, kF32>(r, c) * 16, static_cast<const char*>(a.kc) + from, id >= 0);
@@ -449,7 +451,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         s.last[blockIdx.x] = (st.end - now.left + now.tiles - 1) / st.share;
       }
     }
-    if (kCoded) __syncthreads();  // other caches: behind the item before
+    __syncthreads();
     constexpr int kTurns = S::kRows / (S::kThreads / 32);  // rows of a warp, all loaded before the first is used
     using Pair = std::conditional_t<FQ, float2, __nv_bfloat162>;
     Pair held[kTurns][D / 64];
@@ -576,7 +578,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       const int now_stage = stage;
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
       if (some == 0) continue;
-      const int first = (int)((unsigned)now.lo + (unsigned)t * S::kTile), pos = (int)((unsigned)first + grp * KT);
+      const int first = (int)((unsigned)now.template lo<S::kTile>() + (unsigned)t * S::kTile), pos = (int)((unsigned)first + grp * KT);
       const bool edge = all != kAll || (SHARE ? first > hi_min - S::kTile || first < lo_max : pos > hi_min - KT || pos < lo_max);
       const uint32_t kbase = smem_at(here), vbase = kbase + S::kHalf;
       // ---- scores: c[places][queries]
@@ -933,6 +935,15 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
     const bool whole = t0 == 0 && t1 == now.tiles;
     float2* const stats = reinterpret_cast<float2*>(raw + S::oStats);  // [groups][rows]: maximum, sum
     float scale_by[NT][2];
+    float odd = 0.f;  // plus 0 times the sums: NaN where one is not finite
+    if constexpr (!kCoded) {
+#pragma unroll
+      for (int i = 0; i < OB; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) odd = fmaf(o[i][j][e], 0.f, odd);
+    }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -948,7 +959,7 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         }
         if (g == 0) stats[grp * S::kRows + (wm * NT + j) * 8 + 2 * t4 + e] = make_float2(m, sum);
       }
-    __syncthreads();
+    const bool wild_sums = __syncthreads_or(odd != odd);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -982,7 +993,6 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
         a.lse[out0 + row_place[tid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
       }
     }
-    float odd = 0.f;  // plus 0 times what is stored: NaN where one is not finite
     if constexpr (SHARE) {  // each warp has the sums of its channels
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -999,7 +1009,6 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
 #pragma unroll
           for (int i = 0; i < OB; ++i) {
             const float x = o[i][j][e] * f, z = o[i][j][2 + e] * f;
-            if (!kCoded) odd = fmaf(x, 0.f, fmaf(z, 0.f, odd));
             const int ch = (grp * OB + i) * 16 + (kNext ? 2 * g : g), next = kNext ? 1 : 8;
             if (!whole) {
               part[2 * S::kRows + r * D + ch] = x;
@@ -1056,7 +1065,6 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
             v.x += w.x;
             v.y += w.y;
           }
-          if (!kCoded) odd = fmaf(v.x, 0.f, fmaf(v.y, 0.f, odd));
           if (whole) {
             TQ* to = static_cast<TQ*>(a.out) + (out0 + row_place[r]) * D + q * kSlice + ch;
             if (words && FQ) {
@@ -1074,9 +1082,10 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
       }
     }
     if constexpr (!kCoded) {
-      if (__syncthreads_or(odd != odd)) {
+      if (wild_sums) {
+        __syncthreads();
         using TC = std::conditional_t<kF32, float, __nv_bfloat16>;
-        const int from = now.lo + t0 * S::kTile, to = (int)min((int64_t)now.lo + (int64_t)t1 * S::kTile, (int64_t)now.hi);
+        const int from = now.template lo<S::kTile>() + t0 * S::kTile, to = (int)min((int64_t)now.template lo<S::kTile>() + (int64_t)t1 * S::kTile, (int64_t)now.hi);
 #pragma unroll 1
         for (int i = tid; i < rows * D; i += S::kThreads) {
           const int r = i / D, end = row_end[r];
@@ -1091,7 +1100,6 @@ attn_mma_kernel(AttnArgs a, Split s, bool words) {
           if (whole) *at = from_f32<TQ>(wild);
           else part[2 * S::kRows + i] = wild;
         }
-        __syncthreads();
       }
     }
     now.pass(a, s, t1 - t0);
