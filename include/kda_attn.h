@@ -157,18 +157,18 @@ typedef struct {
 /* q [B,T,q_heads,d], out the same, dense; lse f32 [B,T,q_heads] or NULL.
  * Places that a token would see on a page that is not in the pool count as unseen
  * and are reported (KDA_ERR_INVALID_ARG), as is a lens past the table (the places
- * that it has are seen); the table's other entries may hold anything.  The keys are split over the device by equal numbers of tiles and
- * the parts joined in a fixed order: results repeat bit for bit on one device.
- * Sums and statistics are float32.  With bf16 the scores are exact products in
- * float32, and the weights enter the second product with 16 bits over a bf16
- * cache and with 11 over one of 8 bits; with float32 products keep 22 bits
- * over an 8-bit cache and 24 over a float32 one.  Over 8 bits what counts for a
- * query row is its weight times the value row's power of two: 11 (22) bits for
+ * that it has are seen); the table's other entries may hold anything.  The keys are
+ * split over the device by equal numbers of tiles and the parts joined in a fixed
+ * order: results repeat bit for bit on one device.  Sums and statistics are float32.
+ * With bf16 the scores are exact products in float32, and the weights enter the
+ * second product with 16 bits over a bf16 cache and over one of 8 bits with 22 up to
+ * 8 query rows (T q_heads / kv_heads) and with 11 from 9 on; with float32 products
+ * keep 22 bits over an 8-bit cache and 24 over a float32 one.  Over 8 bits what counts
+ * for a query row is its weight times the value row's power of two: 11 (22) bits for
  * products down to 2^-23 of its largest, 2^-34 of that for those below.  Where all
  * that it sees has powers below 2^-87 (values below 2^-78), bits are lost.
- * workspace:
- * 256-byte aligned, kda_attn_workspace_size(s) bytes; where those are 256 they
- * hold the status alone and may be left out (NULL, 0). */
+ * workspace: 256-byte aligned, kda_attn_workspace_size(s) bytes; where those are 256
+ * they hold the status alone and may be left out (NULL, 0). */
 size_t kda_attn_workspace_size(const kda_attn_shape* s);
 kda_status kda_attn_step(const kda_attn_shape* s, const void* q, const void* k_cache,
                          const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,

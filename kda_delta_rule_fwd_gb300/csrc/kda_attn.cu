@@ -22,7 +22,9 @@
 // exactly; queries become f16 after a power of two per row has brought their largest to 2^13,
 // which keeps every bit down to 2^-27 of it.  A value's power of two joins its weight, and a query
 // row's base follows the largest product of the two that it meets, which f16 gets as 2^9 to 2^15:
-// products down to 2^-23 of the largest keep all 11 bits, what is below is off by 2^-34 of it at most.
+// products down to 2^-23 of the largest keep all 11 bits, what is below is off by 2^-34 of it at most.  Up to
+// 8 rows, where the bytes bind, a second f16 part makes them 22 bits (4 rows over e4m3 195 us with one part or
+// two; 16 rows 201 and 215, 32 rows 298 and 365, 64 rows 507 and 668: one part from 9 rows on).
 // A row of large power takes nothing from the others where its weight is small or it is not seen.
 // (With 2^11 to 2^15 the bases move more often: 32 and 64 rows over int8 330 and 582 us, now 316 and
 // 528, with 2^7 to 2^15 312 and 517.)  The sum of weights is float32 and counts from the same base: its
@@ -232,7 +234,7 @@ template <bool FQ, int CACHE, int D, int NT, int WM, int KT, int PER, bool SHARE
 struct Shape {
   static constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8, kF32 = CACHE == KDA_CACHE_F32;
   // 16-bit parts of a key or value, of a query, of a weight
-  static constexpr int kParts = kF32 ? 3 : 1, kQParts = kF32 ? 3 : FQ ? 2 : 1, kWParts = kF32 ? 3 : kCoded && !FQ ? 1 : 2;
+  static constexpr int kParts = kF32 ? 3 : 1, kQParts = kF32 ? 3 : FQ ? 2 : 1, kWParts = kF32 ? 3 : kCoded && !FQ && NT > 1 ? 1 : 2;
   static constexpr int kThreads = kGroups * WM * 32, kPerSm = PER;
   static constexpr int kRows = 8 * NT * WM, kTile = kGroups * KT, kCost = item_cost(NT) / kTile;
   static constexpr int kElem = kCoded ? 1 : kF32 ? 4 : 2;
