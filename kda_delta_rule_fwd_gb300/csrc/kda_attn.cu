@@ -26,9 +26,9 @@
 // 8 rows, where the bytes bind, a second f16 part makes them 22 bits (4 rows over e4m3 195 us with one part or
 // two; 16 rows 201 and 215, 32 rows 298 and 365, 64 rows 507 and 668: one part from 9 rows on).
 // A row of large power takes nothing from the others where its weight is small or it is not seen.
-// (With 2^11 to 2^15 the bases move more often: 32 and 64 rows over int8 330 and 582 us, now 316 and
-// 528, with 2^7 to 2^15 312 and 517.)  The sum of weights is float32 and counts from the same base: its
-// terms fall with the largest power (2^-112 for 2^121, the largest there is).  A base stays within 2^103
+// (With 2^11 to 2^15 the bases move more often: 32 and 64 rows over int8 330 and 582 us, with 2^9 320 and
+// 532, with 2^7 316 and 520.)  The sum of weights is float32 and counts from the same base: its terms fall
+// with the largest power (2^-112 for 2^121, the largest that is written).  A base stays within 2^103
 // of the largest weight, so that sums of weights of rows of zeros (power 2^-126) stay finite: where all
 // that a row sees has powers below 2^-87, they keep fewer bits.
 //
@@ -1128,7 +1128,7 @@ cudaError_t launch(Shape<FQ, CACHE, D, NT, WM, KT, PER, SHARE>, const AttnArgs& 
 // and 2 blocks 488 (before the ends were weighed in); 131071 bf16 places: 3 blocks 92, 2 blocks 94;
 // 16 sequences of up to 32768 int8 places, 32 rows: shared weights with 3 blocks to an SM 148, with 4
 // or 2 blocks 160, all channels in each warp 172; 32 sequences of 8192 bf16 places, 32 and 64 rows:
-// shared 226 and 353, not shared 273 and 385.
+// shared 226 and 353, not shared 273 and 385 (shared today 210 and 352; the int8 case 154).
 template <int CACHE, int D, class F>
 auto by_rows(const AttnArgs& a, F f) {
   constexpr bool kCoded = CACHE == KDA_CACHE_E4M3 || CACHE == KDA_CACHE_INT8;
